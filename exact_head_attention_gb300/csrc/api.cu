@@ -13,6 +13,7 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/exattn.h"
+#include "api_internal.h"
 #include "fwd_schedule.h"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -503,6 +504,7 @@ extern "C" const char* attn_status_string(attn_status status) {
     case ATTN_ERR_TIMEOUT: return "a bounded device wait expired";
     case ATTN_ERR_WORKSPACE: return "workspace missing or too small";
     case ATTN_ERR_NOT_IMPLEMENTED: return "not implemented";
+    case ATTN_ERR_PAGE: return "a cache page number or length out of range";
   }
   return "unknown status";
 }
@@ -520,6 +522,11 @@ extern "C" attn_status attn_check_device_error(void* stream) {
     const uint32_t zero = 0;
     if ((e = cudaMemcpy(ds->err_word, &zero, sizeof(zero), cudaMemcpyHostToDevice)) != cudaSuccess)
       return cuda_fail("cudaMemcpy(error word)", e);
+    if (code == kErrPage) {
+      std::snprintf(g_last_error, sizeof(g_last_error),
+                    "device error word 9: a cache call met a page number outside the pool, or a length outside its page table");
+      return ATTN_ERR_PAGE;
+    }
     if (code == 8) {
       std::snprintf(g_last_error, sizeof(g_last_error), "device error word 8: dynamic shared memory not 1024-byte aligned");
       return ATTN_ERR_CUDA;
@@ -935,4 +942,36 @@ extern "C" attn_status attn_kl_fwd_splitkv(const void* Q1, const void* K1, const
   a.splits = num_splits;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return finish(launch_kl_fwd(a, s), s);
+}
+
+// ----------------------------------------------------------------- shared with the other C-ABI units
+
+attn_status exattn::api_device(DeviceInfo* out) {
+  DeviceState* ds = nullptr;
+  const attn_status st = device_state(&ds);
+  if (st != ATTN_OK) return st;
+  *out = DeviceInfo{ds->err_word, ds->sm_count};
+  return ATTN_OK;
+}
+
+int exattn::api_sm_count() { return device_sm_count(); }
+
+uint64_t exattn::api_wait_timeout_ns() { return wait_timeout_ns(); }
+
+attn_status exattn::api_finish(cudaError_t e, cudaStream_t stream) { return finish(e, stream); }
+
+attn_status exattn::api_driver_fail(const char* what, int code) { return driver_fail(what, code); }
+
+bool exattn::api_strides(const attn_strides& in, int B, int H, int d, RowStrides* out) {
+  return normalise_strides(in, B, H, d, out);
+}
+
+CUresult exattn::api_encode_lines(CUtensorMap* map, const void* base, uint64_t lines, uint32_t box_lines) {
+  const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(lines)};
+  const cuuint64_t strides[1] = {128};
+  const cuuint32_t box[2] = {128, box_lines};
+  const cuuint32_t estr[2] = {1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }

@@ -121,6 +121,45 @@ struct KlArgs {
   uint64_t timeout_ns;
 };
 
+// The 8-bit key/value cache (attn_cache) as the kernels take it.
+struct CacheView {
+  uint8_t *k, *v;            // [num_pages][heads][page][d] codes
+  float *k_scale, *v_scale;  // [num_pages][heads]
+  const int* table;          // [B][width]
+  int num_pages, heads, page_shift, d, width;
+  int capacity;  // tokens a table row can name: width << page_shift, at most 2^31 - 1
+  int format;    // attn_cache_format
+};
+
+struct CacheIoArgs {
+  CacheView c;
+  void *k, *v;  // 16-bit [B][heads][N][d], strides sk and sv
+  RowStrides sk, sv;
+  const int *start, *count;  // write: may be nullptr; read: count is lens
+  int B, N;
+  bool bf16;
+  uint32_t* err_word;
+};
+
+// Attention over the cache.  The query rows of a key/value head are its group's heads and the Nq tokens
+// together: row r is token r / group and head r % group of the group, so that the causal limit grows
+// with r.
+struct CacheAttnArgs {
+  CUtensorMap tm_k, tm_v;  // 2-D byte maps {128, lines} over the codes, box {128, lines of box_tokens tokens}
+  CacheView c;
+  const void* q;
+  void* o;
+  RowStrides sq, so;
+  const int* lens;
+  float* lse;     // [B][heads * group][Nq]
+  uint8_t* ws;    // cache_ws_* below
+  uint32_t* err_word;
+  int B, Nq, group, mask, sm_count;
+  bool bf16;
+  float scale;
+  uint64_t timeout_ns;
+};
+
 // Backward steps (bit mask for launch_bwd).  The atomic dQ mode runs pre, main, convert; the
 // deterministic mode (dq_acc == nullptr) runs pre, main (dK and dV only), then the dQ kernel.
 constexpr int kBwdPre = 1, kBwdMain = 2, kBwdConvert = 4, kBwdAll = 7, kBwdDq = 8;
@@ -140,5 +179,11 @@ cudaError_t launch_kl_dk(const KlArgs& a, cudaStream_t stream);
 // Row values + zeroed accumulator, then the one-pass key-tile kernel (dK and the dQ reduce-adds); the
 // caller converts the accumulator with the attention backward's kBwdConvert step.
 cudaError_t launch_kl_bwd_fused(const KlArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_write(const CacheIoArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheIoArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream);
+// Tokens per box of the tensor maps launch_cache_attn wants, and its workspace bytes.
+int cache_attn_box_tokens(int page);
+size_t cache_attn_workspace(int B, int rows, int d, int sm_count);
 
 }  // namespace exattn

@@ -17,7 +17,8 @@ LIB_PATH = os.path.join(_PKG, "libexattn.so")
 
 ATTN_OK = 0
 STATUS_NAMES = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ERR_MISALIGNED",
-                4: "ATTN_ERR_CUDA", 5: "ATTN_ERR_TIMEOUT", 6: "ATTN_ERR_WORKSPACE", 7: "ATTN_ERR_NOT_IMPLEMENTED"}
+                4: "ATTN_ERR_CUDA", 5: "ATTN_ERR_TIMEOUT", 6: "ATTN_ERR_WORKSPACE", 7: "ATTN_ERR_NOT_IMPLEMENTED",
+                8: "ATTN_ERR_PAGE"}
 ATTN_BF16, ATTN_FP16 = 0, 1
 # attn_mask: none, top-left causal (query q sees keys k <= q), bottom-right causal (k <= q + Nk - Nq)
 ATTN_MASK_NONE, ATTN_MASK_CAUSAL, ATTN_MASK_CAUSAL_BOTTOM_RIGHT = 0, 1, 2
@@ -34,6 +35,12 @@ _lib = None
 class Strides(ctypes.Structure):
     """attn_strides: element strides of a [B][H][N][d] view with contiguous d."""
     _fields_ = [("batch", ctypes.c_longlong), ("head", ctypes.c_longlong), ("row", ctypes.c_longlong)]
+
+
+class CacheStruct(ctypes.Structure):
+    """attn_cache"""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "page_table")]
+                + [(n, ctypes.c_int) for n in ("num_pages", "heads", "page_size", "d", "table_width", "format")])
 
 
 class AttnError(RuntimeError):
@@ -107,6 +114,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                 fn = getattr(lib, name)
                 fn.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, vp, sz, vp]
                 fn.restype = i
+            cp = ctypes.POINTER(CacheStruct)
+            lib.attn_cache_write.argtypes = [cp, vp, st, vp, st, vp, vp, i, i, i, vp]
+            lib.attn_cache_write.restype = i
+            lib.attn_cache_read.argtypes = [cp, vp, vp, vp, st, vp, st, i, i, i, vp]
+            lib.attn_cache_read.restype = i
+            lib.attn_fwd_cache.argtypes = [vp, st, cp, vp, vp, st, vp, i, i, i, i, f, i, vp, sz, vp]
+            lib.attn_fwd_cache.restype = i
+            lib.attn_fwd_cache_workspace_size.argtypes = [cp, i, i, i]
+            lib.attn_fwd_cache_workspace_size.restype = sz
             lib.attn_status_string.argtypes = [i]
             lib.attn_status_string.restype = ctypes.c_char_p
             lib.attn_check_device_error.argtypes = [vp]
@@ -480,3 +496,166 @@ def attention_kl(q1, k1, q2, k2, causal=False, scale: float | None = None, train
     """Autograd-aware row-wise KL(P1 || P2) [B,H,Nq]; gradients flow to the trained distribution only."""
     scale = (1.0 / q1.shape[-1] ** 0.5) if scale is None else scale
     return _KlFunction.apply(q1, k1, q2, k2, causal, scale, train, dq_mode)
+
+
+# ------------------------------------------------------------------ 8-bit key/value cache
+
+CACHE_FORMATS = {"e4m3": 0, "int8": 1}
+_CACHE_DTYPES = {torch.float8_e4m3fn: 0, torch.int8: 1}
+
+
+class QuantCache:
+    """An 8-bit key/value cache in pages (attn_cache): the caller's tensors and the struct the library takes.
+
+    k, v: [num_pages, heads, page, d] float8_e4m3fn or int8 codes; k_scale, v_scale: [num_pages, heads] fp32; a
+    code stands for code * scale of its page and head.  page_table: [B, width] int32, the pages of each sequence
+    in order.  All contiguous, on one CUDA device; the tensors are used in place."""
+    __slots__ = ("k", "v", "k_scale", "v_scale", "page_table", "device", "struct", "_ref")
+
+    def __init__(self, k, v, k_scale, v_scale, page_table):
+        fmt = _CACHE_DTYPES.get(k.dtype)
+        if fmt is None or v.dtype != k.dtype:
+            raise TypeError(f"unsupported cache dtypes {k.dtype}, {v.dtype}; expected float8_e4m3fn or int8 for both")
+        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or page_table.dtype != torch.int32:
+            raise TypeError("scales must be float32 and the page table int32")
+        if k.dim() != 4 or v.shape != k.shape or page_table.dim() != 2:
+            raise ValueError("k, v must be [num_pages, heads, page, d] and the page table [B, width]")
+        pages, heads, page, d = k.shape
+        if k_scale.shape != (pages, heads) or v_scale.shape != (pages, heads):
+            raise ValueError("scales must be [num_pages, heads]")
+        device = k.device
+        for t in (k, v, k_scale, v_scale, page_table):
+            if not t.is_cuda or t.device != device or not t.is_contiguous():
+                raise ValueError("cache tensors must be contiguous and on one CUDA device")
+        self.k, self.v, self.k_scale, self.v_scale, self.page_table, self.device = k, v, k_scale, v_scale, page_table, device
+        self.struct = CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                  page_table.data_ptr(), pages, heads, page, d, page_table.shape[1], fmt)
+        self._ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def empty(cls, num_pages: int, heads: int, page: int, d: int, page_table, format: str = "e4m3"):
+        """A cache of zeros on the page table's device."""
+        if format not in CACHE_FORMATS:
+            raise ValueError(f"unknown cache format {format!r}")
+        dtype = {0: torch.float8_e4m3fn, 1: torch.int8}[CACHE_FORMATS[format]]
+        dev = page_table.device
+        k, v = (torch.zeros((num_pages, heads, page, d), dtype=torch.uint8, device=dev).view(dtype) for _ in range(2))
+        ks, vs = (torch.zeros((num_pages, heads), dtype=torch.float32, device=dev) for _ in range(2))
+        return cls(k, v, ks, vs, page_table)
+
+
+def _int32(t, B: int, device, name: str):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.shape != (B,) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of one entry a sequence on the cache's device")
+    return t.data_ptr()
+
+
+def _cache_views(cache: QuantCache, *ts):
+    """Checks 16-bit [B, heads or H, N, d] views against the cache; the views' batch size."""
+    B = cache.page_table.shape[0]
+    for t in ts:
+        if t.dim() != 4 or t.shape[0] != B or t.shape[3] != cache.struct.d:
+            raise ValueError("tensors must be [B, H, N, d] with the page table's B and the cache's d")
+        if t.device != cache.device or t.dtype != ts[0].dtype:
+            raise ValueError("tensors must be of one dtype, on the cache's device")
+    return B
+
+
+class _On:
+    """The device of `cache` current, and `stream` where one is given: what is allocated inside belongs to it."""
+    __slots__ = ("guards",)
+
+    def __init__(self, cache, stream):
+        self.guards = []
+        if cache.device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(cache.device))
+        if stream is not None:
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+
+    def __exit__(self, *e):
+        for g in reversed(self.guards):
+            g.__exit__(*e)
+
+
+def cache_write(cache: QuantCache, k, v, start=None, count=None, stream=None) -> None:
+    """Quantises new tokens into the cache (attn_cache_write).
+
+    k, v: [B, heads, N, d] bf16 or fp16, last dimension contiguous.  Row n of sequence b becomes its token
+    start[b] + n for n < count[b]; start None: 0, count None: N (int32 CUDA tensors otherwise).  Tokens that a
+    reached page already holds keep their codes, or are rounded again where its scale has to grow."""
+    B = _cache_views(cache, k, v)
+    if k.shape != v.shape or k.shape[1] != cache.struct.heads:
+        raise ValueError("k and v must be [B, heads, N, d] with the cache's heads")
+    if k.shape[2] == 0 or B == 0:
+        return
+    with _On(cache, stream):
+        st = load().attn_cache_write(cache._ref, *_view(k), *_view(v), _int32(start, B, cache.device, "start"),
+                                     _int32(count, B, cache.device, "count"), B, k.shape[2], _dtype_code(k),
+                                     _stream(stream))
+    _check(st, "attn_cache_write")
+
+
+def cache_read(cache: QuantCache, lens, rows: int | None = None, start=None, dtype=torch.bfloat16, out=None, stream=None):
+    """Cached tokens back in 16 bits (attn_cache_read): (K, V) [B, heads, rows, d], row n the token start[b] + n.
+
+    Rows at or past lens[b] are left as they were in `out`, a pair of views whose dtype and rows are then taken;
+    without it the result is allocated with zeros in them."""
+    B, heads, d = cache.page_table.shape[0], cache.struct.heads, cache.struct.d
+    with _On(cache, stream):
+        if out is None:
+            if rows is None:
+                raise ValueError("rows or out is needed")
+            out = tuple(torch.zeros((B, heads, rows, d), dtype=dtype, device=cache.device) for _ in range(2))
+        k, v = out
+        _cache_views(cache, k, v)
+        if k.shape != v.shape or k.shape[1] != heads:
+            raise ValueError("outputs must be [B, heads, N, d] with the cache's heads")
+        if k.shape[2] == 0 or B == 0:
+            return k, v
+        st = load().attn_cache_read(cache._ref, _int32(start, B, cache.device, "start"),
+                                    _int32(lens, B, cache.device, "lens"), *_view(k), *_view(v), B, k.shape[2],
+                                    _dtype_code(k), _stream(stream))
+    _check(st, "attn_cache_read")
+    return k, v
+
+
+def cache_workspace_size(cache: QuantCache, H: int, Nq: int) -> int:
+    """Workspace bytes of forward_cache (attn_fwd_cache_workspace_size)."""
+    return int(load().attn_fwd_cache_workspace_size(cache._ref, cache.page_table.shape[0], H, Nq))
+
+
+def fwd_cache_raw(q, cache: QuantCache, lens, o, lse, causal, scale: float, workspace, stream=None) -> int:
+    """Calls attn_fwd_cache on caller-provided tensors; returns the status code."""
+    B, H, Nq, _ = q.shape
+    return load().attn_fwd_cache(*_view(q), cache._ref, _int32(lens, B, cache.device, "lens"), *_view(o), _ptr(lse),
+                                 B, H, Nq, mask_code(causal), float(scale), _dtype_code(q), *_workspace(workspace),
+                                 _stream(stream))
+
+
+def forward_cache(q, cache: QuantCache, lens, causal="bottom_right", scale: float | None = None, workspace=None,
+                  stream=None):
+    """O [B,H,Nq,d] and LSE [B,H,Nq] fp32 of attention over the first lens[b] cached tokens of every sequence.
+
+    q: [B, H, Nq, d] bf16 or fp16, H a multiple of the cache's heads (query head h reads key/value head
+    h // (H // heads)).  causal "bottom_right" (the default): the queries are a sequence's last Nq tokens; also
+    False and True (top-left) as in forward().  lens: int32 CUDA tensor [B].  `workspace` (uint8 CUDA tensor of
+    cache_workspace_size bytes, one for each call that may run at the same time) is allocated if omitted."""
+    B = _cache_views(cache, q)
+    H, Nq = q.shape[1], q.shape[2]
+    scale = (1.0 / cache.struct.d ** 0.5) if scale is None else scale
+    with _On(cache, stream):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=cache.device)
+        if q.numel() == 0:
+            return o, lse
+        if workspace is None:
+            workspace = torch.empty(cache_workspace_size(cache, H, Nq), dtype=torch.uint8, device=cache.device)
+        st = fwd_cache_raw(q, cache, lens, o, lse, causal, scale, workspace, stream)
+    _check(st, "attn_fwd_cache")
+    return o, lse

@@ -62,7 +62,9 @@ typedef enum {
   ATTN_ERR_CUDA = 4,            /* a CUDA runtime/driver call or launch failed */
   ATTN_ERR_TIMEOUT = 5,         /* a bounded device wait expired (kernel exited early) */
   ATTN_ERR_WORKSPACE = 6,       /* workspace null or smaller than attn_bwd_workspace_size */
-  ATTN_ERR_NOT_IMPLEMENTED = 7
+  ATTN_ERR_NOT_IMPLEMENTED = 7,
+  ATTN_ERR_PAGE = 8             /* device error word: a cache call met a page number outside the pool, or a
+                                   length outside its page table (see attn_cache) */
 } attn_status;
 
 typedef enum { ATTN_BF16 = 0, ATTN_FP16 = 1 } attn_dtype;
@@ -507,6 +509,120 @@ attn_status attn_bwd_noalloc(const void* Q, const void* K, const void* V, const 
                              const float* LSE, void* dQ, void* dK, void* dV,
                              int B, int H, int Nq, int Nk, int d, int causal, float scale,
                              attn_dtype dtype, void* stream);
+
+/*
+ * The 8-bit key/value cache: its store (attn_cache_write), its reader
+ * (attn_cache_read) and the attention over it (attn_fwd_cache).  Keys and
+ * values of B sequences lie in pages of page_size tokens.  A page holds, for
+ * every key/value head, page_size x d one-byte codes and one fp32 scale for
+ * the keys and one for the values; a code c stands for c * scale.
+ *   k, v             [num_pages][heads][page_size][d] codes, 16-byte aligned
+ *   k_scale, v_scale [num_pages][heads] fp32
+ *   page_table       [B][table_width] int32 on the device: token t of sequence
+ *                    b lies in page page_table[b][t / page_size], row
+ *                    t % page_size.  Entries past a sequence's last page are
+ *                    not read.  A page may stand in several sequences' tables
+ *                    (a shared prefix), but a write must reach each page from
+ *                    one sequence only.
+ *   heads            key/value heads; page_size 16, 32, 64 or 128; d 64 or 128
+ * num_pages * heads * page_size * d / 128 must be below 2^31.
+ * Lengths and positions are int32 arrays on the device, so that a captured
+ * graph follows them; their values are checked there.  A length below 0
+ * counts as 0 and one past table_width * page_size as that; a page number
+ * outside [0, num_pages) makes its tokens NaN when read and keeps them from
+ * being written.  Each of these records ATTN_ERR_PAGE in the device error word
+ * (attn_check_device_error); no memory outside the arrays is touched.
+ * The pages of the reference describe caches in the attention's own type only;
+ * the 8-bit cache has no counterpart there.
+ */
+typedef enum {
+  ATTN_CACHE_E4M3 = 0, /* 8-bit floats, 4 exponent and 3 mantissa bits, largest 448 */
+  ATTN_CACHE_INT8 = 1  /* integers, written in [-127, 127] */
+} attn_cache_format;
+
+typedef struct attn_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  const int* page_table;
+  int num_pages;
+  int heads;
+  int page_size;
+  int d;
+  int table_width;
+  int format; /* an attn_cache_format value */
+} attn_cache;
+
+/*
+ * Quantises new tokens into the cache.  K, V: [B, heads, N, d] 16-bit views
+ * (attn_strides); row n of sequence b becomes its token start[b] + n, for
+ * n < count[b].  start NULL: every sequence starts at 0; count NULL: N rows of
+ * every sequence.  For each page and head that the new tokens reach, and for
+ * keys and values apart:
+ *   a = max |x| over the new tokens in the page
+ *   f = a * u with u the fp32 number nearest 1/448 (E4M3) or 1/127 (INT8);
+ *       0 where that is below 2^-126
+ *   s = f where no token before start[b] lies in the page, else max(old scale, f)
+ *   new codes      round(x * (1 / s)), nearest even, at most the largest code
+ *   earlier codes  round(code * (old scale * (1 / s))) where s > old scale,
+ *                  else unchanged
+ * in fp32; with s = 0 the codes are 0.  A NaN or infinity among a page's new
+ * values makes that page's scale for the head NaN: all its tokens read as NaN.
+ * Rows of a page past start + count keep their codes.  A sequence whose start
+ * is negative, or the part of one past its page table, is not written
+ * (ATTN_ERR_PAGE in the error word); count[b] is taken within [0, N].  One
+ * launch; no workspace.  Errors as attn_fwd_strided, plus ATTN_ERR_INVALID_ARG
+ * for a cache that breaks the rules above.  The pages have no counterpart.
+ */
+attn_status attn_cache_write(const attn_cache* cache, const void* K, attn_strides k_strides, const void* V,
+                             attn_strides v_strides, const int* start, const int* count, int B, int N,
+                             attn_dtype dtype, void* stream);
+
+/*
+ * Reads cached tokens back: row n of K and V ([B, heads, N, d] 16-bit views)
+ * of sequence b becomes code * scale of its token start[b] + n, rounded to the
+ * dtype, where that token is below lens[b]; other rows are left as they were.
+ * start NULL: 0 for every sequence.  A negative start counts as 0
+ * (ATTN_ERR_PAGE in the error word).  One launch; no workspace.  Errors as
+ * attn_cache_write.  The pages have no counterpart.
+ */
+attn_status attn_cache_read(const attn_cache* cache, const int* start, const int* lens, void* K,
+                            attn_strides k_strides, void* V, attn_strides v_strides, int B, int N, attn_dtype dtype,
+                            void* stream);
+
+/*
+ * Attention over the cache: O and LSE of attn_fwd, with the keys and values of
+ * sequence b its first lens[b] cached tokens (Nk = lens[b] in the mask's
+ * rules, so ATTN_MASK_CAUSAL_BOTTOM_RIGHT makes the Nq queries a sequence's
+ * last tokens).  Q, O: [B, H, Nq, d] 16-bit views; LSE [B, H, Nq] fp32.  H is
+ * a multiple of cache->heads, and query head h reads key/value head
+ * h / (H / cache->heads).  A row that sees no token gets O = 0, LSE = -inf.  A
+ * NaN token makes the rows that see it NaN, and no others.
+ * The codes are multiplied as they are (fp16 holds every code exactly) and the
+ * scales applied to the products; Q in bf16 is scaled by a power of two per
+ * row to fit fp16; the probabilities are rounded to fp16, sums are fp32.  The
+ * same bits on every run.
+ * workspace: attn_fwd_cache_workspace_size bytes, 256-byte aligned, contents
+ * on entry irrelevant; calls that may run at the same time need one each.
+ * Errors as attn_fwd_strided, plus ATTN_ERR_INVALID_ARG for a cache that
+ * breaks the rules of attn_cache or an H that is no multiple of its heads, and
+ * ATTN_ERR_WORKSPACE.  The division of the key axis over the SMs and the merge
+ * of its parts by their log-sum-exp follow the StreamKL summary's split-K
+ * variant; the cache has no counterpart on the pages.
+ */
+attn_status attn_fwd_cache(const void* Q, attn_strides q_strides, const attn_cache* cache, const int* lens, void* O,
+                           attn_strides o_strides, float* LSE, int B, int H, int Nq, int causal, float scale,
+                           attn_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Workspace bytes of attn_fwd_cache on the current device: the fp32 partial
+ * results of rows whose keys are divided between SMs, and the division itself.
+ * It does not depend on the lengths.  0 for invalid arguments or where no
+ * device answers.  The partial results are the per-slice state of the StreamKL
+ * summary's split-K variant; the pages do not size them.
+ */
+size_t attn_fwd_cache_workspace_size(const attn_cache* cache, int B, int H, int Nq);
 
 /* Static description of a status code (a diagnostic of this library; the
  * pages have no counterpart).  Never NULL: unknown codes give

@@ -279,3 +279,82 @@ def test_every_entry_point_is_documented_with_its_source():
         cites = any(p in comment for p in pages) or "no counterpart" in comment
         refers = any(other in comment for other in names if other != name)
         assert cites or refers, f"{name}: its comment neither cites a page nor refers to a documented entry point"
+
+
+# ------------------------------------------------------------------ the 8-bit cache
+
+def _cache(**kw):
+    from exact_head_attention_gb300 import exattn
+    f = dict(k=FAKE, v=FAKE, k_scale=FAKE, v_scale=FAKE, page_table=FAKE, num_pages=10, heads=2, page_size=16, d=64,
+             table_width=4, format=0)
+    f.update(kw)
+    return exattn.CacheStruct(**f)
+
+
+BAD_CACHES = [
+    (dict(k=None), 1), (dict(v=None), 1), (dict(k_scale=None), 1), (dict(v_scale=None), 1), (dict(page_table=None), 1),
+    (dict(num_pages=0), 1), (dict(heads=0), 1), (dict(heads=-2), 1), (dict(table_width=0), 1), (dict(page_size=0), 1),
+    (dict(page_size=24), 1), (dict(page_size=256), 1), (dict(format=2), 1), (dict(format=-1), 1), (dict(d=96), 2),
+    (dict(num_pages=2 ** 31 - 1), 1), (dict(num_pages=2 ** 28, page_size=128, d=128), 1), (dict(k=FAKE + 8), 3),
+    (dict(v=FAKE + 1), 3), (dict(k_scale=FAKE + 2), 3), (dict(v_scale=FAKE + 1), 3), (dict(page_table=FAKE + 3), 3),
+]
+
+
+def _cache_calls(lib, c, B=2, N=3, H=4, Nq=1, dtype=0, causal=2, scale=0.125, x=FAKE, y=FAKE, lens=FAKE, lse=FAKE,
+                 ws=FAKE, ws_bytes=1 << 40, row=64):
+    """Status of the three calls with the given arguments."""
+    from exact_head_attention_gb300 import exattn
+    ref, vp = ctypes.byref(c) if c is not None else None, ctypes.c_void_p
+    st = exattn.Strides(8192, 2048, row)
+    return {
+        "write": lib.attn_cache_write(ref, vp(x), st, vp(y), st, vp(lens), None, B, N, dtype, None),
+        "read": lib.attn_cache_read(ref, None, vp(lens), vp(x), st, vp(y), st, B, N, dtype, None),
+        "attend": lib.attn_fwd_cache(vp(x), st, ref, vp(lens), vp(y), st, vp(lse), B, H, Nq, causal, scale, dtype, vp(ws),
+                                     ws_bytes, None),
+    }
+
+
+@pytest.mark.parametrize("kw,code", BAD_CACHES, ids=str)
+def test_cache_rules(lib, kw, code):
+    got = _cache_calls(lib, _cache(**kw))
+    assert got == {"write": code, "read": code, "attend": code}
+    assert lib.attn_fwd_cache_workspace_size(ctypes.byref(_cache(**kw)), 2, 4, 1) == 0 or code == 3
+
+
+@pytest.mark.parametrize("kw,calls,code", [
+    (dict(B=0), "write read attend", 1), (dict(B=-1), "write read attend", 1), (dict(N=0), "write read", 1),
+    (dict(N=-5), "write read", 1), (dict(H=0), "attend", 1), (dict(H=3), "attend", 1), (dict(Nq=0), "attend", 1),
+    (dict(dtype=2), "write read attend", 1), (dict(x=None), "write read attend", 1), (dict(y=None), "write read attend", 1),
+    (dict(lens=None), "read attend", 1), (dict(lse=None), "attend", 1), (dict(causal=3), "attend", 1),
+    (dict(scale=0.0), "attend", 1), (dict(scale=float("nan")), "attend", 1), (dict(scale=float("inf")), "attend", 1),
+    (dict(x=FAKE + 2), "write read attend", 3), (dict(y=FAKE + 8), "write read attend", 3),
+    (dict(lens=FAKE + 2), "write read attend", 3), (dict(lse=FAKE + 1), "attend", 3), (dict(ws=FAKE + 128), "attend", 3),
+    (dict(ws=None), "attend", 6), (dict(row=63), "write read attend", 1), (dict(row=68), "write read attend", 1),
+    (dict(row=-64), "write read attend", 1), (dict(B=2 ** 30, H=4), "write read attend", 1),
+    (dict(N=2 ** 31 - 1, B=64), "write read", 1), (dict(Nq=2 ** 30, B=2), "attend", 1),
+], ids=str)
+def test_cache_call_rules(lib, kw, calls, code):
+    got = _cache_calls(lib, _cache(), **kw)
+    for name in calls.split():
+        assert got[name] == code, (name, got)
+
+
+def test_null_cache(lib):
+    assert set(_cache_calls(lib, None).values()) == {1}
+    assert lib.attn_fwd_cache_workspace_size(None, 1, 1, 1) == 0
+
+
+def test_cache_binding_refuses_what_it_cannot_pass_on():
+    import torch
+
+    from exact_head_attention_gb300 import exattn
+    k = torch.zeros((4, 2, 16, 64), dtype=torch.int8)
+    s = torch.zeros((4, 2))
+    t = torch.zeros((1, 2), dtype=torch.int32)
+    for args in [(k.float(), k, s, s, t), (k, k.view(torch.float8_e4m3fn), s, s, t), (k, k, s.double(), s, t),
+                 (k, k, s, s, t.long())]:
+        with pytest.raises(TypeError):
+            exattn.QuantCache(*args)
+    for args in [(k[0], k[0], s, s, t), (k, k[:3], s, s, t), (k, k, s[:3], s, t), (k, k, s, s, t[0]), (k, k, s, s, t)]:
+        with pytest.raises(ValueError):  # the last: not on a CUDA device
+            exattn.QuantCache(*args)
