@@ -19,10 +19,16 @@ __device__ __forceinline__ int cache_len(const CacheView& c, int len) {
   return max(0, min(len, c.capacity));
 }
 
-// Page that holds token t (0 <= t < capacity) of sequence b, or -1 for a number outside the pool.
-__device__ __forceinline__ int cache_page(const CacheView& c, int b, int t) {
-  const int p = __ldg(c.table + static_cast<long long>(b) * c.width + (t >> c.page_shift));
+// The table's entry for token t (0 <= t < capacity) of sequence b, and that as a page: -1 for a number
+// outside the pool.
+__device__ __forceinline__ int cache_page_number(const CacheView& c, int b, int t) {
+  return __ldg(c.table + static_cast<long long>(b) * c.width + (t >> c.page_shift));
+}
+__device__ __forceinline__ int cache_page_checked(const CacheView& c, int p) {
   return static_cast<unsigned>(p) < static_cast<unsigned>(c.num_pages) ? p : -1;
+}
+__device__ __forceinline__ int cache_page(const CacheView& c, int b, int t) {
+  return cache_page_checked(c, cache_page_number(c, b, t));
 }
 
 // Four codes as two fp16 pairs: bytes 0, 1 and bytes 2, 3.  fp16 holds every code exactly: e4m3 has 4

@@ -68,13 +68,18 @@ attn_status io_args(const attn_cache* cache, const void* K, attn_strides ks, con
   return ATTN_OK;
 }
 
-// Sizes of attn_fwd_cache; the rows of all heads together are counted in 32 bits by the merge's launch.
+// Sizes of attn_fwd_cache; the rows of all heads together, and the tiles of the longest sequences that the
+// table allows, are counted in 32 bits.
 attn_status check_attn(const attn_cache* cache, int B, int H, int Nq, CacheView* view) {
   if (B <= 0 || H <= 0 || Nq <= 0) return ATTN_ERR_INVALID_ARG;
   const attn_status st = check_cache(cache, view);
   if (st != ATTN_OK) return st;
   if (H % cache->heads != 0) return ATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * H > 0x7fffffffLL / Nq) return ATTN_ERR_INVALID_ARG;
+  const long long rows = static_cast<long long>(H / cache->heads) * Nq;
+  const CacheAttnShape sh = cache_attn_shape(rows, cache->d);
+  const long long items = static_cast<long long>(B) * cache->heads * ((rows + sh.rows - 1) / sh.rows);
+  if (items > 0x7fffffffLL / (view->capacity / sh.keys + kCacheItemCost)) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
 
@@ -138,7 +143,7 @@ extern "C" attn_status attn_fwd_cache(const void* Q, attn_strides q_strides, con
   const int group = H / cache->heads;
   if (workspace_bytes < cache_attn_workspace(B, group * Nq, cache->d, dev.sm_count)) return ATTN_ERR_WORKSPACE;
   const uint64_t lines = static_cast<uint64_t>(cache->num_pages) * cache->heads * cache->page_size * cache->d / 128;
-  const uint32_t box = static_cast<uint32_t>(cache_attn_box_tokens(cache->page_size) * cache->d / 128);
+  const uint32_t box = static_cast<uint32_t>(cache_attn_box_tokens(cache->page_size, cache->d) * cache->d / 128);
   CUresult r;
   if ((r = api_encode_lines(&a.tm_k, cache->k, lines, box)) != CUDA_SUCCESS ||
       (r = api_encode_lines(&a.tm_v, cache->v, lines, box)) != CUDA_SUCCESS)

@@ -3,24 +3,31 @@
 //
 // Mathematics.  With codes k, v and the scales ks, vs of their page, a score is s = c (q . k) ks with
 // c = scale * log2(e), and the online softmax keeps m >= max s - 8, l = sum 2^(s - m) and
-// O = sum 2^(s - m) (vs / vref) v with vref the largest vs met so far, so that the probabilities times
-// vs / vref stay below 2^15 in fp16 whatever the scales are.  The codes enter the products as they are
-// (fp16 holds them exactly).  Pieces of the key axis are merged by their log-sum-exp.
+// O = sum 2^(s - m) (vs / vref) v with vref >= vs / 16 for every vs met so far, so that the probabilities
+// times vs / vref stay below 2^15 in fp16 whatever the scales are.  The codes enter the products as they
+// are (fp16 holds them exactly).  Pieces of the key axis are merged by their log-sum-exp.
 //
 // Bound.  With one to some tens of query rows a key/value head the time is that of reading the codes: 2 d
-// bytes a token and head against 4 d rows flops.  A block (one an SM) therefore keeps up to 128 KB of
-// copies in flight: warp 8 walks the block's share of the work (cache_sched.cuh), looks the pages up and
-// has the copy engine fill a ring of 32-token tiles for each of the eight computing warps.  Each of these
-// owns every eighth tile of a piece and its own (m, l, O), and meets the others only at the end of a
-// piece, where the eight results are joined in shared memory.
+// bytes a token and head against 4 d rows flops.  A block (one an SM) therefore keeps 128 to 192 KB of
+// copies under way: four producer warps walk the block's share of the work (cache_sched.cuh), look the pages
+// up and have the copy engine fill, for each of the 8 or 12 computing warps, a ring of two tiles of 4 KB of
+// keys and 4 KB of values.  A computing warp owns every eighth or twelfth tile of a piece and its own
+// (m, l, O), and meets the others only at the end of a piece, where their results are joined in shared memory.
 //
-// Products.  The tensor cores are far from busy here, so the rows go through the warp-level
-// m16n8k16 product: the rows are its M (16, padded), and both the code-to-fp16 conversion and the operand
-// layout happen in registers:
-//   S = Q K^T: a lane reads 16-byte pieces of its key's row; which 4 d-positions form a k-step is the same
-//     for Q and K, so any order serves, and no transposition is needed.
-//   O = P V: the accumulator layout of S is the operand layout of P; a lane reads 16-byte (d = 128) or
-//     8-byte (d = 64) pieces of the four key rows its B operand wants and pairs their bytes.
+// Measured on GB300 (12 heads of 128, one token over 32k cached tokens of 8 sequences, 805 MB of codes):
+// 129 us, 92 % of the measured copy rate.  From 162 us: four producer warps instead of one (142), 32-bit
+// arithmetic and one pass in the division of the work, and a merge that loads its pieces side by side
+// (130), the query rows copied ahead with each piece (128).
+//
+// Products.  The tensor cores are far from busy here, so the work goes through the warp-level m16n8k16
+// product with keys (for the scores) and d positions (for O) as its M and query rows as its N, eight at a
+// time: a head without a group wastes the least that way.  Conversion to fp16 and operand layout both
+// happen in registers:
+//   S^T = K Q^T: a lane reads 16-byte pieces of its keys' rows; which d positions form a k-step is the same for
+//     Q and K, so any order serves, and no transposition is needed.
+//   O^T = V^T P^T: a lane reads 16-byte (d = 128) or 8-byte (d = 64) pieces of the four key rows that its
+//     operand wants and pairs their bytes; P^T is S^T's accumulator with its 8 x 8 blocks transposed
+//     between the lanes (movmatrix).
 // Two 64-byte rows share a 128-byte line at d = 64; tiles are stored with the 128-byte swizzle, and the order of
 // keys inside a tile (key_row) is chosen for either d so that no read of 8 lanes meets a bank twice.
 #include <cuda_bf16.h>
@@ -34,65 +41,72 @@
 namespace exattn {
 namespace {
 
-constexpr int kWarps = 8;                       // computing warps
-constexpr int kThreads = 32 * (kWarps + 4);     // and a warpgroup of which one warp is the producer
-// Registers: 168 a thread at launch (65,536 over 384 threads); the third warpgroup gives most of its share to
-// the first two, which hold O and the codes in flight: 2 x 216 + 72 = 3 x 168.
-constexpr int kComputeRegs = 216, kProducerRegs = 72;
-constexpr int kTileKeys = 32;
-constexpr int kPieceRing = 4;                   // pieces announced ahead
-constexpr float kShift = 7.f;                   // P is held times 2^7: fewer of the small ones become subnormal
+constexpr int kPieceRing = 3;                   // pieces announced ahead
+// P is held times 2^kShift, so that fewer of the small ones become subnormal in fp16.  It stays below 2^15: the
+// running maximum may lag by 2^8, and vref by kVrefLag = 2^4.
+constexpr float kShift = 3.f, kVrefLag = 16.f;
 
-template <int D, int MT>
+// NT: query rows in eights.
+template <int D, int NT>
 struct Cfg {
-  static constexpr int R = 16 * MT;                           // query rows an item
-  static constexpr int TILE = kTileKeys * D;                  // bytes of codes, K or V
-  static constexpr int STAGES = D == 128 ? 2 : 4;             // of K and V together, a warp
-  static constexpr int RING = kWarps * STAGES * 2 * TILE;     // 128 KB
-  static constexpr int JOIN = kWarps * 16 * D * 4;            // one 16-row tile of O from every warp
-  static constexpr int QBYTES = MT > 1 ? MT * (D / 16) * 32 * 16 : 0;
+  static constexpr int R = 8 * NT;                            // query rows an item
+  // Computing warps.  The code of a tile is a chain of long-latency steps, and the more warps the more
+  // of it overlaps; O takes D NT / 4 registers, which leaves room for 12 warps at NT = 1 and for 8 above.
+  static constexpr int W = NT == 1 ? 12 : 8;
+  static constexpr int THREADS = 32 * (W + 4);                // and a warpgroup of producers
+  // Registers: 128 or 168 a thread at launch (65,536 over the threads); the last warpgroup gives a part of its
+  // share to the others: 3 x 144 + 80 = 4 x 128, and 2 x 208 + 88 = 3 x 168.
+  static constexpr int COMPUTE_REGS = NT == 1 ? 144 : 208, PRODUCER_REGS = NT == 1 ? 80 : 88;
+  static_assert((W / 4) * COMPUTE_REGS + PRODUCER_REGS == (W / 4 + 1) * (NT == 1 ? 128 : 168), "register split must match the launch");
+  static constexpr int TK = 4096 / D;                         // tokens a tile: 32 or 64
+  static constexpr int NH = TK / 16;                          // 16-token groups of it, each in one page
+  static constexpr int TILE = TK * D;                         // bytes of codes, K or V
+  static constexpr int STAGES = 2;                            // of K and V together, a warp
+  static constexpr int RING = W * STAGES * 2 * TILE;          // 192 or 128 KB
+  static constexpr int JR = NT == 1 ? 512 / D : 8;            // rows joined at a time
+  static constexpr int JOIN = W * JR * D * 4;
+  static constexpr bool Q_IN_SMEM = NT > 2;                   // registers hold Q up to 16 rows
+  static constexpr int QBYTES = Q_IN_SMEM ? NT * (D / 16) * 32 * 8 : 0;
+  static constexpr int QROWS = R * D * 2;                     // the rows of one piece as they lie in memory
   static constexpr int OFF_JOIN = RING;
-  static constexpr int OFF_Q = OFF_JOIN + JOIN;
-  static constexpr int OFF_META = OFF_Q + QBYTES;             // [warp][stage] {ks0, ks1, vs0, vs1}
-  static constexpr int OFF_STAT = OFF_META + kWarps * STAGES * 16;  // m[warp][R], l[warp][R], vref[warp]
-  static constexpr int OFF_PIECE = OFF_STAT + (2 * kWarps * R + kWarps) * 4;
+  static constexpr int OFF_QROWS = OFF_JOIN + JOIN;
+  static constexpr int OFF_Q = OFF_QROWS + kPieceRing * QROWS;
+  static constexpr int OFF_META = OFF_Q + QBYTES;             // [warp][stage][group] {ks, vs}
+  static constexpr int OFF_STAT = (OFF_META + W * STAGES * NH * 8 + 15) & ~15;  // m[R][W], l[R][W], vref[W]
+  static constexpr int OFF_PIECE = OFF_STAT + (2 * W * R + W) * 4;
   static constexpr int OFF_BAR = (OFF_PIECE + kPieceRing * 32 + 7) & ~7;
-  static constexpr int OFF_MISC = OFF_BAR + 8 * (2 * kWarps * STAGES + 2 * kPieceRing + 1);
+  static constexpr int OFF_MISC = OFF_BAR + 8 * (2 * W * STAGES + 2 * kPieceRing + 1);
   static constexpr int OFF_SCHED = (OFF_MISC + 16 + 7) & ~7;
-  static constexpr int BYTES = OFF_SCHED + static_cast<int>(sizeof(typename CacheWalk<R, kTileKeys, kThreads, kWarps>::Shared));
+  static constexpr int BYTES = OFF_SCHED + static_cast<int>(sizeof(typename CacheWalk<R, TK, 128, W>::Shared));
   static_assert(BYTES <= 232448, "shared memory of a block");
 };
 
-// Row of the 32-token tile that stands at column n of 8-key block nb of the score product.
+// Row of the tile that stands at place n of its 8-key block nb in the products.
 template <int D>
 __device__ __forceinline__ constexpr int key_row(int nb, int n) {
   return D == 128 ? nb * 8 + n : 4 * (n >> 1) + (n & 1) + 2 * (nb & 1) + 16 * (nb >> 1);
 }
 
-// Shared-memory address of byte `col` of token row r in a tile.
+// Offset of byte `col` of token row r in a tile.
 template <int D>
-__device__ __forceinline__ uint32_t tile_at(uint32_t base, int r, int col) {
-  if constexpr (D == 128) return base + r * 128 + ((((col >> 4) ^ r) & 7) << 4) + (col & 15);
+__device__ __forceinline__ int tile_at(int r, int col) {
+  if constexpr (D == 128) return r * 128 + ((((col >> 4) ^ r) & 7) << 4) + (col & 15);
   const int line = r >> 1;
-  return base + line * 128 + (((((r & 1) * 4 + (col >> 4)) ^ line) & 7) << 4) + (col & 15);
+  return line * 128 + (((((r & 1) * 4 + (col >> 4)) ^ line) & 7) << 4) + (col & 15);
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 block of 16-bit values held by the warp (lane 4 i + j: row i, columns 2 j and 2 j + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 __device__ __forceinline__ void tma_load_lines(uint32_t dst, const CUtensorMap* map, int line, uint32_t bar) {
@@ -104,30 +118,22 @@ __device__ __forceinline__ void tma_load_lines(uint32_t dst, const CUtensorMap* 
 
 __device__ __forceinline__ float qnan() { return __int_as_float(0x7fffffff); }
 
-// One query row in fp16 for a lane: 4-value groups of its d positions, times the power of two `mul`.
-template <bool BF16>
-__device__ __forceinline__ uint2 q_to_f16(uint2 w, float mul) {
-  if constexpr (!BF16) return w;
-  return make_uint2(pack2<false>(unpack_lo<true>(w.x) * mul, unpack_hi<true>(w.x) * mul),
-                    pack2<false>(unpack_lo<true>(w.y) * mul, unpack_hi<true>(w.y) * mul));
-}
-
-template <int D, int FMT, bool BF16, int MT>
-__global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_constant__ CacheAttnArgs a) {
-  using C = Cfg<D, MT>;
-  using Walk = CacheWalk<C::R, kTileKeys, kThreads, kWarps>;
-  constexpr int NST = C::STAGES, KS = D / 16, NB = D / 8;  // k-steps of S; 8-column blocks of O
-  griddep_launch_dependents();  // the merge may start; it waits for this kernel before it reads
+template <int D, int FMT, bool BF16, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(const __grid_constant__ CacheAttnArgs a) {
+  using C = Cfg<D, NT>;
+  constexpr int W = C::W, NST = C::STAGES, NH = C::NH;
+  constexpr int KS = D / 16, MT = D / 16;  // k-steps of S^T; 16-row tiles of O^T
+  using Walk = CacheWalk<C::R, C::TK, 128, W>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t sbase = smem_u32(smem_raw);
   if (!smem_base_aligned(sbase, a.err_word)) return;
   const uint32_t bars = sbase + C::OFF_BAR;
   auto full = [&](int w, int s) { return bars + 8 * (w * NST + s); };
-  auto empty = [&](int w, int s) { return bars + 8 * (kWarps * NST + w * NST + s); };
-  auto piece_full = [&](int i) { return bars + 8 * (2 * kWarps * NST + i); };
-  auto piece_empty = [&](int i) { return bars + 8 * (2 * kWarps * NST + kPieceRing + i); };
-  const uint32_t join_bar = bars + 8 * (2 * kWarps * NST + 2 * kPieceRing);
-  float4* meta = reinterpret_cast<float4*>(smem_raw + C::OFF_META);
+  auto empty = [&](int w, int s) { return bars + 8 * (W * NST + w * NST + s); };
+  auto piece_full = [&](int i) { return bars + 8 * (2 * W * NST + i); };
+  auto piece_empty = [&](int i) { return bars + 8 * (2 * W * NST + kPieceRing + i); };
+  const uint32_t join_bar = bars + 8 * (2 * W * NST + 2 * kPieceRing);
+  float2* meta = reinterpret_cast<float2*>(smem_raw + C::OFF_META);
   int* pieces = reinterpret_cast<int*>(smem_raw + C::OFF_PIECE);  // [kPieceRing][8]
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_raw + C::OFF_MISC);
   const WaitCtx wc{abort_flag, a.err_word, a.timeout_ns};
@@ -135,109 +141,150 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
 
   if (threadIdx.x == 0) {
     *abort_flag = 0u;
-    for (int i = 0; i < kWarps * NST; ++i) {
-      mbar_init(bars + 8 * i, 1);
-      mbar_init(bars + 8 * (kWarps * NST + i), 1);
+    for (int i = 0; i < W * NST; ++i) {
+      mbar_init(bars + 8 * i, NH);
+      mbar_init(bars + 8 * (W * NST + i), 1);
     }
     for (int i = 0; i < kPieceRing; ++i) {
       mbar_init(piece_full(i), 1);
-      mbar_init(piece_empty(i), kWarps);
+      mbar_init(piece_empty(i), W);
     }
-    mbar_init(join_bar, kWarps);
+    mbar_init(join_bar, W);
     fence_mbar_init();
     prefetch_tmap(&a.tm_k);
     prefetch_tmap(&a.tm_v);
   }
-  // Ends with a barrier of the block, after which the mbarriers above are set up too.
-  Walk walk(a, *reinterpret_cast<typename Walk::Shared*>(smem_raw + C::OFF_SCHED), blockIdx.x, gridDim.x);
+  __syncthreads();
+  // A dependent launch: what is ahead on the stream has written its results before anything is read.
+  griddep_wait();
+  griddep_launch_dependents();  // the merge may start; it waits for this kernel in the same way
 
-  if (warp >= kWarps) {
-    regs_decrease<kProducerRegs>();
-    if (warp > kWarps) return;
-    // ------------------------------------------------------------ producer: lane w feeds computing warp w
+  if (warp >= W) {
+    regs_decrease<C::PRODUCER_REGS>();
+    // ------------------------------------------------------------ producers
+    // Producer warp p feeds the computing warps w = 4 i + p, with one lane for each 16-token group of their
+    // tiles.  One warp alone took 190 cycles for each 4 KB box it had copied, more than the 175 in which they
+    // arrive at the memory's rate; four share the work.
+    // A warp works in rounds of one tile a computing warp.  A group's page number, then its scales and codes
+    // hang on one another, so the rounds run through three stages, one behind the other: the pages of
+    // one are loaded while the scales of the round before are, and the codes of the one before that copied.
+    Walk walk(a, *reinterpret_cast<typename Walk::Shared*>(smem_raw + C::OFF_SCHED), threadIdx.x - 32 * W, 1, blockIdx.x,
+              gridDim.x);
     const int psh = a.c.page_shift;
-    const uint32_t ring = sbase + lane * (NST * 2 * C::TILE);
-    int issued = 0;
-    bool ok = true;
-    CachePiece p;
-    for (int i = 0; ; ++i) {
-      const bool more = ok && walk.next(p);
-      ok = mbar_wait_warp(piece_empty(i % kPieceRing), ((i / kPieceRing) & 1) ^ 1, wc) && ok;
-      if (lane == 0) {
-        int* d = pieces + (i % kPieceRing) * 8;
-        d[0] = more && ok ? p.b : -1;
-        d[1] = p.head;
-        d[2] = p.rt;
-        d[3] = p.len;
-        d[4] = p.begin;
-        d[5] = p.end;
-        d[6] = p.slot;
-        mbar_arrive(piece_full(i % kPieceRing));
-      }
-      if (!more || !ok) break;
-      for (int base = p.begin; base < p.end; base += kWarps) {
-        const int t = base + lane;
-        if (lane < kWarps && t < p.end && ok) {
-          const int s = issued % NST;
-          const int key = t * kTileKeys;
-          // The pages of the tile's two halves (the same one where a page holds 32 tokens or more).
-          const int pg0 = cache_page(a.c, p.b, key);
-          const bool two = psh == 4;
-          const bool second = two && key + 16 < p.len;
-          const int pg1 = second ? cache_page(a.c, p.b, key + 16) : pg0;
-          const long long h0 = static_cast<long long>(pg0) * a.c.heads + p.head;
-          const long long h1 = static_cast<long long>(pg1) * a.c.heads + p.head;
-          float4 sc;
-          sc.x = pg0 >= 0 ? __ldg(a.c.k_scale + h0) : qnan();
-          sc.z = pg0 >= 0 ? __ldg(a.c.v_scale + h0) : qnan();
-          sc.y = sc.x;
-          sc.w = sc.z;
-          if (two) {
-            sc.y = pg1 >= 0 ? __ldg(a.c.k_scale + h1) : qnan();
-            sc.w = pg1 >= 0 ? __ldg(a.c.v_scale + h1) : qnan();
+    const int pw = warp - W;
+    const bool feeds = lane < W / 4 * NH;
+    const int cw = feeds ? 4 * (lane / NH) + pw : 0;  // the computing warp
+    const int group = lane % NH;
+    const int box = min(1 << psh, C::TK);              // tokens a copy
+    const bool leads = ((16 * group) & (box - 1)) == 0;  // this lane's copy takes the groups behind it along
+    const uint32_t ring = sbase + cw * (NST * 2 * C::TILE);
+    constexpr int kNoTile = -2;  // as `page`: no tile here; -1: not a page, or behind the sequence's end
+    struct Round {
+      int key, page, head;
+      float ks, vs;
+    };
+    CachePiece p{};
+    int base = 0, announced = 0, issued = 0, left = 3;  // left: 3, then rounds until the last is through
+    bool have = false, ok = true;
+    Round r0, r1, r2;
+    r1.page = r2.page = kNoTile;
+    while (left > 0) {
+      r0 = r1;
+      r1 = r2;
+      // Third stage: this round's copies, and the bytes that its barrier waits for.
+      if (r0.page != kNoTile) {
+        const int s = issued % NST;
+        if (mbar_wait(empty(cw, s), ((issued / NST) & 1) ^ 1, wc)) {
+          const uint32_t bar = full(cw, s);
+          uint32_t bytes = 0;
+          if (leads && r0.page >= 0) {
+            const long long at = ((static_cast<long long>(r0.page) * a.c.heads + r0.head) << psh) + (r0.key & ((1 << psh) - 1));
+            const int line = static_cast<int>(at >> (D == 128 ? 0 : 1));  // two tokens a 128-byte line at d = 64
+            const uint32_t bk = ring + s * 2 * C::TILE + group * 16 * D;
+            tma_load_lines(bk, &a.tm_k, line, bar);
+            tma_load_lines(bk + C::TILE, &a.tm_v, line, bar);
+            bytes = 2 * box * D;
           }
-          if (pg0 < 0 || pg1 < 0) record_page_error(a.err_word);
-          if (mbar_wait(empty(lane, s), ((issued / NST) & 1) ^ 1, wc)) {
-            const uint32_t bk = ring + s * 2 * C::TILE, bv = bk + C::TILE, bar = full(lane, s);
-            uint32_t bytes = 0;
-            constexpr int kLineShift = D == 128 ? 0 : 1;  // tokens a 128-byte line
-            if (pg0 >= 0) {
-              const int line = static_cast<int>(((h0 << psh) + (key & ((1 << psh) - 1))) >> kLineShift);
-              tma_load_lines(bk, &a.tm_k, line, bar);
-              tma_load_lines(bv, &a.tm_v, line, bar);
-              bytes += two ? C::TILE : 2 * C::TILE;
-            }
-            if (second && pg1 >= 0) {
-              const int line = static_cast<int>((h1 << psh) >> kLineShift);
-              tma_load_lines(bk + C::TILE / 2, &a.tm_k, line, bar);
-              tma_load_lines(bv + C::TILE / 2, &a.tm_v, line, bar);
-              bytes += C::TILE;
-            }
-            meta[lane * NST + s] = sc;
-            mbar_arrive_expect_tx(bar, bytes);
-            ++issued;
-          } else {
-            ok = false;
+          meta[(cw * NST + s) * NH + group] = make_float2(r0.ks, r0.vs);
+          mbar_arrive_expect_tx(bar, bytes);
+          ++issued;
+        } else {
+          ok = false;
+        }
+      }
+      // First stage: the next round, its piece announced where it is new, and its page numbers.
+      r2.page = kNoTile;
+      base += W;
+      if (left == 3 && (!have || base >= p.end)) {
+        have = ok && walk.next(p);
+        if (!have) left = 2;
+        base = p.begin;
+        if (pw == 0) {
+          const int i = announced++ % kPieceRing;
+          ok = mbar_wait_warp(piece_empty(i), (((announced - 1) / kPieceRing) & 1) ^ 1, wc) && ok;
+          const int nrows = have && ok ? min(C::R, a.group * a.Nq - p.rt * C::R) : 0;
+          if (lane == 0) {
+            int* d = pieces + i * 8;
+            d[0] = have ? p.b : -1;
+            d[1] = p.head;
+            d[2] = p.rt;
+            d[3] = p.len;
+            d[4] = p.begin;
+            d[5] = p.end;
+            d[6] = p.slot;
+            mbar_arrive_expect_tx(piece_full(i), nrows * D * 2);
+          }
+          if (lane < nrows) {
+            const int r = p.rt * C::R + lane, tok = r / a.group, hg = r - tok * a.group;
+            bulk_load(sbase + C::OFF_QROWS + i * C::QROWS + lane * D * 2,
+                      static_cast<const uint16_t*>(a.q) + p.b * a.sq.b +
+                          (static_cast<long long>(p.head) * a.group + hg) * a.sq.h + tok * a.sq.n,
+                      D * 2, piece_full(i));
           }
         }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+      } else if (left < 3) {
+        --left;
       }
+      if (have && feeds && base + cw < p.end) {
+        r2.head = p.head;
+        r2.key = (base + cw) * C::TK + 16 * group;
+        r2.page = r2.key < p.len ? cache_page_number(a.c, p.b, r2.key) : 0x7fffffff;  // no entry there
+        r2.ks = r2.key < p.len ? 0.f : 1.f;
+      }
+      // Second stage: the scales.
+      if (r1.page != kNoTile) {
+        const bool there = r1.ks == 0.f;
+        r1.page = cache_page_checked(a.c, r1.page);
+        r1.ks = r1.vs = there ? qnan() : 0.f;
+        if (r1.page >= 0) {
+          const long long h = static_cast<long long>(r1.page) * a.c.heads + r1.head;
+          r1.ks = __ldg(a.c.k_scale + h);
+          r1.vs = __ldg(a.c.v_scale + h);
+        } else if (there) {
+          record_page_error(a.err_word);
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
     }
     // Every copy issued must land before the block exits, also where the computing warps gave up.
-    if (lane < kWarps)
-      for (int n = max(0, issued - NST); n < issued; ++n) mbar_drain(full(lane, n % NST), (n / NST) & 1, a.timeout_ns);
+    if (feeds)
+      for (int n = max(0, issued - NST); n < issued; ++n) mbar_drain(full(cw, n % NST), (n / NST) & 1, a.timeout_ns);
+    if (pw == 0)
+      for (int n = max(0, announced - kPieceRing); n < announced; ++n)
+        mbar_drain(piece_full(n % kPieceRing), (n / kPieceRing) & 1, a.timeout_ns);
     return;
   }
 
   // -------------------------------------------------------------- computing warps
-  regs_increase<kComputeRegs>();
+  regs_increase<C::COMPUTE_REGS>();
   const int g = lane >> 2, t4 = lane & 3;
-  const uint32_t ring = sbase + warp * (NST * 2 * C::TILE);
+  const uint8_t* ring = smem_raw + warp * (NST * 2 * C::TILE);
   float* st_m = reinterpret_cast<float*>(smem_raw + C::OFF_STAT);
-  float* st_l = st_m + kWarps * C::R;
-  float* st_v = st_l + kWarps * C::R;
+  float* st_l = st_m + W * C::R;
+  float* st_v = st_l + W * C::R;
   float4* join = reinterpret_cast<float4*>(smem_raw + C::OFF_JOIN);
+  uint2* qs = reinterpret_cast<uint2*>(smem_raw + C::OFF_Q);
   const CacheWs ws = cache_ws(a.ws, a.B, C::R, D, a.sm_count);
   const int rows = a.group * a.Nq;
   int used = 0;
@@ -259,238 +306,230 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
     if (b < 0) break;
     const int row0 = rt * C::R;
 
-    // Query rows: lane (g, t4) holds d positions [t4 D/4, (t4 + 1) D/4) of rows g and g + 8 of each 16.
-    uint32_t qf[MT == 1 ? KS : 1][4];
-    float fac[MT][2];  // c over the power of two in Q
-    int lim[MT][2];
+    // Query rows: lane (g, t4) holds d positions [t4 D/4, (t4 + 1) D/4) of row g of each eight.
+    uint2 qf[C::Q_IN_SMEM ? 1 : NT][KS];
+    float fac[NT][2];  // c over the power of two in Q, of the rows 2 t4 and 2 t4 + 1
+    int lim[NT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      uint4 raw[2][D / 32];
-      float mul[2];
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + nt * 8 + g;
+      const uint4* src = reinterpret_cast<const uint4*>(smem_raw + C::OFF_QROWS + (pi % kPieceRing) * C::QROWS +
+                                                        (nt * 8 + g) * D * 2 + t4 * (D / 2));
+      uint4 raw[D / 32];
+      uint32_t mx = 0u;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = min(row0 + mt * 16 + h * 8 + g, rows - 1);
-        const int tok = r / a.group, hg = r - tok * a.group;
-        lim[mt][h] = cache_row_limit(a.mask, len, a.Nq, tok);
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(a.q) + b * a.sq.b +
-            (static_cast<long long>(head) * a.group + hg) * a.sq.h + tok * a.sq.n + t4 * (D / 4));
-        uint32_t mx = 0u;
+      for (int i = 0; i < D / 32; ++i) raw[i] = r < rows ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+      float mul = 1.f, back = 1.f;
+      if constexpr (BF16) {
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          raw[h][i] = __ldg(src + i);
-          if constexpr (BF16) {
-            mx = __vmaxu2(mx, raw[h][i].x & 0x7fff7fffu);
-            mx = __vmaxu2(mx, raw[h][i].y & 0x7fff7fffu);
-            mx = __vmaxu2(mx, raw[h][i].z & 0x7fff7fffu);
-            mx = __vmaxu2(mx, raw[h][i].w & 0x7fff7fffu);
-          }
+          mx = __vmaxu2(mx, raw[i].x & 0x7fff7fffu);
+          mx = __vmaxu2(mx, raw[i].y & 0x7fff7fffu);
+          mx = __vmaxu2(mx, raw[i].z & 0x7fff7fffu);
+          mx = __vmaxu2(mx, raw[i].w & 0x7fff7fffu);
         }
-        mul[h] = 1.f;
-        float back = 1.f;
-        if constexpr (BF16) {
-          mx = max(mx & 0xffffu, mx >> 16);
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          // Exponent e of the largest value: times 2^(14 - e) it lies in [2^14, 2^15), and the row keeps 38
-          // binades.  The factor is held to [2^-113, 2^113]; rows of zeros, NaN or infinity stay as they are.
-          const int e = static_cast<int>(mx >> 7) - 127;
-          if (mx != 0u && e < 128) {
-            const int k = min(14 - e, 113);
-            mul[h] = __int_as_float((127 + k) << 23);
-            back = __int_as_float((127 - k) << 23);
-          }
+        mx = max(mx & 0xffffu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // Exponent e of the largest value: times 2^(14 - e) it lies in [2^14, 2^15), and the row keeps 38
+        // binades.  The factor is held to [2^-113, 2^113]; rows of zeros, NaN or infinity stay as they are.
+        const int e = static_cast<int>(mx >> 7) - 127;
+        if (mx != 0u && e < 128) {
+          const int k = min(14 - e, 113);
+          mul = __int_as_float((127 + k) << 23);
+          back = __int_as_float((127 - k) << 23);
         }
-        fac[mt][h] = a.scale * 1.4426950408889634f * back;
+      }
+      const float f = a.scale * 1.4426950408889634f * back;
+      const int lm = cache_row_limit(a.mask, len, a.Nq, min(r, rows - 1) / a.group);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        fac[nt][e] = __shfl_sync(0xffffffffu, f, (2 * t4 + e) * 4);
+        lim[nt][e] = __shfl_sync(0xffffffffu, lm, (2 * t4 + e) * 4);
       }
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
-        const uint32_t* r0 = reinterpret_cast<const uint32_t*>(&raw[0][0]) + 2 * j;
-        const uint32_t* r1 = reinterpret_cast<const uint32_t*>(&raw[1][0]) + 2 * j;
-        const uint2 x = q_to_f16<BF16>(make_uint2(r0[0], r0[1]), mul[0]);
-        const uint2 y = q_to_f16<BF16>(make_uint2(r1[0], r1[1]), mul[1]);
-        if constexpr (MT == 1) {
-          qf[j][0] = x.x;
-          qf[j][1] = y.x;
-          qf[j][2] = x.y;
-          qf[j][3] = y.y;
-        } else if (warp == 0) {  // every warp holds the same: one writes them
-          st_shared_v4(sbase + C::OFF_Q + ((mt * KS + j) * 32 + lane) * 16, x.x, y.x, x.y, y.y);
-        }
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(raw) + 2 * j;
+        uint2 x = make_uint2(w[0], w[1]);
+        if constexpr (BF16)
+          x = make_uint2(pack2<false>(unpack_lo<true>(w[0]) * mul, unpack_hi<true>(w[0]) * mul),
+                         pack2<false>(unpack_lo<true>(w[1]) * mul, unpack_hi<true>(w[1]) * mul));
+        if constexpr (!C::Q_IN_SMEM)
+          qf[nt][j] = x;
+        else if (warp == 0)  // every warp holds the same: one writes them
+          qs[(nt * KS + j) * 32 + lane] = x;
       }
     }
-    if constexpr (MT > 1) ok = sync_warps();
-    const int tok0 = row0 / a.group;
-    const int lim_min = cache_row_limit(a.mask, len, a.Nq, tok0);  // of the tile's first row
+    if constexpr (C::Q_IN_SMEM) ok = sync_warps();
+    const int lim_min = cache_row_limit(a.mask, len, a.Nq, row0 / a.group);  // of the item's first row
 
-    float o[MT][NB][4];
-    float m[MT][2], l[MT][2];
+    float o[NT][MT][4];
+    float m[NT][2], l[NT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
+      for (int j = 0; j < MT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
-      m[mt][0] = m[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.f;
+        for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
     }
-    float vref = 0.f;
+    float vref = 0.f, vinv = 0.f;
 
-    for (int t = begin + warp; t < end; t += kWarps, ++used) {
+    for (int t = begin + warp; t < end; t += W, ++used) {
       const int s = used % NST;
       if (ok) ok = mbar_wait_warp(full(warp, s), (used / NST) & 1, wc);
       if (!ok) break;
-      const uint32_t bk = ring + s * 2 * C::TILE, bv = bk + C::TILE;
-      const float4 sc = meta[warp * NST + s];
-      const int key0 = t * kTileKeys;
+      const uint8_t *bk = ring + s * 2 * C::TILE, *bv = bk + C::TILE;
+      float2 sc[NH];
+#pragma unroll
+      for (int i = 0; i < NH; ++i) sc[i] = meta[(warp * NST + s) * NH + i];
+      const int key0 = t * C::TK;
 
-      // S = Q K^T over the codes
-      float sv[MT][4][4];
+      // S^T = K Q^T over the codes.  sv[i][nt][2 h + e]: key place g of block 2 i + h, row 2 t4 + e.
+      float sv[NH][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int i = 0; i < NH; ++i)
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sv[mt][nb][e] = 0.f;
+          for (int e = 0; e < 4; ++e) sv[i][nt][e] = 0.f;
 #pragma unroll
       for (int c16 = 0; c16 < D / 64; ++c16) {  // 16 of the lane's d positions at a time
-        uint4 kw[4];
+        uint4 kw[2 * NH];
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) kw[nb] = lds128(tile_at<D>(bk, key_row<D>(nb, g), t4 * (D / 4) + c16 * 16));
+        for (int nb = 0; nb < 2 * NH; ++nb)
+          kw[nb] = *reinterpret_cast<const uint4*>(bk + tile_at<D>(key_row<D>(nb, g), t4 * (D / 4) + c16 * 16));
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const int j = c16 * 4 + w;
-          uint32_t qa[MT][4];
+          uint2 qb[NT];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            if constexpr (MT == 1) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) qa[mt][e] = qf[j][e];
-            } else {
-              const uint4 x = lds128(sbase + C::OFF_Q + ((mt * KS + j) * 32 + lane) * 16);
-              qa[mt][0] = x.x;
-              qa[mt][1] = x.y;
-              qa[mt][2] = x.z;
-              qa[mt][3] = x.w;
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (C::Q_IN_SMEM) qb[nt] = qs[(nt * KS + j) * 32 + lane]; else qb[nt] = qf[nt][j];
           }
 #pragma unroll
-          for (int nb = 0; nb < 4; ++nb) {
-            const uint32_t word = w == 0 ? kw[nb].x : w == 1 ? kw[nb].y : w == 2 ? kw[nb].z : kw[nb].w;
-            uint32_t b0, b1;
-            codes_to_f16<FMT>(word, b0, b1);
+          for (int i = 0; i < NH; ++i) {
+            const uint4 &x = kw[2 * i], &y = kw[2 * i + 1];
+            uint32_t a0, a1, a2, a3;
+            codes_to_f16<FMT>(w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w, a0, a2);
+            codes_to_f16<FMT>(w == 0 ? y.x : w == 1 ? y.y : w == 2 ? y.z : y.w, a1, a3);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma16816(sv[mt][nb], qa[mt], b0, b1);
+            for (int nt = 0; nt < NT; ++nt) mma16816(sv[i][nt], a0, a1, a2, a3, qb[nt].x, qb[nt].y);
           }
         }
       }
 
-      // Online softmax.  kf: score of a unit product, for each 16-key half of the tile.
-      const bool masked = key0 + kTileKeys > lim_min;
-      const float vnew = fmaxf(vref, fmaxf(sc.z, sc.w));  // a NaN scale is passed over here and met below
-      bool grow = vnew > vref;
-      float mnew[MT][2];
+      // Online softmax; group i of the tile has one page and so one scale.  The maximum is looked for only where
+      // a score passes the running one by more than 2^8: until then it may lag.
+      const bool masked = key0 + C::TK > lim_min;
+      float vnew = sc[0].y;  // a NaN scale is passed over here and met below
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int i = 1; i < NH; ++i) vnew = fmaxf(vnew, sc[i].y);
+      bool grow = vnew > vref * kVrefLag;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float f0 = fac[mt][h] * sc.x, f1 = fac[mt][h] * sc.y;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nb = 0; nb < 4; ++nb) {
-            const float f = nb < 2 ? f0 : f1;
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& x = sv[mt][nb][2 * h + e];
+          for (int i = 0; i < NH; ++i) {
+            const float f = fac[nt][e] * sc[i].x;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float& x = sv[i][nt][2 * h + e];
               x *= f;
-              if (masked && key0 + key_row<D>(nb, 2 * t4 + e) >= lim[mt][h]) x = -INFINITY;
+              if (masked && key0 + key_row<D>(2 * i + h, g) >= lim[nt][e]) x = -INFINITY;
+              grow = grow || x > m[nt][e] + 8.f;
             }
           }
-          float mx = sv[mt][0][2 * h];
-#pragma unroll
-          for (int nb = 0; nb < 4; ++nb) mx = fmaxf(mx, fmaxf(sv[mt][nb][2 * h], sv[mt][nb][2 * h + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          mnew[mt][h] = mx;
-          grow = grow || mx > m[mt][h] + 8.f;
-        }
       if (__any_sync(0xffffffffu, grow)) {
-        const float vr = vnew > 0.f ? vref / vnew : 1.f;
-        vref = vnew;
+        float vr = 1.f;
+        if (vnew > vref) {
+          vr = vref / vnew;
+          vref = vnew;
+          vinv = 1.f / vref;
+        }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float to = fmaxf(m[mt][h], mnew[mt][h]);
-            const float al = to == -INFINITY ? 1.f : ex2_approx(m[mt][h] - to);
-            m[mt][h] = to;
-            l[mt][h] *= al;
+          for (int e = 0; e < 2; ++e) {
+            float to = m[nt][e];
+#pragma unroll
+            for (int i = 0; i < NH; ++i) to = fmaxf(to, fmaxf(sv[i][nt][e], sv[i][nt][2 + e]));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, x));
+            const float al = to == -INFINITY ? 1.f : ex2_approx(m[nt][e] - to);
+            m[nt][e] = to;
+            l[nt][e] *= al;
             const float ov = al * vr;
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-              o[mt][j][2 * h] *= ov;
-              o[mt][j][2 * h + 1] *= ov;
+            for (int j = 0; j < MT; ++j) {
+              o[nt][j][e] *= ov;
+              o[nt][j][2 + e] *= ov;
             }
           }
       }
-      const float vinv = vref > 0.f ? 1.f / vref : 0.f;
-      const float r0 = sc.z * vinv, r1 = sc.w * vinv;
-      uint32_t pf[MT][2][4];  // operand of each 16-key half
+      uint32_t pb[NT][2 * NH];  // P^T operand of each 8-key block
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt) {
+        const float ms0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kShift;
+        const float ms1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kShift;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float ms = m[mt][h] == -INFINITY ? 0.f : m[mt][h] - kShift;
-#pragma unroll
-          for (int nb = 0; nb < 4; ++nb) {
-            const float r = nb < 2 ? r0 : r1;
-            const float x0 = sv[mt][nb][2 * h], x1 = sv[mt][nb][2 * h + 1];
-            const float p0 = ex2_approx(x0 - ms), p1 = ex2_approx(x1 - ms);
-            l[mt][h] += p0 + p1;
-            float y0 = p0 * r, y1 = p1 * r;
-            if (masked) {  // a hidden key must not bring in a NaN scale
-              y0 = x0 == -INFINITY ? 0.f : y0;
-              y1 = x1 == -INFINITY ? 0.f : y1;
-            }
-            pf[mt][nb >> 1][(nb & 1) * 2 + h] = pack2<false>(y0, y1);
+        for (int nb = 0; nb < 2 * NH; ++nb) {
+          const float r = sc[nb >> 1].y * vinv;
+          const float x0 = sv[nb >> 1][nt][2 * (nb & 1)], x1 = sv[nb >> 1][nt][2 * (nb & 1) + 1];
+          const float p0 = ex2_approx(x0 - ms0), p1 = ex2_approx(x1 - ms1);
+          l[nt][0] += p0;
+          l[nt][1] += p1;
+          float y0 = p0 * r, y1 = p1 * r;
+          if (masked) {  // a hidden key must not bring in a NaN scale
+            y0 = x0 == -INFINITY ? 0.f : y0;
+            y1 = x1 == -INFINITY ? 0.f : y1;
           }
+          pb[nt][nb] = transpose8(pack2<false>(y0, y1));
         }
+      }
 
-      // O += P V over the codes
+      // O^T += V^T P^T over the codes
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        constexpr int WORDS = D / 32;  // words of a lane's piece of a key row: NB values
+      for (int half = 0; half < NH; ++half) {
+        constexpr int WORDS = D / 32;  // words of a lane's piece of a key row
         uint32_t vw[4][WORDS];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = key_row<D>(2 * half + (i >> 1), 2 * t4 + (i & 1));
           if constexpr (D == 128) {
-            const uint4 x = lds128(tile_at<D>(bv, r, g * 16));
+            const uint4 x = *reinterpret_cast<const uint4*>(bv + tile_at<D>(r, g * 16));
             vw[i][0] = x.x;
             vw[i][1] = x.y;
             vw[i][2] = x.z;
             vw[i][3] = x.w;
           } else {
-            const uint2 x = lds64(tile_at<D>(bv, r, g * 8));
+            const uint2 x = *reinterpret_cast<const uint2*>(bv + tile_at<D>(r, g * 8));
             vw[i][0] = x.x;
             vw[i][1] = x.y;
           }
-          // Codes past the sequence's end may be anything, a NaN among them.
-          if (key0 + kTileKeys > len && key0 + r >= len) {
+        }
+        if (key0 + C::TK > len) {  // codes past the sequence's end may be anything, a NaN among them
 #pragma unroll
-            for (int w = 0; w < WORDS; ++w) vw[i][w] = 0u;
-          }
+          for (int i = 0; i < 4; ++i)
+            if (key0 + key_row<D>(2 * half + (i >> 1), 2 * t4 + (i & 1)) >= len) {
+#pragma unroll
+              for (int w = 0; w < WORDS; ++w) vw[i][w] = 0u;
+            }
         }
 #pragma unroll
         for (int w = 0; w < WORDS; ++w) {
-          uint32_t b0[4], b1[4];  // of d positions 4 w .. 4 w + 3 of the lane's piece
-          codes_to_f16<FMT>(__byte_perm(vw[0][w], vw[1][w], 0x5140), b0[0], b0[1]);
-          codes_to_f16<FMT>(__byte_perm(vw[0][w], vw[1][w], 0x7362), b0[2], b0[3]);
-          codes_to_f16<FMT>(__byte_perm(vw[2][w], vw[3][w], 0x5140), b1[0], b1[1]);
-          codes_to_f16<FMT>(__byte_perm(vw[2][w], vw[3][w], 0x7362), b1[2], b1[3]);
+          uint32_t x[4], y[4];  // d positions 4 w .. 4 w + 3 of the lane's piece; first and second pair of keys
+          codes_to_f16<FMT>(__byte_perm(vw[0][w], vw[1][w], 0x5140), x[0], x[1]);
+          codes_to_f16<FMT>(__byte_perm(vw[0][w], vw[1][w], 0x7362), x[2], x[3]);
+          codes_to_f16<FMT>(__byte_perm(vw[2][w], vw[3][w], 0x5140), y[0], y[1]);
+          codes_to_f16<FMT>(__byte_perm(vw[2][w], vw[3][w], 0x7362), y[2], y[3]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
+          for (int h = 0; h < 2; ++h)  // tile rows g and g + 8: d positions 2 j and 2 j + 1 of the piece
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * w + e], pf[mt][half], b0[e], b1[e]);
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(o[nt][2 * w + h], x[2 * h], x[2 * h + 1], y[2 * h], y[2 * h + 1], pb[nt][2 * half], pb[nt][2 * half + 1]);
         }
       }
       __syncwarp();  // every lane has read the tile
@@ -500,62 +539,65 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
     // ------------------------------------------------------------ join the warps' results
     const int nrows = min(C::R, rows - row0);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float x = l[mt][h];
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if (t4 == 0) {
-          st_m[warp * C::R + mt * 16 + h * 8 + g] = m[mt][h];
-          st_l[warp * C::R + mt * 16 + h * 8 + g] = x;
+      for (int e = 0; e < 2; ++e) {
+        float x = l[nt][e];
+#pragma unroll
+        for (int i = 4; i < 32; i <<= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
+        if (g == 0) {
+          st_m[(nt * 8 + 2 * t4 + e) * W + warp] = m[nt][e];
+          st_l[(nt * 8 + 2 * t4 + e) * W + warp] = x;
         }
       }
     if (lane == 0) {
       st_v[warp] = vref;
       mbar_arrive(piece_empty(pi % kPieceRing));
     }
-    constexpr int Q4 = D / 4;       // float4s a row
-    constexpr int LQ = D / 16;      // float4s of a lane's row part (dims t4 D/4 ..)
-    auto place = [&](int r, int q) {  // bank-conflict-free order of a row's float4s
-      const int k = D == 128 ? ((q >> 3) | ((r & 1) << 2)) : ((q >> 3) | ((r & 1) << 1));
-      return r * Q4 + (q ^ k);
+    constexpr int Q4 = D / 4;   // float4s a row
+    constexpr int LQ = D / 32;  // float4s of a lane's part of a row (d positions g D/8 ..)
+    auto place = [&](int r, int q) {  // order of a row's float4s in which 8 lanes never meet a bank twice
+      const int t = (r >> 1) & 3;
+      return (r & (C::JR - 1)) * Q4 + (q ^ (D == 128 ? t : (t & 1) | ((t & 2) << 1)));
     };
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt * 16 >= nrows) break;  // the same for all warps
+    for (int base = 0; base < nrows; base += C::JR) {  // the same for all warps
       if (begin + warp < end) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (mt * 16 + h * 8 + g < nrows) {
-            float4* dst = join + warp * (16 * Q4);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int q = 0; q < LQ; ++q) {
-              // d position t4 D/4 + 4 q + e is column 2 t4 + (q >= LQ/2) of block 4 (q % (LQ/2)) + e
-              const int col = q >= LQ / 2 ? 1 : 0, j = 4 * (q % (LQ / 2));
-              dst[place(h * 8 + g, t4 * LQ + q)] = make_float4(o[mt][j][2 * h + col], o[mt][j + 1][2 * h + col],
-                                                               o[mt][j + 2][2 * h + col], o[mt][j + 3][2 * h + col]);
+          for (int e = 0; e < 2; ++e) {
+            const int r = nt * 8 + 2 * t4 + e;
+            if (r >= base && r < min(nrows, base + C::JR)) {
+#pragma unroll
+              for (int q = 0; q < LQ; ++q)
+                join[warp * (C::JR * Q4) + place(r, g * LQ + q)] =
+                    make_float4(o[nt][2 * q][e], o[nt][2 * q][2 + e], o[nt][2 * q + 1][e], o[nt][2 * q + 1][2 + e]);
             }
           }
-        }
       }
       if (!(ok = ok && sync_warps())) break;
-      const int nr = min(16, nrows - mt * 16);
-      for (int i = threadIdx.x; i < nr * Q4; i += 32 * kWarps) {
-        const int r = i / Q4, q = i % Q4, ri = mt * 16 + r;
-        float mx = -INFINITY;
+      const int nr = min(C::JR, nrows - base);
+      for (int i = threadIdx.x; i < nr * Q4; i += 32 * W) {
+        const int ri = base + i / Q4, q = i % Q4;
+        float sm[W], sl[W], vr[W];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, st_m[w * C::R + ri]);
+        for (int w = 0; w < W; w += 4) {
+          *reinterpret_cast<float4*>(sm + w) = *reinterpret_cast<const float4*>(st_m + ri * W + w);
+          *reinterpret_cast<float4*>(sl + w) = *reinterpret_cast<const float4*>(st_l + ri * W + w);
+          *reinterpret_cast<float4*>(vr + w) = *reinterpret_cast<const float4*>(st_v + w);
+        }
+        float mx = sm[0];
+#pragma unroll
+        for (int w = 1; w < W; ++w) mx = fmaxf(mx, sm[w]);
         const float ms = mx == -INFINITY ? 0.f : mx;
         float lsum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float lw = st_l[w * C::R + ri];
-          if (lw != 0.f) {
-            const float e = ex2_approx(st_m[w * C::R + ri] - ms), ev = e * st_v[w];
-            const float4 x = join[w * (16 * Q4) + place(r, q)];
-            lsum = fmaf(e, lw, lsum);
+        for (int w = 0; w < W; ++w) {
+          if (sl[w] != 0.f) {
+            const float e = ex2_approx(sm[w] - ms), ev = e * vr[w];
+            const float4 x = join[w * (C::JR * Q4) + place(ri, q)];
+            lsum = fmaf(e, sl[w], lsum);
             acc.x = fmaf(ev, x.x, acc.x);
             acc.y = fmaf(ev, x.y, acc.y);
             acc.z = fmaf(ev, x.z, acc.z);
@@ -585,97 +627,23 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
   }
 }
 
-// Merge of the pieces of divided items, one warp a query row, and the rows that see no token:
-// L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s over the row's pieces in key order.
-template <int D, bool BF16, int R, int TK>
-__global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant__ CacheAttnArgs a) {
-  griddep_wait();
-  constexpr int V = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const CacheItems<R, TK> items(a);
-  const long long rid = static_cast<long long>(blockIdx.x) * 8 + warp;
-  if (rid >= static_cast<long long>(a.B) * a.c.heads * items.rows) return;
-  const int r = static_cast<int>(rid % items.rows);
-  const long long bh = rid / items.rows;
-  const int head = static_cast<int>(bh % a.c.heads), b = static_cast<int>(bh / a.c.heads);
-  const int rt = r / R;
-  const CacheWs ws = cache_ws(a.ws, a.B, R, D, a.sm_count);
-  const int len = items.seq_len(a, b);
-  const int nt = items.tiles(a, len, rt);
-  const int C = ws.head->per_piece;
-  long long first = 0;
-  int pieces = 0;
-  if (nt > 0) {
-    first = ws.first[b];
-    if (head > 0) first += head * items.head_units(a, len, 0);
-    for (int i = 0; i < rt; ++i) first += items.tiles(a, len, i);
-    pieces = ws.head->pieces ? (nt + C - 1) / C : static_cast<int>((first + nt - 1) / C - first / C) + 1;
-    if (pieces == 1) return;  // written by the block that had all of it
-  }
-  const bool by_piece = ws.head->pieces != 0;
-  auto row_of = [&](int i) {  // workspace row of piece i
-    const long long start = by_piece ? first + static_cast<long long>(i) * C : (i == 0 ? first : (first / C + i) * C);
-    return static_cast<size_t>(2 * (start / C) + (i != 0)) * R + (r - rt * R);
-  };
-  float mx = -INFINITY;
-  for (int i = lane; i < pieces; i += 32) mx = fmaxf(mx, ws.l[row_of(i)]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const float ms = mx == -INFINITY ? 0.f : mx;
-  float acc[V], sum = 0.f;
-#pragma unroll
-  for (int e = 0; e < V; ++e) acc[e] = 0.f;
-  for (int i = 0; i < pieces; ++i) {
-    const size_t at = row_of(i);
-    const float w = ex2_approx(ws.l[at] - ms);
-    if (w != 0.f) {  // a NaN counts
-      const float* op = ws.o + at * D + lane * V;
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(w, op[e], acc[e]);
-      sum += w;
-    }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int tok = r / a.group, hq = head * a.group + r - tok * a.group;
-  uint16_t* dst = static_cast<uint16_t*>(a.o) + b * a.so.b + hq * a.so.h + tok * a.so.n + lane * V;
-  if constexpr (V == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack2<BF16>(acc[0] * inv, acc[1] * inv);
-  if (lane == 0)
-    a.lse[(static_cast<long long>(b) * a.c.heads * a.group + hq) * a.Nq + tok] =
-        sum == 0.f ? -INFINITY : (ms + __log2f(sum)) * 0.6931471805599453f;
-}
-
-template <int D, bool BF16, int R, int TK>
-cudaError_t launch_merge(const CacheAttnArgs& a, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(a.B) * a.c.heads * a.group * a.Nq;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, BF16, R, TK>, a);
-}
-
-template <int D, int FMT, bool BF16, int MT>
+template <int D, int FMT, bool BF16, int NT>
 cudaError_t launch_t(const CacheAttnArgs& a, cudaStream_t stream) {
-  using C = Cfg<D, MT>;
-  auto kern = cache_attn_kernel<D, FMT, BF16, MT>;
+  using C = Cfg<D, NT>;
+  auto kern = cache_attn_kernel<D, FMT, BF16, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;
-  kern<<<a.sm_count, kThreads, C::BYTES, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_merge<D, BF16, C::R, kTileKeys>(a, stream);
+  if ((e = launch_dependent(kern, dim3(a.sm_count), dim3(C::THREADS), C::BYTES, stream, a)) != cudaSuccess) return e;
+  return launch_cache_merge<D, BF16, C::R, C::TK, C::W>(a, stream);
 }
 
 template <int D, int FMT, bool BF16>
 cudaError_t launch_m(const CacheAttnArgs& a, cudaStream_t stream) {
-  return static_cast<long long>(a.group) * a.Nq <= 16 ? launch_t<D, FMT, BF16, 1>(a, stream) : launch_t<D, FMT, BF16, 2>(a, stream);
+  const long long rows = static_cast<long long>(a.group) * a.Nq;
+  if (rows <= 8) return launch_t<D, FMT, BF16, 1>(a, stream);
+  if (rows <= 16) return launch_t<D, FMT, BF16, 2>(a, stream);
+  if (rows <= 24) return launch_t<D, FMT, BF16, 3>(a, stream);
+  return launch_t<D, FMT, BF16, 4>(a, stream);
 }
 
 template <int D>
@@ -686,11 +654,14 @@ cudaError_t launch_d(const CacheAttnArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int cache_attn_box_tokens(int page) { return page < kTileKeys ? page : kTileKeys; }
+int cache_attn_box_tokens(int page, int d) { return page < 4096 / d ? page : 4096 / d; }
 
-size_t cache_attn_workspace(int B, int rows, int d, int sm_count) {
-  const int R = rows <= 16 ? 16 : 32;
-  return cache_align256(cache_ws_first_bytes(B) + cache_slots(sm_count) * R * (static_cast<size_t>(d) + 1) * sizeof(float));
+CacheAttnShape cache_attn_shape(long long rows, int d) { return {rows >= 32 ? 32 : static_cast<int>((rows + 7) / 8 * 8), 4096 / d}; }
+
+size_t cache_attn_workspace(int B, long long rows, int d, int sm_count) {
+  const size_t R = cache_attn_shape(rows, d).rows;
+  const size_t n = cache_ws_first_bytes(B) + cache_slots(sm_count) * R * (static_cast<size_t>(d) + 1) * sizeof(float);
+  return (n + 255) & ~static_cast<size_t>(255);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream) {

@@ -2,14 +2,18 @@
 //
 // An item is one tile of query rows of one key/value head of one sequence; its keys are cut into tiles of
 // TK tokens.  All tiles of all items, in the order (sequence, head, row tile, key tile), are numbered
-// 0 .. T - 1.  With C = ceil(T / P) for P blocks,
+// 0 .. T - 1 (below 2^31: the host checks the largest T that the page table allows).  With
+// C = ceil(T / P) for P blocks,
 //   * more than kMinTiles tiles a block: block c takes the tiles [c C, (c + 1) C), whichever items they
 //     belong to, so every block has the same work however uneven the lengths are;
 //   * fewer: C = kMinTiles, and a block takes whole pieces of at most C tiles that begin at an item's
 //     start or C, 2 C, ... tiles behind it, so that short items are not cut for nothing.
+// In the first form an item also counts kItemCost tiles that are not there, before its own: what it costs to
+// begin and to end a piece.  Without them a block whose share were many short sequences took 1.6 times as
+// long as the average block (64 sequences spread over 1 to 8191 tokens, 8 heads).
 // A piece is a run of an item's tiles in one block.  Where an item has several, each leaves a partial
 // result in slot 2 (start / C) + (start != item's first tile) of the workspace, `start` being the number
-// of the piece's first tile: at most one piece in each block begins an item that it does not finish, and
+// of the piece's first tile (kItemCost past the item's first number): at most one piece in each block begins an item that it does not finish, and
 // at most one continues an item, so no two pieces share a slot.
 #pragma once
 
@@ -22,33 +26,35 @@ namespace exattn {
 // Workspace: a header, the first tile number of every sequence, then the slots (fp32 rows of D values,
 // normalised by the piece's own sum) and their base-2 log-sum-exps.
 struct CacheSchedHeader {
-  long long total;
   int per_piece;  // C
   int pieces;     // 1: the second form above
 };
 
-inline size_t cache_align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
 struct CacheWs {
   CacheSchedHeader* head;
-  long long* first;  // [B]
-  float* o;          // [slots][R][D]
-  float* l;          // [slots][R]
+  int* first;  // [B]
+  float* o;    // [slots][R][D]
+  float* l;    // [slots][R]
 };
 
-// Slots are numbered below 2 (T / C + 1) <= 2 (P + 1).
+// Slots are numbered below 2 (T / C + 1) <= 2 (P + 1), T with the items' costs.
 inline __host__ __device__ size_t cache_slots(int sm_count) { return 2 * (static_cast<size_t>(sm_count) + 1); }
 
-inline __host__ __device__ size_t cache_ws_first_bytes(int B) { return (256 + 8 * static_cast<size_t>(B) + 255) & ~static_cast<size_t>(255); }
+inline __host__ __device__ size_t cache_ws_first_bytes(int B) {
+  return (256 + 4 * static_cast<size_t>(B) + 255) & ~static_cast<size_t>(255);
+}
 
-__host__ __device__ inline CacheWs cache_ws(uint8_t* ws, int B, int R, int D, int sm_count) {
+inline __host__ __device__ CacheWs cache_ws(uint8_t* ws, int B, int R, int D, int sm_count) {
   CacheWs w;
   w.head = reinterpret_cast<CacheSchedHeader*>(ws);
-  w.first = reinterpret_cast<long long*>(ws + 256);
+  w.first = reinterpret_cast<int*>(ws + 256);
   w.o = reinterpret_cast<float*>(ws + cache_ws_first_bytes(B));
   w.l = w.o + cache_slots(sm_count) * R * D;
   return w;
 }
+
+// Beginning and ending a piece takes a block about the time in which 48 KB of codes arrive.
+constexpr __host__ __device__ int cache_item_cost(int TK) { return 384 / TK; }
 
 // Number of keys that token i of Nq queries sees in a sequence of `len` tokens.
 __device__ __forceinline__ int cache_row_limit(int mask, int len, int Nq, int i) {
@@ -58,45 +64,35 @@ __device__ __forceinline__ int cache_row_limit(int mask, int len, int Nq, int i)
 }
 
 // R query rows an item, TK keys a tile.
-template <int R, int TK>
+template <int R, int TK, int kMinTiles>
 struct CacheItems {
+  static constexpr int kItemCost = cache_item_cost(TK);
   int rows, row_tiles;
   __device__ explicit CacheItems(const CacheAttnArgs& a) : rows(a.group * a.Nq), row_tiles((a.group * a.Nq + R - 1) / R) {}
 
   __device__ int tiles(const CacheAttnArgs& a, int len, int rt) const {
-    const int last = min(rows, (rt + 1) * R) - 1;
-    return (cache_row_limit(a.mask, len, a.Nq, last / a.group) + TK - 1) / TK;
+    // the item's last row sees the most; the last item ends with the last token
+    const int tok = rt + 1 == row_tiles ? a.Nq - 1 : ((rt + 1) * R - 1) / a.group;
+    return (cache_row_limit(a.mask, len, a.Nq, tok) + TK - 1) / TK;
   }
-  // Units of one head of a sequence: its tiles, or with C > 0 its pieces of at most C tiles.
-  __device__ long long head_units(const CacheAttnArgs& a, int len, int C) const {
-    long long n = 0;
+  __device__ static int cost(int tiles) { return tiles > 0 ? tiles + kItemCost : 0; }
+  // Tiles of one head of a sequence with the items' costs, and its pieces of at most kMinTiles tiles.
+  __device__ void head_units(const CacheAttnArgs& a, int len, int& ntiles, int& npieces) const {
+    ntiles = npieces = 0;
+#pragma unroll 1
     for (int rt = 0; rt < row_tiles; ++rt) {
       const int t = tiles(a, len, rt);
-      n += C > 0 ? (t + C - 1) / C : t;
+      ntiles += cost(t);
+      npieces += (t + kMinTiles - 1) / kMinTiles;
     }
-    return n;
+  }
+  __device__ int head_tiles(const CacheAttnArgs& a, int len) const {
+    int t, p;
+    head_units(a, len, t, p);
+    return t;
   }
   __device__ int seq_len(const CacheAttnArgs& a, int b) const { return cache_len(a.c, __ldg(a.lens + b)); }
 };
-
-// Exclusive prefix sums over the block's threads of one value each; `out` has NT + 1 entries.
-template <int NT>
-__device__ void block_prefix(long long v, long long* out, long long* warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  long long base = 0;
-  for (int w = 0; w < warp; ++w) base += warp_sums[w];
-  out[threadIdx.x + 1] = base + x;
-  if (threadIdx.x == 0) out[0] = 0;
-  __syncthreads();
-}
 
 // A piece of an item for one block.
 struct CachePiece {
@@ -105,106 +101,132 @@ struct CachePiece {
   int slot;           // -1: the whole item, else its place in the workspace
 };
 
-// The division, and a block's walk over its pieces.  Built by all NT threads of a block; next() is then
-// called by one warp, all lanes alike.
+// The division, and a block's walk over its pieces.  Built by NT threads of a block (numbered `tid`, whole
+// warps that meet at hardware barrier `bar`), then walked by each of their warps, all lanes alike.
 template <int R, int TK, int NT, int kMinTiles>
 struct CacheWalk {
-  struct Shared {
-    long long tiles[NT + 1], units[NT + 1], warp_sums[NT / 32];
+  struct Shared {  // first tile and first unit of each of the NT runs that the sequences are summed in
+    int tiles[NT + 1], units[NT + 1], warp_sums[2 * (NT / 32)];
   };
   const CacheAttnArgs& a;
   Shared& sh;
-  CacheItems<R, TK> items;
-  long long total, at, stop;  // first form: tile numbers; second: piece numbers
-  int C, per;                 // per: sequences a thread of the prefix sums
-  bool by_piece;
-  int step;
+  CacheItems<R, TK, kMinTiles> items;
+  int at, stop, step;  // first form: tile numbers; second: piece numbers
+  int C, per;          // per: sequences a run
+  bool by_piece, placed = false;
   // place of the next tile (first form)
-  int b = 0, head = 0, rt = 0, len = 0, tile = 0, ntiles = 0;
-  long long item_first = 0;
-  bool placed = false;
+  int b = 0, head = 0, rt = 0, len = 0, tile = 0, ntiles = 0, item_first = 0;
 
-  __device__ CacheWalk(const CacheAttnArgs& args, Shared& s, int block, int blocks)
+  __device__ CacheWalk(const CacheAttnArgs& args, Shared& s, int tid, int bar, int block, int blocks)
       : a(args), sh(s), items(args) {
     per = (a.B + NT - 1) / NT;
-    const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
-    long long n = 0;
-    for (int i = b0; i < b1; ++i) n += a.c.heads * items.head_units(a, items.seq_len(a, i), 0);
-    block_prefix<NT>(n, sh.tiles, sh.warp_sums);
-    total = sh.tiles[NT];
-    by_piece = total <= static_cast<long long>(blocks) * kMinTiles;
-    C = by_piece ? kMinTiles : static_cast<int>((total + blocks - 1) / blocks);
+    const int b0 = static_cast<int>(min(static_cast<long long>(a.B), static_cast<long long>(tid) * per));
+    const int b1 = min(a.B - b0, per) + b0;
+    int n = 0, m = 0;
+    for (int i = b0; i < b1; ++i) {
+      const int raw = __ldg(a.lens + i), l = cache_len(a.c, raw);
+      if (raw != l && block == 0) record_page_error(a.err_word);
+      int t, p;
+      items.head_units(a, l, t, p);
+      n += a.c.heads * t;
+      m += a.c.heads * p;
+    }
+    // inclusive sums over the warp, then over the warps
+    const int lane = tid & 31, warp = tid >> 5;
+    int x = n, y = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) {
+        x += u;
+        y += v;
+      }
+    }
+    if (lane == 31) {
+      sh.warp_sums[2 * warp] = x;
+      sh.warp_sums[2 * warp + 1] = y;
+    }
+    sync(bar);
+    int total = 0, pieces = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w < warp) {
+        x += sh.warp_sums[2 * w];
+        y += sh.warp_sums[2 * w + 1];
+      }
+      total += sh.warp_sums[2 * w];
+      pieces += sh.warp_sums[2 * w + 1];
+    }
+    by_piece = total <= blocks * kMinTiles;
+    C = by_piece ? kMinTiles : (total - 1) / blocks + 1;
+    sh.tiles[tid + 1] = x;
+    sh.units[tid + 1] = by_piece ? y : x;
+    if (tid == 0) sh.tiles[0] = sh.units[0] = 0;
+    sync(bar);
     if (by_piece) {
-      n = 0;
-      for (int i = b0; i < b1; ++i) n += a.c.heads * items.head_units(a, items.seq_len(a, i), C);
-      block_prefix<NT>(n, sh.units, sh.warp_sums);
       at = block;
-      stop = sh.units[NT];
+      stop = pieces;
       step = blocks;
     } else {
-      sh.units[threadIdx.x + 1] = sh.tiles[threadIdx.x + 1];
-      if (threadIdx.x == 0) sh.units[0] = 0;
-      at = static_cast<long long>(block) * C;
+      at = block * C;
       stop = min(total, at + C);
       step = 0;
     }
-    __syncthreads();
     if (block == 0) {  // for the merge
       const CacheWs ws = cache_ws(a.ws, a.B, R, a.c.d, a.sm_count);
-      long long f = sh.tiles[threadIdx.x];
+      int f = x - n;
       for (int i = b0; i < b1; ++i) {
         ws.first[i] = f;
-        const int raw = __ldg(a.lens + i), l = cache_len(a.c, raw);
-        if (raw != l) record_page_error(a.err_word);
-        f += a.c.heads * items.head_units(a, l, 0);
+        f += a.c.heads * items.head_tiles(a, items.seq_len(a, i));
       }
-      if (threadIdx.x == 0) *ws.head = CacheSchedHeader{total, C, by_piece ? 1 : 0};
+      if (tid == 0) *ws.head = CacheSchedHeader{C, by_piece ? 1 : 0};
     }
   }
 
+  __device__ static void sync(int bar) {
+    if constexpr (NT > 32) named_bar_sync(bar, NT); else __syncwarp();
+  }
+
   // Finds unit x: sets b, len, head, rt and item_first, and returns the unit's number inside its item.
-  __device__ long long locate(long long x) {
-    int lo = 0, hi = NT;  // units[lo] <= x < units[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (sh.units[mid] <= x) lo = mid; else hi = mid;
-    }
-    x -= sh.units[lo];
-    item_first = sh.tiles[lo];
-    const int piece = by_piece ? C : 0;
-    long long hu = 0;
-    for (b = lo * per;; ++b) {
+  __device__ int locate(int x) {
+    // the run: the last whose first unit is at most x
+    int run = -1;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) run += __popc(__ballot_sync(0xffffffffu, sh.units[i * 32 + (threadIdx.x & 31)] <= x));
+    x -= sh.units[run];
+    item_first = sh.tiles[run];
+    int ht, hp, hu;
+    for (b = run * per;; ++b) {
       len = items.seq_len(a, b);
-      hu = items.head_units(a, len, piece);
+      items.head_units(a, len, ht, hp);
+      hu = by_piece ? hp : ht;
       if (x < hu * a.c.heads) break;
       x -= hu * a.c.heads;
-      item_first += a.c.heads * items.head_units(a, len, 0);
+      item_first += a.c.heads * ht;
     }
-    head = static_cast<int>(x / hu);
+    head = x / hu;
     x -= head * hu;
-    item_first += head * items.head_units(a, len, 0);
+    item_first += head * ht;
     for (rt = 0;; ++rt) {
       ntiles = items.tiles(a, len, rt);
-      const long long u = by_piece ? (ntiles + C - 1) / C : ntiles;
+      const int u = by_piece ? (ntiles + kMinTiles - 1) / kMinTiles : items.cost(ntiles);
       if (x < u) break;
       x -= u;
-      item_first += ntiles;
+      item_first += items.cost(ntiles);
     }
     return x;
   }
 
   __device__ bool next(CachePiece& p) {
-    if (at >= stop) return false;
-    if (by_piece) {
-      tile = static_cast<int>(locate(at)) * C;
-      at += step;
-    } else {
-      if (!placed) {
-        tile = static_cast<int>(locate(at));
+    for (;;) {
+      if (at >= stop) return false;
+      int x;  // unit of the item at which the piece begins
+      if (by_piece || !placed) {
+        x = locate(at);
         placed = true;
       } else {  // the item after the last one, passing those without tiles
-        item_first += ntiles;
-        tile = 0;
+        item_first += items.cost(ntiles);
+        x = 0;
         do {
           if (++rt == items.row_tiles) {
             rt = 0;
@@ -217,19 +239,116 @@ struct CacheWalk {
           ntiles = items.tiles(a, len, rt);
         } while (ntiles == 0);
       }
+      if (by_piece) {
+        tile = x * kMinTiles;
+        p.end = min(ntiles, tile + kMinTiles);
+        at += step;
+      } else {
+        const int y = min(items.cost(ntiles), x + (stop - at));
+        at += y - x;
+        if (y <= items.kItemCost) continue;  // nothing but the item's cost
+        tile = max(0, x - items.kItemCost);
+        p.end = y - items.kItemCost;
+      }
+      break;
     }
     p.b = b;
     p.head = head;
     p.rt = rt;
     p.len = len;
     p.begin = tile;
-    p.end = by_piece ? min(ntiles, tile + C)
-                     : static_cast<int>(min(static_cast<long long>(ntiles), tile + (stop - at)));
-    const long long start = item_first + tile;
-    p.slot = (p.begin == 0 && p.end == ntiles) ? -1 : static_cast<int>(2 * (start / C) + (tile != 0));
-    if (!by_piece) at += p.end - p.begin;
+    p.slot = tile == 0 && p.end == ntiles ? -1 : 2 * ((item_first + items.kItemCost + tile) / C) + (tile != 0);
     return true;
   }
 };
+
+// Merge of the pieces of divided items, one warp a query row, and the rows that see no token:
+// L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s over the row's pieces in key order.
+template <int D, bool BF16, int R, int TK, int kMinTiles>
+__global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant__ CacheAttnArgs a) {
+  constexpr int V = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const CacheItems<R, TK, kMinTiles> items(a);
+  const unsigned rid = blockIdx.x * 8u + warp;
+  const bool mine = rid < static_cast<unsigned>(a.B) * a.c.heads * items.rows;
+  const int r = static_cast<int>(rid % items.rows);
+  const int bh = static_cast<int>(rid / items.rows);
+  const int head = bh % a.c.heads, b = bh / a.c.heads;
+  const int rt = r / R;
+  const CacheWs ws = cache_ws(a.ws, a.B, R, D, a.sm_count);
+  const int tok = r / a.group, hq = head * a.group + r - tok * a.group;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (!mine) return;
+  const int len = items.seq_len(a, b);
+  const CacheSchedHeader hd = *ws.head;
+  int first = ws.first[b];
+  const int nt = items.tiles(a, len, rt), C = hd.per_piece;
+  int pieces = 0;
+  if (nt > 0) {
+    if (items.row_tiles == 1) {
+      first += head * items.cost(nt);
+    } else {
+      first += head * items.head_tiles(a, len);
+      for (int i = 0; i < rt; ++i) first += items.cost(items.tiles(a, len, i));
+    }
+    first += items.kItemCost;  // number of its first tile
+    pieces = hd.pieces ? (nt + C - 1) / C : (first + nt - 1) / C - first / C + 1;
+    if (pieces == 1) return;  // written by the block that had all of it
+  }
+  // Lane i keeps piece i (of each 32): its workspace row and its log-sum-exp.
+  const int c0 = first / C;
+  auto row_of = [&](int i) {
+    const int start = hd.pieces ? first + i * C : (i == 0 ? first : (c0 + i) * C);
+    return (2 * (hd.pieces ? start / C : c0 + i) + (i != 0)) * R + (r - rt * R);
+  };
+  float mx = -INFINITY;
+  for (int i = lane; i < pieces; i += 32) mx = fmaxf(mx, ws.l[row_of(i)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float ms = mx == -INFINITY ? 0.f : mx;
+  float acc[V], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+  for (int base = 0; base < pieces; base += 32) {
+    const int i = base + lane;
+    const int at = i < pieces ? row_of(i) : 0;
+    const float w = i < pieces ? ex2_approx(ws.l[at] - ms) : 0.f;  // NaN where the piece is
+    const int n = min(32, pieces - base);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const float* op = ws.o + static_cast<size_t>(__shfl_sync(0xffffffffu, at, k)) * D + lane * V;
+      if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(op);
+        acc[0] = fmaf(wk, x.x, acc[0]);
+        acc[1] = fmaf(wk, x.y, acc[1]);
+        acc[2] = fmaf(wk, x.z, acc[2]);
+        acc[3] = fmaf(wk, x.w, acc[3]);
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(op);
+        acc[0] = fmaf(wk, x.x, acc[0]);
+        acc[1] = fmaf(wk, x.y, acc[1]);
+      }
+      sum += wk;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint16_t* dst = static_cast<uint16_t*>(a.o) + b * a.so.b + hq * a.so.h + tok * a.so.n + lane * V;
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack2<BF16>(acc[0] * inv, acc[1] * inv);
+  if (lane == 0)
+    a.lse[(static_cast<long long>(b) * a.c.heads * a.group + hq) * a.Nq + tok] =
+        sum == 0.f ? -INFINITY : (ms + __log2f(sum)) * 0.6931471805599453f;
+}
+
+template <int D, bool BF16, int R, int TK, int kMinTiles>
+cudaError_t launch_cache_merge(const CacheAttnArgs& a, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(a.B) * a.c.heads * a.group * a.Nq;
+  return launch_dependent(cache_merge_kernel<D, BF16, R, TK, kMinTiles>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0,
+                          stream, a);
+}
 
 }  // namespace exattn

@@ -165,6 +165,24 @@ struct CacheAttnArgs {
 constexpr int kBwdPre = 1, kBwdMain = 2, kBwdConvert = 4, kBwdAll = 7, kBwdDq = 8;
 constexpr int kBwdDeterministic = kBwdPre | kBwdMain | kBwdDq;
 
+// Launches a kernel with programmatic stream serialisation: it may start before the kernel ahead of it
+// on the stream has finished, and waits for that itself (griddep_wait).
+template <typename Args>
+cudaError_t launch_dependent(void (*kernel)(const Args), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                             const Args& args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 // Sets the message attn_last_error returns on this host thread.
 void set_last_error(const char* msg);
 
@@ -182,8 +200,14 @@ cudaError_t launch_kl_bwd_fused(const KlArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_write(const CacheIoArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheIoArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream);
-// Tokens per box of the tensor maps launch_cache_attn wants, and its workspace bytes.
-int cache_attn_box_tokens(int page);
-size_t cache_attn_workspace(int B, int rows, int d, int sm_count);
+// Tokens per box of the tensor maps launch_cache_attn wants; query rows and keys of its tiles for so many
+// rows a key/value head; its workspace bytes.
+int cache_attn_box_tokens(int page, int d);
+constexpr int kCacheItemCost = 16;  // above every cache_item_cost plus a rounded-up tile
+struct CacheAttnShape {
+  int rows, keys;
+};
+CacheAttnShape cache_attn_shape(long long rows, int d);
+size_t cache_attn_workspace(int B, long long rows, int d, int sm_count);
 
 }  // namespace exattn

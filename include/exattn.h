@@ -605,9 +605,11 @@ attn_status attn_cache_read(const attn_cache* cache, const int* start, const int
  * same bits on every run.
  * workspace: attn_fwd_cache_workspace_size bytes, 256-byte aligned, contents
  * on entry irrelevant; calls that may run at the same time need one each.
- * Errors as attn_fwd_strided, plus ATTN_ERR_INVALID_ARG for a cache that
- * breaks the rules of attn_cache or an H that is no multiple of its heads, and
- * ATTN_ERR_WORKSPACE.  The division of the key axis over the SMs and the merge
+ * Errors as attn_fwd_strided, plus ATTN_ERR_WORKSPACE, and
+ * ATTN_ERR_INVALID_ARG for a cache that breaks the rules of attn_cache, an H
+ * that is no multiple of its heads, and more than 2^31 - 1 query rows, or tiles
+ * of 32 tokens and 8 query rows of one key/value head, in B sequences as long
+ * as the page table allows.  The division of the key axis over the SMs and the merge
  * of its parts by their log-sum-exp follow the StreamKL summary's split-K
  * variant; the cache has no counterpart on the pages.
  */
