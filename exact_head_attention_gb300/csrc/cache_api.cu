@@ -145,8 +145,9 @@ extern "C" attn_status attn_fwd_cache(const void* Q, attn_strides q_strides, con
   const uint64_t lines = static_cast<uint64_t>(cache->num_pages) * cache->heads * cache->page_size * cache->d / 128;
   const uint32_t box = static_cast<uint32_t>(cache_attn_box_tokens(cache->page_size, cache->d) * cache->d / 128);
   CUresult r;
-  if ((r = api_encode_lines(&a.tm_k, cache->k, lines, box)) != CUDA_SUCCESS ||
-      (r = api_encode_lines(&a.tm_v, cache->v, lines, box)) != CUDA_SUCCESS)
+  if (group * static_cast<long long>(Nq) <= kCacheStreamRows &&
+      ((r = api_encode_lines(&a.tm_k, cache->k, lines, box)) != CUDA_SUCCESS ||
+       (r = api_encode_lines(&a.tm_v, cache->v, lines, box)) != CUDA_SUCCESS))
     return api_driver_fail("cuTensorMapEncodeTiled", r);
   a.q = Q;
   a.o = O;

@@ -656,7 +656,10 @@ cudaError_t launch_d(const CacheAttnArgs& a, cudaStream_t stream) {
 
 int cache_attn_box_tokens(int page, int d) { return page < 4096 / d ? page : 4096 / d; }
 
-CacheAttnShape cache_attn_shape(long long rows, int d) { return {rows >= 32 ? 32 : static_cast<int>((rows + 7) / 8 * 8), 4096 / d}; }
+CacheAttnShape cache_attn_shape(long long rows, int d) {
+  if (rows > kCacheStreamRows) return {rows > 128 ? 256 : 128, 128};
+  return {static_cast<int>((rows + 7) / 8 * 8), 4096 / d};
+}
 
 size_t cache_attn_workspace(int B, long long rows, int d, int sm_count) {
   const size_t R = cache_attn_shape(rows, d).rows;
@@ -665,6 +668,7 @@ size_t cache_attn_workspace(int B, long long rows, int d, int sm_count) {
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream) {
+  if (static_cast<long long>(a.group) * a.Nq > kCacheStreamRows) return launch_cache_tile(a, stream);
   return a.c.d == 128 ? launch_d<128>(a, stream) : launch_d<64>(a, stream);
 }
 

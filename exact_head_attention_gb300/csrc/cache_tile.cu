@@ -1,0 +1,732 @@
+// Attention over the 8-bit cache for many query rows a key/value head (chunks of a prompt, drafted tokens
+// under shared heads): the tensor-core form of cache_attn.cu.
+//
+// Mathematics as there: codes as they are in fp16, the key scale on the scores, the value scale over a lagging
+// vref on the probabilities.
+//
+// Bound.  4 d flops for each row and key: the tensor cores, which tcgen05 reaches with 128 x 128 tiles in
+// tensor memory.  Its operands are fp16 in shared memory, so two warps turn each 128-token tile of codes, copied
+// in by the copy engine, into the swizzled operand tiles; 256 query rows share that work.
+//
+// Two chains of (scores, softmax, product) alternate on the tensor cores, one softmax warpgroup each, in the
+// order S0[0] S1[0] | PV0[j] S0[j+1] PV1[j] S1[j+1] | ..., so that one chain's softmax hides behind the other's
+// products:
+//   PAIR    more than 128 rows: an item has 256, chain t works on rows [128 t, 128 t + 128)
+//   else    an item has 128 rows, and chain t works on every second key tile; the two results are joined in
+//           the epilogue.  Both chains then have work at any number of rows.
+//
+// Warp roles (384 threads, registers re-split per warpgroup):
+//   warps 0-3, 4-7  softmax of chain 0 and 1 (thread = query row = TMEM lane); they also bring the query rows
+//                   into their operand tile and write the results
+//   warp  8         MMA issuer (one thread) and TMEM owner
+//   warp  9         producer: walks the block's pieces (cache_sched.cuh), looks pages up, copies codes
+//   warps 10-11     converters, 64 tokens of each tile apiece
+// Tensor memory: S_t (P_t over its first 64 columns) at 128 t, O_t at 256 + 128 t.
+// Every role walks the same pieces and counts tiles on, so the barriers are never re-armed.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "cache8.cuh"
+#include "cache_sched.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace exattn {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr uint32_t kRegsSoftmax = 208, kRegsControl = 88;
+static_assert(2 * kRegsSoftmax + kRegsControl == 3 * 168, "register split must match the launch");
+constexpr int kTK = 128;
+constexpr uint32_t kChunk = 128 * 128;  // 128 rows x 128 bytes
+constexpr int kPieceRing = 3, kMetaRing = 8;
+constexpr float kShift = 3.f, kVrefLag = 16.f;  // as in cache_attn.cu
+
+template <int D, bool PAIR>
+struct Cfg {
+  static constexpr int R = PAIR ? 256 : 128;
+  static constexpr int MIN_TILES = PAIR ? 2 : 4;
+  static constexpr uint32_t TILE = 128 * D * 2;                // an fp16 operand tile
+  static constexpr uint32_t RAW = 128 * D;                     // a tile of codes
+  static constexpr int NS = D == 128 ? 2 : 3;                  // K and V operand slots
+  static constexpr int NR = D == 128 ? (PAIR ? 2 : 3) : 4;     // slots of codes, K and V in turn
+  // Scales stay in use from a tile's copy to its softmax: NS + NR / 2 + 2 tiles at most.
+  static_assert(NS + (NR + 1) / 2 + 2 <= kMetaRing, "scales of the tiles under way");
+  using Walk = CacheWalk<R, kTK, 32, MIN_TILES>;
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_K = OFF_Q + (PAIR ? 2 : 1) * TILE;
+  static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
+  static constexpr uint32_t OFF_RAW = OFF_V + NS * TILE;
+  static constexpr uint32_t OFF_META = OFF_RAW + NR * RAW;           // [kMetaRing][8] {ks, vs}
+  static constexpr uint32_t OFF_STAT = OFF_META + kMetaRing * 64;    // !PAIR: {m, l} [2][128], vref [2][4]
+  static constexpr uint32_t OFF_PIECE = OFF_STAT + (PAIR ? 0 : 2 * 128 * 8 + 32);
+  static constexpr uint32_t OFF_BAR = OFF_PIECE + kPieceRing * 32;
+  static constexpr int NBAR = 2 + 4 * NS + 2 * NR + 6 + kMetaRing + 2 * kPieceRing + 2;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr uint32_t OFF_SCHED = OFF_MISC + 16;
+  static constexpr uint32_t BYTES = OFF_SCHED + sizeof(typename Walk::Shared);
+  static_assert(BYTES <= 232448, "shared memory of a block");
+};
+
+template <int NS, int NR>
+struct Bars {
+  uint32_t base;
+  __device__ uint32_t at(int i) const { return base + 8 * i; }
+  __device__ uint32_t q_full(int t) const { return at(t); }
+  __device__ uint32_t k_full(int s) const { return at(2 + s); }
+  __device__ uint32_t k_empty(int s) const { return at(2 + NS + s); }
+  __device__ uint32_t v_full(int s) const { return at(2 + 2 * NS + s); }
+  __device__ uint32_t v_empty(int s) const { return at(2 + 3 * NS + s); }
+  __device__ uint32_t raw_full(int s) const { return at(2 + 4 * NS + s); }
+  __device__ uint32_t raw_empty(int s) const { return at(2 + 4 * NS + NR + s); }
+  static constexpr int kB = 2 + 4 * NS + 2 * NR;
+  __device__ uint32_t s_full(int t) const { return at(kB + t); }
+  __device__ uint32_t p_full(int t) const { return at(kB + 2 + t); }
+  __device__ uint32_t o_full(int t) const { return at(kB + 4 + t); }
+  __device__ uint32_t meta_full(int s) const { return at(kB + 6 + s); }
+  __device__ uint32_t piece_full(int s) const { return at(kB + 6 + kMetaRing + s); }
+  __device__ uint32_t piece_empty(int s) const { return at(kB + 6 + kMetaRing + kPieceRing + s); }
+  __device__ uint32_t join() const { return at(kB + 6 + kMetaRing + 2 * kPieceRing); }
+  __device__ uint32_t mma_done() const { return at(kB + 7 + kMetaRing + 2 * kPieceRing); }
+};
+
+// One key tile of the online softmax for this thread's query row.  Scores of the 16-token group g count
+// fac * ks[g]; P goes out in fp16 times vs[g] / vref.  Columns at or past `lim` are hidden (MASKED).
+template <int D, bool MASKED>
+__device__ __forceinline__ void softmax_scaled(uint32_t tS, uint32_t tO, const float2* sc, int lim, float fac, bool first,
+                                               float& m, float& l, float& vref) {
+  uint32_t sr[4][32];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
+  tmem_wait_ld();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) reg_fence32(sr[c]);
+  if constexpr (MASKED) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (c * 32 + i >= lim) sr[c][i] = __float_as_uint(-INFINITY);
+  }
+  float m_new = -INFINITY, v_new = -INFINITY;
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    float a = -INFINITY, b = -INFINITY;  // a NaN is passed over: it is met below
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const uint32_t* s = &sr[g >> 1][(g & 1) * 16 + i];
+      a = max3(a, __uint_as_float(s[0]), __uint_as_float(s[1]));
+      b = max3(b, __uint_as_float(s[2]), __uint_as_float(s[3]));
+    }
+    const float2 x = sc[g];
+    m_new = fmaxf(m_new, fmaxf(a, b) * (fac * x.x));
+    v_new = fmaxf(v_new, x.y);
+  }
+  if (first) {
+    m = m_new;
+    vref = fmaxf(v_new, 0.f);
+  } else {
+    const bool need = m_new > m + 8.0f;
+    if (__any_sync(0xffffffffu, need || v_new > vref * kVrefLag)) {
+      // O is complete for the previous key tile of this chain: S was issued after its last product.
+      const float to = need ? m_new : m;
+      const float al = need ? ex2_approx(m - to) : 1.0f;
+      float ov = al;
+      if (v_new > vref) {
+        ov *= vref / v_new;
+        vref = v_new;
+      }
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + c * 32, o);
+        tmem_wait_ld();
+        reg_fence32(o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ov);
+        tmem_st32(tO + c * 32, o);
+      }
+      tmem_wait_st();
+      l *= al;
+      m = to;
+    }
+  }
+  const float ms = m == -INFINITY ? 0.f : m - kShift;
+  const float vinv = vref > 0.f ? 1.0f / vref : 0.f;
+  const uint64_t nm2 = f2_pack(-ms, -ms);
+  uint64_t acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = f2_pack(0.f, 0.f);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pk[32];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float2 s = sc[4 * h + g];
+      const float f = fac * s.x, r = s.y * vinv;
+      const uint64_t f2 = f2_pack(f, f), r2 = f2_pack(r, r);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = g * 8 + k, p = h * 32 + i;  // score pair (2 p, 2 p + 1)
+        const uint64_t x = f2_fma(f2_pack(__uint_as_float(sr[p >> 4][(2 * p) & 31]), __uint_as_float(sr[p >> 4][(2 * p + 1) & 31])),
+                                  f2, nm2);
+        float x0, x1;
+        f2_unpack(x, x0, x1);
+        float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+        if constexpr (MASKED) {  // whatever the scale
+          p0 = 2 * p >= lim ? 0.f : p0;
+          p1 = 2 * p + 1 >= lim ? 0.f : p1;
+        }
+        acc[i & 3] = f2_add(acc[i & 3], f2_pack(p0, p1));
+        float y0, y1;
+        f2_unpack(f2_mul(f2_pack(p0, p1), r2), y0, y1);
+        if constexpr (MASKED) {
+          y0 = 2 * p >= lim ? 0.f : y0;
+          y1 = 2 * p + 1 >= lim ? 0.f : y1;
+        }
+        pk[i] = pack2<false>(y0, y1);
+      }
+    }
+    tmem_st32(tS + h * 32, pk);
+  }
+  float s0, s1;
+  f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+  l += s0 + s1;
+}
+
+// A query row in fp16 into an operand tile, 16-byte units [u0, u1) of it (all chunks together), times a power
+// of two where it is bf16; returns the factor that undoes it.  A row that is not there is zero.
+template <int D, bool BF16>
+__device__ __forceinline__ float stage_query_row(const uint16_t* src, bool there, uint32_t tile, int r, int u0, int u1) {
+  float mul = 1.f, back = 1.f;
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+  if constexpr (BF16) {
+    uint32_t mx = 0u;
+    if (there) {
+#pragma unroll
+      for (int u = 0; u < D / 8; ++u) {
+        const uint4 x = __ldg(s + u);
+        mx = __vmaxu2(__vmaxu2(mx, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
+        mx = __vmaxu2(__vmaxu2(mx, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
+      }
+    }
+    mx = max(mx & 0xffffu, mx >> 16);
+    // As in cache_attn.cu: the largest value comes to lie in [2^14, 2^15).
+    const int e = static_cast<int>(mx >> 7) - 127;
+    if (mx != 0u && e < 128) {
+      const int k = min(14 - e, 113);
+      mul = __int_as_float((127 + k) << 23);
+      back = __int_as_float((127 - k) << 23);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < D / 8; ++u) {
+    if (u < u0 || u >= u1) continue;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (there) x = __ldg(s + u);
+    if constexpr (BF16) {
+      x.x = pack2<false>(unpack_lo<true>(x.x) * mul, unpack_hi<true>(x.x) * mul);
+      x.y = pack2<false>(unpack_lo<true>(x.y) * mul, unpack_hi<true>(x.y) * mul);
+      x.z = pack2<false>(unpack_lo<true>(x.z) * mul, unpack_hi<true>(x.z) * mul);
+      x.w = pack2<false>(unpack_lo<true>(x.w) * mul, unpack_hi<true>(x.w) * mul);
+    }
+    st_shared_v4(tile + (u >> 3) * kChunk + sw128_offset(r, u & 7), x.x, x.y, x.z, x.w);
+  }
+  return back;
+}
+
+// 64 of a tile's 128 tokens (half `cw`) from codes to the operand tile; tokens at or past `valid` become zero.
+// A warp takes 16-code units such that neither its reads nor its two writes meet a bank twice in 8 lanes.
+template <int D, int FMT>
+__device__ __forceinline__ void convert_half(const uint8_t* raw, uint32_t tile, int cw, int lane, int valid) {
+  constexpr int ROWS = D == 128 ? 4 : 8;  // token rows a step
+#pragma unroll 4
+  for (int it = 0; it < 64 / ROWS; ++it) {
+    int row, chunk;
+    const int q = lane & 3;
+    if constexpr (D == 128) {
+      const int p = (lane >> 2) & 1;
+      row = cw * 64 + it * ROWS + p + 2 * (lane >> 4);
+      chunk = p ^ ((lane >> 3) & 1);
+    } else {
+      row = cw * 64 + it * ROWS + (lane >> 2);
+      chunk = 0;
+    }
+    const uint4 c = *reinterpret_cast<const uint4*>(raw + row * D + chunk * 64 + q * 16);
+    uint32_t o[8];
+    codes_to_f16<FMT>(c.x, o[0], o[1]);
+    codes_to_f16<FMT>(c.y, o[2], o[3]);
+    codes_to_f16<FMT>(c.z, o[4], o[5]);
+    codes_to_f16<FMT>(c.w, o[6], o[7]);
+    if (row >= valid) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = 0u;
+    }
+    const uint32_t dst = tile + chunk * kChunk;
+    st_shared_v4(dst + sw128_offset(row, 2 * q), o[0], o[1], o[2], o[3]);
+    st_shared_v4(dst + sw128_offset(row, 2 * q + 1), o[4], o[5], o[6], o[7]);
+  }
+}
+
+template <int D, int FMT, bool BF16, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_constant__ CacheAttnArgs a) {
+  using C = Cfg<D, PAIR>;
+  constexpr int NS = C::NS, NR = C::NR;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t sbase = smem_u32(smem_raw);
+  if (!smem_base_aligned(sbase, a.err_word)) return;
+  const Bars<NS, NR> bars{sbase + C::OFF_BAR};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + C::OFF_MISC);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_raw + C::OFF_MISC + 4);
+  const WaitCtx wc{abort_flag, a.err_word, a.timeout_ns};
+  int* pieces = reinterpret_cast<int*>(smem_raw + C::OFF_PIECE);  // [kPieceRing][8]
+  float2* meta = reinterpret_cast<float2*>(smem_raw + C::OFF_META);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0u;
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bars.q_full(t), 4);
+      mbar_init(bars.s_full(t), 1);
+      mbar_init(bars.p_full(t), 4);
+      mbar_init(bars.o_full(t), 1);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(bars.k_full(s), 2);
+      mbar_init(bars.k_empty(s), 1);
+      mbar_init(bars.v_full(s), 2);
+      mbar_init(bars.v_empty(s), 1);
+    }
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(bars.raw_full(s), 1);
+      mbar_init(bars.raw_empty(s), 2);
+    }
+    for (int s = 0; s < kMetaRing; ++s) mbar_init(bars.meta_full(s), 1);
+    for (int s = 0; s < kPieceRing; ++s) {
+      mbar_init(bars.piece_full(s), 1);
+      mbar_init(bars.piece_empty(s), 11);  // 8 softmax warps, 2 converters, the MMA issuer
+    }
+    mbar_init(bars.join(), 8);
+    mbar_init(bars.mma_done(), 1);
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // A dependent launch: what is ahead on the stream has written its results before anything is read.
+  griddep_wait();
+  griddep_launch_dependents();
+  const int rows = a.group * a.Nq;
+
+  struct Piece {
+    int b, head, rt, len, begin, end, slot;
+    int nrows, n0, n1;  // rows of the item; key tiles of each chain
+  };
+  // The i-th piece; false at the end, or after a failed wait.
+  auto next_piece = [&](int i, Piece& p, bool one_thread) -> bool {
+    const uint32_t bar = bars.piece_full(i % kPieceRing), ph = (i / kPieceRing) & 1;
+    if (!(one_thread ? mbar_wait(bar, ph, wc) : mbar_wait_warp(bar, ph, wc))) return false;
+    const int* d = pieces + (i % kPieceRing) * 8;
+    p.b = d[0];
+    p.head = d[1];
+    p.rt = d[2];
+    p.len = d[3];
+    p.begin = d[4];
+    p.end = d[5];
+    p.slot = d[6];
+    p.nrows = min(C::R, rows - p.rt * C::R);
+    const int n = p.end - p.begin;
+    p.n0 = PAIR ? n : (n + 1) / 2;
+    p.n1 = PAIR ? (p.nrows > 128 ? n : 0) : n / 2;
+    return p.b >= 0;
+  };
+
+  if (warp >= 8) {
+    regs_decrease<kRegsControl>();
+    if (warp == 9) {
+      // ------------------------------------------------------------ producer
+      // Lane g < 8 looks after 16-token group g of a tile.  Page numbers, scales and copies of a tile hang on
+      // one another, so tiles run through three stages, one behind the other.
+      typename C::Walk walk(a, *reinterpret_cast<typename C::Walk::Shared*>(smem_raw + C::OFF_SCHED), lane, 0, blockIdx.x,
+                            gridDim.x);
+      const int psh = a.c.page_shift, box = min(1 << psh, kTK);
+      const bool feeds = lane < 8;
+      const bool leads = feeds && ((16 * lane) & (box - 1)) == 0;
+      constexpr int kNoTile = -2;
+      struct Round {
+        int key, page, head, tile;  // tile: kNoTile for none (the same for all lanes)
+        float ks, vs;
+      };
+      CachePiece p{};
+      int tile = 0, announced = 0, issued = 0, raws = 0, left = 3;
+      bool have = false, ok = true;
+      Round r0, r1, r2;
+      r1.tile = r2.tile = kNoTile;
+      auto copy = [&](const uint8_t* codes, const Round& r) -> bool {
+        const int s = raws % NR;
+        if (!mbar_wait_warp(bars.raw_empty(s), ((raws / NR) & 1) ^ 1, wc)) return false;
+        const bool mine = leads && r.page >= 0;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
+        if (lane == 0) mbar_arrive_expect_tx(bars.raw_full(s), n * box * D);
+        __syncwarp();
+        if (mine) {
+          const long long row = ((static_cast<long long>(r.page) * a.c.heads + r.head) << psh) + (r.key & ((1 << psh) - 1));
+          bulk_load(sbase + C::OFF_RAW + s * C::RAW + lane * 16 * D, codes + row * D, box * D, bars.raw_full(s));
+        }
+        ++raws;
+        return true;
+      };
+      while (left > 0 && ok) {
+        r0 = r1;
+        r1 = r2;
+        if (r0.tile != kNoTile) {
+          ok = copy(a.c.k, r0);
+          if (ok) {
+            const int ms = issued % kMetaRing;
+            if (feeds) meta[ms * 8 + lane] = make_float2(r0.ks, r0.vs);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.meta_full(ms));
+            ++issued;
+            ok = copy(a.c.v, r0);
+          }
+          if (!ok) break;
+        }
+        r2.tile = kNoTile;
+        ++tile;
+        if (left == 3 && (!have || tile >= p.end)) {
+          have = walk.next(p);
+          if (!have) left = 2;
+          tile = p.begin;
+          const int i = announced % kPieceRing;
+          ok = mbar_wait_warp(bars.piece_empty(i), ((announced / kPieceRing) & 1) ^ 1, wc);
+          if (!ok) break;
+          ++announced;
+          if (lane == 0) {
+            int* d = pieces + i * 8;
+            d[0] = have ? p.b : -1;
+            d[1] = p.head;
+            d[2] = p.rt;
+            d[3] = p.len;
+            d[4] = p.begin;
+            d[5] = p.end;
+            d[6] = p.slot;
+            mbar_arrive(bars.piece_full(i));
+          }
+        } else if (left < 3) {
+          --left;
+        }
+        if (have && left == 3) {
+          r2.tile = tile;
+          r2.head = p.head;
+          r2.key = tile * kTK + 16 * lane;
+          const bool there = feeds && r2.key < p.len;
+          r2.page = there ? cache_page_number(a.c, p.b, r2.key) : 0x7fffffff;
+          r2.ks = there ? 0.f : 1.f;
+        }
+        if (r1.tile != kNoTile) {
+          const bool there = r1.ks == 0.f;
+          r1.page = cache_page_checked(a.c, r1.page);
+          r1.ks = r1.vs = there ? __int_as_float(0x7fffffff) : 0.f;
+          if (r1.page >= 0) {
+            const long long h = static_cast<long long>(r1.page) * a.c.heads + r1.head;
+            r1.ks = __ldg(a.c.k_scale + h);
+            r1.vs = __ldg(a.c.v_scale + h);
+          } else if (there) {
+            record_page_error(a.err_word);
+          }
+        }
+      }
+      // Every copy issued must land before the block exits, also where the other roles gave up.
+      if (lane == 0)
+        for (int n = max(0, raws - NR); n < raws; ++n) mbar_drain(bars.raw_full(n % NR), (n / NR) & 1, a.timeout_ns);
+    } else if (warp == 8) {
+      // ------------------------------------------------------------ MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idS = idesc_f16(128, 128, false, false, false);
+        constexpr uint32_t idPV = idesc_f16(128, D, false, false, true);
+        constexpr uint32_t kTileLo = C::TILE >> 4;
+        const uint32_t q_lo = sdesc_lo(sbase + C::OFF_Q, 16), k_lo = sdesc_lo(sbase + C::OFF_K, 16),
+                       v_lo = sdesc_lo(sbase + C::OFF_V, kChunk);
+        int kt = 0;  // key tiles of earlier pieces
+        uint32_t pc[2] = {0, 0}, qc[2] = {0, 0};
+        bool ok = true;
+        Piece p;
+        for (int pi = 0; ok && next_piece(pi, p, true); ++pi) {
+          const int nt[2] = {p.n0, p.n1};
+          const bool both = p.n1 > 0;
+          auto tile_of = [&](int t, int j) { return kt + (PAIR ? j : 2 * j + t); };
+          auto issue_S = [&](int t, int j) -> bool {
+            const int n = tile_of(t, j), s = n % NS;
+            if (!mbar_wait(bars.k_full(s), (n / NS) & 1, wc)) return false;
+            tc_fence_after();
+            const uint32_t d = tmem + t * 128, a_lo = q_lo + (PAIR ? t * kTileLo : 0), b_lo = k_lo + s * kTileLo;
+            mma_ss_lo<false>(d, a_lo, b_lo, idS);
+#pragma unroll
+            for (int k = 1; k < D / 16; ++k) {
+              const uint32_t off = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
+              mma_ss_lo<true>(d, a_lo + off, b_lo + off, idS);
+            }
+            mma_commit(bars.s_full(t));
+            if (!PAIR || t == 1 || !both) mma_commit(bars.k_empty(s));  // the slot's last reader
+            return true;
+          };
+          auto issue_PV = [&](int t, int j) -> bool {
+            const int n = tile_of(t, j), s = n % NS;
+            if (!mbar_wait(bars.v_full(s), (n / NS) & 1, wc)) return false;
+            if (!mbar_wait(bars.p_full(t), pc[t] & 1, wc)) return false;
+            ++pc[t];
+            tc_fence_after();
+            const uint32_t d = tmem + 256 + t * 128, pa = tmem + t * 128, b_lo = v_lo + s * kTileLo;
+            mma_ts_lo_rt(d, pa, b_lo, idPV, j > 0 ? 1u : 0u);
+#pragma unroll
+            for (int k = 1; k < kTK / 16; ++k) mma_ts_lo<true>(d, pa + k * 8, b_lo + k * (2048 >> 4), idPV);
+            if (!PAIR || t == 1 || !both) mma_commit(bars.v_empty(s));
+            if (j == nt[t] - 1) mma_commit(bars.o_full(t));
+            return true;
+          };
+          // the query tiles: each chain's own, or halves of one from both warpgroups
+          for (int t = 0; ok && t < 2; ++t)
+            if (!PAIR || nt[t] > 0) ok = mbar_wait(bars.q_full(t), qc[t]++ & 1, wc);
+          if (!ok) break;
+          tc_fence_after();
+          ok = issue_S(0, 0);
+          if (ok && both) ok = issue_S(1, 0);
+          for (int j = 0; ok && j < p.n0; ++j) {
+            if (!(ok = issue_PV(0, j))) break;
+            if (j + 1 < p.n0 && !(ok = issue_S(0, j + 1))) break;
+            if (j < p.n1) {
+              if (!(ok = issue_PV(1, j))) break;
+              if (j + 1 < p.n1 && !(ok = issue_S(1, j + 1))) break;
+            }
+          }
+          kt += p.end - p.begin;
+          if (ok) mbar_arrive(bars.piece_empty(pi % kPieceRing));
+        }
+        // Every product issued above completes before TMEM can be released.
+        mma_commit(bars.mma_done());
+        mbar_drain(bars.mma_done(), 0, a.timeout_ns);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------ converters
+      const int cw = warp - 10;
+      int kt = 0, raws = 0;
+      bool ok = true;
+      Piece p;
+      for (int pi = 0; ok && next_piece(pi, p, false); ++pi) {
+        for (int t = p.begin; ok && t < p.end; ++t, ++kt) {
+          const int s = kt % NS;
+          const uint32_t ph = ((kt / NS) & 1) ^ 1;
+#pragma unroll 1
+          for (int v = 0; v < 2; ++v, ++raws) {
+            const int rs = raws % NR;
+            if (!(ok = mbar_wait_warp(bars.raw_full(rs), (raws / NR) & 1, wc))) break;
+            if (!(ok = mbar_wait_warp(v ? bars.v_empty(s) : bars.k_empty(s), ph, wc))) break;
+            // Hidden keys' scores are set aside by the softmax; their values must be finite.
+            convert_half<D, FMT>(smem_raw + C::OFF_RAW + rs * C::RAW, sbase + (v ? C::OFF_V : C::OFF_K) + s * C::TILE, cw,
+                                 lane, p.len - t * kTK);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bars.raw_empty(rs));
+              mbar_arrive(v ? bars.v_full(s) : bars.k_full(s));
+            }
+          }
+        }
+        if (ok && lane == 0) mbar_arrive(bars.piece_empty(pi % kPieceRing));
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    regs_increase<kRegsSoftmax>();
+    const int t = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // row of the operand tile = TMEM lane
+    const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + t * 128 + lane_bits, tO = tmem + 256 + t * 128 + lane_bits;
+    const CacheWs ws = cache_ws(a.ws, a.B, C::R, D, a.sm_count);
+    float2* stat = reinterpret_cast<float2*>(smem_raw + C::OFF_STAT);
+    float* stat_v = reinterpret_cast<float*>(smem_raw + C::OFF_STAT + 2 * 128 * 8);
+    int kt = 0;
+    uint32_t sc = 0, oc[2] = {0, 0}, jc = 0;
+    bool ok = true;
+    Piece p;
+    // Both softmax warpgroups meet (!PAIR).  A bounded wait: after a failed one elsewhere this gives up too.
+    auto join = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars.join());
+      return mbar_wait_warp(bars.join(), jc++ & 1, wc);
+    };
+    for (int pi = 0; ok && next_piece(pi, p, false); ++pi) {
+      const int n = t ? p.n1 : p.n0;
+      const int ri = (PAIR ? t * 128 : 0) + r;  // row of the item
+      const int row = p.rt * C::R + ri;
+      const bool there = row < rows;
+      const int rc = min(row, rows - 1), tok = rc / a.group, hq = p.head * a.group + rc - tok * a.group;
+      if (!PAIR || n > 0) {
+        // The previous piece's score products have completed: this chain's with its o_full, the other's
+        // with the join that ended its epilogue.
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + p.b * a.sq.b + hq * a.sq.h + tok * a.sq.n;
+        const uint32_t tile = sbase + C::OFF_Q + (PAIR ? t * C::TILE : 0);
+        const float back = PAIR ? stage_query_row<D, BF16>(src, there, tile, r, 0, D / 8)
+                                : stage_query_row<D, BF16>(src, there, tile, r, t * (D / 16), (t + 1) * (D / 16));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.q_full(t));
+        const float fac = a.scale * 1.4426950408889634f * back;
+        const int lim_row = cache_row_limit(a.mask, p.len, a.Nq, tok);
+        // the least of this warp's rows
+        const int lim_min = cache_row_limit(a.mask, p.len, a.Nq, min(row - lane, rows - 1) / a.group);
+        const bool idle = row - lane >= rows;  // a warp of rows that are not there
+        float m = -INFINITY, l = 0.f, vref = 0.f;
+        for (int j = 0; j < n; ++j) {
+          const int i = PAIR ? j : 2 * j + t, nt = kt + i;
+          if (!(ok = mbar_wait_warp(bars.s_full(t), sc++ & 1, wc))) break;
+          if (!(ok = mbar_wait_warp(bars.meta_full(nt % kMetaRing), (nt / kMetaRing) & 1, wc))) break;
+          tc_fence_after();
+          const int key0 = (p.begin + i) * kTK;
+          if (!idle) {
+            const float2* scales = meta + (nt % kMetaRing) * 8;
+            if (key0 + kTK > lim_min)
+              softmax_scaled<D, true>(tS, tO, scales, lim_row - key0, fac, j == 0, m, l, vref);
+            else
+              softmax_scaled<D, false>(tS, tO, scales, kTK, fac, j == 0, m, l, vref);
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.p_full(t));
+        }
+        if (ok && n > 0) ok = mbar_wait_warp(bars.o_full(t), oc[t]++ & 1, wc);
+
+        // ------------------------------------------------------------ epilogue
+        float w0 = 0.f, w1 = 0.f, lse2;  // factors of O_0 and O_1 (PAIR: of O_t)
+        bool use1 = false;
+        if constexpr (PAIR) {
+          w0 = l == 0.f ? 0.f : vref / l;
+          lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) - kShift + __log2f(l);
+        } else {
+          stat[t * 128 + r] = make_float2(m, l);
+          if (lane == 0) stat_v[t * 4 + quarter] = vref;
+          if (!(ok = ok && join())) break;
+          if (p.n1 > 0) ok = mbar_wait_warp(bars.o_full(1 - t), oc[1 - t]++ & 1, wc);
+          else if (t == 1) ok = mbar_wait_warp(bars.o_full(0), oc[0]++ & 1, wc);
+          if (!ok) break;
+          const float2 x = stat[r], y = stat[128 + r];
+          use1 = p.n1 > 0;
+          const float mx = fmaxf(x.x, y.x), ms = mx == -INFINITY ? 0.f : mx;
+          const float e0 = x.y == 0.f ? 0.f : ex2_approx(x.x - ms), e1 = y.y == 0.f ? 0.f : ex2_approx(y.x - ms);
+          const float sum = (x.y == 0.f ? 0.f : e0 * x.y) + (y.y == 0.f ? 0.f : e1 * y.y);
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          w0 = e0 * stat_v[quarter] * inv;
+          w1 = use1 ? e1 * stat_v[4 + quarter] * inv : 0.f;
+          lse2 = sum == 0.f ? -INFINITY : ms - kShift + __log2f(sum);
+        }
+        tc_fence_after();
+        if (ok && !idle) {
+          constexpr int COLS = PAIR ? D : D / 2;  // this thread's columns of its row
+          const int c0 = PAIR ? 0 : t * COLS;
+          uint16_t* dst = static_cast<uint16_t*>(a.o) + p.b * a.so.b + hq * a.so.h + tok * a.so.n + c0;
+          float4* part = reinterpret_cast<float4*>(ws.o + (static_cast<size_t>(max(p.slot, 0)) * C::R + ri) * D + c0);
+          const uint32_t at0 = PAIR ? tO : tmem + 256 + lane_bits;
+#pragma unroll
+          for (int c = 0; c < COLS / 32; ++c) {
+            uint32_t x[32];
+            tmem_ld32(at0 + c0 + c * 32, x);
+            if constexpr (PAIR) {
+              tmem_wait_ld();
+              reg_fence32(x);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * w0);
+            } else {
+              uint32_t y[32];
+              if (use1) tmem_ld32(at0 + 128 + c0 + c * 32, y);
+              tmem_wait_ld();
+              reg_fence32(x);
+              if (use1) {
+                reg_fence32(y);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  x[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), w1, __uint_as_float(x[e]) * w0));
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * w0);
+              }
+            }
+            if (there) {
+              if (p.slot < 0) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    w[k] = pack2<BF16>(__uint_as_float(x[e + 2 * k]), __uint_as_float(x[e + 2 * k + 1]));
+                  *reinterpret_cast<uint4*>(dst + c * 32 + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                  part[c * 8 + e / 4] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]),
+                                                    __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+              }
+            }
+          }
+          if (there && (PAIR || t == 0)) {
+            if (p.slot < 0)
+              a.lse[(static_cast<long long>(p.b) * a.c.heads * a.group + hq) * a.Nq + tok] = lse2 * 0.6931471805599453f;
+            else
+              ws.l[static_cast<size_t>(p.slot) * C::R + ri] = lse2;
+          }
+        }
+        tc_fence_before();
+        // O_t, the statistics and the query tile are free once both warpgroups are here.
+        if (!PAIR && !(ok = ok && join())) break;
+      }
+      kt += p.end - p.begin;
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(bars.piece_empty(pi % kPieceRing));
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, int FMT, bool BF16, bool PAIR>
+cudaError_t launch_t(const CacheAttnArgs& a, cudaStream_t stream) {
+  using C = Cfg<D, PAIR>;
+  auto kern = cache_tile_kernel<D, FMT, BF16, PAIR>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_dependent(kern, dim3(a.sm_count), dim3(kThreads), C::BYTES, stream, a)) != cudaSuccess) return e;
+  return launch_cache_merge<D, BF16, C::R, kTK, C::MIN_TILES>(a, stream);
+}
+
+template <int D, int FMT, bool BF16>
+cudaError_t launch_p(const CacheAttnArgs& a, cudaStream_t stream) {
+  return static_cast<long long>(a.group) * a.Nq > 128 ? launch_t<D, FMT, BF16, true>(a, stream)
+                                                     : launch_t<D, FMT, BF16, false>(a, stream);
+}
+
+template <int D>
+cudaError_t launch_d(const CacheAttnArgs& a, cudaStream_t stream) {
+  if (a.c.format == kE4M3) return a.bf16 ? launch_p<D, kE4M3, true>(a, stream) : launch_p<D, kE4M3, false>(a, stream);
+  return a.bf16 ? launch_p<D, kInt8, true>(a, stream) : launch_p<D, kInt8, false>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_tile(const CacheAttnArgs& a, cudaStream_t stream) {
+  return a.c.d == 128 ? launch_d<128>(a, stream) : launch_d<64>(a, stream);
+}
+
+}  // namespace exattn

@@ -200,6 +200,10 @@ cudaError_t launch_kl_bwd_fused(const KlArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_write(const CacheIoArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheIoArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_tile(const CacheAttnArgs& a, cudaStream_t stream);
+// Up to this many query rows a key/value head attn_fwd_cache streams the codes through the warp-level
+// products (cache_attn.cu), above it through the tensor-memory ones (cache_tile.cu).
+constexpr int kCacheStreamRows = 32;
 // Tokens per box of the tensor maps launch_cache_attn wants; query rows and keys of its tiles for so many
 // rows a key/value head; its workspace bytes.
 int cache_attn_box_tokens(int page, int d);
