@@ -5,7 +5,7 @@
 // vref on the probabilities.
 //
 // Bound.  4 d flops for each row and key: the tensor cores, which tcgen05 reaches with 128 x 128 tiles in
-// tensor memory.  Its operands are fp16 in shared memory, so two warps turn each 128-token tile of codes, copied
+// tensor memory.  Its operands are fp16 in shared memory, so six warps turn each 128-token tile of codes, copied
 // in by the copy engine, into the swizzled operand tiles; 256 query rows share that work.
 //
 // Two chains of (scores, softmax, product) alternate on the tensor cores, one softmax warpgroup each, in the
@@ -15,12 +15,12 @@
 //   else    an item has 128 rows, and chain t works on every second key tile; the two results are joined in
 //           the epilogue.  Both chains then have work at any number of rows.
 //
-// Warp roles (384 threads, registers re-split per warpgroup):
+// Warp roles (512 threads, registers re-split per warpgroup):
 //   warps 0-3, 4-7  softmax of chain 0 and 1 (thread = query row = TMEM lane); they also bring the query rows
 //                   into their operand tile and write the results
 //   warp  8         MMA issuer (one thread) and TMEM owner
 //   warp  9         producer: walks the block's pieces (cache_sched.cuh), looks pages up, copies codes
-//   warps 10-11     converters, 64 tokens of each tile apiece
+//   warps 10-12, 13-15  converters of the keys and of the values, about 43 tokens of each tile apiece
 // Tensor memory: S_t (P_t over its first 64 columns) at 128 t, O_t at 256 + 128 t.
 // Every role walks the same pieces and counts tiles on, so the barriers are never re-armed.
 #include <cuda_bf16.h>
@@ -34,9 +34,10 @@
 namespace exattn {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr uint32_t kRegsSoftmax = 208, kRegsControl = 88;
-static_assert(2 * kRegsSoftmax + kRegsControl == 3 * 168, "register split must match the launch");
+constexpr int kThreads = 512;
+// Registers: 128 a thread at launch; the softmax warpgroups hold a row of 128 scores.
+constexpr uint32_t kRegsSoftmax = 176, kRegsOther = 80;
+static_assert(2 * kRegsSoftmax + 2 * kRegsOther == 4 * 128, "register split must match the launch");
 constexpr int kTK = 128;
 constexpr uint32_t kChunk = 128 * 128;  // 128 rows x 128 bytes
 constexpr int kPieceRing = 3, kMetaRing = 8;
@@ -57,7 +58,7 @@ struct Cfg {
   static constexpr uint32_t OFF_K = OFF_Q + (PAIR ? 2 : 1) * TILE;
   static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
   static constexpr uint32_t OFF_RAW = OFF_V + NS * TILE;
-  static constexpr uint32_t OFF_META = OFF_RAW + NR * RAW;           // [kMetaRing][8] {ks, vs}
+  static constexpr uint32_t OFF_META = OFF_RAW + NR * RAW;           // [kMetaRing] ks[8], vs[8]
   static constexpr uint32_t OFF_STAT = OFF_META + kMetaRing * 64;    // !PAIR: {m, l} [2][128], vref [2][4]
   static constexpr uint32_t OFF_PIECE = OFF_STAT + (PAIR ? 0 : 2 * 128 * 8 + 32);
   static constexpr uint32_t OFF_BAR = OFF_PIECE + kPieceRing * 32;
@@ -66,6 +67,31 @@ struct Cfg {
   static constexpr uint32_t OFF_SCHED = OFF_MISC + 16;
   static constexpr uint32_t BYTES = OFF_SCHED + sizeof(typename Walk::Shared);
   static_assert(BYTES <= 232448, "shared memory of a block");
+};
+
+// 16 consecutive 32-bit columns of a warp's 32 lanes; the load waits for its values.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+template <int T>
+struct Chain {
+  static constexpr int value = T;
 };
 
 template <int NS, int NR>
@@ -91,106 +117,122 @@ struct Bars {
 };
 
 // One key tile of the online softmax for this thread's query row.  Scores of the 16-token group g count
-// fac * ks[g]; P goes out in fp16 times vs[g] / vref.  Columns at or past `lim` are hidden (MASKED).
+// fac * ks[g]; P goes out in fp16 times vs[g] / vref (sc: ks[8], vs[8]).  Columns at or past `lim` are hidden
+// (MASKED).  All 128 scores are read for the maximum; the upper 64 are read again for P, which saves the
+// registers that they would hold meanwhile.  P's packed columns overwrite scores of the lower 64 only.
 template <int D, bool MASKED>
-__device__ __forceinline__ void softmax_scaled(uint32_t tS, uint32_t tO, const float2* sc, int lim, float fac, bool first,
-                                               float& m, float& l, float& vref) {
+__device__ __forceinline__ void softmax_scaled(uint32_t tS, uint32_t tO, const float* sc, int lim, float fac, bool first,
+                                               float& m, float& l, float& vref, float& vinv) {
   uint32_t sr[4][32];
 #pragma unroll
   for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
+  float f[8], vs[8];
+#pragma unroll
+  for (int g = 0; g < 8; g += 4) {
+    const float4 k = *reinterpret_cast<const float4*>(sc + g), v = *reinterpret_cast<const float4*>(sc + 8 + g);
+    f[g] = fac * k.x;
+    f[g + 1] = fac * k.y;
+    f[g + 2] = fac * k.z;
+    f[g + 3] = fac * k.w;
+    vs[g] = v.x;
+    vs[g + 1] = v.y;
+    vs[g + 2] = v.z;
+    vs[g + 3] = v.w;
+  }
   tmem_wait_ld();
 #pragma unroll
   for (int c = 0; c < 4; ++c) reg_fence32(sr[c]);
-  if constexpr (MASKED) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (c * 32 + i >= lim) sr[c][i] = __float_as_uint(-INFINITY);
-  }
   float m_new = -INFINITY, v_new = -INFINITY;
 #pragma unroll
   for (int g = 0; g < 8; ++g) {
     float a = -INFINITY, b = -INFINITY;  // a NaN is passed over: it is met below
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
-      const uint32_t* s = &sr[g >> 1][(g & 1) * 16 + i];
-      a = max3(a, __uint_as_float(s[0]), __uint_as_float(s[1]));
-      b = max3(b, __uint_as_float(s[2]), __uint_as_float(s[3]));
-    }
-    const float2 x = sc[g];
-    m_new = fmaxf(m_new, fmaxf(a, b) * (fac * x.x));
-    v_new = fmaxf(v_new, x.y);
-  }
-  if (first) {
-    m = m_new;
-    vref = fmaxf(v_new, 0.f);
-  } else {
-    const bool need = m_new > m + 8.0f;
-    if (__any_sync(0xffffffffu, need || v_new > vref * kVrefLag)) {
-      // O is complete for the previous key tile of this chain: S was issued after its last product.
-      const float to = need ? m_new : m;
-      const float al = need ? ex2_approx(m - to) : 1.0f;
-      float ov = al;
-      if (v_new > vref) {
-        ov *= vref / v_new;
-        vref = v_new;
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = __uint_as_float(sr[g >> 1][(g & 1) * 16 + i + e]);
+        if constexpr (MASKED) v[e] = g * 16 + i + e >= lim ? -INFINITY : v[e];
       }
+      a = max3(a, v[0], v[1]);
+      b = max3(b, v[2], v[3]);
+    }
+    m_new = fmaxf(m_new, fmaxf(a, b) * f[g]);
+    v_new = fmaxf(v_new, vs[g]);
+  }
+  const bool need = first || m_new > m + 8.0f;
+  if (__any_sync(0xffffffffu, need || v_new > vref * kVrefLag)) {
+    const float to = need ? m_new : m;
+    const float al = need && !first ? ex2_approx(m - to) : 1.0f;
+    float ov = al;
+    if (first || v_new > vref) {
+      const float v = fmaxf(v_new, 0.f);
+      ov *= vref / v;
+      vref = v;
+      vinv = v > 0.f ? 1.0f / v : 0.f;
+    }
+    if (!first) {
+      // O is complete for the previous key tile of this chain: S was issued after its last product.
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t o[16];
+        tmem_ld16(tO + c * 16, o);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tO + c * 32, o);
-        tmem_wait_ld();
-        reg_fence32(o);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ov);
-        tmem_st32(tO + c * 32, o);
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ov);
+        tmem_st16(tO + c * 16, o);
       }
       tmem_wait_st();
-      l *= al;
-      m = to;
     }
+    l *= al;
+    m = to;
   }
   const float ms = m == -INFINITY ? 0.f : m - kShift;
-  const float vinv = vref > 0.f ? 1.0f / vref : 0.f;
   const uint64_t nm2 = f2_pack(-ms, -ms);
-  uint64_t acc[4];
+  uint64_t acc[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = f2_pack(0.f, 0.f);
+  for (int i = 0; i < 2; ++i) acc[i] = f2_pack(0.f, 0.f);
+  auto chunk = [&](int c, const uint32_t (&x)[32]) __attribute__((always_inline)) {
+    uint32_t pk[16];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t pk[32];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const float2 s = sc[4 * h + g];
-      const float f = fac * s.x, r = s.y * vinv;
-      const uint64_t f2 = f2_pack(f, f), r2 = f2_pack(r, r);
+    for (int h = 0; h < 2; ++h) {
+      const float r = vs[2 * c + h] * vinv;
+      const uint64_t f2 = f2_pack(f[2 * c + h], f[2 * c + h]), r2 = f2_pack(r, r);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int i = g * 8 + k, p = h * 32 + i;  // score pair (2 p, 2 p + 1)
-        const uint64_t x = f2_fma(f2_pack(__uint_as_float(sr[p >> 4][(2 * p) & 31]), __uint_as_float(sr[p >> 4][(2 * p + 1) & 31])),
-                                  f2, nm2);
-        float x0, x1;
-        f2_unpack(x, x0, x1);
-        float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+        const int i = h * 8 + k, col = c * 32 + 2 * i;  // scores col and col + 1
+        const uint64_t z = f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f2, nm2);
+        float z0, z1;
+        f2_unpack(z, z0, z1);
+        float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
         if constexpr (MASKED) {  // whatever the scale
-          p0 = 2 * p >= lim ? 0.f : p0;
-          p1 = 2 * p + 1 >= lim ? 0.f : p1;
+          p0 = col >= lim ? 0.f : p0;
+          p1 = col + 1 >= lim ? 0.f : p1;
         }
-        acc[i & 3] = f2_add(acc[i & 3], f2_pack(p0, p1));
+        acc[k & 1] = f2_add(acc[k & 1], f2_pack(p0, p1));
         float y0, y1;
         f2_unpack(f2_mul(f2_pack(p0, p1), r2), y0, y1);
         if constexpr (MASKED) {
-          y0 = 2 * p >= lim ? 0.f : y0;
-          y1 = 2 * p + 1 >= lim ? 0.f : y1;
+          y0 = col >= lim ? 0.f : y0;
+          y1 = col + 1 >= lim ? 0.f : y1;
         }
         pk[i] = pack2<false>(y0, y1);
       }
     }
-    tmem_st32(tS + h * 32, pk);
-  }
+    tmem_st16(tS + c * 16, pk);
+  };
+  chunk(0, sr[0]);
+  uint32_t x2[32], x3[32];
+  tmem_ld32(tS + 64, x2);
+  chunk(1, sr[1]);
+  tmem_wait_ld();
+  reg_fence32(x2);
+  tmem_ld32(tS + 96, x3);
+  chunk(2, x2);
+  tmem_wait_ld();
+  reg_fence32(x3);
+  chunk(3, x3);
   float s0, s1;
-  f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+  f2_unpack(f2_add(acc[0], acc[1]), s0, s1);
   l += s0 + s1;
 }
 
@@ -235,36 +277,48 @@ __device__ __forceinline__ float stage_query_row(const uint16_t* src, bool there
   return back;
 }
 
-// 64 of a tile's 128 tokens (half `cw`) from codes to the operand tile; tokens at or past `valid` become zero.
+// A third of a tile's 128 tokens from codes to the operand tile; tokens at or past `valid` become zero.
 // A warp takes 16-code units such that neither its reads nor its two writes meet a bank twice in 8 lanes.
 template <int D, int FMT>
-__device__ __forceinline__ void convert_half(const uint8_t* raw, uint32_t tile, int cw, int lane, int valid) {
-  constexpr int ROWS = D == 128 ? 4 : 8;  // token rows a step
-#pragma unroll 4
-  for (int it = 0; it < 64 / ROWS; ++it) {
-    int row, chunk;
-    const int q = lane & 3;
-    if constexpr (D == 128) {
-      const int p = (lane >> 2) & 1;
-      row = cw * 64 + it * ROWS + p + 2 * (lane >> 4);
-      chunk = p ^ ((lane >> 3) & 1);
-    } else {
-      row = cw * 64 + it * ROWS + (lane >> 2);
-      chunk = 0;
-    }
-    const uint4 c = *reinterpret_cast<const uint4*>(raw + row * D + chunk * 64 + q * 16);
-    uint32_t o[8];
-    codes_to_f16<FMT>(c.x, o[0], o[1]);
-    codes_to_f16<FMT>(c.y, o[2], o[3]);
-    codes_to_f16<FMT>(c.z, o[4], o[5]);
-    codes_to_f16<FMT>(c.w, o[6], o[7]);
-    if (row >= valid) {
+__device__ __forceinline__ void convert_third(const uint8_t* raw, uint32_t tile, int third, int lane, int valid) {
+  constexpr int ROWS = D == 128 ? 4 : 8;            // token rows a step
+  constexpr int STEPS = 128 / ROWS, MOST = (STEPS + 2) / 3;
+  const int s0 = third * MOST;
+  const int q = lane & 3;
+  int row0, chunk;
+  if constexpr (D == 128) {
+    const int p = (lane >> 2) & 1;
+    row0 = s0 * ROWS + p + 2 * (lane >> 4);
+    chunk = p ^ ((lane >> 3) & 1);
+  } else {
+    row0 = s0 * ROWS + (lane >> 2);
+    chunk = 0;
+  }
+  const uint8_t* src = raw + row0 * D + chunk * 64 + q * 16;
+  constexpr int BATCH = 6;  // steps whose codes are loaded together, so that their latencies overlap
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = 0u;
+  for (int base = 0; base < MOST; base += BATCH) {
+    uint4 c[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (base + i < MOST && s0 + base + i < STEPS) c[i] = *reinterpret_cast<const uint4*>(src + (base + i) * ROWS * D);
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (base + i >= MOST || s0 + base + i >= STEPS) break;
+      const int row = row0 + (base + i) * ROWS;
+      uint32_t o[8];
+      codes_to_f16<FMT>(c[i].x, o[0], o[1]);
+      codes_to_f16<FMT>(c[i].y, o[2], o[3]);
+      codes_to_f16<FMT>(c[i].z, o[4], o[5]);
+      codes_to_f16<FMT>(c[i].w, o[6], o[7]);
+      if (row >= valid) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = 0u;
+      }
+      const uint32_t dst = tile + chunk * kChunk;
+      st_shared_v4(dst + sw128_offset(row, 2 * q), o[0], o[1], o[2], o[3]);
+      st_shared_v4(dst + sw128_offset(row, 2 * q + 1), o[4], o[5], o[6], o[7]);
     }
-    const uint32_t dst = tile + chunk * kChunk;
-    st_shared_v4(dst + sw128_offset(row, 2 * q), o[0], o[1], o[2], o[3]);
-    st_shared_v4(dst + sw128_offset(row, 2 * q + 1), o[4], o[5], o[6], o[7]);
   }
 }
 
@@ -280,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_raw + C::OFF_MISC + 4);
   const WaitCtx wc{abort_flag, a.err_word, a.timeout_ns};
   int* pieces = reinterpret_cast<int*>(smem_raw + C::OFF_PIECE);  // [kPieceRing][8]
-  float2* meta = reinterpret_cast<float2*>(smem_raw + C::OFF_META);
+  float* meta = reinterpret_cast<float*>(smem_raw + C::OFF_META);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -292,19 +346,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       mbar_init(bars.o_full(t), 1);
     }
     for (int s = 0; s < NS; ++s) {
-      mbar_init(bars.k_full(s), 2);
+      mbar_init(bars.k_full(s), 3);
       mbar_init(bars.k_empty(s), 1);
-      mbar_init(bars.v_full(s), 2);
+      mbar_init(bars.v_full(s), 3);
       mbar_init(bars.v_empty(s), 1);
     }
     for (int s = 0; s < NR; ++s) {
       mbar_init(bars.raw_full(s), 1);
-      mbar_init(bars.raw_empty(s), 2);
+      mbar_init(bars.raw_empty(s), 3);
     }
     for (int s = 0; s < kMetaRing; ++s) mbar_init(bars.meta_full(s), 1);
     for (int s = 0; s < kPieceRing; ++s) {
       mbar_init(bars.piece_full(s), 1);
-      mbar_init(bars.piece_empty(s), 11);  // 8 softmax warps, 2 converters, the MMA issuer
+      mbar_init(bars.piece_empty(s), 15);  // 8 softmax warps, 6 converters, the MMA issuer
     }
     mbar_init(bars.join(), 8);
     mbar_init(bars.mma_done(), 1);
@@ -347,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
   };
 
   if (warp >= 8) {
-    regs_decrease<kRegsControl>();
+    regs_decrease<kRegsOther>();
     if (warp == 9) {
       // ------------------------------------------------------------ producer
       // Lane g < 8 looks after 16-token group g of a tile.  Page numbers, scales and copies of a tile hang on
@@ -388,7 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           ok = copy(a.c.k, r0);
           if (ok) {
             const int ms = issued % kMetaRing;
-            if (feeds) meta[ms * 8 + lane] = make_float2(r0.ks, r0.vs);
+            if (feeds) {
+              meta[ms * 16 + lane] = r0.ks;
+              meta[ms * 16 + 8 + lane] = r0.vs;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.meta_full(ms));
             ++issued;
@@ -453,15 +510,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         const uint32_t q_lo = sdesc_lo(sbase + C::OFF_Q, 16), k_lo = sdesc_lo(sbase + C::OFF_K, 16),
                        v_lo = sdesc_lo(sbase + C::OFF_V, kChunk);
         int kt = 0;  // key tiles of earlier pieces
-        uint32_t pc[2] = {0, 0}, qc[2] = {0, 0};
+        uint32_t p0 = 0, p1 = 0, q0 = 0, q1 = 0;  // waits of p_full and q_full
         bool ok = true;
         Piece p;
         for (int pi = 0; ok && next_piece(pi, p, true); ++pi) {
-          const int nt[2] = {p.n0, p.n1};
-          const bool both = p.n1 > 0;
-          auto tile_of = [&](int t, int j) { return kt + (PAIR ? j : 2 * j + t); };
-          auto issue_S = [&](int t, int j) -> bool {
-            const int n = tile_of(t, j), s = n % NS;
+          const int n0 = p.n0, n1 = p.n1;
+          const bool both = n1 > 0;
+          // T: the chain, an integral constant (its barriers and addresses are then constants too)
+          auto issue_S = [&](auto T, int j) __attribute__((always_inline)) -> bool {
+            constexpr int t = decltype(T)::value;
+            const int n = kt + (PAIR ? j : 2 * j + t), s = n % NS;
             if (!mbar_wait(bars.k_full(s), (n / NS) & 1, wc)) return false;
             tc_fence_after();
             const uint32_t d = tmem + t * 128, a_lo = q_lo + (PAIR ? t * kTileLo : 0), b_lo = k_lo + s * kTileLo;
@@ -475,33 +533,35 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
             if (!PAIR || t == 1 || !both) mma_commit(bars.k_empty(s));  // the slot's last reader
             return true;
           };
-          auto issue_PV = [&](int t, int j) -> bool {
-            const int n = tile_of(t, j), s = n % NS;
+          auto issue_PV = [&](auto T, int j, bool last) __attribute__((always_inline)) -> bool {
+            constexpr int t = decltype(T)::value;
+            const int n = kt + (PAIR ? j : 2 * j + t), s = n % NS;
             if (!mbar_wait(bars.v_full(s), (n / NS) & 1, wc)) return false;
-            if (!mbar_wait(bars.p_full(t), pc[t] & 1, wc)) return false;
-            ++pc[t];
+            if (!mbar_wait(bars.p_full(t), (t ? p1++ : p0++) & 1, wc)) return false;
             tc_fence_after();
             const uint32_t d = tmem + 256 + t * 128, pa = tmem + t * 128, b_lo = v_lo + s * kTileLo;
             mma_ts_lo_rt(d, pa, b_lo, idPV, j > 0 ? 1u : 0u);
 #pragma unroll
             for (int k = 1; k < kTK / 16; ++k) mma_ts_lo<true>(d, pa + k * 8, b_lo + k * (2048 >> 4), idPV);
             if (!PAIR || t == 1 || !both) mma_commit(bars.v_empty(s));
-            if (j == nt[t] - 1) mma_commit(bars.o_full(t));
+            if (last) mma_commit(bars.o_full(t));
             return true;
           };
+          constexpr Chain<0> c0{};
+          constexpr Chain<1> c1{};
           // the query tiles: each chain's own, or halves of one from both warpgroups
-          for (int t = 0; ok && t < 2; ++t)
-            if (!PAIR || nt[t] > 0) ok = mbar_wait(bars.q_full(t), qc[t]++ & 1, wc);
+          ok = mbar_wait(bars.q_full(0), q0++ & 1, wc);
+          if (ok && (!PAIR || both)) ok = mbar_wait(bars.q_full(1), q1++ & 1, wc);
           if (!ok) break;
           tc_fence_after();
-          ok = issue_S(0, 0);
-          if (ok && both) ok = issue_S(1, 0);
-          for (int j = 0; ok && j < p.n0; ++j) {
-            if (!(ok = issue_PV(0, j))) break;
-            if (j + 1 < p.n0 && !(ok = issue_S(0, j + 1))) break;
-            if (j < p.n1) {
-              if (!(ok = issue_PV(1, j))) break;
-              if (j + 1 < p.n1 && !(ok = issue_S(1, j + 1))) break;
+          ok = issue_S(c0, 0);
+          if (ok && both) ok = issue_S(c1, 0);
+          for (int j = 0; ok && j < n0; ++j) {
+            if (!(ok = issue_PV(c0, j, j + 1 == n0))) break;
+            if (j + 1 < n0 && !(ok = issue_S(c0, j + 1))) break;
+            if (j < n1) {
+              if (!(ok = issue_PV(c1, j, j + 1 == n1))) break;
+              if (j + 1 < n1 && !(ok = issue_S(c1, j + 1))) break;
             }
           }
           kt += p.end - p.begin;
@@ -514,28 +574,23 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       __syncwarp();
     } else {
       // ------------------------------------------------------------ converters
-      const int cw = warp - 10;
-      int kt = 0, raws = 0;
+      const int v = warp >= 13, third = warp - (v ? 13 : 10);
+      int kt = 0;
       bool ok = true;
       Piece p;
       for (int pi = 0; ok && next_piece(pi, p, false); ++pi) {
-        for (int t = p.begin; ok && t < p.end; ++t, ++kt) {
-          const int s = kt % NS;
-          const uint32_t ph = ((kt / NS) & 1) ^ 1;
-#pragma unroll 1
-          for (int v = 0; v < 2; ++v, ++raws) {
-            const int rs = raws % NR;
-            if (!(ok = mbar_wait_warp(bars.raw_full(rs), (raws / NR) & 1, wc))) break;
-            if (!(ok = mbar_wait_warp(v ? bars.v_empty(s) : bars.k_empty(s), ph, wc))) break;
-            // Hidden keys' scores are set aside by the softmax; their values must be finite.
-            convert_half<D, FMT>(smem_raw + C::OFF_RAW + rs * C::RAW, sbase + (v ? C::OFF_V : C::OFF_K) + s * C::TILE, cw,
-                                 lane, p.len - t * kTK);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(bars.raw_empty(rs));
-              mbar_arrive(v ? bars.v_full(s) : bars.k_full(s));
-            }
+        for (int t = p.begin; t < p.end; ++t, ++kt) {
+          const int s = kt % NS, raws = 2 * kt + v, rs = raws % NR;
+          if (!(ok = mbar_wait_warp(bars.raw_full(rs), (raws / NR) & 1, wc))) break;
+          if (!(ok = mbar_wait_warp(v ? bars.v_empty(s) : bars.k_empty(s), ((kt / NS) & 1) ^ 1, wc))) break;
+          // Hidden keys' scores are set aside by the softmax; their values must be finite.
+          convert_third<D, FMT>(smem_raw + C::OFF_RAW + rs * C::RAW, sbase + (v ? C::OFF_V : C::OFF_K) + s * C::TILE, third,
+                                lane, p.len - t * kTK);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bars.raw_empty(rs));
+            mbar_arrive(v ? bars.v_full(s) : bars.k_full(s));
           }
         }
         if (ok && lane == 0) mbar_arrive(bars.piece_empty(pi % kPieceRing));
@@ -552,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     float2* stat = reinterpret_cast<float2*>(smem_raw + C::OFF_STAT);
     float* stat_v = reinterpret_cast<float*>(smem_raw + C::OFF_STAT + 2 * 128 * 8);
     int kt = 0;
-    uint32_t sc = 0, oc[2] = {0, 0}, jc = 0;
+    uint32_t sc = 0, oc_own = 0, oc_other = 0, jc = 0;  // waits of s_full, of both o_full, of the join
     bool ok = true;
     Piece p;
     // Both softmax warpgroups meet (!PAIR).  A bounded wait: after a failed one elsewhere this gives up too.
@@ -582,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         // the least of this warp's rows
         const int lim_min = cache_row_limit(a.mask, p.len, a.Nq, min(row - lane, rows - 1) / a.group);
         const bool idle = row - lane >= rows;  // a warp of rows that are not there
-        float m = -INFINITY, l = 0.f, vref = 0.f;
+        float m = -INFINITY, l = 0.f, vref = 0.f, vinv = 0.f;
         for (int j = 0; j < n; ++j) {
           const int i = PAIR ? j : 2 * j + t, nt = kt + i;
           if (!(ok = mbar_wait_warp(bars.s_full(t), sc++ & 1, wc))) break;
@@ -590,18 +645,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           tc_fence_after();
           const int key0 = (p.begin + i) * kTK;
           if (!idle) {
-            const float2* scales = meta + (nt % kMetaRing) * 8;
+            const float* scales = meta + (nt % kMetaRing) * 16;
             if (key0 + kTK > lim_min)
-              softmax_scaled<D, true>(tS, tO, scales, lim_row - key0, fac, j == 0, m, l, vref);
+              softmax_scaled<D, true>(tS, tO, scales, lim_row - key0, fac, j == 0, m, l, vref, vinv);
             else
-              softmax_scaled<D, false>(tS, tO, scales, kTK, fac, j == 0, m, l, vref);
+              softmax_scaled<D, false>(tS, tO, scales, kTK, fac, j == 0, m, l, vref, vinv);
             tmem_wait_st();
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bars.p_full(t));
         }
-        if (ok && n > 0) ok = mbar_wait_warp(bars.o_full(t), oc[t]++ & 1, wc);
+        if (ok && n > 0) ok = mbar_wait_warp(bars.o_full(t), oc_own++ & 1, wc);
 
         // ------------------------------------------------------------ epilogue
         float w0 = 0.f, w1 = 0.f, lse2;  // factors of O_0 and O_1 (PAIR: of O_t)
@@ -613,8 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           stat[t * 128 + r] = make_float2(m, l);
           if (lane == 0) stat_v[t * 4 + quarter] = vref;
           if (!(ok = ok && join())) break;
-          if (p.n1 > 0) ok = mbar_wait_warp(bars.o_full(1 - t), oc[1 - t]++ & 1, wc);
-          else if (t == 1) ok = mbar_wait_warp(bars.o_full(0), oc[0]++ & 1, wc);
+          if (t == 1 || p.n1 > 0) ok = mbar_wait_warp(bars.o_full(1 - t), oc_other++ & 1, wc);
           if (!ok) break;
           const float2 x = stat[r], y = stat[128 + r];
           use1 = p.n1 > 0;
