@@ -89,10 +89,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
-template <int T>
-struct Chain {
-  static constexpr int value = T;
-};
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0u;
+}
 
 template <int NS, int NR>
 struct Bars {
@@ -382,9 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     int nrows, n0, n1;  // rows of the item; key tiles of each chain
   };
   // The i-th piece; false at the end, or after a failed wait.
-  auto next_piece = [&](int i, Piece& p, bool one_thread) -> bool {
+  auto next_piece = [&](int i, Piece& p) -> bool {
     const uint32_t bar = bars.piece_full(i % kPieceRing), ph = (i / kPieceRing) & 1;
-    if (!(one_thread ? mbar_wait(bar, ph, wc) : mbar_wait_warp(bar, ph, wc))) return false;
+    if (!mbar_wait_warp(bar, ph, wc)) return false;
     const int* d = pieces + (i % kPieceRing) * 8;
     p.b = d[0];
     p.head = d[1];
@@ -503,71 +504,79 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         for (int n = max(0, raws - NR); n < raws; ++n) mbar_drain(bars.raw_full(n % NR), (n / NR) & 1, a.timeout_ns);
     } else if (warp == 8) {
       // ------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t idS = idesc_f16(128, 128, false, false, false);
-        constexpr uint32_t idPV = idesc_f16(128, D, false, false, true);
-        constexpr uint32_t kTileLo = C::TILE >> 4;
-        const uint32_t q_lo = sdesc_lo(sbase + C::OFF_Q, 16), k_lo = sdesc_lo(sbase + C::OFF_K, 16),
-                       v_lo = sdesc_lo(sbase + C::OFF_V, kChunk);
-        int kt = 0;  // key tiles of earlier pieces
-        uint32_t p0 = 0, p1 = 0, q0 = 0, q1 = 0;  // waits of p_full and q_full
-        bool ok = true;
-        Piece p;
-        for (int pi = 0; ok && next_piece(pi, p, true); ++pi) {
-          const int n0 = p.n0, n1 = p.n1;
-          const bool both = n1 > 0;
-          // T: the chain, an integral constant (its barriers and addresses are then constants too)
-          auto issue_S = [&](auto T, int j) __attribute__((always_inline)) -> bool {
-            constexpr int t = decltype(T)::value;
-            const int n = kt + (PAIR ? j : 2 * j + t), s = n % NS;
-            if (!mbar_wait(bars.k_full(s), (n / NS) & 1, wc)) return false;
+      // The warp stays together and one elected lane issues: what the issue takes is then the same for all
+      // lanes as the compiler sees it (hence the shuffles), and needs no moves to uniform registers for each
+      // product.  The chains share their code: what this warp runs between its turns has to come back into an
+      // instruction cache that the softmax fills.
+      constexpr uint32_t idS = idesc_f16(128, 128, false, false, false);
+      constexpr uint32_t idPV = idesc_f16(128, D, false, false, true);
+      constexpr uint32_t kTileLo = C::TILE >> 4;
+      const uint32_t ubase = __shfl_sync(0xffffffffu, sbase, 0), utmem = __shfl_sync(0xffffffffu, tmem, 0);
+      const Bars<NS, NR> ub{ubase + C::OFF_BAR};
+      const uint32_t q_lo = sdesc_lo(ubase + C::OFF_Q, 16), k_lo = sdesc_lo(ubase + C::OFF_K, 16),
+                     v_lo = sdesc_lo(ubase + C::OFF_V, kChunk);
+      int ks = 0, vs = 0;            // next slots of K and V ...
+      uint32_t kph = 0, vph = 0;     // ... and the parities of their waits
+      uint32_t phase_p = 0;          // bit t: parity of the next wait of p_full(t)
+      uint32_t q0 = 0, q1 = 0;
+      bool ok = true;
+      Piece p;
+      for (int pi = 0; ok && next_piece(pi, p); ++pi) {
+        const int n0 = __shfl_sync(0xffffffffu, p.n0, 0), n1 = __shfl_sync(0xffffffffu, p.n1, 0);
+        const bool both = n1 > 0;
+        // the query tiles: each chain's own, or halves of one from both warpgroups
+        ok = mbar_wait_warp(ub.q_full(0), q0++ & 1, wc);
+        if (ok && (!PAIR || both)) ok = mbar_wait_warp(ub.q_full(1), q1++ & 1, wc);
+        // step i: chain t = i & 1 (or 0 alone), O_t += P_t V of its key tile j - 1, then S_t of its key tile j
+        const int last = both ? 2 * n0 + 1 : 2 * n0;
+#pragma unroll 1
+        for (int i = 0; ok && i <= last; i += both ? 1 : 2) {
+          const int t = i & 1, j = i >> 1, nt = t ? n1 : n0;
+          const bool slot_ends = !PAIR || t == 1 || !both;  // this chain is its slots' last reader
+          if (j > 0 && j <= nt) {
+            if (!(ok = mbar_wait_warp(ub.v_full(vs), vph, wc))) break;
+            if (!(ok = mbar_wait_warp(ub.p_full(t), (phase_p >> t) & 1, wc))) break;
+            phase_p ^= 1u << t;
             tc_fence_after();
-            const uint32_t d = tmem + t * 128, a_lo = q_lo + (PAIR ? t * kTileLo : 0), b_lo = k_lo + s * kTileLo;
-            mma_ss_lo<false>(d, a_lo, b_lo, idS);
+            const uint32_t d = utmem + 256 + t * 128, pa = utmem + t * 128, b_lo = v_lo + vs * kTileLo;
+            if (elect_one()) {
+              mma_ts_lo_rt(d, pa, b_lo, idPV, j - 1);
 #pragma unroll
-            for (int k = 1; k < D / 16; ++k) {
-              const uint32_t off = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
-              mma_ss_lo<true>(d, a_lo + off, b_lo + off, idS);
+              for (int k = 1; k < kTK / 16; ++k) mma_ts_lo<true>(d, pa + k * 8, b_lo + k * (2048 >> 4), idPV);
+              if (slot_ends) mma_commit(ub.v_empty(vs));
+              if (j == nt) mma_commit(ub.o_full(t));
             }
-            mma_commit(bars.s_full(t));
-            if (!PAIR || t == 1 || !both) mma_commit(bars.k_empty(s));  // the slot's last reader
-            return true;
-          };
-          auto issue_PV = [&](auto T, int j, bool last) __attribute__((always_inline)) -> bool {
-            constexpr int t = decltype(T)::value;
-            const int n = kt + (PAIR ? j : 2 * j + t), s = n % NS;
-            if (!mbar_wait(bars.v_full(s), (n / NS) & 1, wc)) return false;
-            if (!mbar_wait(bars.p_full(t), (t ? p1++ : p0++) & 1, wc)) return false;
-            tc_fence_after();
-            const uint32_t d = tmem + 256 + t * 128, pa = tmem + t * 128, b_lo = v_lo + s * kTileLo;
-            mma_ts_lo_rt(d, pa, b_lo, idPV, j > 0 ? 1u : 0u);
-#pragma unroll
-            for (int k = 1; k < kTK / 16; ++k) mma_ts_lo<true>(d, pa + k * 8, b_lo + k * (2048 >> 4), idPV);
-            if (!PAIR || t == 1 || !both) mma_commit(bars.v_empty(s));
-            if (last) mma_commit(bars.o_full(t));
-            return true;
-          };
-          constexpr Chain<0> c0{};
-          constexpr Chain<1> c1{};
-          // the query tiles: each chain's own, or halves of one from both warpgroups
-          ok = mbar_wait(bars.q_full(0), q0++ & 1, wc);
-          if (ok && (!PAIR || both)) ok = mbar_wait(bars.q_full(1), q1++ & 1, wc);
-          if (!ok) break;
-          tc_fence_after();
-          ok = issue_S(c0, 0);
-          if (ok && both) ok = issue_S(c1, 0);
-          for (int j = 0; ok && j < n0; ++j) {
-            if (!(ok = issue_PV(c0, j, j + 1 == n0))) break;
-            if (j + 1 < n0 && !(ok = issue_S(c0, j + 1))) break;
-            if (j < n1) {
-              if (!(ok = issue_PV(c1, j, j + 1 == n1))) break;
-              if (j + 1 < n1 && !(ok = issue_S(c1, j + 1))) break;
+            if (slot_ends && ++vs == NS) {
+              vs = 0;
+              vph ^= 1;
             }
           }
-          kt += p.end - p.begin;
-          if (ok) mbar_arrive(bars.piece_empty(pi % kPieceRing));
+          if (j < nt) {
+            if (!(ok = mbar_wait_warp(ub.k_full(ks), kph, wc))) break;
+            tc_fence_after();
+            const uint32_t d = utmem + t * 128, a_lo = q_lo + (PAIR ? t * kTileLo : 0), b_lo = k_lo + ks * kTileLo;
+            if (elect_one()) {
+              mma_ss_lo<false>(d, a_lo, b_lo, idS);
+#pragma unroll
+              for (int k = 1; k < D / 16; ++k) {
+                const uint32_t off = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
+                mma_ss_lo<true>(d, a_lo + off, b_lo + off, idS);
+              }
+              mma_commit(ub.s_full(t));
+              if (slot_ends) mma_commit(ub.k_empty(ks));
+            }
+            if (slot_ends && ++ks == NS) {
+              ks = 0;
+              kph ^= 1;
+            }
+          }
         }
-        // Every product issued above completes before TMEM can be released.
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bars.piece_empty(pi % kPieceRing));
+      }
+      // Every product issued above completes before TMEM can be released.
+      __syncwarp();
+      if (elect_one()) {
         mma_commit(bars.mma_done());
         mbar_drain(bars.mma_done(), 0, a.timeout_ns);
       }
@@ -578,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       int kt = 0;
       bool ok = true;
       Piece p;
-      for (int pi = 0; ok && next_piece(pi, p, false); ++pi) {
+      for (int pi = 0; ok && next_piece(pi, p); ++pi) {
         for (int t = p.begin; t < p.end; ++t, ++kt) {
           const int s = kt % NS, raws = 2 * kt + v, rs = raws % NR;
           if (!(ok = mbar_wait_warp(bars.raw_full(rs), (raws / NR) & 1, wc))) break;
@@ -616,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       if (lane == 0) mbar_arrive(bars.join());
       return mbar_wait_warp(bars.join(), jc++ & 1, wc);
     };
-    for (int pi = 0; ok && next_piece(pi, p, false); ++pi) {
+    for (int pi = 0; ok && next_piece(pi, p); ++pi) {
       const int n = t ? p.n1 : p.n0;
       const int ri = (PAIR ? t * 128 : 0) + r;  // row of the item
       const int row = p.rt * C::R + ri;
