@@ -631,7 +631,8 @@ template <int D, int FMT, bool BF16, int NT>
 cudaError_t launch_t(const CacheAttnArgs& a, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   auto kern = cache_attn_kernel<D, FMT, BF16, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kern, C::BYTES, done);
   if (e != cudaSuccess) return e;
   if ((e = launch_dependent(kern, dim3(a.sm_count), dim3(C::THREADS), C::BYTES, stream, a)) != cudaSuccess) return e;
   return launch_cache_merge<D, BF16, C::R, C::TK, C::W>(a, stream);

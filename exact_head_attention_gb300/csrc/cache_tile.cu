@@ -768,7 +768,8 @@ template <int D, int FMT, bool BF16, bool PAIR>
 cudaError_t launch_t(const CacheAttnArgs& a, cudaStream_t stream) {
   using C = Cfg<D, PAIR>;
   auto kern = cache_tile_kernel<D, FMT, BF16, PAIR>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kern, C::BYTES, done);
   if (e != cudaSuccess) return e;
   if ((e = launch_dependent(kern, dim3(a.sm_count), dim3(kThreads), C::BYTES, stream, a)) != cudaSuccess) return e;
   return launch_cache_merge<D, BF16, C::R, kTK, C::MIN_TILES>(a, stream);

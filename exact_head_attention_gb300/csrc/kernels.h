@@ -2,6 +2,7 @@
 // translation units.  Not part of the public header.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -164,6 +165,19 @@ struct CacheAttnArgs {
 // deterministic mode (dq_acc == nullptr) runs pre, main (dK and dV only), then the dQ kernel.
 constexpr int kBwdPre = 1, kBwdMain = 2, kBwdConvert = 4, kBwdAll = 7, kBwdDq = 8;
 constexpr int kBwdDeterministic = kBwdPre | kBwdMain | kBwdDq;
+
+// Allows `kernel` its dynamic shared memory, once on each device (`done`: a bit for each of the first 64).
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Launches a kernel with programmatic stream serialisation: it may start before the kernel ahead of it
 // on the stream has finished, and waits for that itself (griddep_wait).

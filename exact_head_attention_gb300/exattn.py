@@ -59,6 +59,8 @@ def last_error() -> str:
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the library (raises OSError if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -510,7 +512,7 @@ class QuantCache:
     k, v: [num_pages, heads, page, d] float8_e4m3fn or int8 codes; k_scale, v_scale: [num_pages, heads] fp32; a
     code stands for code * scale of its page and head.  page_table: [B, width] int32, the pages of each sequence
     in order.  All contiguous, on one CUDA device; the tensors are used in place."""
-    __slots__ = ("k", "v", "k_scale", "v_scale", "page_table", "device", "struct", "_ref")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "page_table", "device", "index", "B", "heads", "d", "struct", "_ref")
 
     def __init__(self, k, v, k_scale, v_scale, page_table):
         fmt = _CACHE_DTYPES.get(k.dtype)
@@ -518,18 +520,20 @@ class QuantCache:
             raise TypeError(f"unsupported cache dtypes {k.dtype}, {v.dtype}; expected float8_e4m3fn or int8 for both")
         if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or page_table.dtype != torch.int32:
             raise TypeError("scales must be float32 and the page table int32")
-        if k.dim() != 4 or v.shape != k.shape or page_table.dim() != 2:
+        shape, rows = k.shape, page_table.shape
+        if len(shape) != 4 or v.shape != shape or len(rows) != 2:
             raise ValueError("k, v must be [num_pages, heads, page, d] and the page table [B, width]")
-        pages, heads, page, d = k.shape
+        pages, heads, page, d = shape
         if k_scale.shape != (pages, heads) or v_scale.shape != (pages, heads):
             raise ValueError("scales must be [num_pages, heads]")
-        device = k.device
+        index = k.get_device()
         for t in (k, v, k_scale, v_scale, page_table):
-            if not t.is_cuda or t.device != device or not t.is_contiguous():
+            if not t.is_cuda or t.get_device() != index or not t.is_contiguous():
                 raise ValueError("cache tensors must be contiguous and on one CUDA device")
-        self.k, self.v, self.k_scale, self.v_scale, self.page_table, self.device = k, v, k_scale, v_scale, page_table, device
+        self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
+        self.device, self.index, self.B, self.heads, self.d = k.device, index, rows[0], heads, d
         self.struct = CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                  page_table.data_ptr(), pages, heads, page, d, page_table.shape[1], fmt)
+                                  page_table.data_ptr(), pages, heads, page, d, rows[1], fmt)
         self._ref = ctypes.byref(self.struct)
 
     @classmethod
@@ -544,43 +548,50 @@ class QuantCache:
         return cls(k, v, ks, vs, page_table)
 
 
-def _int32(t, B: int, device, name: str):
+def _int32(t, cache: QuantCache, name: str):
+    """Address of an int32 tensor of one entry a sequence, or None."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.shape != (B,) or t.device != device or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != (cache.B,) or t.get_device() != cache.index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of one entry a sequence on the cache's device")
     return t.data_ptr()
 
 
-def _cache_views(cache: QuantCache, *ts):
-    """Checks 16-bit [B, heads or H, N, d] views against the cache; the views' batch size."""
-    B = cache.page_table.shape[0]
-    for t in ts:
-        if t.dim() != 4 or t.shape[0] != B or t.shape[3] != cache.struct.d:
-            raise ValueError("tensors must be [B, H, N, d] with the page table's B and the cache's d")
-        if t.device != cache.device or t.dtype != ts[0].dtype:
-            raise ValueError("tensors must be of one dtype, on the cache's device")
-    return B
+_STRIDES: dict = {}  # Strides objects by their values (building one costs more than the rest of a view's marshalling)
 
 
-class _On:
-    """The device of `cache` current, and `stream` where one is given: what is allocated inside belongs to it."""
-    __slots__ = ("guards",)
+def _cache_view(t, cache: QuantCache, dtype):
+    """(pointer, Strides) of a 16-bit [B, H, N, d] view that goes with the cache."""
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != cache.B or shape[3] != cache.d:
+        raise ValueError("tensors must be [B, H, N, d] with the page table's B and the cache's d")
+    if t.get_device() != cache.index or t.dtype != dtype:
+        raise ValueError("tensors must be of one dtype, on the cache's device")
+    sb, sh, sn, sd = t.stride()
+    if sd != 1:
+        raise ValueError("tensors must have a contiguous last dimension")
+    st = _STRIDES.get((sb, sh, sn))
+    if st is None:
+        if len(_STRIDES) >= 4096:
+            _STRIDES.clear()
+        st = _STRIDES[(sb, sh, sn)] = Strides(sb, sh, sn)
+    return t.data_ptr(), st
 
-    def __init__(self, cache, stream):
-        self.guards = []
-        if cache.device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(cache.device))
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(stream))
 
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
+def _on(cache: QuantCache, stream, call):
+    """Runs `call` with the cache's device current and, where given, on `stream`: what it allocates belongs to it."""
+    with torch.cuda.device(cache.device):
+        if stream is None:
+            return call(_stream(None))
+        with torch.cuda.stream(stream):
+            return call(_stream(stream))
 
-    def __exit__(self, *e):
-        for g in reversed(self.guards):
-            g.__exit__(*e)
+
+def _run(cache: QuantCache, stream, call):
+    index = torch.cuda.current_device()
+    if stream is None and index == cache.index and _RAW_STREAM is not None:
+        return call(_RAW_STREAM(index))
+    return _on(cache, stream, call)
 
 
 def cache_write(cache: QuantCache, k, v, start=None, count=None, stream=None) -> None:
@@ -589,16 +600,18 @@ def cache_write(cache: QuantCache, k, v, start=None, count=None, stream=None) ->
     k, v: [B, heads, N, d] bf16 or fp16, last dimension contiguous.  Row n of sequence b becomes its token
     start[b] + n for n < count[b]; start None: 0, count None: N (int32 CUDA tensors otherwise).  Tokens that a
     reached page already holds keep their codes, or are rounded again where its scale has to grow."""
-    B = _cache_views(cache, k, v)
-    if k.shape != v.shape or k.shape[1] != cache.struct.heads:
+    shape = k.shape
+    if v.shape != shape or len(shape) != 4 or shape[1] != cache.heads:
         raise ValueError("k and v must be [B, heads, N, d] with the cache's heads")
-    if k.shape[2] == 0 or B == 0:
+    kp, ks = _cache_view(k, cache, k.dtype)
+    vp, vs = _cache_view(v, cache, k.dtype)
+    args = (cache._ref, kp, ks, vp, vs, _int32(start, cache, "start"), _int32(count, cache, "count"), shape[0], shape[2],
+            _dtype_code(k))
+    if shape[0] == 0 or shape[2] == 0:
         return
-    with _On(cache, stream):
-        st = load().attn_cache_write(cache._ref, *_view(k), *_view(v), _int32(start, B, cache.device, "start"),
-                                     _int32(count, B, cache.device, "count"), B, k.shape[2], _dtype_code(k),
-                                     _stream(stream))
-    _check(st, "attn_cache_write")
+    st = _run(cache, stream, lambda handle: load().attn_cache_write(*args, handle))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache_write")
 
 
 def cache_read(cache: QuantCache, lens, rows: int | None = None, start=None, dtype=torch.bfloat16, out=None, stream=None):
@@ -606,36 +619,42 @@ def cache_read(cache: QuantCache, lens, rows: int | None = None, start=None, dty
 
     Rows at or past lens[b] are left as they were in `out`, a pair of views whose dtype and rows are then taken;
     without it the result is allocated with zeros in them."""
-    B, heads, d = cache.page_table.shape[0], cache.struct.heads, cache.struct.d
-    with _On(cache, stream):
-        if out is None:
-            if rows is None:
-                raise ValueError("rows or out is needed")
-            out = tuple(torch.zeros((B, heads, rows, d), dtype=dtype, device=cache.device) for _ in range(2))
-        k, v = out
-        _cache_views(cache, k, v)
-        if k.shape != v.shape or k.shape[1] != heads:
+    if out is None and rows is None:
+        raise ValueError("rows or out is needed")
+    lens_at, start_at = _int32(lens, cache, "lens"), _int32(start, cache, "start")
+
+    def call(handle):
+        k, v = out if out is not None else (
+            torch.zeros((cache.B, cache.heads, rows, cache.d), dtype=dtype, device=cache.device) for _ in range(2))
+        shape = k.shape
+        if v.shape != shape or len(shape) != 4 or shape[1] != cache.heads:
             raise ValueError("outputs must be [B, heads, N, d] with the cache's heads")
-        if k.shape[2] == 0 or B == 0:
-            return k, v
-        st = load().attn_cache_read(cache._ref, _int32(start, B, cache.device, "start"),
-                                    _int32(lens, B, cache.device, "lens"), *_view(k), *_view(v), B, k.shape[2],
-                                    _dtype_code(k), _stream(stream))
-    _check(st, "attn_cache_read")
-    return k, v
+        kp, ks = _cache_view(k, cache, k.dtype)
+        vp, vs = _cache_view(v, cache, k.dtype)
+        code = _dtype_code(k)
+        if shape[0] and shape[2]:
+            st = load().attn_cache_read(cache._ref, start_at, lens_at, kp, ks, vp, vs, shape[0], shape[2], code, handle)
+            if st != ATTN_OK:
+                raise AttnError(st, "attn_cache_read")
+        return k, v
+
+    return _run(cache, stream, call)
 
 
 def cache_workspace_size(cache: QuantCache, H: int, Nq: int) -> int:
     """Workspace bytes of forward_cache (attn_fwd_cache_workspace_size)."""
-    return int(load().attn_fwd_cache_workspace_size(cache._ref, cache.page_table.shape[0], H, Nq))
+    return int(load().attn_fwd_cache_workspace_size(cache._ref, cache.B, H, Nq))
 
 
 def fwd_cache_raw(q, cache: QuantCache, lens, o, lse, causal, scale: float, workspace, stream=None) -> int:
     """Calls attn_fwd_cache on caller-provided tensors; returns the status code."""
     B, H, Nq, _ = q.shape
-    return load().attn_fwd_cache(*_view(q), cache._ref, _int32(lens, B, cache.device, "lens"), *_view(o), _ptr(lse),
-                                 B, H, Nq, mask_code(causal), float(scale), _dtype_code(q), *_workspace(workspace),
-                                 _stream(stream))
+    qp, qs = _cache_view(q, cache, q.dtype)
+    op, os_ = _cache_view(o, cache, q.dtype)
+    if o.shape != q.shape or lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or lse.get_device() != cache.index:
+        raise ValueError("o must be shaped as q, lse float32 [B, H, Nq], on the cache's device")
+    return load().attn_fwd_cache(qp, qs, cache._ref, _int32(lens, cache, "lens"), op, os_, _ptr(lse), B, H, Nq,
+                                 mask_code(causal), scale, _dtype_code(q), *_workspace(workspace), _stream(stream))
 
 
 def forward_cache(q, cache: QuantCache, lens, causal="bottom_right", scale: float | None = None, workspace=None,
@@ -646,16 +665,26 @@ def forward_cache(q, cache: QuantCache, lens, causal="bottom_right", scale: floa
     h // (H // heads)).  causal "bottom_right" (the default): the queries are a sequence's last Nq tokens; also
     False and True (top-left) as in forward().  lens: int32 CUDA tensor [B].  `workspace` (uint8 CUDA tensor of
     cache_workspace_size bytes, one for each call that may run at the same time) is allocated if omitted."""
-    B = _cache_views(cache, q)
-    H, Nq = q.shape[1], q.shape[2]
-    scale = (1.0 / cache.struct.d ** 0.5) if scale is None else scale
-    with _On(cache, stream):
+    qp, qs = _cache_view(q, cache, q.dtype)
+    B, H, Nq, d = q.shape
+    code, mask, lens_at = _dtype_code(q), mask_code(causal), _int32(lens, cache, "lens")
+    scale = (1.0 / d ** 0.5) if scale is None else scale
+
+    def call(handle):
         o = torch.empty_like(q)
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=cache.device)
-        if q.numel() == 0:
-            return o, lse
-        if workspace is None:
-            workspace = torch.empty(cache_workspace_size(cache, H, Nq), dtype=torch.uint8, device=cache.device)
-        st = fwd_cache_raw(q, cache, lens, o, lse, causal, scale, workspace, stream)
-    _check(st, "attn_fwd_cache")
-    return o, lse
+        if B and H and Nq:
+            lib = load()
+            if workspace is None:
+                size = lib.attn_fwd_cache_workspace_size(cache._ref, B, H, Nq)
+                space = torch.empty(size, dtype=torch.uint8, device=cache.device)
+            else:
+                size, space = workspace.numel() * workspace.element_size(), workspace
+            op, os_ = _cache_view(o, cache, q.dtype)
+            st = lib.attn_fwd_cache(qp, qs, cache._ref, lens_at, op, os_, lse.data_ptr(), B, H, Nq, mask, scale, code,
+                                    space.data_ptr(), size, handle)
+            if st != ATTN_OK:
+                raise AttnError(st, "attn_fwd_cache")
+        return o, lse
+
+    return _run(cache, stream, call)
