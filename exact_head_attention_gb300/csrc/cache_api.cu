@@ -1,6 +1,8 @@
 // C-ABI entry points of the 8-bit key/value cache: argument checks, tensor maps and dispatch.
+#include <atomic>
 #include <cmath>
 #include <cstring>
+#include <random>
 
 #include "api_internal.h"
 #include "kernels.h"
@@ -10,6 +12,20 @@ using namespace exattn;
 namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// A number that no earlier call and no old contents of a workspace are likely to hold: a counter from a random
+// start, through the finaliser of the splitmix64 generator (Steele, Lea and Flood, 2014).
+unsigned long long next_tag() {
+  static std::atomic<unsigned long long> count{[] {
+    std::random_device r;
+    return (static_cast<unsigned long long>(r()) << 32) ^ r();
+  }()};
+  unsigned long long z = count.fetch_add(0x9e3779b97f4a7c15ull, std::memory_order_relaxed);
+  z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
+  z = (z ^ (z >> 27)) * 0x94d049bb133111ebull;
+  z ^= z >> 31;
+  return z ? z : 1ull;  // zero is a flag at rest
+}
 
 // The rules of attn_cache, and its view for the kernels.
 attn_status check_cache(const attn_cache* c, CacheView* out) {
@@ -117,7 +133,7 @@ extern "C" size_t attn_fwd_cache_workspace_size(const attn_cache* cache, int B, 
   if (check_attn(cache, B, H, Nq, &view) != ATTN_OK) return 0;
   const int sms = api_sm_count();
   if (sms <= 0) return 0;
-  return cache_attn_workspace(B, H / cache->heads * Nq, cache->d, sms);
+  return cache_attn_workspace(static_cast<long long>(H / cache->heads) * Nq, cache->d, sms);
 }
 
 extern "C" attn_status attn_fwd_cache(const void* Q, attn_strides q_strides, const attn_cache* cache, const int* lens,
@@ -141,7 +157,8 @@ extern "C" attn_status attn_fwd_cache(const void* Q, attn_strides q_strides, con
   DeviceInfo dev;
   if ((st = api_device(&dev)) != ATTN_OK) return st;
   const int group = H / cache->heads;
-  if (workspace_bytes < cache_attn_workspace(B, group * Nq, cache->d, dev.sm_count)) return ATTN_ERR_WORKSPACE;
+  if (workspace_bytes < cache_attn_workspace(static_cast<long long>(group) * Nq, cache->d, dev.sm_count))
+    return ATTN_ERR_WORKSPACE;
   const uint64_t lines = static_cast<uint64_t>(cache->num_pages) * cache->heads * cache->page_size * cache->d / 128;
   const uint32_t box = static_cast<uint32_t>(cache_attn_box_tokens(cache->page_size, cache->d) * cache->d / 128);
   CUresult r;
@@ -154,6 +171,7 @@ extern "C" attn_status attn_fwd_cache(const void* Q, attn_strides q_strides, con
   a.lens = lens;
   a.lse = LSE;
   a.ws = static_cast<uint8_t*>(workspace);
+  a.tag = next_tag();
   a.err_word = dev.err_word;
   a.B = B;
   a.Nq = Nq;

@@ -63,7 +63,7 @@ struct Cfg {
   static constexpr int TILE = TK * D;                         // bytes of codes, K or V
   static constexpr int STAGES = 2;                            // of K and V together, a warp
   static constexpr int RING = W * STAGES * 2 * TILE;          // 192 or 128 KB
-  static constexpr int JR = NT == 1 ? 512 / D : 8;            // rows joined at a time
+  static constexpr int JR = NT == 1 ? 512 / D : 1024 / D;     // rows joined at a time
   static constexpr int JOIN = W * JR * D * 4;
   static constexpr bool Q_IN_SMEM = NT > 2;                   // registers hold Q up to 16 rows
   static constexpr int QBYTES = Q_IN_SMEM ? NT * (D / 16) * 32 * 8 : 0;
@@ -74,7 +74,7 @@ struct Cfg {
   static constexpr int OFF_META = OFF_Q + QBYTES;             // [warp][stage][group] {ks, vs}
   static constexpr int OFF_STAT = (OFF_META + W * STAGES * NH * 8 + 15) & ~15;  // m[R][W], l[R][W], vref[W]
   static constexpr int OFF_PIECE = OFF_STAT + (2 * W * R + W) * 4;
-  static constexpr int OFF_BAR = (OFF_PIECE + kPieceRing * 32 + 7) & ~7;
+  static constexpr int OFF_BAR = (OFF_PIECE + kPieceRing * kPieceInts * 4 + 7) & ~7;
   static constexpr int OFF_MISC = OFF_BAR + 8 * (2 * W * STAGES + 2 * kPieceRing + 1);
   static constexpr int OFF_SCHED = (OFF_MISC + 16 + 7) & ~7;
   static constexpr int BYTES = OFF_SCHED + static_cast<int>(sizeof(typename CacheWalk<R, TK, 128, W>::Shared));
@@ -134,8 +134,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
   auto piece_empty = [&](int i) { return bars + 8 * (2 * W * NST + kPieceRing + i); };
   const uint32_t join_bar = bars + 8 * (2 * W * NST + 2 * kPieceRing);
   float2* meta = reinterpret_cast<float2*>(smem_raw + C::OFF_META);
-  int* pieces = reinterpret_cast<int*>(smem_raw + C::OFF_PIECE);  // [kPieceRing][8]
+  CachePiece* pieces = reinterpret_cast<CachePiece*>(smem_raw + C::OFF_PIECE);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_raw + C::OFF_MISC);
+  volatile uint32_t* merge_flag = reinterpret_cast<volatile uint32_t*>(smem_raw + C::OFF_MISC + 4);
   const WaitCtx wc{abort_flag, a.err_word, a.timeout_ns};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
   __syncthreads();
   // A dependent launch: what is ahead on the stream has written its results before anything is read.
   griddep_wait();
-  griddep_launch_dependents();  // the merge may start; it waits for this kernel in the same way
+  griddep_launch_dependents();
 
   if (warp >= W) {
     regs_decrease<C::PRODUCER_REGS>();
@@ -224,14 +225,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
           ok = mbar_wait_warp(piece_empty(i), (((announced - 1) / kPieceRing) & 1) ^ 1, wc) && ok;
           const int nrows = have && ok ? min(C::R, a.group * a.Nq - p.rt * C::R) : 0;
           if (lane == 0) {
-            int* d = pieces + i * 8;
-            d[0] = have ? p.b : -1;
-            d[1] = p.head;
-            d[2] = p.rt;
-            d[3] = p.len;
-            d[4] = p.begin;
-            d[5] = p.end;
-            d[6] = p.slot;
+            pieces[i] = p;
+            if (!have) pieces[i].b = -1;
             mbar_arrive_expect_tx(piece_full(i), nrows * D * 2);
           }
           if (lane < nrows) {
@@ -267,6 +262,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
     }
+    cache_empty_items<D, C::R, C::TK, W>(a, blockIdx.x * 4 + pw, gridDim.x * 4);
     // Every copy issued must land before the block exits, also where the computing warps gave up.
     if (feeds)
       for (int n = max(0, issued - NST); n < issued; ++n) mbar_drain(full(cw, n % NST), (n / NST) & 1, a.timeout_ns);
@@ -285,7 +281,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
   float* st_v = st_l + W * C::R;
   float4* join = reinterpret_cast<float4*>(smem_raw + C::OFF_JOIN);
   uint2* qs = reinterpret_cast<uint2*>(smem_raw + C::OFF_Q);
-  const CacheWs ws = cache_ws(a.ws, a.B, C::R, D, a.sm_count);
+  const CacheWs ws = cache_ws(a.ws, C::R, D, a.sm_count);
   const int rows = a.group * a.Nq;
   int used = 0;
   bool ok = true;
@@ -301,8 +297,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
   for (int pi = 0; ; ++pi) {
     ok = mbar_wait_warp(piece_full(pi % kPieceRing), (pi / kPieceRing) & 1, wc) && ok;
     if (!ok) break;
-    const int* d = pieces + (pi % kPieceRing) * 8;
-    const int b = d[0], head = d[1], rt = d[2], len = d[3], begin = d[4], end = d[5], slot = d[6];
+    const CachePiece piece = pieces[pi % kPieceRing];
+    const int b = piece.b, head = piece.head, rt = piece.rt, len = piece.len, begin = piece.begin, end = piece.end,
+              slot = piece.slot;
     if (b < 0) break;
     const int row0 = rt * C::R;
 
@@ -618,12 +615,94 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
             a.lse[(static_cast<long long>(b) * a.c.heads * a.group + hq) * a.Nq + tok] = lse2 * 0.6931471805599453f;
         } else {
           reinterpret_cast<float4*>(ws.o)[(static_cast<size_t>(slot) * C::R + ri) * Q4 + q] = acc;
-          if (q == 0) ws.l[static_cast<size_t>(slot) * C::R + ri] = lse2;
+          if (q == 0) ws.l[static_cast<size_t>(slot) * 2 * C::R + ri] = lse2;
         }
       }
       if (!(ok = sync_warps())) break;
     }
     if (!ok) break;
+
+    // ------------------------------------------------------------ merge, where this piece completes its item
+    if (slot >= 0) {
+      if (warp == 0) {
+        const bool all = cache_piece_done(ws, piece, 0, a.tag);
+        if (lane == 0) *merge_flag = all;
+      }
+      if (!(ok = sync_warps())) break;
+      if (*merge_flag) {
+        // L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s over the row's pieces.  Where threads are left over, G of them
+        // share a row's four columns, each with every G-th piece, and join in shared memory.
+        const int n = piece.pieces(), cells = nrows * Q4;
+        const int G = max(1, min(n, 32 * W / cells));
+        float4* m_acc = join;
+        float2* m_stat = reinterpret_cast<float2*>(join + 32 * W);
+        static_assert(C::JOIN >= 32 * W * 24, "room for the shares");
+        for (int i = threadIdx.x; i < cells * G; i += 32 * W) {
+          const int cell = i % cells, g0 = i / cells, ri = cell / Q4, q = cell % Q4;
+          float mx = -INFINITY, sum = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int k = g0; k < n; k += G) {
+            const size_t at = static_cast<size_t>(piece.slot_of(k));
+            const float L = __ldcg(ws.l + at * 2 * C::R + ri);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(ws.o) + (at * C::R + ri) * Q4 + q);
+            const float to = fmaxf(mx, L), mt = to == -INFINITY ? 0.f : to;
+            const float e0 = mx == -INFINITY ? 0.f : ex2_approx(mx - mt), e1 = ex2_approx(L - mt);  // a NaN counts
+            mx = to;
+            sum = fmaf(sum, e0, e1);
+            acc.x = fmaf(acc.x, e0, e1 * x.x);
+            acc.y = fmaf(acc.y, e0, e1 * x.y);
+            acc.z = fmaf(acc.z, e0, e1 * x.z);
+            acc.w = fmaf(acc.w, e0, e1 * x.w);
+          }
+          auto finish = [&]() {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int rr = row0 + ri, tok = rr / a.group, hq = head * a.group + rr - tok * a.group;
+            uint16_t* dst = static_cast<uint16_t*>(a.o) + b * a.so.b + hq * a.so.h + tok * a.so.n + q * 4;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+            if (q == 0)
+              a.lse[(static_cast<long long>(b) * a.c.heads * a.group + hq) * a.Nq + tok] =
+                  sum == 0.f ? -INFINITY : ((mx == -INFINITY ? 0.f : mx) + __log2f(sum)) * 0.6931471805599453f;
+          };
+          if (G == 1) {
+            finish();
+          } else {  // cells * G threads at most: one turn of the loop
+            m_acc[i] = acc;
+            m_stat[i] = make_float2(mx, sum);
+          }
+        }
+        if (G > 1) {
+          if (!(ok = sync_warps())) break;
+          for (int cell = threadIdx.x; cell < cells; cell += 32 * W) {
+            const int ri = cell / Q4, q = cell % Q4;
+            float mx = -INFINITY;
+            for (int k = 0; k < G; ++k) mx = fmaxf(mx, m_stat[k * cells + cell].x);
+            const float ms = mx == -INFINITY ? 0.f : mx;
+            float sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < G; ++k) {
+              const float2 st = m_stat[k * cells + cell];
+              if (st.y == 0.f) continue;
+              const float4 x = m_acc[k * cells + cell];
+              const float e = ex2_approx(st.x - ms);
+              sum = fmaf(e, st.y, sum);
+              acc.x = fmaf(e, x.x, acc.x);
+              acc.y = fmaf(e, x.y, acc.y);
+              acc.z = fmaf(e, x.z, acc.z);
+              acc.w = fmaf(e, x.w, acc.w);
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int rr = row0 + ri, tok = rr / a.group, hq = head * a.group + rr - tok * a.group;
+            uint16_t* dst = static_cast<uint16_t*>(a.o) + b * a.so.b + hq * a.so.h + tok * a.so.n + q * 4;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+            if (q == 0)
+              a.lse[(static_cast<long long>(b) * a.c.heads * a.group + hq) * a.Nq + tok] =
+                  sum == 0.f ? -INFINITY : (ms + __log2f(sum)) * 0.6931471805599453f;
+          }
+        }
+        if (!(ok = sync_warps())) break;  // `join` is free again
+      }
+    }
   }
 }
 
@@ -632,10 +711,9 @@ cudaError_t launch_t(const CacheAttnArgs& a, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   auto kern = cache_attn_kernel<D, FMT, BF16, NT>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(kern, C::BYTES, done);
+  const cudaError_t e = allow_smem(kern, C::BYTES, done);
   if (e != cudaSuccess) return e;
-  if ((e = launch_dependent(kern, dim3(a.sm_count), dim3(C::THREADS), C::BYTES, stream, a)) != cudaSuccess) return e;
-  return launch_cache_merge<D, BF16, C::R, C::TK, C::W>(a, stream);
+  return launch_dependent(kern, dim3(a.sm_count), dim3(C::THREADS), C::BYTES, stream, a);
 }
 
 template <int D, int FMT, bool BF16>
@@ -662,10 +740,8 @@ CacheAttnShape cache_attn_shape(long long rows, int d) {
   return {static_cast<int>((rows + 7) / 8 * 8), 4096 / d};
 }
 
-size_t cache_attn_workspace(int B, long long rows, int d, int sm_count) {
-  const size_t R = cache_attn_shape(rows, d).rows;
-  const size_t n = cache_ws_first_bytes(B) + cache_slots(sm_count) * R * (static_cast<size_t>(d) + 1) * sizeof(float);
-  return (n + 255) & ~static_cast<size_t>(255);
+size_t cache_attn_workspace(long long rows, int d, int sm_count) {
+  return (cache_ws_bytes(cache_attn_shape(rows, d).rows, d, sm_count) + 255) & ~static_cast<size_t>(255);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream) {

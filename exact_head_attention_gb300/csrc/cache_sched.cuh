@@ -23,32 +23,32 @@
 
 namespace exattn {
 
-// Workspace: a header, the first tile number of every sequence, then the slots (fp32 rows of D values,
-// normalised by the piece's own sum) and their base-2 log-sum-exps.
-struct CacheSchedHeader {
-  int per_piece;  // C
-  int pieces;     // 1: the second form above
-};
+// Merging.  The block whose piece completes an item merges all its pieces, in key order, so the result does
+// not depend on which block that is.  A block that has stored its partial result sets the slot's flag to the
+// call's tag and then looks at the flags of the item's other pieces: the last to set one sees all.  (Two
+// blocks may both; they write the same bits.)  The merging block puts the flags back to zero.  The
+// workspace needs no preparation: what lies there before is taken for a flag only if it equals a 64-bit
+// tag drawn for the call, and a captured call, whose tag is the same at each replay, finds zeros.
 
+// Workspace: flags, then the slots (fp32 rows of D values, normalised by the piece's own sum) and their
+// base-2 log-sum-exps.  Flags and log-sum-exps are kept twice, for the two warpgroups of cache_tile.cu.
 struct CacheWs {
-  CacheSchedHeader* head;
-  int* first;  // [B]
-  float* o;    // [slots][R][D]
-  float* l;    // [slots][R]
+  unsigned long long* flag;  // [slots][2]
+  float* o;                  // [slots][R][D]
+  float* l;                  // [slots][2][R]
 };
 
 // Slots are numbered below 2 (T / C + 1) <= 2 (P + 1), T with the items' costs.
 inline __host__ __device__ size_t cache_slots(int sm_count) { return 2 * (static_cast<size_t>(sm_count) + 1); }
 
-inline __host__ __device__ size_t cache_ws_first_bytes(int B) {
-  return (256 + 4 * static_cast<size_t>(B) + 255) & ~static_cast<size_t>(255);
+inline __host__ __device__ size_t cache_ws_bytes(int R, int D, int sm_count) {
+  return cache_slots(sm_count) * (16 + static_cast<size_t>(R) * (D + 2) * sizeof(float));
 }
 
-inline __host__ __device__ CacheWs cache_ws(uint8_t* ws, int B, int R, int D, int sm_count) {
+inline __host__ __device__ CacheWs cache_ws(uint8_t* ws, int R, int D, int sm_count) {
   CacheWs w;
-  w.head = reinterpret_cast<CacheSchedHeader*>(ws);
-  w.first = reinterpret_cast<int*>(ws + 256);
-  w.o = reinterpret_cast<float*>(ws + cache_ws_first_bytes(B));
+  w.flag = reinterpret_cast<unsigned long long*>(ws);
+  w.o = reinterpret_cast<float*>(ws + cache_slots(sm_count) * 16);
   w.l = w.o + cache_slots(sm_count) * R * D;
   return w;
 }
@@ -94,12 +94,41 @@ struct CacheItems {
   __device__ int seq_len(const CacheAttnArgs& a, int b) const { return cache_len(a.c, __ldg(a.lens + b)); }
 };
 
-// A piece of an item for one block.
+// A piece of an item for one block, as the producer announces it (12 ints of shared memory).
 struct CachePiece {
-  int b, head, rt, len;
-  int begin, end;     // key tiles of the item
-  int slot;           // -1: the whole item, else its place in the workspace
+  int b, head, rt, len;  // b < 0: there are no more
+  int begin, end;        // key tiles of the item
+  int slot;              // -1: the whole item, else its place in the workspace
+  int first, ntiles;     // number of the item's first tile, and its tiles
+  int C, by_piece;
+
+  // Pieces of the item, and the slot of the i-th.
+  __device__ int pieces() const { return by_piece ? (ntiles + C - 1) / C : (first + ntiles - 1) / C - first / C + 1; }
+  __device__ int slot_of(int i) const {
+    const int c = by_piece ? (first + i * C) / C : first / C + i;
+    return 2 * c + (i != 0);
+  }
 };
+constexpr int kPieceInts = 12;
+
+// Called by a warp (all lanes) after the block, or the warpgroup `part`, has stored its piece and met: sets the
+// piece's flag; true where every piece of the item is then there, and their flags are zero again.
+__device__ __forceinline__ bool cache_piece_done(const CacheWs& ws, const CachePiece& p, int part, unsigned long long tag) {
+  const int lane = threadIdx.x & 31;
+  __threadfence();
+  if (lane == 0) atomicExch(ws.flag + 2 * p.slot + part, tag);
+  __syncwarp();
+  __threadfence();
+  const int n = p.pieces();
+  bool all = true;
+  for (int i = lane; i < n; i += 32) all = all && *reinterpret_cast<volatile unsigned long long*>(ws.flag + 2 * p.slot_of(i) + part) == tag;
+  all = __all_sync(0xffffffffu, all);
+  if (all) {
+    __threadfence();  // the other blocks' partial results are read after their flags
+    for (int i = lane; i < n; i += 32) ws.flag[2 * p.slot_of(i) + part] = 0ull;
+  }
+  return all;
+}
 
 // The division, and a block's walk over its pieces.  Built by NT threads of a block (numbered `tid`, whole
 // warps that meet at hardware barrier `bar`), then walked by each of their warps, all lanes alike.
@@ -171,15 +200,6 @@ struct CacheWalk {
       at = block * C;
       stop = min(total, at + C);
       step = 0;
-    }
-    if (block == 0) {  // for the merge
-      const CacheWs ws = cache_ws(a.ws, a.B, R, a.c.d, a.sm_count);
-      int f = x - n;
-      for (int i = b0; i < b1; ++i) {
-        ws.first[i] = f;
-        f += a.c.heads * items.head_tiles(a, items.seq_len(a, i));
-      }
-      if (tid == 0) *ws.head = CacheSchedHeader{C, by_piece ? 1 : 0};
     }
   }
 
@@ -257,98 +277,32 @@ struct CacheWalk {
     p.rt = rt;
     p.len = len;
     p.begin = tile;
-    p.slot = tile == 0 && p.end == ntiles ? -1 : 2 * ((item_first + items.kItemCost + tile) / C) + (tile != 0);
+    p.first = item_first + items.kItemCost;
+    p.ntiles = ntiles;
+    p.C = C;
+    p.by_piece = by_piece;
+    p.slot = tile == 0 && p.end == ntiles ? -1 : 2 * ((p.first + tile) / C) + (tile != 0);
     return true;
   }
 };
 
-// Merge of the pieces of divided items, one warp a query row, and the rows that see no token:
-// L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s over the row's pieces in key order.
-template <int D, bool BF16, int R, int TK, int kMinTiles>
-__global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant__ CacheAttnArgs a) {
-  constexpr int V = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// O = 0 and LSE = -inf for the rows of items without a key tile (sequences without tokens, and queries before
+// the first token), the items dealt out to all `warps` of the grid.
+template <int D, int R, int TK, int kMinTiles>
+__device__ void cache_empty_items(const CacheAttnArgs& a, int warp, int warps) {
   const CacheItems<R, TK, kMinTiles> items(a);
-  const unsigned rid = blockIdx.x * 8u + warp;
-  const bool mine = rid < static_cast<unsigned>(a.B) * a.c.heads * items.rows;
-  const int r = static_cast<int>(rid % items.rows);
-  const int bh = static_cast<int>(rid / items.rows);
-  const int head = bh % a.c.heads, b = bh / a.c.heads;
-  const int rt = r / R;
-  const CacheWs ws = cache_ws(a.ws, a.B, R, D, a.sm_count);
-  const int tok = r / a.group, hq = head * a.group + r - tok * a.group;
-  griddep_launch_dependents();
-  griddep_wait();
-  if (!mine) return;
-  const int len = items.seq_len(a, b);
-  const CacheSchedHeader hd = *ws.head;
-  int first = ws.first[b];
-  const int nt = items.tiles(a, len, rt), C = hd.per_piece;
-  int pieces = 0;
-  if (nt > 0) {
-    if (items.row_tiles == 1) {
-      first += head * items.cost(nt);
-    } else {
-      first += head * items.head_tiles(a, len);
-      for (int i = 0; i < rt; ++i) first += items.cost(items.tiles(a, len, i));
-    }
-    first += items.kItemCost;  // number of its first tile
-    pieces = hd.pieces ? (nt + C - 1) / C : (first + nt - 1) / C - first / C + 1;
-    if (pieces == 1) return;  // written by the block that had all of it
-  }
-  // Lane i keeps piece i (of each 32): its workspace row and its log-sum-exp.
-  const int c0 = first / C;
-  auto row_of = [&](int i) {
-    const int start = hd.pieces ? first + i * C : (i == 0 ? first : (c0 + i) * C);
-    return (2 * (hd.pieces ? start / C : c0 + i) + (i != 0)) * R + (r - rt * R);
-  };
-  float mx = -INFINITY;
-  for (int i = lane; i < pieces; i += 32) mx = fmaxf(mx, ws.l[row_of(i)]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const float ms = mx == -INFINITY ? 0.f : mx;
-  float acc[V], sum = 0.f;
-#pragma unroll
-  for (int e = 0; e < V; ++e) acc[e] = 0.f;
-  for (int base = 0; base < pieces; base += 32) {
-    const int i = base + lane;
-    const int at = i < pieces ? row_of(i) : 0;
-    const float w = i < pieces ? ex2_approx(ws.l[at] - ms) : 0.f;  // NaN where the piece is
-    const int n = min(32, pieces - base);
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const float* op = ws.o + static_cast<size_t>(__shfl_sync(0xffffffffu, at, k)) * D + lane * V;
-      if constexpr (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(op);
-        acc[0] = fmaf(wk, x.x, acc[0]);
-        acc[1] = fmaf(wk, x.y, acc[1]);
-        acc[2] = fmaf(wk, x.z, acc[2]);
-        acc[3] = fmaf(wk, x.w, acc[3]);
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(op);
-        acc[0] = fmaf(wk, x.x, acc[0]);
-        acc[1] = fmaf(wk, x.y, acc[1]);
-      }
-      sum += wk;
+  const int lane = threadIdx.x & 31, n = a.B * a.c.heads * items.row_tiles;  // below 2^31: the host has counted tiles
+  for (int i = warp; i < n; i += warps) {
+    const int rt = i % items.row_tiles, bh = i / items.row_tiles, head = bh % a.c.heads, b = bh / a.c.heads;
+    if (items.tiles(a, items.seq_len(a, b), rt) != 0) continue;
+    for (int r = rt * R; r < min(items.rows, (rt + 1) * R); ++r) {
+      const int tok = r / a.group, hq = head * a.group + r - tok * a.group;
+      if (lane < D / 8)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + b * a.so.b + hq * a.so.h + tok * a.so.n + lane * 8) =
+            make_uint4(0u, 0u, 0u, 0u);
+      if (lane == 0) a.lse[(static_cast<long long>(b) * a.c.heads * a.group + hq) * a.Nq + tok] = -INFINITY;
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint16_t* dst = static_cast<uint16_t*>(a.o) + b * a.so.b + hq * a.so.h + tok * a.so.n + lane * V;
-  if constexpr (V == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack2<BF16>(acc[0] * inv, acc[1] * inv);
-  if (lane == 0)
-    a.lse[(static_cast<long long>(b) * a.c.heads * a.group + hq) * a.Nq + tok] =
-        sum == 0.f ? -INFINITY : (ms + __log2f(sum)) * 0.6931471805599453f;
-}
-
-template <int D, bool BF16, int R, int TK, int kMinTiles>
-cudaError_t launch_cache_merge(const CacheAttnArgs& a, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(a.B) * a.c.heads * a.group * a.Nq;
-  return launch_dependent(cache_merge_kernel<D, BF16, R, TK, kMinTiles>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0,
-                          stream, a);
 }
 
 }  // namespace exattn

@@ -61,8 +61,8 @@ struct Cfg {
   static constexpr uint32_t OFF_META = OFF_RAW + NR * RAW;           // [kMetaRing] ks[8], vs[8]
   static constexpr uint32_t OFF_STAT = OFF_META + kMetaRing * 64;    // !PAIR: {m, l} [2][128], vref [2][4]
   static constexpr uint32_t OFF_PIECE = OFF_STAT + (PAIR ? 0 : 2 * 128 * 8 + 32);
-  static constexpr uint32_t OFF_BAR = OFF_PIECE + kPieceRing * 32;
-  static constexpr int NBAR = 2 + 4 * NS + 2 * NR + 6 + kMetaRing + 2 * kPieceRing + 2;
+  static constexpr uint32_t OFF_BAR = OFF_PIECE + kPieceRing * kPieceInts * 4;
+  static constexpr int NBAR = 2 + 4 * NS + 2 * NR + 6 + kMetaRing + 2 * kPieceRing + 4;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t OFF_SCHED = OFF_MISC + 16;
   static constexpr uint32_t BYTES = OFF_SCHED + sizeof(typename Walk::Shared);
@@ -115,6 +115,7 @@ struct Bars {
   __device__ uint32_t piece_empty(int s) const { return at(kB + 6 + kMetaRing + kPieceRing + s); }
   __device__ uint32_t join() const { return at(kB + 6 + kMetaRing + 2 * kPieceRing); }
   __device__ uint32_t mma_done() const { return at(kB + 7 + kMetaRing + 2 * kPieceRing); }
+  __device__ uint32_t stored(int t) const { return at(kB + 8 + kMetaRing + 2 * kPieceRing + t); }
 };
 
 // One key tile of the online softmax for this thread's query row.  Scores of the 16-token group g count
@@ -334,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + C::OFF_MISC);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_raw + C::OFF_MISC + 4);
   const WaitCtx wc{abort_flag, a.err_word, a.timeout_ns};
-  int* pieces = reinterpret_cast<int*>(smem_raw + C::OFF_PIECE);  // [kPieceRing][8]
+  CachePiece* pieces = reinterpret_cast<CachePiece*>(smem_raw + C::OFF_PIECE);
+  volatile uint32_t* merge_flag = reinterpret_cast<volatile uint32_t*>(smem_raw + C::OFF_MISC + 8);  // [2]
   float* meta = reinterpret_cast<float*>(smem_raw + C::OFF_META);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -345,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       mbar_init(bars.s_full(t), 1);
       mbar_init(bars.p_full(t), 4);
       mbar_init(bars.o_full(t), 1);
+      mbar_init(bars.stored(t), 4);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(bars.k_full(s), 3);
@@ -378,27 +381,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
   griddep_launch_dependents();
   const int rows = a.group * a.Nq;
 
-  struct Piece {
-    int b, head, rt, len, begin, end, slot;
-    int nrows, n0, n1;  // rows of the item; key tiles of each chain
+  // The i-th piece, where it lies in shared memory (until this warp's arrival at piece_empty); nullptr at the
+  // end, or after a failed wait.
+  auto next_piece = [&](int i) -> const CachePiece* {
+    if (!mbar_wait_warp(bars.piece_full(i % kPieceRing), (i / kPieceRing) & 1, wc)) return nullptr;
+    const CachePiece* p = pieces + i % kPieceRing;
+    return p->b >= 0 ? p : nullptr;
   };
-  // The i-th piece; false at the end, or after a failed wait.
-  auto next_piece = [&](int i, Piece& p) -> bool {
-    const uint32_t bar = bars.piece_full(i % kPieceRing), ph = (i / kPieceRing) & 1;
-    if (!mbar_wait_warp(bar, ph, wc)) return false;
-    const int* d = pieces + (i % kPieceRing) * 8;
-    p.b = d[0];
-    p.head = d[1];
-    p.rt = d[2];
-    p.len = d[3];
-    p.begin = d[4];
-    p.end = d[5];
-    p.slot = d[6];
-    p.nrows = min(C::R, rows - p.rt * C::R);
+  // Key tiles of chain t in a piece.
+  auto chain_tiles = [&](const CachePiece& p, int t) {
     const int n = p.end - p.begin;
-    p.n0 = PAIR ? n : (n + 1) / 2;
-    p.n1 = PAIR ? (p.nrows > 128 ? n : 0) : n / 2;
-    return p.b >= 0;
+    if (PAIR) return t == 0 || rows - p.rt * C::R > 128 ? n : 0;
+    return t == 0 ? (n + 1) / 2 : n / 2;
   };
 
   if (warp >= 8) {
@@ -465,14 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           if (!ok) break;
           ++announced;
           if (lane == 0) {
-            int* d = pieces + i * 8;
-            d[0] = have ? p.b : -1;
-            d[1] = p.head;
-            d[2] = p.rt;
-            d[3] = p.len;
-            d[4] = p.begin;
-            d[5] = p.end;
-            d[6] = p.slot;
+            pieces[i] = p;
+            if (!have) pieces[i].b = -1;
             mbar_arrive(bars.piece_full(i));
           }
         } else if (left < 3) {
@@ -499,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           }
         }
       }
+      cache_empty_items<D, C::R, kTK, C::MIN_TILES>(a, blockIdx.x, gridDim.x);
       // Every copy issued must land before the block exits, also where the other roles gave up.
       if (lane == 0)
         for (int n = max(0, raws - NR); n < raws; ++n) mbar_drain(bars.raw_full(n % NR), (n / NR) & 1, a.timeout_ns);
@@ -520,9 +509,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       uint32_t phase_p = 0;          // bit t: parity of the next wait of p_full(t)
       uint32_t q0 = 0, q1 = 0;
       bool ok = true;
-      Piece p;
-      for (int pi = 0; ok && next_piece(pi, p); ++pi) {
-        const int n0 = __shfl_sync(0xffffffffu, p.n0, 0), n1 = __shfl_sync(0xffffffffu, p.n1, 0);
+      const CachePiece* p;
+      for (int pi = 0; ok && (p = next_piece(pi)) != nullptr; ++pi) {
+        const int n0 = __shfl_sync(0xffffffffu, chain_tiles(*p, 0), 0), n1 = __shfl_sync(0xffffffffu, chain_tiles(*p, 1), 0);
         const bool both = n1 > 0;
         // the query tiles: each chain's own, or halves of one from both warpgroups
         ok = mbar_wait_warp(ub.q_full(0), q0++ & 1, wc);
@@ -586,15 +575,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       const int v = warp >= 13, third = warp - (v ? 13 : 10);
       int kt = 0;
       bool ok = true;
-      Piece p;
-      for (int pi = 0; ok && next_piece(pi, p); ++pi) {
-        for (int t = p.begin; t < p.end; ++t, ++kt) {
+      const CachePiece* p;
+      for (int pi = 0; ok && (p = next_piece(pi)) != nullptr; ++pi) {
+        const int len = p->len, end = p->end;
+        for (int t = p->begin; t < end; ++t, ++kt) {
           const int s = kt % NS, raws = 2 * kt + v, rs = raws % NR;
           if (!(ok = mbar_wait_warp(bars.raw_full(rs), (raws / NR) & 1, wc))) break;
           if (!(ok = mbar_wait_warp(v ? bars.v_empty(s) : bars.k_empty(s), ((kt / NS) & 1) ^ 1, wc))) break;
           // Hidden keys' scores are set aside by the softmax; their values must be finite.
           convert_third<D, FMT>(smem_raw + C::OFF_RAW + rs * C::RAW, sbase + (v ? C::OFF_V : C::OFF_K) + s * C::TILE, third,
-                                lane, p.len - t * kTK);
+                                lane, len - t * kTK);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -612,58 +602,80 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     const int r = quarter * 32 + lane;  // row of the operand tile = TMEM lane
     const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + t * 128 + lane_bits, tO = tmem + 256 + t * 128 + lane_bits;
-    const CacheWs ws = cache_ws(a.ws, a.B, C::R, D, a.sm_count);
+    const CacheWs ws = cache_ws(a.ws, C::R, D, a.sm_count);
     float2* stat = reinterpret_cast<float2*>(smem_raw + C::OFF_STAT);
     float* stat_v = reinterpret_cast<float*>(smem_raw + C::OFF_STAT + 2 * 128 * 8);
     int kt = 0;
-    uint32_t sc = 0, oc_own = 0, oc_other = 0, jc = 0;  // waits of s_full, of both o_full, of the join
+    uint32_t sc = 0, oc_own = 0, oc_other = 0, jc = 0, dc = 0;  // waits of s_full, of both o_full, of join, of stored
     bool ok = true;
-    Piece p;
-    // Both softmax warpgroups meet (!PAIR).  A bounded wait: after a failed one elsewhere this gives up too.
+    const int ri = (PAIR ? t * 128 : 0) + r;  // row of the item
+    // Both softmax warpgroups meet (!PAIR), or one.  Bounded waits: after a failed one elsewhere these give up too.
     auto join = [&]() -> bool {
       __syncwarp();
       if (lane == 0) mbar_arrive(bars.join());
       return mbar_wait_warp(bars.join(), jc++ & 1, wc);
     };
-    for (int pi = 0; ok && next_piece(pi, p); ++pi) {
-      const int n = t ? p.n1 : p.n0;
-      const int ri = (PAIR ? t * 128 : 0) + r;  // row of the item
-      const int row = p.rt * C::R + ri;
-      const bool there = row < rows;
-      const int rc = min(row, rows - 1), tok = rc / a.group, hq = p.head * a.group + rc - tok * a.group;
+    auto stored = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars.stored(t));
+      return mbar_wait_warp(bars.stored(t), dc++ & 1, wc);
+    };
+    // What the key-tile loop does not need is read from the piece in shared memory again after it.
+    struct Row {
+      bool there;
+      int tok, hq;
+    };
+    auto row_of = [&](const CachePiece& p) -> Row {
+      const int row = p.rt * C::R + ri, rc = min(row, rows - 1), tok = rc / a.group;
+      return {row < rows, tok, p.head * a.group + rc - tok * a.group};
+    };
+    auto out_row = [&](const CachePiece& p, const Row& w) {
+      return static_cast<uint16_t*>(a.o) + p.b * a.so.b + w.hq * a.so.h + w.tok * a.so.n;
+    };
+    auto out_lse = [&](const CachePiece& p, const Row& w) {
+      return a.lse + (static_cast<long long>(p.b) * a.c.heads * a.group + w.hq) * a.Nq + w.tok;
+    };
+    const CachePiece* pp;
+    for (int pi = 0; ok && (pp = next_piece(pi)) != nullptr; ++pi) {
+      const CachePiece& p = *pp;
+      const int n = chain_tiles(p, t);
       if (!PAIR || n > 0) {
-        // The previous piece's score products have completed: this chain's with its o_full, the other's
-        // with the join that ended its epilogue.
-        const uint16_t* src = static_cast<const uint16_t*>(a.q) + p.b * a.sq.b + hq * a.sq.h + tok * a.sq.n;
-        const uint32_t tile = sbase + C::OFF_Q + (PAIR ? t * C::TILE : 0);
-        const float back = PAIR ? stage_query_row<D, BF16>(src, there, tile, r, 0, D / 8)
-                                : stage_query_row<D, BF16>(src, there, tile, r, t * (D / 16), (t + 1) * (D / 16));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars.q_full(t));
-        const float fac = a.scale * 1.4426950408889634f * back;
-        const int lim_row = cache_row_limit(a.mask, p.len, a.Nq, tok);
-        // the least of this warp's rows
-        const int lim_min = cache_row_limit(a.mask, p.len, a.Nq, min(row - lane, rows - 1) / a.group);
-        const bool idle = row - lane >= rows;  // a warp of rows that are not there
+        const int row_first = p.rt * C::R + ri - lane;  // of this warp
+        const bool idle = row_first >= rows;            // a warp of rows that are not there
         float m = -INFINITY, l = 0.f, vref = 0.f, vinv = 0.f;
-        for (int j = 0; j < n; ++j) {
-          const int i = PAIR ? j : 2 * j + t, nt = kt + i;
-          if (!(ok = mbar_wait_warp(bars.s_full(t), sc++ & 1, wc))) break;
-          if (!(ok = mbar_wait_warp(bars.meta_full(nt % kMetaRing), (nt / kMetaRing) & 1, wc))) break;
-          tc_fence_after();
-          const int key0 = (p.begin + i) * kTK;
-          if (!idle) {
-            const float* scales = meta + (nt % kMetaRing) * 16;
-            if (key0 + kTK > lim_min)
-              softmax_scaled<D, true>(tS, tO, scales, lim_row - key0, fac, j == 0, m, l, vref, vinv);
-            else
-              softmax_scaled<D, false>(tS, tO, scales, kTK, fac, j == 0, m, l, vref, vinv);
-            tmem_wait_st();
-          }
-          tc_fence_before();
+        {
+          // The previous piece's score products have completed: this chain's with its o_full, the other's
+          // with the join that ended its epilogue.
+          const Row w = row_of(p);
+          const uint16_t* src = static_cast<const uint16_t*>(a.q) + p.b * a.sq.b + w.hq * a.sq.h + w.tok * a.sq.n;
+          const uint32_t tile = sbase + C::OFF_Q + (PAIR ? t * C::TILE : 0);
+          const float back = PAIR ? stage_query_row<D, BF16>(src, w.there, tile, r, 0, D / 8)
+                                  : stage_query_row<D, BF16>(src, w.there, tile, r, t * (D / 16), (t + 1) * (D / 16));
+          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bars.p_full(t));
+          if (lane == 0) mbar_arrive(bars.q_full(t));
+          const float fac = a.scale * 1.4426950408889634f * back;
+          const int key_first = p.begin * kTK;
+          const int lim_row = cache_row_limit(a.mask, p.len, a.Nq, w.tok) - key_first;
+          // the least of this warp's rows
+          const int lim_min = cache_row_limit(a.mask, p.len, a.Nq, min(row_first, rows - 1) / a.group) - key_first;
+          for (int j = 0; j < n; ++j) {
+            const int i = PAIR ? j : 2 * j + t, nt = kt + i;
+            if (!(ok = mbar_wait_warp(bars.s_full(t), sc++ & 1, wc))) break;
+            if (!(ok = mbar_wait_warp(bars.meta_full(nt % kMetaRing), (nt / kMetaRing) & 1, wc))) break;
+            tc_fence_after();
+            if (!idle) {
+              const float* scales = meta + (nt % kMetaRing) * 16;
+              if ((i + 1) * kTK > lim_min)
+                softmax_scaled<D, true>(tS, tO, scales, lim_row - i * kTK, fac, j == 0, m, l, vref, vinv);
+              else
+                softmax_scaled<D, false>(tS, tO, scales, kTK, fac, j == 0, m, l, vref, vinv);
+              tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.p_full(t));
+          }
         }
         if (ok && n > 0) ok = mbar_wait_warp(bars.o_full(t), oc_own++ & 1, wc);
 
@@ -677,10 +689,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           stat[t * 128 + r] = make_float2(m, l);
           if (lane == 0) stat_v[t * 4 + quarter] = vref;
           if (!(ok = ok && join())) break;
-          if (t == 1 || p.n1 > 0) ok = mbar_wait_warp(bars.o_full(1 - t), oc_other++ & 1, wc);
+          use1 = chain_tiles(p, 1) > 0;
+          if (t == 1 || use1) ok = mbar_wait_warp(bars.o_full(1 - t), oc_other++ & 1, wc);
           if (!ok) break;
           const float2 x = stat[r], y = stat[128 + r];
-          use1 = p.n1 > 0;
           const float mx = fmaxf(x.x, y.x), ms = mx == -INFINITY ? 0.f : mx;
           const float e0 = x.y == 0.f ? 0.f : ex2_approx(x.x - ms), e1 = y.y == 0.f ? 0.f : ex2_approx(y.x - ms);
           const float sum = (x.y == 0.f ? 0.f : e0 * x.y) + (y.y == 0.f ? 0.f : e1 * y.y);
@@ -689,65 +701,135 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           w1 = use1 ? e1 * stat_v[4 + quarter] * inv : 0.f;
           lse2 = sum == 0.f ? -INFINITY : ms - kShift + __log2f(sum);
         }
+        if (!ok) break;
         tc_fence_after();
-        if (ok && !idle) {
-          constexpr int COLS = PAIR ? D : D / 2;  // this thread's columns of its row
-          const int c0 = PAIR ? 0 : t * COLS;
-          uint16_t* dst = static_cast<uint16_t*>(a.o) + p.b * a.so.b + hq * a.so.h + tok * a.so.n + c0;
-          float4* part = reinterpret_cast<float4*>(ws.o + (static_cast<size_t>(max(p.slot, 0)) * C::R + ri) * D + c0);
+        constexpr int COLS = PAIR ? D : D / 2;  // this thread's columns of its row
+        const int c0 = PAIR ? 0 : t * COLS;
+        const Row w = row_of(p);
+        const int slot = p.slot;
+        if (!idle) {
+          uint16_t* dst = out_row(p, w) + c0;
+          float4* part = reinterpret_cast<float4*>(ws.o + (static_cast<size_t>(max(slot, 0)) * C::R + ri) * D + c0);
           const uint32_t at0 = PAIR ? tO : tmem + 256 + lane_bits;
+#pragma unroll 1
+          for (int c = 0; c < COLS; c += 16) {
+            uint32_t x[16];
+            tmem_ld16(at0 + c0 + c, x);
+            if (!PAIR && use1) {
+              uint32_t y[16];
+              tmem_ld16(at0 + 128 + c0 + c, y);
 #pragma unroll
-          for (int c = 0; c < COLS / 32; ++c) {
-            uint32_t x[32];
-            tmem_ld32(at0 + c0 + c * 32, x);
-            if constexpr (PAIR) {
-              tmem_wait_ld();
-              reg_fence32(x);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * w0);
+              for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), w1, __uint_as_float(x[e]) * w0));
             } else {
-              uint32_t y[32];
-              if (use1) tmem_ld32(at0 + 128 + c0 + c * 32, y);
-              tmem_wait_ld();
-              reg_fence32(x);
-              if (use1) {
-                reg_fence32(y);
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  x[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), w1, __uint_as_float(x[e]) * w0));
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * w0);
-              }
+              for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * w0);
             }
-            if (there) {
-              if (p.slot < 0) {
+            if (w.there) {
+              if (slot < 0) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                  uint32_t w[4];
+                for (int e = 0; e < 16; e += 8) {
+                  uint32_t z[4];
 #pragma unroll
                   for (int k = 0; k < 4; ++k)
-                    w[k] = pack2<BF16>(__uint_as_float(x[e + 2 * k]), __uint_as_float(x[e + 2 * k + 1]));
-                  *reinterpret_cast<uint4*>(dst + c * 32 + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                    z[k] = pack2<BF16>(__uint_as_float(x[e + 2 * k]), __uint_as_float(x[e + 2 * k + 1]));
+                  *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(z[0], z[1], z[2], z[3]);
                 }
               } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  part[c * 8 + e / 4] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]),
-                                                    __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                for (int e = 0; e < 16; e += 4)
+                  part[(c + e) / 4] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]), __uint_as_float(x[e + 2]),
+                                                  __uint_as_float(x[e + 3]));
               }
             }
           }
-          if (there && (PAIR || t == 0)) {
-            if (p.slot < 0)
-              a.lse[(static_cast<long long>(p.b) * a.c.heads * a.group + hq) * a.Nq + tok] = lse2 * 0.6931471805599453f;
-            else
-              ws.l[static_cast<size_t>(p.slot) * C::R + ri] = lse2;
+          if (w.there) {
+            if (slot >= 0)
+              ws.l[(static_cast<size_t>(slot) * 2 + t) * C::R + ri] = lse2;
+            else if (PAIR || t == 0)
+              *out_lse(p, w) = lse2 * 0.6931471805599453f;
           }
         }
         tc_fence_before();
+
+        // ------------------------------------------------------------ merge, where this piece completes its item
+        // Each warpgroup for itself: it has its own rows (PAIR) or columns.
+        if (slot >= 0) {
+          if (!(ok = stored())) break;
+          if (quarter == 0) {
+            const bool all = cache_piece_done(ws, p, t, a.tag);
+            if (lane == 0) merge_flag[t] = all;
+          }
+          if (!(ok = stored())) break;
+          if (merge_flag[t]) {
+            // L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s over a row's pieces in key order.  A warp has 32 rows: lane k
+            // works out row k's weights, then the lanes stand side by side over the columns of eight rows at a time.
+            constexpr int V = COLS / 32;  // columns a lane: 1, 2 or 4
+            const int np = p.pieces(), nr = min(32, rows - row_first);
+            auto lse_at = [&](int i) { return __ldcg(ws.l + (static_cast<size_t>(p.slot_of(i)) * 2 + t) * C::R + ri); };
+            float ms = 0.f, inv = 0.f;
+            if (w.there) {
+              float mx = -INFINITY, sum = 0.f;
+#pragma unroll 4
+              for (int i = 0; i < np; ++i) {
+                const float L = lse_at(i), to = fmaxf(mx, L), mt = to == -INFINITY ? 0.f : to;
+                sum = fmaf(sum, mx == -INFINITY ? 0.f : ex2_approx(mx - mt), ex2_approx(L - mt));  // a NaN counts
+                mx = to;
+              }
+              ms = mx == -INFINITY ? 0.f : mx;
+              inv = sum == 0.f ? 0.f : 1.f / sum;
+              if (PAIR || t == 0) *out_lse(p, w) = sum == 0.f ? -INFINITY : (ms + __log2f(sum)) * 0.6931471805599453f;
+            }
+#pragma unroll 1
+            for (int kb = 0; kb < nr; kb += 8) {
+              float acc[8][V];
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[k][e] = 0.f;
+#pragma unroll 2
+              for (int i = 0; i < np; ++i) {
+                const float wi = w.there ? ex2_approx(lse_at(i) - ms) * inv : 0.f;
+                // rows past the last one lie in the slot all the same
+                const float* src = ws.o + (static_cast<size_t>(p.slot_of(i)) * C::R + (ri - lane + kb)) * D + c0 + lane * V;
+                float x[8][V];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  if constexpr (V == 4) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4*>(src + k * D));
+                    x[k][0] = y.x;
+                    x[k][1] = y.y;
+                    x[k][2] = y.z;
+                    x[k][3] = y.w;
+                  } else {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) x[k][e] = __ldcg(src + k * D + e);
+                  }
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float wk = __shfl_sync(0xffffffffu, wi, kb + k);
+#pragma unroll
+                  for (int e = 0; e < V; ++e) acc[k][e] = fmaf(wk, x[k][e], acc[k][e]);
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                if (kb + k >= nr) break;
+                const int row = row_first + kb + k, tok = row / a.group;
+                const Row wk{true, tok, p.head * a.group + row - tok * a.group};
+                uint16_t* dst = out_row(p, wk) + c0 + lane * V;
+                if constexpr (V == 4)
+                  *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(acc[k][0], acc[k][1]), pack2<BF16>(acc[k][2], acc[k][3]));
+                else if constexpr (V == 2)
+                  *reinterpret_cast<uint32_t*>(dst) = pack2<BF16>(acc[k][0], acc[k][1]);
+                else
+                  *dst = static_cast<uint16_t>(pack2<BF16>(acc[k][0], 0.f));
+              }
+            }
+          }
+        }
         // O_t, the statistics and the query tile are free once both warpgroups are here.
-        if (!PAIR && !(ok = ok && join())) break;
+        if (!PAIR && !(ok = join())) break;
       }
       kt += p.end - p.begin;
       __syncwarp();
@@ -769,10 +851,9 @@ cudaError_t launch_t(const CacheAttnArgs& a, cudaStream_t stream) {
   using C = Cfg<D, PAIR>;
   auto kern = cache_tile_kernel<D, FMT, BF16, PAIR>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(kern, C::BYTES, done);
+  const cudaError_t e = allow_smem(kern, C::BYTES, done);
   if (e != cudaSuccess) return e;
-  if ((e = launch_dependent(kern, dim3(a.sm_count), dim3(kThreads), C::BYTES, stream, a)) != cudaSuccess) return e;
-  return launch_cache_merge<D, BF16, C::R, kTK, C::MIN_TILES>(a, stream);
+  return launch_dependent(kern, dim3(a.sm_count), dim3(kThreads), C::BYTES, stream, a);
 }
 
 template <int D, int FMT, bool BF16>

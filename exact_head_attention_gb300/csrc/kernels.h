@@ -153,7 +153,8 @@ struct CacheAttnArgs {
   RowStrides sq, so;
   const int* lens;
   float* lse;     // [B][heads * group][Nq]
-  uint8_t* ws;    // cache_ws_* below
+  uint8_t* ws;    // cache_sched.cuh
+  unsigned long long tag;  // of this call's flags in ws
   uint32_t* err_word;
   int B, Nq, group, mask, sm_count;
   bool bf16;
@@ -226,6 +227,6 @@ struct CacheAttnShape {
   int rows, keys;
 };
 CacheAttnShape cache_attn_shape(long long rows, int d);
-size_t cache_attn_workspace(int B, long long rows, int d, int sm_count);
+size_t cache_attn_workspace(long long rows, int d, int sm_count);
 
 }  // namespace exattn
