@@ -30,11 +30,11 @@ namespace exattn {
 // workspace needs no preparation: what lies there before is taken for a flag only if it equals a 64-bit
 // tag drawn for the call, and a captured call, whose tag is the same at each replay, finds zeros.
 
-// Workspace: flags, then the slots (fp32 rows of D values, normalised by the piece's own sum) and their
-// base-2 log-sum-exps.  Flags and log-sum-exps are kept twice, for the two warpgroups of cache_tile.cu.
+// Workspace: flags, then the slots (R rows of D values in fp32, normalised by the piece's own sum, in an order
+// that each kernel chooses) and their base-2 log-sum-exps.  Flags and log-sum-exps are kept twice, for the two warpgroups of cache_tile.cu.
 struct CacheWs {
   unsigned long long* flag;  // [slots][2]
-  float* o;                  // [slots][R][D]
+  float* o;                  // [slots][R * D]
   float* l;                  // [slots][2][R]
 };
 
@@ -115,16 +115,16 @@ constexpr int kPieceInts = 12;
 // piece's flag; true where every piece of the item is then there, and their flags are zero again.
 __device__ __forceinline__ bool cache_piece_done(const CacheWs& ws, const CachePiece& p, int part, unsigned long long tag) {
   const int lane = threadIdx.x & 31;
-  __threadfence();
-  if (lane == 0) atomicExch(ws.flag + 2 * p.slot + part, tag);
+  asm volatile("fence.acq_rel.gpu;" ::: "memory");  // the partial result, before its flag
+  if (lane == 0) *reinterpret_cast<volatile unsigned long long*>(ws.flag + 2 * p.slot + part) = tag;
   __syncwarp();
-  __threadfence();
+  asm volatile("fence.sc.gpu;" ::: "memory");  // of two blocks that set their flags, one at least sees both
   const int n = p.pieces();
   bool all = true;
   for (int i = lane; i < n; i += 32) all = all && *reinterpret_cast<volatile unsigned long long*>(ws.flag + 2 * p.slot_of(i) + part) == tag;
   all = __all_sync(0xffffffffu, all);
   if (all) {
-    __threadfence();  // the other blocks' partial results are read after their flags
+    asm volatile("fence.acq_rel.gpu;" ::: "memory");  // the other blocks' partial results, after their flags
     for (int i = lane; i < n; i += 32) ws.flag[2 * p.slot_of(i) + part] = 0ull;
   }
   return all;

@@ -238,43 +238,46 @@ __device__ __forceinline__ void softmax_scaled(uint32_t tS, uint32_t tO, const f
   l += s0 + s1;
 }
 
-// A query row in fp16 into an operand tile, 16-byte units [u0, u1) of it (all chunks together), times a power
-// of two where it is bf16; returns the factor that undoes it.  A row that is not there is zero.
-template <int D, bool BF16>
-__device__ __forceinline__ float stage_query_row(const uint16_t* src, bool there, uint32_t tile, int r, int u0, int u1) {
-  float mul = 1.f, back = 1.f;
-  const uint4* s = reinterpret_cast<const uint4*>(src);
-  if constexpr (BF16) {
-    uint32_t mx = 0u;
-    if (there) {
+// A warp's 32 query rows in fp16 into an operand tile (rows tile_row ..), 16-byte units [u0, u1) of each, times
+// a power of two where they are bf16.  Returns, for row `lane`, the factor that undoes it.  Lanes stand side by
+// side over a row's units, so that the loads are whole lines; row_at(r) is where row r lies, nullptr a row that
+// is not there, which becomes zero.
+template <int D, bool BF16, typename RowAt>
+__device__ __forceinline__ float stage_query_rows(RowAt&& row_at, uint32_t tile, int tile_row, int u0, int u1) {
+  constexpr int UNITS = D / 8, ROWS = 32 / UNITS;  // units a row, rows a step
+  const int lane = threadIdx.x & 31, u = lane % UNITS;
+  float back = 1.f;
+  constexpr int BATCH = 8;  // steps whose rows are loaded together, so that their latencies overlap
+#pragma unroll 1
+  for (int kb = 0; kb < 32; kb += BATCH * ROWS) {
+    uint4 xs[BATCH];
 #pragma unroll
-      for (int u = 0; u < D / 8; ++u) {
-        const uint4 x = __ldg(s + u);
-        mx = __vmaxu2(__vmaxu2(mx, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
-        mx = __vmaxu2(__vmaxu2(mx, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
+    for (int i = 0; i < BATCH; ++i) {
+      const uint16_t* src = row_at(kb + i * ROWS + lane / UNITS);
+      xs[i] = src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src) + u) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int k = kb + i * ROWS, r = k + lane / UNITS;
+      uint4 x = xs[i];
+      if constexpr (BF16) {
+        uint32_t mx = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+        mx = max(mx & 0xffffu, mx >> 16);
+#pragma unroll
+        for (int o = 1; o < UNITS; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        // As in cache_attn.cu: the largest value comes to lie in [2^14, 2^15).
+        const int e = static_cast<int>(mx >> 7) - 127;
+        const int p = mx != 0u && e < 128 ? min(14 - e, 113) : 0;
+        const float mul = __int_as_float((127 + p) << 23);
+        x.x = pack2<false>(unpack_lo<true>(x.x) * mul, unpack_hi<true>(x.x) * mul);
+        x.y = pack2<false>(unpack_lo<true>(x.y) * mul, unpack_hi<true>(x.y) * mul);
+        x.z = pack2<false>(unpack_lo<true>(x.z) * mul, unpack_hi<true>(x.z) * mul);
+        x.w = pack2<false>(unpack_lo<true>(x.w) * mul, unpack_hi<true>(x.w) * mul);
+        const int q = __shfl_sync(0xffffffffu, p, (lane % ROWS) * UNITS);  // of row k + lane % ROWS
+        if (lane / ROWS == k / ROWS) back = __int_as_float((127 - q) << 23);
       }
+      if (u >= u0 && u < u1) st_shared_v4(tile + (u >> 3) * kChunk + sw128_offset(tile_row + r, u & 7), x.x, x.y, x.z, x.w);
     }
-    mx = max(mx & 0xffffu, mx >> 16);
-    // As in cache_attn.cu: the largest value comes to lie in [2^14, 2^15).
-    const int e = static_cast<int>(mx >> 7) - 127;
-    if (mx != 0u && e < 128) {
-      const int k = min(14 - e, 113);
-      mul = __int_as_float((127 + k) << 23);
-      back = __int_as_float((127 - k) << 23);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < D / 8; ++u) {
-    if (u < u0 || u >= u1) continue;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (there) x = __ldg(s + u);
-    if constexpr (BF16) {
-      x.x = pack2<false>(unpack_lo<true>(x.x) * mul, unpack_hi<true>(x.x) * mul);
-      x.y = pack2<false>(unpack_lo<true>(x.y) * mul, unpack_hi<true>(x.y) * mul);
-      x.z = pack2<false>(unpack_lo<true>(x.z) * mul, unpack_hi<true>(x.z) * mul);
-      x.w = pack2<false>(unpack_lo<true>(x.w) * mul, unpack_hi<true>(x.w) * mul);
-    }
-    st_shared_v4(tile + (u >> 3) * kChunk + sw128_offset(r, u & 7), x.x, x.y, x.z, x.w);
   }
   return back;
 }
@@ -647,10 +650,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           // The previous piece's score products have completed: this chain's with its o_full, the other's
           // with the join that ended its epilogue.
           const Row w = row_of(p);
-          const uint16_t* src = static_cast<const uint16_t*>(a.q) + p.b * a.sq.b + w.hq * a.sq.h + w.tok * a.sq.n;
-          const uint32_t tile = sbase + C::OFF_Q + (PAIR ? t * C::TILE : 0);
-          const float back = PAIR ? stage_query_row<D, BF16>(src, w.there, tile, r, 0, D / 8)
-                                  : stage_query_row<D, BF16>(src, w.there, tile, r, t * (D / 16), (t + 1) * (D / 16));
+          auto row_at = [&](int k) -> const uint16_t* {
+            const int row = row_first + k, tok = row / a.group;
+            if (row >= rows) return nullptr;
+            return static_cast<const uint16_t*>(a.q) + p.b * a.sq.b +
+                   (static_cast<long long>(p.head) * a.group + row - tok * a.group) * a.sq.h + tok * a.sq.n;
+          };
+          const float back = stage_query_rows<D, BF16>(row_at, sbase + C::OFF_Q + (PAIR ? t * C::TILE : 0), quarter * 32,
+                                                       PAIR ? 0 : t * (D / 16), PAIR ? D / 8 : (t + 1) * (D / 16));
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bars.q_full(t));
@@ -707,9 +714,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         const int c0 = PAIR ? 0 : t * COLS;
         const Row w = row_of(p);
         const int slot = p.slot;
+        // A partial result lies column by column, four at a time, so that the lanes (rows) stand side by side.
+        auto part_of = [&](int slot) {
+          return reinterpret_cast<float4*>(ws.o) + (static_cast<size_t>(slot) * (D / 4) + c0 / 4) * C::R + ri;
+        };
         if (!idle) {
           uint16_t* dst = out_row(p, w) + c0;
-          float4* part = reinterpret_cast<float4*>(ws.o + (static_cast<size_t>(max(slot, 0)) * C::R + ri) * D + c0);
+          float4* part = part_of(max(slot, 0));
           const uint32_t at0 = PAIR ? tO : tmem + 256 + lane_bits;
 #pragma unroll 1
           for (int c = 0; c < COLS; c += 16) {
@@ -724,35 +735,31 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
 #pragma unroll
               for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * w0);
             }
-            if (w.there) {
-              if (slot < 0) {
+            if (slot >= 0) {
 #pragma unroll
-                for (int e = 0; e < 16; e += 8) {
-                  uint32_t z[4];
+              for (int e = 0; e < 16; e += 4)
+                part[(c + e) / 4 * C::R] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]), __uint_as_float(x[e + 2]),
+                                                       __uint_as_float(x[e + 3]));
+            } else if (w.there) {
 #pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    z[k] = pack2<BF16>(__uint_as_float(x[e + 2 * k]), __uint_as_float(x[e + 2 * k + 1]));
-                  *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(z[0], z[1], z[2], z[3]);
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 16; e += 4)
-                  part[(c + e) / 4] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]), __uint_as_float(x[e + 2]),
-                                                  __uint_as_float(x[e + 3]));
-              }
+              for (int e = 0; e < 16; e += 8)
+                *reinterpret_cast<uint4*>(dst + c + e) =
+                    make_uint4(pack2<BF16>(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                               pack2<BF16>(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])),
+                               pack2<BF16>(__uint_as_float(x[e + 4]), __uint_as_float(x[e + 5])),
+                               pack2<BF16>(__uint_as_float(x[e + 6]), __uint_as_float(x[e + 7])));
             }
           }
-          if (w.there) {
-            if (slot >= 0)
-              ws.l[(static_cast<size_t>(slot) * 2 + t) * C::R + ri] = lse2;
-            else if (PAIR || t == 0)
-              *out_lse(p, w) = lse2 * 0.6931471805599453f;
-          }
+          if (slot >= 0)
+            ws.l[(static_cast<size_t>(slot) * 2 + t) * C::R + ri] = lse2;
+          else if (w.there && (PAIR || t == 0))
+            *out_lse(p, w) = lse2 * 0.6931471805599453f;
         }
         tc_fence_before();
 
         // ------------------------------------------------------------ merge, where this piece completes its item
-        // Each warpgroup for itself: it has its own rows (PAIR) or columns.
+        // Each warpgroup for itself: it has its own rows (PAIR) or columns.  (What runs once a piece is kept short: its
+        // instructions come from far each time.)
         if (slot >= 0) {
           if (!(ok = stored())) break;
           if (quarter == 0) {
@@ -760,72 +767,51 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
             if (lane == 0) merge_flag[t] = all;
           }
           if (!(ok = stored())) break;
-          if (merge_flag[t]) {
-            // L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s over a row's pieces in key order.  A warp has 32 rows: lane k
-            // works out row k's weights, then the lanes stand side by side over the columns of eight rows at a time.
-            constexpr int V = COLS / 32;  // columns a lane: 1, 2 or 4
-            const int np = p.pieces(), nr = min(32, rows - row_first);
-            auto lse_at = [&](int i) { return __ldcg(ws.l + (static_cast<size_t>(p.slot_of(i)) * 2 + t) * C::R + ri); };
-            float ms = 0.f, inv = 0.f;
-            if (w.there) {
-              float mx = -INFINITY, sum = 0.f;
-#pragma unroll 4
-              for (int i = 0; i < np; ++i) {
-                const float L = lse_at(i), to = fmaxf(mx, L), mt = to == -INFINITY ? 0.f : to;
-                sum = fmaf(sum, mx == -INFINITY ? 0.f : ex2_approx(mx - mt), ex2_approx(L - mt));  // a NaN counts
-                mx = to;
-              }
-              ms = mx == -INFINITY ? 0.f : mx;
-              inv = sum == 0.f ? 0.f : 1.f / sum;
-              if (PAIR || t == 0) *out_lse(p, w) = sum == 0.f ? -INFINITY : (ms + __log2f(sum)) * 0.6931471805599453f;
-            }
+          if (merge_flag[t] && !idle) {
+            // L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s over the row's pieces in key order.
+            const int np = p.pieces();
+            auto lse_at = [&](int s) { return __ldcg(ws.l + (static_cast<size_t>(s) * 2 + t) * C::R + ri); };
+            float mx = -INFINITY, sum = 0.f;
 #pragma unroll 1
-            for (int kb = 0; kb < nr; kb += 8) {
-              float acc[8][V];
+            for (int i = 0; i < np; ++i) {
+              const float L = lse_at(p.slot_of(i)), to = fmaxf(mx, L), mt = to == -INFINITY ? 0.f : to;
+              sum = fmaf(sum, mx == -INFINITY ? 0.f : ex2_approx(mx - mt), ex2_approx(L - mt));  // a NaN counts
+              mx = to;
+            }
+            const float ms = mx == -INFINITY ? 0.f : mx, inv = sum == 0.f ? 0.f : 1.f / sum;
+            uint16_t* dst = out_row(p, w) + c0;
+            constexpr int CH = COLS < 64 ? COLS : 64;  // columns whose loads are under way together
+#pragma unroll 1
+            for (int c = 0; c < COLS; c += CH) {
+              float4 acc[CH / 4];
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-#pragma unroll
-                for (int e = 0; e < V; ++e) acc[k][e] = 0.f;
-#pragma unroll 2
+              for (int e = 0; e < CH / 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
               for (int i = 0; i < np; ++i) {
-                const float wi = w.there ? ex2_approx(lse_at(i) - ms) * inv : 0.f;
-                // rows past the last one lie in the slot all the same
-                const float* src = ws.o + (static_cast<size_t>(p.slot_of(i)) * C::R + (ri - lane + kb)) * D + c0 + lane * V;
-                float x[8][V];
+                const int s = p.slot_of(i);
+                const float4* src = part_of(s) + c / 4 * C::R;
+                float4 x[CH / 4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  if constexpr (V == 4) {
-                    const float4 y = __ldcg(reinterpret_cast<const float4*>(src + k * D));
-                    x[k][0] = y.x;
-                    x[k][1] = y.y;
-                    x[k][2] = y.z;
-                    x[k][3] = y.w;
-                  } else {
+                for (int e = 0; e < CH / 4; ++e) x[e] = __ldcg(src + e * C::R);
+                const float wi = ex2_approx(lse_at(s) - ms) * inv;
 #pragma unroll
-                    for (int e = 0; e < V; ++e) x[k][e] = __ldcg(src + k * D + e);
-                  }
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float wk = __shfl_sync(0xffffffffu, wi, kb + k);
-#pragma unroll
-                  for (int e = 0; e < V; ++e) acc[k][e] = fmaf(wk, x[k][e], acc[k][e]);
+                for (int e = 0; e < CH / 4; ++e) {
+                  acc[e].x = fmaf(wi, x[e].x, acc[e].x);
+                  acc[e].y = fmaf(wi, x[e].y, acc[e].y);
+                  acc[e].z = fmaf(wi, x[e].z, acc[e].z);
+                  acc[e].w = fmaf(wi, x[e].w, acc[e].w);
                 }
               }
+              if (w.there) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                if (kb + k >= nr) break;
-                const int row = row_first + kb + k, tok = row / a.group;
-                const Row wk{true, tok, p.head * a.group + row - tok * a.group};
-                uint16_t* dst = out_row(p, wk) + c0 + lane * V;
-                if constexpr (V == 4)
-                  *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(acc[k][0], acc[k][1]), pack2<BF16>(acc[k][2], acc[k][3]));
-                else if constexpr (V == 2)
-                  *reinterpret_cast<uint32_t*>(dst) = pack2<BF16>(acc[k][0], acc[k][1]);
-                else
-                  *dst = static_cast<uint16_t>(pack2<BF16>(acc[k][0], 0.f));
+                for (int e = 0; e < CH / 4; e += 2)
+                  *reinterpret_cast<uint4*>(dst + c + 4 * e) =
+                      make_uint4(pack2<BF16>(acc[e].x, acc[e].y), pack2<BF16>(acc[e].z, acc[e].w),
+                                 pack2<BF16>(acc[e + 1].x, acc[e + 1].y), pack2<BF16>(acc[e + 1].z, acc[e + 1].w));
               }
             }
+            if (w.there && (PAIR || t == 0))
+              *out_lse(p, w) = sum == 0.f ? -INFINITY : (ms + __log2f(sum)) * 0.6931471805599453f;
           }
         }
         // O_t, the statistics and the query tile are free once both warpgroups are here.
