@@ -8,12 +8,15 @@
 // tensor memory.  Its operands are fp16 in shared memory, so six warps turn each 128-token tile of codes, copied
 // in by the copy engine, into the swizzled operand tiles; 256 query rows share that work.
 //
-// Two chains of (scores, softmax, product) alternate on the tensor cores, one softmax warpgroup each, in the
-// order S0[0] S1[0] | PV0[j] S0[j+1] PV1[j] S1[j+1] | ..., so that one chain's softmax hides behind the other's
-// products:
+// Two chains of (scores, softmax, product) alternate on the tensor cores, one softmax warpgroup each:
 //   PAIR    more than 128 rows: an item has 256, chain t works on rows [128 t, 128 t + 128)
 //   else    an item has 128 rows, and chain t works on every second key tile; the two results are joined in
 //           the epilogue.  Both chains then have work at any number of rows.
+// The chains' steps (one 128-token tile of one chain) form one sequence, and step i has score buffer i mod NB,
+// which its P overwrites: S[0] .. S[NB-1] | O[0] S[NB] O[1] S[NB+1] ...  At d = 64 tensor memory has room for three
+// buffers, so that a chain's next scores are there when its softmax has finished a step; at d = 128 for two.
+// Steps of 64 keys with two buffers a chain were tried for d = 128: a score product of 64 columns takes as long as one
+// of 128 (72 cycles for each 16 positions), and the whole became 1.4 times slower.
 //
 // Warp roles (512 threads, registers re-split per warpgroup):
 //   warps 0-3, 4-7  softmax of chain 0 and 1 (thread = query row = TMEM lane); they also bring the query rows
@@ -21,8 +24,8 @@
 //   warp  8         MMA issuer (one thread) and TMEM owner
 //   warp  9         producer: walks the block's pieces (cache_sched.cuh), looks pages up, copies codes
 //   warps 10-12, 13-15  converters of the keys and of the values, about 43 tokens of each tile apiece
-// Tensor memory: S_t (P_t over its first 64 columns) at 128 t, O_t at 256 + 128 t.
-// Every role walks the same pieces and counts tiles on, so the barriers are never re-armed.
+// Tensor memory: score buffer b (P over its first 64 columns) at 128 b, O_t behind the buffers.
+// Every role walks the same pieces and counts steps on, so the barriers are never re-armed.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -40,7 +43,7 @@ constexpr uint32_t kRegsSoftmax = 176, kRegsOther = 80;
 static_assert(2 * kRegsSoftmax + 2 * kRegsOther == 4 * 128, "register split must match the launch");
 constexpr int kTK = 128;
 constexpr uint32_t kChunk = 128 * 128;  // 128 rows x 128 bytes
-constexpr int kPieceRing = 3, kMetaRing = 8;
+constexpr int kPieceRing = 3, kMetaRing = 16;
 constexpr float kShift = 3.f, kVrefLag = 16.f;  // as in cache_attn.cu
 
 template <int D, bool PAIR>
@@ -51,8 +54,12 @@ struct Cfg {
   static constexpr uint32_t RAW = 128 * D;                     // a tile of codes
   static constexpr int NS = D == 128 ? 2 : 3;                  // K and V operand slots
   static constexpr int NR = D == 128 ? (PAIR ? 2 : 3) : 4;     // slots of codes, K and V in turn
-  // Scales stay in use from a tile's copy to its softmax: NS + NR / 2 + 2 tiles at most.
-  static_assert(NS + (NR + 1) / 2 + 2 <= kMetaRing, "scales of the tiles under way");
+  static constexpr int NB = D == 64 ? 3 : 2;                   // score buffers
+  // Scales stay in use from a tile's copy to its softmax, over tiles of codes, operand tiles, and steps under way.
+  static_assert((NR + 1) / 2 + NS + NB + 1 <= kMetaRing, "scales of the tiles under way");
+  static constexpr uint32_t TM_O = NB * 128;                   // O_t at TM_O + t TM_OT
+  static constexpr uint32_t TM_OT = D;
+  static_assert(TM_O + 2 * TM_OT <= 512, "tensor memory");
   using Walk = CacheWalk<R, kTK, 32, MIN_TILES>;
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_K = OFF_Q + (PAIR ? 2 : 1) * TILE;
@@ -62,7 +69,7 @@ struct Cfg {
   static constexpr uint32_t OFF_STAT = OFF_META + kMetaRing * 64;    // !PAIR: {m, l} [2][128], vref [2][4]
   static constexpr uint32_t OFF_PIECE = OFF_STAT + (PAIR ? 0 : 2 * 128 * 8 + 32);
   static constexpr uint32_t OFF_BAR = OFF_PIECE + kPieceRing * kPieceInts * 4;
-  static constexpr int NBAR = 2 + 4 * NS + 2 * NR + 6 + kMetaRing + 2 * kPieceRing + 4;
+  static constexpr int NBAR = 2 + 4 * NS + 2 * NR + 8 + kMetaRing + 2 * kPieceRing + 4;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t OFF_SCHED = OFF_MISC + 16;
   static constexpr uint32_t BYTES = OFF_SCHED + sizeof(typename Walk::Shared);
@@ -107,24 +114,26 @@ struct Bars {
   __device__ uint32_t raw_full(int s) const { return at(2 + 4 * NS + s); }
   __device__ uint32_t raw_empty(int s) const { return at(2 + 4 * NS + NR + s); }
   static constexpr int kB = 2 + 4 * NS + 2 * NR;
-  __device__ uint32_t s_full(int t) const { return at(kB + t); }
-  __device__ uint32_t p_full(int t) const { return at(kB + 2 + t); }
-  __device__ uint32_t o_full(int t) const { return at(kB + 4 + t); }
-  __device__ uint32_t meta_full(int s) const { return at(kB + 6 + s); }
-  __device__ uint32_t piece_full(int s) const { return at(kB + 6 + kMetaRing + s); }
-  __device__ uint32_t piece_empty(int s) const { return at(kB + 6 + kMetaRing + kPieceRing + s); }
-  __device__ uint32_t join() const { return at(kB + 6 + kMetaRing + 2 * kPieceRing); }
-  __device__ uint32_t mma_done() const { return at(kB + 7 + kMetaRing + 2 * kPieceRing); }
-  __device__ uint32_t stored(int t) const { return at(kB + 8 + kMetaRing + 2 * kPieceRing + t); }
+  __device__ uint32_t s_full(int b) const { return at(kB + b); }
+  __device__ uint32_t p_full(int b) const { return at(kB + 3 + b); }
+  __device__ uint32_t pv_done(int t) const { return at(kB + 6 + t); }
+  static constexpr int kC = kB + 8;
+  __device__ uint32_t meta_full(int s) const { return at(kC + s); }
+  __device__ uint32_t piece_full(int s) const { return at(kC + kMetaRing + s); }
+  __device__ uint32_t piece_empty(int s) const { return at(kC + kMetaRing + kPieceRing + s); }
+  __device__ uint32_t join() const { return at(kC + kMetaRing + 2 * kPieceRing); }
+  __device__ uint32_t mma_done() const { return at(kC + 1 + kMetaRing + 2 * kPieceRing); }
+  __device__ uint32_t stored(int t) const { return at(kC + 2 + kMetaRing + 2 * kPieceRing + t); }
 };
 
 // One key tile of the online softmax for this thread's query row.  Scores of the 16-token group g count
 // fac * ks[g]; P goes out in fp16 times vs[g] / vref (sc: ks[8], vs[8]).  Columns at or past `lim` are hidden
 // (MASKED).  All 128 scores are read for the maximum; the upper 64 are read again for P, which saves the
 // registers that they would hold meanwhile.  P's packed columns overwrite scores of the lower 64 only.
-template <int D, bool MASKED>
+// wait_pv() runs (warp-uniformly) before O is rescaled: the chain's last product may still be under way.
+template <int D, bool MASKED, typename WaitPv>
 __device__ __forceinline__ void softmax_scaled(uint32_t tS, uint32_t tO, const float* sc, int lim, float fac, bool first,
-                                               float& m, float& l, float& vref, float& vinv) {
+                                               float& m, float& l, float& vref, float& vinv, WaitPv&& wait_pv) {
   uint32_t sr[4][32];
 #pragma unroll
   for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
@@ -174,7 +183,7 @@ __device__ __forceinline__ void softmax_scaled(uint32_t tS, uint32_t tO, const f
       vinv = v > 0.f ? 1.0f / v : 0.f;
     }
     if (!first) {
-      // O is complete for the previous key tile of this chain: S was issued after its last product.
+      wait_pv();
 #pragma unroll 1
       for (int c = 0; c < D / 16; ++c) {
         uint32_t o[16];
@@ -347,10 +356,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     *abort_flag = 0u;
     for (int t = 0; t < 2; ++t) {
       mbar_init(bars.q_full(t), 4);
-      mbar_init(bars.s_full(t), 1);
-      mbar_init(bars.p_full(t), 4);
-      mbar_init(bars.o_full(t), 1);
+      mbar_init(bars.pv_done(t), 1);
       mbar_init(bars.stored(t), 4);
+    }
+    for (int b = 0; b < C::NB; ++b) {
+      mbar_init(bars.s_full(b), 1);
+      mbar_init(bars.p_full(b), 4);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(bars.k_full(s), 3);
@@ -391,10 +402,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     const CachePiece* p = pieces + i % kPieceRing;
     return p->b >= 0 ? p : nullptr;
   };
-  // Key tiles of chain t in a piece.
-  auto chain_tiles = [&](const CachePiece& p, int t) {
+  // Whether both chains have steps in a piece, and the steps of chain t.
+  auto both_chains = [&](const CachePiece& p) { return PAIR ? rows - p.rt * C::R > 128 : p.end - p.begin > 1; };
+  auto chain_steps = [&](const CachePiece& p, int t) {
     const int n = p.end - p.begin;
-    if (PAIR) return t == 0 || rows - p.rt * C::R > 128 ? n : 0;
+    if (PAIR) return t == 0 || both_chains(p) ? n : 0;
     return t == 0 ? (n + 1) / 2 : n / 2;
   };
 
@@ -507,46 +519,53 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       const Bars<NS, NR> ub{ubase + C::OFF_BAR};
       const uint32_t q_lo = sdesc_lo(ubase + C::OFF_Q, 16), k_lo = sdesc_lo(ubase + C::OFF_K, 16),
                      v_lo = sdesc_lo(ubase + C::OFF_V, kChunk);
-      int ks = 0, vs = 0;            // next slots of K and V ...
-      uint32_t kph = 0, vph = 0;     // ... and the parities of their waits
-      uint32_t phase_p = 0;          // bit t: parity of the next wait of p_full(t)
-      uint32_t q0 = 0, q1 = 0;
+      constexpr int NB = C::NB;
+      int ks = 0, vs = 0, sb = 0, pb = 0;                       // next slots of K and V, next buffers of S and P ...
+      uint32_t kph = 0, vph = 0, pph = 0, q0 = 0, q1 = 0;  // ... and the parities of their waits; waits of q_full
       bool ok = true;
       const CachePiece* p;
       for (int pi = 0; ok && (p = next_piece(pi)) != nullptr; ++pi) {
-        const int n0 = __shfl_sync(0xffffffffu, chain_tiles(*p, 0), 0), n1 = __shfl_sync(0xffffffffu, chain_tiles(*p, 1), 0);
-        const bool both = n1 > 0;
+        const int n = __shfl_sync(0xffffffffu, chain_steps(*p, 0) + chain_steps(*p, 1), 0);  // steps of the piece
+        const bool both = __shfl_sync(0xffffffffu, both_chains(*p), 0);
+        const bool shared = PAIR && both;  // a tile has two steps, one of each chain, else one
         // the query tiles: each chain's own, or halves of one from both warpgroups
         ok = mbar_wait_warp(ub.q_full(0), q0++ & 1, wc);
         if (ok && (!PAIR || both)) ok = mbar_wait_warp(ub.q_full(1), q1++ & 1, wc);
-        // step i: chain t = i & 1 (or 0 alone), O_t += P_t V of its key tile j - 1, then S_t of its key tile j
-        const int last = both ? 2 * n0 + 1 : 2 * n0;
 #pragma unroll 1
-        for (int i = 0; ok && i <= last; i += both ? 1 : 2) {
-          const int t = i & 1, j = i >> 1, nt = t ? n1 : n0;
-          const bool slot_ends = !PAIR || t == 1 || !both;  // this chain is its slots' last reader
-          if (j > 0 && j <= nt) {
-            if (!(ok = mbar_wait_warp(ub.v_full(vs), vph, wc))) break;
-            if (!(ok = mbar_wait_warp(ub.p_full(t), (phase_p >> t) & 1, wc))) break;
-            phase_p ^= 1u << t;
+        for (int i = 0; ok && i < n + NB; ++i) {
+          if (i >= NB) {  // O_t += P V of step i - NB
+            const int j = i - NB, t = both ? j & 1 : 0;
+            if (!shared || t == 0) {
+              if (!(ok = mbar_wait_warp(ub.v_full(vs), vph, wc))) break;
+            }
+            if (!(ok = mbar_wait_warp(ub.p_full(pb), pph, wc))) break;
             tc_fence_after();
-            const uint32_t d = utmem + 256 + t * 128, pa = utmem + t * 128, b_lo = v_lo + vs * kTileLo;
+            const uint32_t d = utmem + C::TM_O + t * C::TM_OT, pa = utmem + pb * 128, b_lo = v_lo + vs * kTileLo;
+            const bool slot_ends = !shared || t == 1, last = j + (both ? 2 : 1) >= n;
             if (elect_one()) {
-              mma_ts_lo_rt(d, pa, b_lo, idPV, j - 1);
+              mma_ts_lo_rt(d, pa, b_lo, idPV, both ? j >> 1 : j);
 #pragma unroll
               for (int k = 1; k < kTK / 16; ++k) mma_ts_lo<true>(d, pa + k * 8, b_lo + k * (2048 >> 4), idPV);
+              if (NB > 2 || last) mma_commit(ub.pv_done(t));
               if (slot_ends) mma_commit(ub.v_empty(vs));
-              if (j == nt) mma_commit(ub.o_full(t));
             }
             if (slot_ends && ++vs == NS) {
               vs = 0;
               vph ^= 1;
             }
+            if (++pb == NB) {
+              pb = 0;
+              pph ^= 1;
+            }
           }
-          if (j < nt) {
-            if (!(ok = mbar_wait_warp(ub.k_full(ks), kph, wc))) break;
-            tc_fence_after();
-            const uint32_t d = utmem + t * 128, a_lo = q_lo + (PAIR ? t * kTileLo : 0), b_lo = k_lo + ks * kTileLo;
+          if (i < n) {  // the scores of step i
+            const int t = both ? i & 1 : 0;
+            if (!shared || t == 0) {
+              if (!(ok = mbar_wait_warp(ub.k_full(ks), kph, wc))) break;
+              tc_fence_after();
+            }
+            const uint32_t d = utmem + sb * 128, a_lo = q_lo + (PAIR ? t * kTileLo : 0), b_lo = k_lo + ks * kTileLo;
+            const bool slot_ends = !shared || t == 1;
             if (elect_one()) {
               mma_ss_lo<false>(d, a_lo, b_lo, idS);
 #pragma unroll
@@ -554,13 +573,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
                 const uint32_t off = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
                 mma_ss_lo<true>(d, a_lo + off, b_lo + off, idS);
               }
-              mma_commit(ub.s_full(t));
+              mma_commit(ub.s_full(sb));
               if (slot_ends) mma_commit(ub.k_empty(ks));
             }
             if (slot_ends && ++ks == NS) {
               ks = 0;
               kph ^= 1;
             }
+            if (++sb == NB) sb = 0;
           }
         }
         __syncwarp();
@@ -604,12 +624,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     const int t = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // row of the operand tile = TMEM lane
     const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t tS = tmem + t * 128 + lane_bits, tO = tmem + 256 + t * 128 + lane_bits;
+    const uint32_t tS = tmem + lane_bits /* buffer 0 */, tO = tmem + C::TM_O + t * C::TM_OT + lane_bits;
     const CacheWs ws = cache_ws(a.ws, C::R, D, a.sm_count);
     float2* stat = reinterpret_cast<float2*>(smem_raw + C::OFF_STAT);
     float* stat_v = reinterpret_cast<float*>(smem_raw + C::OFF_STAT + 2 * 128 * 8);
+    constexpr int NB = C::NB;
     int kt = 0;
-    uint32_t sc = 0, oc_own = 0, oc_other = 0, jc = 0, dc = 0;  // waits of s_full, of both o_full, of join, of stored
+    uint32_t seq = 0;                        // steps of both chains in earlier pieces
+    uint32_t own = 0, other = 0, jc = 0, dc = 0;  // completions of either pv_done so far; waits of join and stored
     bool ok = true;
     const int ri = (PAIR ? t * 128 : 0) + r;  // row of the item
     // Both softmax warpgroups meet (!PAIR), or one.  Bounded waits: after a failed one elsewhere these give up too.
@@ -641,7 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     const CachePiece* pp;
     for (int pi = 0; ok && (pp = next_piece(pi)) != nullptr; ++pi) {
       const CachePiece& p = *pp;
-      const int n = chain_tiles(p, t);
+      const int n = chain_steps(p, t);
+      const bool both = both_chains(p);
       if (!PAIR || n > 0) {
         const int row_first = p.rt * C::R + ri - lane;  // of this warp
         const bool idle = row_first >= rows;            // a warp of rows that are not there
@@ -667,24 +690,40 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           // the least of this warp's rows
           const int lim_min = cache_row_limit(a.mask, p.len, a.Nq, min(row_first, rows - 1) / a.group) - key_first;
           for (int j = 0; j < n; ++j) {
-            const int i = PAIR ? j : 2 * j + t, nt = kt + i;
-            if (!(ok = mbar_wait_warp(bars.s_full(t), sc++ & 1, wc))) break;
+            const int i = PAIR ? j : 2 * j + t, nt = kt + i;  // key tile
+            const uint32_t g = seq + (both ? 2 * j + t : j), b = g % NB;
+            if (!(ok = mbar_wait_warp(bars.s_full(b), (g / NB) & 1, wc))) break;
             if (!(ok = mbar_wait_warp(bars.meta_full(nt % kMetaRing), (nt / kMetaRing) & 1, wc))) break;
             tc_fence_after();
             if (!idle) {
               const float* scales = meta + (nt % kMetaRing) * 16;
+              // The chain's last product: with two buffers these scores were issued after it.  With three they came
+              // after the one before it, so that the parity says which of the two completions there are.
+              auto wait_pv = [&] {
+                if (NB > 2) {
+                  if (!mbar_wait_warp(bars.pv_done(t), (own + j - 1) & 1, wc)) ok = false;
+                  tc_fence_after();
+                }
+              };
               if ((i + 1) * kTK > lim_min)
-                softmax_scaled<D, true>(tS, tO, scales, lim_row - i * kTK, fac, j == 0, m, l, vref, vinv);
+                softmax_scaled<D, true>(tS + b * 128, tO, scales, lim_row - i * kTK, fac, j == 0, m, l, vref, vinv, wait_pv);
               else
-                softmax_scaled<D, false>(tS, tO, scales, kTK, fac, j == 0, m, l, vref, vinv);
+                softmax_scaled<D, false>(tS + b * 128, tO, scales, kTK, fac, j == 0, m, l, vref, vinv, wait_pv);
               tmem_wait_st();
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars.p_full(t));
+            if (lane == 0) mbar_arrive(bars.p_full(b));
+            if (!ok) break;
           }
         }
-        if (ok && n > 0) ok = mbar_wait_warp(bars.o_full(t), oc_own++ & 1, wc);
+        // Completions of pv_done: of every step, or (two buffers) of the last one of a piece.  The last two may be
+        // under way, and a parity tells two neighbouring completions apart, no more.
+        if (n > 0) {
+          if (NB > 2 && ok && n > 1) ok = mbar_wait_warp(bars.pv_done(t), (own + n - 2) & 1, wc);
+          own += NB > 2 ? n : 1;
+          if (ok) ok = mbar_wait_warp(bars.pv_done(t), (own - 1) & 1, wc);
+        }
 
         // ------------------------------------------------------------ epilogue
         float w0 = 0.f, w1 = 0.f, lse2;  // factors of O_0 and O_1 (PAIR: of O_t)
@@ -695,10 +734,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         } else {
           stat[t * 128 + r] = make_float2(m, l);
           if (lane == 0) stat_v[t * 4 + quarter] = vref;
+          tc_fence_before();
           if (!(ok = ok && join())) break;
-          use1 = chain_tiles(p, 1) > 0;
-          if (t == 1 || use1) ok = mbar_wait_warp(bars.o_full(1 - t), oc_other++ & 1, wc);
-          if (!ok) break;
+          use1 = both;
+          // The other chain has seen its products completed before it joined.
+          if (const int no = chain_steps(p, 1 - t); no > 0) {
+            other += NB > 2 ? no : 1;
+            if (!(ok = mbar_wait_warp(bars.pv_done(1 - t), (other - 1) & 1, wc))) break;
+          }
           const float2 x = stat[r], y = stat[128 + r];
           const float mx = fmaxf(x.x, y.x), ms = mx == -INFINITY ? 0.f : mx;
           const float e0 = x.y == 0.f ? 0.f : ex2_approx(x.x - ms), e1 = y.y == 0.f ? 0.f : ex2_approx(y.x - ms);
@@ -721,14 +764,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         if (!idle) {
           uint16_t* dst = out_row(p, w) + c0;
           float4* part = part_of(max(slot, 0));
-          const uint32_t at0 = PAIR ? tO : tmem + 256 + lane_bits;
+          const uint32_t at0 = PAIR ? tO : tmem + C::TM_O + lane_bits;
 #pragma unroll 1
           for (int c = 0; c < COLS; c += 16) {
             uint32_t x[16];
             tmem_ld16(at0 + c0 + c, x);
             if (!PAIR && use1) {
               uint32_t y[16];
-              tmem_ld16(at0 + 128 + c0 + c, y);
+              tmem_ld16(at0 + C::TM_OT + c0 + c, y);
 #pragma unroll
               for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), w1, __uint_as_float(x[e]) * w0));
             } else {
@@ -818,6 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         if (!PAIR && !(ok = join())) break;
       }
       kt += p.end - p.begin;
+      seq += chain_steps(p, 0) + chain_steps(p, 1);
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(bars.piece_empty(pi % kPieceRing));
     }
