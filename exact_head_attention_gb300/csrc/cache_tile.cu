@@ -53,7 +53,7 @@ struct Cfg {
   static constexpr uint32_t TILE = 128 * D * 2;                // an fp16 operand tile
   static constexpr uint32_t RAW = 128 * D;                     // a tile of codes
   static constexpr int NS = D == 128 ? 2 : 3;                  // K and V operand slots
-  static constexpr int NR = D == 128 ? (PAIR ? 2 : 3) : 4;     // slots of codes, K and V in turn
+  static constexpr int NR = D == 128 ? (PAIR ? 2 : 3) : 8;     // slots of codes, K and V in turn
   static constexpr int NB = D == 64 ? 3 : 2;                   // score buffers
   // Scales stay in use from a tile's copy to its softmax, over tiles of codes, operand tiles, and steps under way.
   static_assert((NR + 1) / 2 + NS + NB + 1 <= kMetaRing, "scales of the tiles under way");
@@ -414,33 +414,32 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     regs_decrease<kRegsOther>();
     if (warp == 9) {
       // ------------------------------------------------------------ producer
-      // Lane g < 8 looks after 16-token group g of a tile.  Page numbers, scales and copies of a tile hang on
-      // one another, so tiles run through three stages, one behind the other.
+      // In rounds of four tiles: lane 8 q + g looks after 16-token group g of the round's tile q.  Page numbers,
+      // scales and copies of a tile hang on one another, so rounds run through three stages, one behind the other.
       typename C::Walk walk(a, *reinterpret_cast<typename C::Walk::Shared*>(smem_raw + C::OFF_SCHED), lane, 0, blockIdx.x,
                             gridDim.x);
       const int psh = a.c.page_shift, box = min(1 << psh, kTK);
-      const bool feeds = lane < 8;
-      const bool leads = feeds && ((16 * lane) & (box - 1)) == 0;
-      constexpr int kNoTile = -2;
+      const int group = lane & 7;
+      const bool leads = ((16 * group) & (box - 1)) == 0;
       struct Round {
-        int key, page, head, tile;  // tile: kNoTile for none (the same for all lanes)
+        int tiles, key, page, head;  // tiles: 0 for none (the same for all lanes)
         float ks, vs;
       };
       CachePiece p{};
       int tile = 0, announced = 0, issued = 0, raws = 0, left = 3;
       bool have = false, ok = true;
       Round r0, r1, r2;
-      r1.tile = r2.tile = kNoTile;
-      auto copy = [&](const uint8_t* codes, const Round& r) -> bool {
+      r1.tiles = r2.tiles = 0;
+      auto copy = [&](const uint8_t* codes, const Round& r, int q) -> bool {
         const int s = raws % NR;
         if (!mbar_wait_warp(bars.raw_empty(s), ((raws / NR) & 1) ^ 1, wc)) return false;
-        const bool mine = leads && r.page >= 0;
+        const bool mine = lane >> 3 == q && leads && r.page >= 0;
         const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
         if (lane == 0) mbar_arrive_expect_tx(bars.raw_full(s), n * box * D);
         __syncwarp();
         if (mine) {
           const long long row = ((static_cast<long long>(r.page) * a.c.heads + r.head) << psh) + (r.key & ((1 << psh) - 1));
-          bulk_load(sbase + C::OFF_RAW + s * C::RAW + lane * 16 * D, codes + row * D, box * D, bars.raw_full(s));
+          bulk_load(sbase + C::OFF_RAW + s * C::RAW + group * 16 * D, codes + row * D, box * D, bars.raw_full(s));
         }
         ++raws;
         return true;
@@ -448,23 +447,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       while (left > 0 && ok) {
         r0 = r1;
         r1 = r2;
-        if (r0.tile != kNoTile) {
-          ok = copy(a.c.k, r0);
-          if (ok) {
-            const int ms = issued % kMetaRing;
-            if (feeds) {
-              meta[ms * 16 + lane] = r0.ks;
-              meta[ms * 16 + 8 + lane] = r0.vs;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars.meta_full(ms));
-            ++issued;
-            ok = copy(a.c.v, r0);
+#pragma unroll 1
+        for (int q = 0; q < r0.tiles; ++q) {
+          if (!(ok = copy(a.c.k, r0, q))) break;
+          const int ms = issued++ % kMetaRing;
+          if (lane >> 3 == q) {
+            meta[ms * 16 + group] = r0.ks;
+            meta[ms * 16 + 8 + group] = r0.vs;
           }
-          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.meta_full(ms));
+          if (!(ok = copy(a.c.v, r0, q))) break;
         }
-        r2.tile = kNoTile;
-        ++tile;
+        if (!ok) break;
+        r2.tiles = 0;
+        tile += 4;
         if (left == 3 && (!have || tile >= p.end)) {
           have = walk.next(p);
           if (!have) left = 2;
@@ -482,14 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           --left;
         }
         if (have && left == 3) {
-          r2.tile = tile;
+          r2.tiles = min(4, p.end - tile);
           r2.head = p.head;
           r2.key = tile * kTK + 16 * lane;
-          const bool there = feeds && r2.key < p.len;
+          const bool there = lane >> 3 < r2.tiles && r2.key < p.len;
           r2.page = there ? cache_page_number(a.c, p.b, r2.key) : 0x7fffffff;
           r2.ks = there ? 0.f : 1.f;
         }
-        if (r1.tile != kNoTile) {
+        if (r1.tiles > 0) {
           const bool there = r1.ks == 0.f;
           r1.page = cache_page_checked(a.c, r1.page);
           r1.ks = r1.vs = there ? __int_as_float(0x7fffffff) : 0.f;
