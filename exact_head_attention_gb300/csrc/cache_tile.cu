@@ -69,7 +69,7 @@ struct Cfg {
   static constexpr uint32_t OFF_STAT = OFF_META + kMetaRing * 64;    // !PAIR: {m, l} [2][128], vref [2][4]
   static constexpr uint32_t OFF_PIECE = OFF_STAT + (PAIR ? 0 : 2 * 128 * 8 + 32);
   static constexpr uint32_t OFF_BAR = OFF_PIECE + kPieceRing * kPieceInts * 4;
-  static constexpr int NBAR = 2 + 4 * NS + 2 * NR + 8 + kMetaRing + 2 * kPieceRing + 4;
+  static constexpr int NBAR = 2 + 4 * NS + 2 * NR + 6 + kMetaRing + 2 * kPieceRing + 4;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t OFF_SCHED = OFF_MISC + 16;
   static constexpr uint32_t BYTES = OFF_SCHED + sizeof(typename Walk::Shared);
@@ -116,8 +116,7 @@ struct Bars {
   static constexpr int kB = 2 + 4 * NS + 2 * NR;
   __device__ uint32_t s_full(int b) const { return at(kB + b); }
   __device__ uint32_t p_full(int b) const { return at(kB + 3 + b); }
-  __device__ uint32_t pv_done(int t) const { return at(kB + 6 + t); }
-  static constexpr int kC = kB + 8;
+  static constexpr int kC = kB + 6;
   __device__ uint32_t meta_full(int s) const { return at(kC + s); }
   __device__ uint32_t piece_full(int s) const { return at(kC + kMetaRing + s); }
   __device__ uint32_t piece_empty(int s) const { return at(kC + kMetaRing + kPieceRing + s); }
@@ -356,7 +355,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     *abort_flag = 0u;
     for (int t = 0; t < 2; ++t) {
       mbar_init(bars.q_full(t), 4);
-      mbar_init(bars.pv_done(t), 1);
       mbar_init(bars.stored(t), 4);
     }
     for (int b = 0; b < C::NB; ++b) {
@@ -518,35 +516,60 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
                      v_lo = sdesc_lo(ubase + C::OFF_V, kChunk);
       constexpr int NB = C::NB;
       int ks = 0, vs = 0, sb = 0, pb = 0;                       // next slots of K and V, next buffers of S and P ...
-      uint32_t kph = 0, vph = 0, pph = 0, q0 = 0, q1 = 0;  // ... and the parities of their waits; waits of q_full
+      uint32_t kph = 0, vph = 0, pph = 0, qph = 0;         // ... and the parities of the next waits
       bool ok = true;
       const CachePiece* p;
       for (int pi = 0; ok && (p = next_piece(pi)) != nullptr; ++pi) {
         const int n = __shfl_sync(0xffffffffu, chain_steps(*p, 0) + chain_steps(*p, 1), 0);  // steps of the piece
         const bool both = __shfl_sync(0xffffffffu, both_chains(*p), 0);
         const bool shared = PAIR && both;  // a tile has two steps, one of each chain, else one
-        // the query tiles: each chain's own, or halves of one from both warpgroups
-        ok = mbar_wait_warp(ub.q_full(0), q0++ & 1, wc);
-        if (ok && (!PAIR || both)) ok = mbar_wait_warp(ub.q_full(1), q1++ & 1, wc);
+        // The query tiles: each chain's own, or halves of one from both warpgroups.  A warpgroup without rows
+        // arrives too: it then has seen the last piece's products end, before any barrier moves on.
+        ok = mbar_wait_warp(ub.q_full(lane & 1), qph, wc);
+        qph ^= 1;
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll 1
-        for (int i = 0; ok && i < n + NB; ++i) {
-          if (i >= NB) {  // O_t += P V of step i - NB
-            const int j = i - NB, t = both ? j & 1 : 0;
-            if (!shared || t == 0) {
-              if (!(ok = mbar_wait_warp(ub.v_full(vs), vph, wc))) break;
-            }
-            if (!(ok = mbar_wait_warp(ub.p_full(pb), pph, wc))) break;
-            tc_fence_after();
-            const uint32_t d = utmem + C::TM_O + t * C::TM_OT, pa = utmem + pb * 128, b_lo = v_lo + vs * kTileLo;
-            const bool slot_ends = !shared || t == 1, last = j + (both ? 2 : 1) >= n;
-            if (elect_one()) {
-              mma_ts_lo_rt(d, pa, b_lo, idPV, both ? j >> 1 : j);
+        for (int i = 0; i < n + NB; ++i) {
+          // Turn i: O_t += P V of step j = i - NB, then the scores of step i.  Its three waits are one: a lane each.
+          const int j = i - NB, tv = both ? j & 1 : 0, tk = both ? i & 1 : 0;
+          const bool pv = j >= 0, sc = i < n;
+          if (!pv && !sc) continue;  // a piece of fewer steps than buffers
+          const bool first_v = pv && !(shared && tv), first_k = sc && !(shared && tk);  // the slot's first reader
+          const bool last_v = !shared || tv, last_k = !shared || tk;                     // and its last
+          uint32_t bar = pv ? ub.p_full(pb) : ub.k_full(ks), par = pv ? pph : kph;
+          if (lane == 1 && first_v) {
+            bar = ub.v_full(vs);
+            par = vph;
+          }
+          if (lane == 2 && first_k) {
+            bar = ub.k_full(ks);
+            par = kph;
+          }
+          if (!(ok = mbar_wait_warp(bar, par, wc))) break;
+          tc_fence_after();
+          const uint32_t o = utmem + C::TM_O + tv * C::TM_OT, pa = utmem + pb * 128, vb = v_lo + vs * kTileLo;
+          const uint32_t d = utmem + sb * 128, a_lo = q_lo + (PAIR ? tk * kTileLo : 0), b_lo = k_lo + ks * kTileLo;
+          if (elect_one()) {
+            if (pv) {
+              mma_ts_lo_rt(o, pa, vb, idPV, both ? j >> 1 : j);
 #pragma unroll
-              for (int k = 1; k < kTK / 16; ++k) mma_ts_lo<true>(d, pa + k * 8, b_lo + k * (2048 >> 4), idPV);
-              if (NB > 2 || last) mma_commit(ub.pv_done(t));
-              if (slot_ends) mma_commit(ub.v_empty(vs));
+              for (int k = 1; k < kTK / 16; ++k) mma_ts_lo<true>(o, pa + k * 8, vb + k * (2048 >> 4), idPV);
+              if (last_v) mma_commit(ub.v_empty(vs));
             }
-            if (slot_ends && ++vs == NS) {
+            if (sc) {
+              mma_ss_lo<false>(d, a_lo, b_lo, idS);
+#pragma unroll
+              for (int k = 1; k < D / 16; ++k) {
+                const uint32_t off = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
+                mma_ss_lo<true>(d, a_lo + off, b_lo + off, idS);
+              }
+              mma_commit(ub.s_full(sb));
+              if (last_k) mma_commit(ub.k_empty(ks));
+            }
+          }
+          if (pv) {
+            if (last_v && ++vs == NS) {
               vs = 0;
               vph ^= 1;
             }
@@ -555,25 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
               pph ^= 1;
             }
           }
-          if (i < n) {  // the scores of step i
-            const int t = both ? i & 1 : 0;
-            if (!shared || t == 0) {
-              if (!(ok = mbar_wait_warp(ub.k_full(ks), kph, wc))) break;
-              tc_fence_after();
-            }
-            const uint32_t d = utmem + sb * 128, a_lo = q_lo + (PAIR ? t * kTileLo : 0), b_lo = k_lo + ks * kTileLo;
-            const bool slot_ends = !shared || t == 1;
-            if (elect_one()) {
-              mma_ss_lo<false>(d, a_lo, b_lo, idS);
-#pragma unroll
-              for (int k = 1; k < D / 16; ++k) {
-                const uint32_t off = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
-                mma_ss_lo<true>(d, a_lo + off, b_lo + off, idS);
-              }
-              mma_commit(ub.s_full(sb));
-              if (slot_ends) mma_commit(ub.k_empty(ks));
-            }
-            if (slot_ends && ++ks == NS) {
+          if (sc) {
+            if (last_k && ++ks == NS) {
               ks = 0;
               kph ^= 1;
             }
@@ -628,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     constexpr int NB = C::NB;
     int kt = 0;
     uint32_t seq = 0;                        // steps of both chains in earlier pieces
-    uint32_t own = 0, other = 0, jc = 0, dc = 0;  // completions of either pv_done so far; waits of join and stored
+    uint32_t jc = 0, dc = 0;                 // waits of join and stored
     bool ok = true;
     const int ri = (PAIR ? t * 128 : 0) + r;  // row of the item
     // Both softmax warpgroups meet (!PAIR), or one.  Bounded waits: after a failed one elsewhere these give up too.
@@ -667,8 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         const bool idle = row_first >= rows;            // a warp of rows that are not there
         float m = -INFINITY, l = 0.f, vref = 0.f, vinv = 0.f;
         {
-          // The previous piece's score products have completed: this chain's with its o_full, the other's
-          // with the join that ended its epilogue.
+          // The previous piece's score products have completed: this warpgroup has seen them all end,
+          // the other (!PAIR) has before the join that ended the epilogue.
           const Row w = row_of(p);
           auto row_at = [&](int k) -> const uint16_t* {
             const int row = row_first + k, tok = row / a.group;
@@ -694,11 +700,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
             tc_fence_after();
             if (!idle) {
               const float* scales = meta + (nt % kMetaRing) * 16;
-              // The chain's last product: with two buffers these scores were issued after it.  With three they came
-              // after the one before it, so that the parity says which of the two completions there are.
+              // The chain's last product: with two buffers these scores were issued after it.  With three, its end
+              // (and that of the other chain's on the same values) frees the tile's slot.
               auto wait_pv = [&] {
                 if (NB > 2) {
-                  if (!mbar_wait_warp(bars.pv_done(t), (own + j - 1) & 1, wc)) ok = false;
+                  const int nv = nt - (PAIR ? 1 : 2);
+                  if (!mbar_wait_warp(bars.v_empty(nv % NS), (nv / NS) & 1, wc)) ok = false;
                   tc_fence_after();
                 }
               };
@@ -714,12 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
             if (!ok) break;
           }
         }
-        // Completions of pv_done: of every step, or (two buffers) of the last one of a piece.  The last two may be
-        // under way, and a parity tells two neighbouring completions apart, no more.
-        if (n > 0) {
-          if (NB > 2 && ok && n > 1) ok = mbar_wait_warp(bars.pv_done(t), (own + n - 2) & 1, wc);
-          own += NB > 2 ? n : 1;
-          if (ok) ok = mbar_wait_warp(bars.pv_done(t), (own - 1) & 1, wc);
+        // Every product of the piece has completed once its last value tile is free: this chain's and the other's.
+        if (ok) {
+          const int nv = kt + p.end - p.begin - 1;
+          ok = mbar_wait_warp(bars.v_empty(nv % NS), (nv / NS) & 1, wc);
         }
 
         // ------------------------------------------------------------ epilogue
@@ -734,11 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           tc_fence_before();
           if (!(ok = ok && join())) break;
           use1 = both;
-          // The other chain has seen its products completed before it joined.
-          if (const int no = chain_steps(p, 1 - t); no > 0) {
-            other += NB > 2 ? no : 1;
-            if (!(ok = mbar_wait_warp(bars.pv_done(1 - t), (other - 1) & 1, wc))) break;
-          }
           const float2 x = stat[r], y = stat[128 + r];
           const float mx = fmaxf(x.x, y.x), ms = mx == -INFINITY ? 0.f : mx;
           const float e0 = x.y == 0.f ? 0.f : ex2_approx(x.x - ms), e1 = y.y == 0.f ? 0.f : ex2_approx(y.x - ms);
@@ -856,6 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         }
         // O_t, the statistics and the query tile are free once both warpgroups are here.
         if (!PAIR && !(ok = join())) break;
+      } else if (lane == 0) {
+        mbar_arrive(bars.q_full(t));
       }
       kt += p.end - p.begin;
       seq += chain_steps(p, 0) + chain_steps(p, 1);
