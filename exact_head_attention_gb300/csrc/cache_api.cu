@@ -24,7 +24,8 @@ unsigned long long next_tag() {
   z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
   z = (z ^ (z >> 27)) * 0x94d049bb133111ebull;
   z ^= z >> 31;
-  return z ? z : 1ull;  // zero is a flag at rest
+  z &= ~0xffffull;                  // the count's place
+  return z ? z : 0x10000ull;  // zero is a count at rest
 }
 
 // The rules of attn_cache, and its view for the kernels.

@@ -41,43 +41,50 @@
 namespace exattn {
 namespace {
 
-constexpr int kPieceRing = 3;                   // pieces announced ahead
 // P is held times 2^kShift, so that fewer of the small ones become subnormal in fp16.  It stays below 2^15: the
 // running maximum may lag by 2^8, and vref by kVrefLag = 2^4.
 constexpr float kShift = 3.f, kVrefLag = 16.f;
+
+constexpr int kWorkers = 2;                     // of a block: each with its own share of the work
+constexpr int kGroup = 4;                       // computing warps of a worker
+constexpr int W = kWorkers * kGroup;
+constexpr int kThreads = 32 * (W + 4);          // and a warpgroup of producers, two warps a worker
+// Registers: 168 a thread at launch (65,536 over 384 threads); the producers give a part of their share to the
+// computing warps, which hold O, Q and the codes in flight: 2 x 208 + 88 = 3 x 168.
+constexpr int kComputeRegs = 208, kProducerRegs = 88;
+static_assert(2 * kComputeRegs + kProducerRegs == 3 * 168, "register split must match the launch");
+constexpr int kMinTiles = 2 * kGroup;           // the smallest piece: two tiles a warp
 
 // NT: query rows in eights.
 template <int D, int NT>
 struct Cfg {
   static constexpr int R = 8 * NT;                            // query rows an item
-  // Computing warps.  The code of a tile is a chain of long-latency steps, and the more warps the more
-  // of it overlaps; O takes D NT / 4 registers, which leaves room for 12 warps at NT = 1 and for 8 above.
-  static constexpr int W = NT == 1 ? 12 : 8;
-  static constexpr int THREADS = 32 * (W + 4);                // and a warpgroup of producers
-  // Registers: 128 or 168 a thread at launch (65,536 over the threads); the last warpgroup gives a part of its
-  // share to the others: 3 x 144 + 80 = 4 x 128, and 2 x 208 + 88 = 3 x 168.
-  static constexpr int COMPUTE_REGS = NT == 1 ? 144 : 208, PRODUCER_REGS = NT == 1 ? 80 : 88;
-  static_assert((W / 4) * COMPUTE_REGS + PRODUCER_REGS == (W / 4 + 1) * (NT == 1 ? 128 : 168), "register split must match the launch");
   static constexpr int TK = 4096 / D;                         // tokens a tile: 32 or 64
   static constexpr int NH = TK / 16;                          // 16-token groups of it, each in one page
   static constexpr int TILE = TK * D;                         // bytes of codes, K or V
-  static constexpr int STAGES = 2;                            // of K and V together, a warp
+  static constexpr int STAGES = NT == 1 ? 3 : 2;              // of K and V together, a warp
   static constexpr int RING = W * STAGES * 2 * TILE;          // 192 or 128 KB
   static constexpr int JR = NT == 1 ? 512 / D : 1024 / D;     // rows joined at a time
-  static constexpr int JOIN = W * JR * D * 4;
+  static constexpr int JOIN = kGroup * JR * D * 4;            // a worker
   static constexpr bool Q_IN_SMEM = NT > 2;                   // registers hold Q up to 16 rows
   static constexpr int QBYTES = Q_IN_SMEM ? NT * (D / 16) * 32 * 8 : 0;
+  static constexpr int RINGQ = 2;                             // pieces announced ahead
   static constexpr int QROWS = R * D * 2;                     // the rows of one piece as they lie in memory
-  static constexpr int OFF_JOIN = RING;
-  static constexpr int OFF_QROWS = OFF_JOIN + JOIN;
-  static constexpr int OFF_Q = OFF_QROWS + kPieceRing * QROWS;
-  static constexpr int OFF_META = OFF_Q + QBYTES;             // [warp][stage][group] {ks, vs}
-  static constexpr int OFF_STAT = (OFF_META + W * STAGES * NH * 8 + 15) & ~15;  // m[R][W], l[R][W], vref[W]
-  static constexpr int OFF_PIECE = OFF_STAT + (2 * W * R + W) * 4;
-  static constexpr int OFF_BAR = (OFF_PIECE + kPieceRing * kPieceInts * 4 + 7) & ~7;
-  static constexpr int OFF_MISC = OFF_BAR + 8 * (2 * W * STAGES + 2 * kPieceRing + 1);
-  static constexpr int OFF_SCHED = (OFF_MISC + 16 + 7) & ~7;
-  static constexpr int BYTES = OFF_SCHED + static_cast<int>(sizeof(typename CacheWalk<R, TK, 128, W>::Shared));
+  static constexpr int STAT = (2 * kGroup * R + kGroup) * 4;  // m[R][warp], l[R][warp], vref[warp]
+  using Walk = CacheWalk<R, TK, 64, kMinTiles>;
+  // a worker's part of shared memory
+  static constexpr int W_JOIN = 0;
+  static constexpr int W_QROWS = W_JOIN + JOIN;
+  static constexpr int W_Q = W_QROWS + RINGQ * QROWS;
+  static constexpr int W_STAT = W_Q + QBYTES;
+  static constexpr int W_PIECE = W_STAT + STAT;
+  static constexpr int W_SCHED = W_PIECE + RINGQ * kPieceInts * 4;
+  static constexpr int WORKER = (W_SCHED + static_cast<int>(sizeof(typename Walk::Shared)) + 15) & ~15;
+  static constexpr int OFF_WORKER = RING;
+  static constexpr int OFF_META = OFF_WORKER + kWorkers * WORKER;  // [warp][stage][group] {ks, vs}
+  static constexpr int OFF_BAR = OFF_META + W * STAGES * NH * 8;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * (2 * W * STAGES + kWorkers * (2 * RINGQ + 1));
+  static constexpr int BYTES = OFF_MISC + 16;
   static_assert(BYTES <= 232448, "shared memory of a block");
 };
 
@@ -119,26 +126,27 @@ __device__ __forceinline__ void tma_load_lines(uint32_t dst, const CUtensorMap* 
 __device__ __forceinline__ float qnan() { return __int_as_float(0x7fffffff); }
 
 template <int D, int FMT, bool BF16, int NT>
-__global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(const __grid_constant__ CacheAttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_constant__ CacheAttnArgs a) {
   using C = Cfg<D, NT>;
-  constexpr int W = C::W, NST = C::STAGES, NH = C::NH;
+  constexpr int NST = C::STAGES, NH = C::NH, RQ = C::RINGQ;
   constexpr int KS = D / 16, MT = D / 16;  // k-steps of S^T; 16-row tiles of O^T
-  using Walk = CacheWalk<C::R, C::TK, 128, W>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t sbase = smem_u32(smem_raw);
   if (!smem_base_aligned(sbase, a.err_word)) return;
-  const uint32_t bars = sbase + C::OFF_BAR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int worker = warp < W ? warp / kGroup : (warp - W) / 2;
+  uint8_t* wmem = smem_raw + C::OFF_WORKER + worker * C::WORKER;
+  const uint32_t bars = sbase + C::OFF_BAR, wbars = bars + 8 * (2 * W * NST + worker * (2 * RQ + 1));
   auto full = [&](int w, int s) { return bars + 8 * (w * NST + s); };
   auto empty = [&](int w, int s) { return bars + 8 * (W * NST + w * NST + s); };
-  auto piece_full = [&](int i) { return bars + 8 * (2 * W * NST + i); };
-  auto piece_empty = [&](int i) { return bars + 8 * (2 * W * NST + kPieceRing + i); };
-  const uint32_t join_bar = bars + 8 * (2 * W * NST + 2 * kPieceRing);
+  auto piece_full = [&](int i) { return wbars + 8 * i; };
+  auto piece_empty = [&](int i) { return wbars + 8 * (RQ + i); };
+  const uint32_t join_bar = wbars + 8 * (2 * RQ);
   float2* meta = reinterpret_cast<float2*>(smem_raw + C::OFF_META);
-  CachePiece* pieces = reinterpret_cast<CachePiece*>(smem_raw + C::OFF_PIECE);
+  CachePiece* pieces = reinterpret_cast<CachePiece*>(wmem + C::W_PIECE);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_raw + C::OFF_MISC);
-  volatile uint32_t* merge_flag = reinterpret_cast<volatile uint32_t*>(smem_raw + C::OFF_MISC + 4);
+  volatile uint32_t* merge_flag = reinterpret_cast<volatile uint32_t*>(smem_raw + C::OFF_MISC + 4 + 4 * worker);
   const WaitCtx wc{abort_flag, a.err_word, a.timeout_ns};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     *abort_flag = 0u;
@@ -146,11 +154,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
       mbar_init(bars + 8 * i, NH);
       mbar_init(bars + 8 * (W * NST + i), 1);
     }
-    for (int i = 0; i < kPieceRing; ++i) {
-      mbar_init(piece_full(i), 1);
-      mbar_init(piece_empty(i), W);
+    for (int k = 0; k < kWorkers; ++k) {
+      const uint32_t at = bars + 8 * (2 * W * NST + k * (2 * RQ + 1));
+      for (int i = 0; i < RQ; ++i) {
+        mbar_init(at + 8 * i, 1);
+        mbar_init(at + 8 * (RQ + i), kGroup);
+      }
+      mbar_init(at + 8 * (2 * RQ), kGroup);
     }
-    mbar_init(join_bar, W);
     fence_mbar_init();
     prefetch_tmap(&a.tm_k);
     prefetch_tmap(&a.tm_v);
@@ -161,20 +172,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
   griddep_launch_dependents();
 
   if (warp >= W) {
-    regs_decrease<C::PRODUCER_REGS>();
+    regs_decrease<kProducerRegs>();
     // ------------------------------------------------------------ producers
-    // Producer warp p feeds the computing warps w = 4 i + p, with one lane for each 16-token group of their
-    // tiles.  One warp alone took 190 cycles for each 4 KB box it had copied, more than the 175 in which they
-    // arrive at the memory's rate; four share the work.
+    // Producer p of a worker feeds its computing warps 2 p and 2 p + 1, with one lane for each 16-token group of
+    // their tiles.  (One warp that copied for a whole block took 190 cycles for each 4 KB box, more than the 175 in
+    // which they arrive at the memory's rate.)
     // A warp works in rounds of one tile a computing warp.  A group's page number, then its scales and codes
     // hang on one another, so the rounds run through three stages, one behind the other: the pages of
     // one are loaded while the scales of the round before are, and the codes of the one before that copied.
-    Walk walk(a, *reinterpret_cast<typename Walk::Shared*>(smem_raw + C::OFF_SCHED), threadIdx.x - 32 * W, 1, blockIdx.x,
-              gridDim.x);
+    const int pw = (warp - W) & 1;
+    typename C::Walk walk(a, *reinterpret_cast<typename C::Walk::Shared*>(wmem + C::W_SCHED), pw * 32 + lane, 1 + worker,
+                          blockIdx.x * kWorkers + worker, gridDim.x * kWorkers);
     const int psh = a.c.page_shift;
-    const int pw = warp - W;
-    const bool feeds = lane < W / 4 * NH;
-    const int cw = feeds ? 4 * (lane / NH) + pw : 0;  // the computing warp
+    const bool feeds = lane < 2 * NH;
+    const int gw = feeds ? 2 * pw + lane / NH : 0;  // the computing warp in its worker
+    const int cw = worker * kGroup + gw;
     const int group = lane % NH;
     const int box = min(1 << psh, C::TK);              // tokens a copy
     const bool leads = ((16 * group) & (box - 1)) == 0;  // this lane's copy takes the groups behind it along
@@ -215,14 +227,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
       }
       // First stage: the next round, its piece announced where it is new, and its page numbers.
       r2.page = kNoTile;
-      base += W;
+      base += kGroup;
       if (left == 3 && (!have || base >= p.end)) {
         have = ok && walk.next(p);
         if (!have) left = 2;
         base = p.begin;
         if (pw == 0) {
-          const int i = announced++ % kPieceRing;
-          ok = mbar_wait_warp(piece_empty(i), (((announced - 1) / kPieceRing) & 1) ^ 1, wc) && ok;
+          const int i = announced++ % RQ;
+          ok = mbar_wait_warp(piece_empty(i), (((announced - 1) / RQ) & 1) ^ 1, wc) && ok;
           const int nrows = have && ok ? min(C::R, a.group * a.Nq - p.rt * C::R) : 0;
           if (lane == 0) {
             pieces[i] = p;
@@ -231,7 +243,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
           }
           if (lane < nrows) {
             const int r = p.rt * C::R + lane, tok = r / a.group, hg = r - tok * a.group;
-            bulk_load(sbase + C::OFF_QROWS + i * C::QROWS + lane * D * 2,
+            bulk_load(smem_u32(wmem) + C::W_QROWS + i * C::QROWS + lane * D * 2,
                       static_cast<const uint16_t*>(a.q) + p.b * a.sq.b +
                           (static_cast<long long>(p.head) * a.group + hg) * a.sq.h + tok * a.sq.n,
                       D * 2, piece_full(i));
@@ -240,9 +252,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
       } else if (left < 3) {
         --left;
       }
-      if (have && feeds && base + cw < p.end) {
+      if (have && feeds && base + gw < p.end) {
         r2.head = p.head;
-        r2.key = (base + cw) * C::TK + 16 * group;
+        r2.key = (base + gw) * C::TK + 16 * group;
         r2.page = r2.key < p.len ? cache_page_number(a.c, p.b, r2.key) : 0x7fffffff;  // no entry there
         r2.ks = r2.key < p.len ? 0.f : 1.f;
       }
@@ -262,30 +274,30 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
     }
-    cache_empty_items<D, C::R, C::TK, W>(a, blockIdx.x * 4 + pw, gridDim.x * 4);
+    cache_empty_items<D, C::R, C::TK, kMinTiles>(a, blockIdx.x * 4 + warp - W, gridDim.x * 4);
     // Every copy issued must land before the block exits, also where the computing warps gave up.
     if (feeds)
       for (int n = max(0, issued - NST); n < issued; ++n) mbar_drain(full(cw, n % NST), (n / NST) & 1, a.timeout_ns);
     if (pw == 0)
-      for (int n = max(0, announced - kPieceRing); n < announced; ++n)
-        mbar_drain(piece_full(n % kPieceRing), (n / kPieceRing) & 1, a.timeout_ns);
+      for (int n = max(0, announced - RQ); n < announced; ++n) mbar_drain(piece_full(n % RQ), (n / RQ) & 1, a.timeout_ns);
     return;
   }
 
   // -------------------------------------------------------------- computing warps
-  regs_increase<C::COMPUTE_REGS>();
+  regs_increase<kComputeRegs>();
+  const int gw = warp % kGroup, tid = threadIdx.x % (32 * kGroup);  // in the worker
   const int g = lane >> 2, t4 = lane & 3;
   const uint8_t* ring = smem_raw + warp * (NST * 2 * C::TILE);
-  float* st_m = reinterpret_cast<float*>(smem_raw + C::OFF_STAT);
-  float* st_l = st_m + W * C::R;
-  float* st_v = st_l + W * C::R;
-  float4* join = reinterpret_cast<float4*>(smem_raw + C::OFF_JOIN);
-  uint2* qs = reinterpret_cast<uint2*>(smem_raw + C::OFF_Q);
-  const CacheWs ws = cache_ws(a.ws, C::R, D, a.sm_count);
+  float* st_m = reinterpret_cast<float*>(wmem + C::W_STAT);
+  float* st_l = st_m + kGroup * C::R;
+  float* st_v = st_l + kGroup * C::R;
+  float4* join = reinterpret_cast<float4*>(wmem + C::W_JOIN);
+  uint2* qs = reinterpret_cast<uint2*>(wmem + C::W_Q);
+  const CacheWs ws = cache_ws(a.ws, C::R, D, a.sm_count * kWorkers);
   const int rows = a.group * a.Nq;
   int used = 0;
   bool ok = true;
-  // Barrier of the computing warps.  After a failed wait a warp leaves, so this one gives up too (a
+  // Barrier of the worker's computing warps.  After a failed wait a warp leaves, so this one gives up too (a
   // hardware barrier would wait for it for ever).
   uint32_t joins = 0;
   auto sync_warps = [&]() -> bool {
@@ -295,9 +307,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
   };
 
   for (int pi = 0; ; ++pi) {
-    ok = mbar_wait_warp(piece_full(pi % kPieceRing), (pi / kPieceRing) & 1, wc) && ok;
+    ok = mbar_wait_warp(piece_full(pi % RQ), (pi / RQ) & 1, wc) && ok;
     if (!ok) break;
-    const CachePiece piece = pieces[pi % kPieceRing];
+    const CachePiece piece = pieces[pi % RQ];
     const int b = piece.b, head = piece.head, rt = piece.rt, len = piece.len, begin = piece.begin, end = piece.end,
               slot = piece.slot;
     if (b < 0) break;
@@ -310,7 +322,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = row0 + nt * 8 + g;
-      const uint4* src = reinterpret_cast<const uint4*>(smem_raw + C::OFF_QROWS + (pi % kPieceRing) * C::QROWS +
+      const uint4* src = reinterpret_cast<const uint4*>(wmem + C::W_QROWS + (pi % RQ) * C::QROWS +
                                                         (nt * 8 + g) * D * 2 + t4 * (D / 2));
       uint4 raw[D / 32];
       uint32_t mx = 0u;
@@ -353,7 +365,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
                          pack2<false>(unpack_lo<true>(w[1]) * mul, unpack_hi<true>(w[1]) * mul));
         if constexpr (!C::Q_IN_SMEM)
           qf[nt][j] = x;
-        else if (warp == 0)  // every warp holds the same: one writes them
+        else if (gw == 0)  // every warp holds the same: one writes them
           qs[(nt * KS + j) * 32 + lane] = x;
       }
     }
@@ -373,7 +385,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
     }
     float vref = 0.f, vinv = 0.f;
 
-    for (int t = begin + warp; t < end; t += W, ++used) {
+    for (int t = begin + gw; t < end; t += kGroup, ++used) {
       const int s = used % NST;
       if (ok) ok = mbar_wait_warp(full(warp, s), (used / NST) & 1, wc);
       if (!ok) break;
@@ -543,13 +555,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
         if (g == 0) {
-          st_m[(nt * 8 + 2 * t4 + e) * W + warp] = m[nt][e];
-          st_l[(nt * 8 + 2 * t4 + e) * W + warp] = x;
+          st_m[(nt * 8 + 2 * t4 + e) * kGroup + gw] = m[nt][e];
+          st_l[(nt * 8 + 2 * t4 + e) * kGroup + gw] = x;
         }
       }
     if (lane == 0) {
-      st_v[warp] = vref;
-      mbar_arrive(piece_empty(pi % kPieceRing));
+      st_v[gw] = vref;
+      mbar_arrive(piece_empty(pi % RQ));
     }
     constexpr int Q4 = D / 4;   // float4s a row
     constexpr int LQ = D / 32;  // float4s of a lane's part of a row (d positions g D/8 ..)
@@ -558,7 +570,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
       return (r & (C::JR - 1)) * Q4 + (q ^ (D == 128 ? t : (t & 1) | ((t & 2) << 1)));
     };
     for (int base = 0; base < nrows; base += C::JR) {  // the same for all warps
-      if (begin + warp < end) {
+      if (begin + gw < end) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -567,30 +579,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
             if (r >= base && r < min(nrows, base + C::JR)) {
 #pragma unroll
               for (int q = 0; q < LQ; ++q)
-                join[warp * (C::JR * Q4) + place(r, g * LQ + q)] =
+                join[gw * (C::JR * Q4) + place(r, g * LQ + q)] =
                     make_float4(o[nt][2 * q][e], o[nt][2 * q][2 + e], o[nt][2 * q + 1][e], o[nt][2 * q + 1][2 + e]);
             }
           }
       }
       if (!(ok = ok && sync_warps())) break;
       const int nr = min(C::JR, nrows - base);
-      for (int i = threadIdx.x; i < nr * Q4; i += 32 * W) {
+      for (int i = tid; i < nr * Q4; i += 32 * kGroup) {
         const int ri = base + i / Q4, q = i % Q4;
-        float sm[W], sl[W], vr[W];
-#pragma unroll
-        for (int w = 0; w < W; w += 4) {
-          *reinterpret_cast<float4*>(sm + w) = *reinterpret_cast<const float4*>(st_m + ri * W + w);
-          *reinterpret_cast<float4*>(sl + w) = *reinterpret_cast<const float4*>(st_l + ri * W + w);
-          *reinterpret_cast<float4*>(vr + w) = *reinterpret_cast<const float4*>(st_v + w);
-        }
-        float mx = sm[0];
-#pragma unroll
-        for (int w = 1; w < W; ++w) mx = fmaxf(mx, sm[w]);
+        const float4 sm4 = *reinterpret_cast<const float4*>(st_m + ri * kGroup), sl4 = *reinterpret_cast<const float4*>(st_l + ri * kGroup),
+                     sv4 = *reinterpret_cast<const float4*>(st_v);
+        const float sm[kGroup] = {sm4.x, sm4.y, sm4.z, sm4.w}, sl[kGroup] = {sl4.x, sl4.y, sl4.z, sl4.w},
+                    vr[kGroup] = {sv4.x, sv4.y, sv4.z, sv4.w};
+        const float mx = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
         const float ms = mx == -INFINITY ? 0.f : mx;
         float lsum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
+        for (int w = 0; w < kGroup; ++w) {
           if (sl[w] != 0.f) {
             const float e = ex2_approx(sm[w] - ms), ev = e * vr[w];
             const float4 x = join[w * (C::JR * Q4) + place(ri, q)];
@@ -624,7 +631,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
 
     // ------------------------------------------------------------ merge, where this piece completes its item
     if (slot >= 0) {
-      if (warp == 0) {
+      if (gw == 0) {
         const bool all = cache_piece_done(ws, piece, 0, a.tag);
         if (lane == 0) *merge_flag = all;
       }
@@ -632,12 +639,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
       if (*merge_flag) {
         // L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s over the row's pieces.  Where threads are left over, G of them
         // share a row's four columns, each with every G-th piece, and join in shared memory.
-        const int n = piece.pieces(), cells = nrows * Q4;
-        const int G = max(1, min(n, 32 * W / cells));
+        const int n = piece.pieces, cells = nrows * Q4;
+        const int G = max(1, min(n, 32 * kGroup / cells));
         float4* m_acc = join;
-        float2* m_stat = reinterpret_cast<float2*>(join + 32 * W);
-        static_assert(C::JOIN >= 32 * W * 24, "room for the shares");
-        for (int i = threadIdx.x; i < cells * G; i += 32 * W) {
+        float2* m_stat = reinterpret_cast<float2*>(join + 32 * kGroup);
+        static_assert(C::JOIN >= 32 * kGroup * 24, "room for the shares");
+        for (int i = tid; i < cells * G; i += 32 * kGroup) {
           const int cell = i % cells, g0 = i / cells, ri = cell / Q4, q = cell % Q4;
           float mx = -INFINITY, sum = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -673,7 +680,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, 1) cache_attn_kernel(cons
         }
         if (G > 1) {
           if (!(ok = sync_warps())) break;
-          for (int cell = threadIdx.x; cell < cells; cell += 32 * W) {
+          for (int cell = tid; cell < cells; cell += 32 * kGroup) {
             const int ri = cell / Q4, q = cell % Q4;
             float mx = -INFINITY;
             for (int k = 0; k < G; ++k) mx = fmaxf(mx, m_stat[k * cells + cell].x);
@@ -713,7 +720,7 @@ cudaError_t launch_t(const CacheAttnArgs& a, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(kern, C::BYTES, done);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3(a.sm_count), dim3(C::THREADS), C::BYTES, stream, a);
+  return launch_dependent(kern, dim3(a.sm_count), dim3(kThreads), C::BYTES, stream, a);
 }
 
 template <int D, int FMT, bool BF16>
@@ -741,7 +748,8 @@ CacheAttnShape cache_attn_shape(long long rows, int d) {
 }
 
 size_t cache_attn_workspace(long long rows, int d, int sm_count) {
-  return (cache_ws_bytes(cache_attn_shape(rows, d).rows, d, sm_count) + 255) & ~static_cast<size_t>(255);
+  const int workers = rows > kCacheStreamRows ? sm_count : sm_count * kWorkers;
+  return (cache_ws_bytes(cache_attn_shape(rows, d).rows, d, workers) + 255) & ~static_cast<size_t>(255);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream) {

@@ -3,7 +3,7 @@
 // An item is one tile of query rows of one key/value head of one sequence; its keys are cut into tiles of
 // TK tokens.  All tiles of all items, in the order (sequence, head, row tile, key tile), are numbered
 // 0 .. T - 1 (below 2^31: the host checks the largest T that the page table allows).  With
-// C = ceil(T / P) for P blocks,
+// C = ceil(T / P) for P blocks (or workers, several to a block),
 //   * more than kMinTiles tiles a block: block c takes the tiles [c C, (c + 1) C), whichever items they
 //     belong to, so every block has the same work however uneven the lengths are;
 //   * fewer: C = kMinTiles, and a block takes whole pieces of at most C tiles that begin at an item's
@@ -24,18 +24,17 @@
 namespace exattn {
 
 // Merging.  The block whose piece completes an item merges all its pieces, in key order, so the result does
-// not depend on which block that is.  A block that has stored its partial result sets the slot's flag to the
-// call's tag and then looks at the flags of the item's other pieces: the last to set one sees all.  (Two
-// blocks may both; they write the same bits.)  The merging block puts the flags back to zero.  The
-// workspace needs no preparation: what lies there before is taken for a flag only if it equals a 64-bit
-// tag drawn for the call, and a captured call, whose tag is the same at each replay, finds zeros.
+// not depend on which block that is.  Each piece, once stored, adds one to its item's count, in the first
+// slot's word; the one that brings it to the number of pieces merges, and sets the word back to zero.  The
+// workspace needs no preparation: a word counts from nothing unless its upper 48 bits are a tag drawn for the call,
+// and a captured call, whose tag is the same at each replay, finds zeros.
 
-// Workspace: flags, then the slots (R rows of D values in fp32, normalised by the piece's own sum, in an order
-// that each kernel chooses) and their base-2 log-sum-exps.  Flags and log-sum-exps are kept twice, for the two warpgroups of cache_tile.cu.
+// Workspace: counts, then the slots (R rows of D values in fp32, normalised by the piece's own sum, in an order
+// that each kernel chooses) and their base-2 log-sum-exps.  Counts and log-sum-exps are kept twice, for the two warpgroups of cache_tile.cu.
 struct CacheWs {
-  unsigned long long* flag;  // [slots][2]
-  float* o;                  // [slots][R * D]
-  float* l;                  // [slots][2][R]
+  unsigned long long* count;  // [slots][2]
+  float* o;                   // [slots][R * D]
+  float* l;                   // [slots][2][R]
 };
 
 // Slots are numbered below 2 (T / C + 1) <= 2 (P + 1), T with the items' costs.
@@ -47,14 +46,14 @@ inline __host__ __device__ size_t cache_ws_bytes(int R, int D, int sm_count) {
 
 inline __host__ __device__ CacheWs cache_ws(uint8_t* ws, int R, int D, int sm_count) {
   CacheWs w;
-  w.flag = reinterpret_cast<unsigned long long*>(ws);
+  w.count = reinterpret_cast<unsigned long long*>(ws);
   w.o = reinterpret_cast<float*>(ws + cache_slots(sm_count) * 16);
   w.l = w.o + cache_slots(sm_count) * R * D;
   return w;
 }
 
-// Beginning and ending a piece takes a block about the time in which 48 KB of codes arrive.
-constexpr __host__ __device__ int cache_item_cost(int TK) { return 384 / TK; }
+// Beginning and ending a piece takes about as long as 768 of its tokens (256, 384 and 768 were tried).
+constexpr __host__ __device__ int cache_item_cost(int TK) { return 768 / TK; }
 
 // Number of keys that token i of Nq queries sees in a sequence of `len` tokens.
 __device__ __forceinline__ int cache_row_limit(int mask, int len, int Nq, int i) {
@@ -94,42 +93,41 @@ struct CacheItems {
   __device__ int seq_len(const CacheAttnArgs& a, int b) const { return cache_len(a.c, __ldg(a.lens + b)); }
 };
 
-// A piece of an item for one block, as the producer announces it (12 ints of shared memory).
+// A piece of an item for one worker, as the producer announces it.
 struct CachePiece {
   int b, head, rt, len;  // b < 0: there are no more
   int begin, end;        // key tiles of the item
   int slot;              // -1: the whole item, else its place in the workspace
-  int first, ntiles;     // number of the item's first tile, and its tiles
-  int C, by_piece;
+  int bucket, pieces;    // first / C of the item's first tile, and the item's pieces
 
-  // Pieces of the item, and the slot of the i-th.
-  __device__ int pieces() const { return by_piece ? (ntiles + C - 1) / C : (first + ntiles - 1) / C - first / C + 1; }
-  __device__ int slot_of(int i) const {
-    const int c = by_piece ? (first + i * C) / C : first / C + i;
-    return 2 * c + (i != 0);
-  }
+  __device__ int slot_of(int i) const { return 2 * (bucket + i) + (i != 0); }  // of the item's i-th piece
 };
-constexpr int kPieceInts = 12;
+constexpr int kPieceInts = 12;  // room for one
 
-// Called by a warp (all lanes) after the block, or the warpgroup `part`, has stored its piece and met: sets the
-// piece's flag; true where every piece of the item is then there, and their flags are zero again.
+// Called by a warp (all lanes) after the block's worker, or the warpgroup `part`, has stored its piece and met:
+// counts the piece; true where every piece of the item has been, and the count is at rest again.
 __device__ __forceinline__ bool cache_piece_done(const CacheWs& ws, const CachePiece& p, int part, unsigned long long tag) {
-  const int lane = threadIdx.x & 31;
-  asm volatile("fence.acq_rel.gpu;" ::: "memory");  // the partial result, before its flag
-  if (lane == 0) *reinterpret_cast<volatile unsigned long long*>(ws.flag + 2 * p.slot + part) = tag;
-  __syncwarp();
-  asm volatile("fence.sc.gpu;" ::: "memory");  // of two blocks that set their flags, one at least sees both
-  const int n = p.pieces();
-  bool all = true;
-  for (int i = lane; i < n; i += 32) all = all && *reinterpret_cast<volatile unsigned long long*>(ws.flag + 2 * p.slot_of(i) + part) == tag;
-  all = __all_sync(0xffffffffu, all);
-  if (all) {
-    asm volatile("fence.acq_rel.gpu;" ::: "memory");  // the other blocks' partial results, after their flags
-    for (int i = lane; i < n; i += 32) ws.flag[2 * p.slot_of(i) + part] = 0ull;
+  bool all = false;
+  if ((threadIdx.x & 31) == 0) {
+    unsigned long long* at = ws.count + 2 * p.slot_of(0) + part;
+    const unsigned long long n = static_cast<unsigned long long>(p.pieces);
+    unsigned long long seen, old;
+    // release: the partial result before the count; acquire: the others' partial results after it
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(seen) : "l"(at) : "memory");
+    for (;;) {
+      if ((seen & ~0xffffull) == tag) {  // nobody puts it to rest before this piece is counted
+        asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;" : "=l"(old) : "l"(at), "l"(1ull) : "memory");
+        all = (old & 0xffffull) + 1ull == n;
+        if (all) asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(at), "l"(0ull) : "memory");
+        break;
+      }
+      asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;" : "=l"(old) : "l"(at), "l"(seen), "l"(tag | 1ull) : "memory");
+      if (old == seen) break;  // the first of several
+      seen = old;
+    }
   }
-  return all;
+  return __shfl_sync(0xffffffffu, all, 0);
 }
-
 // The division, and a block's walk over its pieces.  Built by NT threads of a block (numbered `tid`, whole
 // warps that meet at hardware barrier `bar`), then walked by each of their warps, all lanes alike.
 template <int R, int TK, int NT, int kMinTiles>
@@ -277,11 +275,10 @@ struct CacheWalk {
     p.rt = rt;
     p.len = len;
     p.begin = tile;
-    p.first = item_first + items.kItemCost;
-    p.ntiles = ntiles;
-    p.C = C;
-    p.by_piece = by_piece;
-    p.slot = tile == 0 && p.end == ntiles ? -1 : 2 * ((p.first + tile) / C) + (tile != 0);
+    const int first = item_first + items.kItemCost;
+    p.bucket = first / C;
+    p.pieces = by_piece ? (ntiles + C - 1) / C : (first + ntiles - 1) / C - p.bucket + 1;
+    p.slot = p.pieces == 1 ? -1 : p.slot_of(by_piece ? tile / C : (first + tile) / C - p.bucket);
     return true;
   }
 };

@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           if (!(ok = stored())) break;
           if (merge_flag[t] && !idle) {
             // L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s over the row's pieces in key order.
-            const int np = p.pieces();
+            const int np = p.pieces;
             auto lse_at = [&](int s) { return __ldcg(ws.l + (static_cast<size_t>(s) * 2 + t) * C::R + ri); };
             float mx = -INFINITY, sum = 0.f;
 #pragma unroll 1

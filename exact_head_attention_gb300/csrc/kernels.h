@@ -154,7 +154,7 @@ struct CacheAttnArgs {
   const int* lens;
   float* lse;     // [B][heads * group][Nq]
   uint8_t* ws;    // cache_sched.cuh
-  unsigned long long tag;  // of this call's flags in ws
+  unsigned long long tag;  // of this call's counts in ws: not zero, the low 16 bits are
   uint32_t* err_word;
   int B, Nq, group, mask, sm_count;
   bool bf16;
@@ -222,7 +222,7 @@ constexpr int kCacheStreamRows = 32;
 // Tokens per box of the tensor maps launch_cache_attn wants; query rows and keys of its tiles for so many
 // rows a key/value head; its workspace bytes.
 int cache_attn_box_tokens(int page, int d);
-constexpr int kCacheItemCost = 16;  // above every cache_item_cost plus a rounded-up tile
+constexpr int kCacheItemCost = 32;  // above every cache_item_cost plus a rounded-up tile
 struct CacheAttnShape {
   int rows, keys;
 };
