@@ -290,35 +290,43 @@ __device__ __forceinline__ float stage_query_rows(RowAt&& row_at, uint32_t tile,
   return back;
 }
 
-// A third of a tile's 128 tokens from codes to the operand tile; tokens at or past `valid` become zero.
-// A warp takes 16-code units such that neither its reads nor its two writes meet a bank twice in 8 lanes.
-template <int D, int FMT>
-__device__ __forceinline__ void convert_third(const uint8_t* raw, uint32_t tile, int third, int lane, int valid) {
-  constexpr int ROWS = D == 128 ? 4 : 8;            // token rows a step
-  constexpr int STEPS = 128 / ROWS, MOST = (STEPS + 2) / 3;
-  const int s0 = third * MOST;
-  const int q = lane & 3;
-  int row0, chunk;
-  if constexpr (D == 128) {
-    const int p = (lane >> 2) & 1;
-    row0 = s0 * ROWS + p + 2 * (lane >> 4);
-    chunk = p ^ ((lane >> 3) & 1);
-  } else {
-    row0 = s0 * ROWS + (lane >> 2);
-    chunk = 0;
+// A converter warp's third of a tile's 128 tokens, in two steps: the codes into registers, which frees their slot
+// for the next copy (that takes longer than the conversion), then from there to the operand tile; tokens at or past
+// `valid` become zero.  A warp takes 16-code units such that neither its reads nor its two writes meet a bank twice in
+// 8 lanes.
+template <int D>
+struct Third {
+  static constexpr int ROWS = D == 128 ? 4 : 8;  // token rows a step
+  static constexpr int STEPS = 128 / ROWS, MOST = (STEPS + 2) / 3, LEAST = STEPS - 2 * MOST;  // in all, and of a third
+  int q, row0, chunk, steps;
+  uint4 c[MOST];
+
+  __device__ Third(int third, int lane) {
+    q = lane & 3;
+    const int s0 = third * MOST;
+    steps = min(MOST, STEPS - s0);
+    if constexpr (D == 128) {
+      const int p = (lane >> 2) & 1;
+      row0 = s0 * ROWS + p + 2 * (lane >> 4);
+      chunk = p ^ ((lane >> 3) & 1);
+    } else {
+      row0 = s0 * ROWS + (lane >> 2);
+      chunk = 0;
+    }
   }
-  const uint8_t* src = raw + row0 * D + chunk * 64 + q * 16;
-  constexpr int BATCH = 6;  // steps whose codes are loaded together, so that their latencies overlap
+  __device__ __forceinline__ void load(const uint8_t* raw) {
+    const uint8_t* src = raw + row0 * D + chunk * 64 + q * 16;
 #pragma unroll
-  for (int base = 0; base < MOST; base += BATCH) {
-    uint4 c[BATCH];
+    for (int i = 0; i < MOST; ++i)
+      if (i < LEAST || i < steps) c[i] = *reinterpret_cast<const uint4*>(src + i * ROWS * D);
+  }
+  template <int FMT>
+  __device__ __forceinline__ void store(uint32_t tile, int valid) const {
+    const uint32_t dst = tile + chunk * kChunk;
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i)
-      if (base + i < MOST && s0 + base + i < STEPS) c[i] = *reinterpret_cast<const uint4*>(src + (base + i) * ROWS * D);
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      if (base + i >= MOST || s0 + base + i >= STEPS) break;
-      const int row = row0 + (base + i) * ROWS;
+    for (int i = 0; i < MOST; ++i) {
+      if (i >= LEAST && i >= steps) break;
+      const int row = row0 + i * ROWS;
       uint32_t o[8];
       codes_to_f16<FMT>(c[i].x, o[0], o[1]);
       codes_to_f16<FMT>(c[i].y, o[2], o[3]);
@@ -328,12 +336,11 @@ __device__ __forceinline__ void convert_third(const uint8_t* raw, uint32_t tile,
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = 0u;
       }
-      const uint32_t dst = tile + chunk * kChunk;
       st_shared_v4(dst + sw128_offset(row, 2 * q), o[0], o[1], o[2], o[3]);
       st_shared_v4(dst + sw128_offset(row, 2 * q + 1), o[4], o[5], o[6], o[7]);
     }
   }
-}
+};
 
 template <int D, int FMT, bool BF16, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_constant__ CacheAttnArgs a) {
@@ -601,22 +608,22 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       const int v = warp >= 13, third = warp - (v ? 13 : 10);
       int kt = 0;
       bool ok = true;
+      Third<D> part(third, lane);
       const CachePiece* p;
       for (int pi = 0; ok && (p = next_piece(pi)) != nullptr; ++pi) {
         const int len = p->len, end = p->end;
         for (int t = p->begin; t < end; ++t, ++kt) {
           const int s = kt % NS, raws = 2 * kt + v, rs = raws % NR;
           if (!(ok = mbar_wait_warp(bars.raw_full(rs), (raws / NR) & 1, wc))) break;
+          part.load(smem_raw + C::OFF_RAW + rs * C::RAW);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.raw_empty(rs));
           if (!(ok = mbar_wait_warp(v ? bars.v_empty(s) : bars.k_empty(s), ((kt / NS) & 1) ^ 1, wc))) break;
           // Hidden keys' scores are set aside by the softmax; their values must be finite.
-          convert_third<D, FMT>(smem_raw + C::OFF_RAW + rs * C::RAW, sbase + (v ? C::OFF_V : C::OFF_K) + s * C::TILE, third,
-                                lane, len - t * kTK);
+          part.template store<FMT>(sbase + (v ? C::OFF_V : C::OFF_K) + s * C::TILE, len - t * kTK);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bars.raw_empty(rs));
-            mbar_arrive(v ? bars.v_full(s) : bars.k_full(s));
-          }
+          if (lane == 0) mbar_arrive(v ? bars.v_full(s) : bars.k_full(s));
         }
         if (ok && lane == 0) mbar_arrive(bars.piece_empty(pi % kPieceRing));
       }
