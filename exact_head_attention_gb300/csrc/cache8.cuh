@@ -19,10 +19,13 @@ __device__ __forceinline__ int cache_len(const CacheView& c, int len) {
   return max(0, min(len, c.capacity));
 }
 
+// The kernels that use these are launched before the one ahead of them has finished, which may write what they
+// read: no load of theirs is a read-only one.
+
 // The table's entry for token t (0 <= t < capacity) of sequence b, and that as a page: -1 for a number
 // outside the pool.
 __device__ __forceinline__ int cache_page_number(const CacheView& c, int b, int t) {
-  return __ldg(c.table + static_cast<long long>(b) * c.width + (t >> c.page_shift));
+  return c.table[static_cast<long long>(b) * c.width + (t >> c.page_shift)];
 }
 __device__ __forceinline__ int cache_page_checked(const CacheView& c, int p) {
   return static_cast<unsigned>(p) < static_cast<unsigned>(c.num_pages) ? p : -1;

@@ -73,8 +73,8 @@ attn_status io_args(const attn_cache* cache, const void* K, attn_strides ks, con
   if (!api_strides(ks, B, cache->heads, cache->d, &a->sk) || !api_strides(vs, B, cache->heads, cache->d, &a->sv))
     return ATTN_ERR_INVALID_ARG;
   if (!aligned(K, 16) || !aligned(V, 16) || !aligned(start, 4) || !aligned(count, 4)) return ATTN_ERR_MISALIGNED;
-  // blocks of the launches, at the fewest rows (16) that one takes
-  if (static_cast<long long>(B) * cache->heads > 0x7fffffffLL / (N / 16 + 2)) return ATTN_ERR_INVALID_ARG;
+  // units of the launches, at the fewest rows (16) that one takes
+  if (static_cast<long long>(B) * cache->heads > 0x3fffffffLL / (N / 16 + 2)) return ATTN_ERR_INVALID_ARG;
   a->k = const_cast<void*>(K);
   a->v = const_cast<void*>(V);
   a->start = start;
@@ -111,6 +111,7 @@ extern "C" attn_status attn_cache_write(const attn_cache* cache, const void* K, 
   DeviceInfo dev;
   if ((st = api_device(&dev)) != ATTN_OK) return st;
   a.err_word = dev.err_word;
+  a.sm_count = dev.sm_count;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return api_finish(launch_cache_write(a, s), s);
 }
@@ -125,6 +126,7 @@ extern "C" attn_status attn_cache_read(const attn_cache* cache, const int* start
   DeviceInfo dev;
   if ((st = api_device(&dev)) != ATTN_OK) return st;
   a.err_word = dev.err_word;
+  a.sm_count = dev.sm_count;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return api_finish(launch_cache_read(a, s), s);
 }

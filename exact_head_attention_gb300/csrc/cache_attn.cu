@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
         r1.ks = r1.vs = there ? qnan() : 0.f;
         if (r1.page >= 0) {
           const long long h = static_cast<long long>(r1.page) * a.c.heads + r1.head;
-          r1.ks = __ldg(a.c.k_scale + h);
-          r1.vs = __ldg(a.c.v_scale + h);
+          r1.ks = a.c.k_scale[h];
+          r1.vs = a.c.v_scale[h];
         } else if (there) {
           record_page_error(a.err_word);
         }

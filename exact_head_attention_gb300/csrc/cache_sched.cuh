@@ -90,7 +90,7 @@ struct CacheItems {
     head_units(a, len, t, p);
     return t;
   }
-  __device__ int seq_len(const CacheAttnArgs& a, int b) const { return cache_len(a.c, __ldg(a.lens + b)); }
+  __device__ int seq_len(const CacheAttnArgs& a, int b) const { return cache_len(a.c, a.lens[b]); }
 };
 
 // A piece of an item for one worker, as the producer announces it.
@@ -151,7 +151,7 @@ struct CacheWalk {
     const int b1 = min(a.B - b0, per) + b0;
     int n = 0, m = 0;
     for (int i = b0; i < b1; ++i) {
-      const int raw = __ldg(a.lens + i), l = cache_len(a.c, raw);
+      const int raw = a.lens[i], l = cache_len(a.c, raw);
       if (raw != l && block == 0) record_page_error(a.err_word);
       int t, p;
       items.head_units(a, l, t, p);

@@ -262,7 +262,7 @@ __device__ __forceinline__ float stage_query_rows(RowAt&& row_at, uint32_t tile,
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       const uint16_t* src = row_at(kb + i * ROWS + lane / UNITS);
-      xs[i] = src != nullptr ? __ldg(reinterpret_cast<const uint4*>(src) + u) : make_uint4(0u, 0u, 0u, 0u);
+      xs[i] = src != nullptr ? reinterpret_cast<const uint4*>(src)[u] : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
@@ -497,8 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           r1.ks = r1.vs = there ? __int_as_float(0x7fffffff) : 0.f;
           if (r1.page >= 0) {
             const long long h = static_cast<long long>(r1.page) * a.c.heads + r1.head;
-            r1.ks = __ldg(a.c.k_scale + h);
-            r1.vs = __ldg(a.c.v_scale + h);
+            r1.ks = a.c.k_scale[h];
+            r1.vs = a.c.v_scale[h];
           } else if (there) {
             record_page_error(a.err_word);
           }

@@ -138,6 +138,8 @@ struct CacheIoArgs {
   RowStrides sk, sv;
   const int *start, *count;  // write: may be nullptr; read: count is lens
   int B, N;
+  int parts;  // units a sequence and head: pages that N tokens can reach (write), groups of rows (read)
+  int sm_count;
   bool bf16;
   uint32_t* err_word;
 };
@@ -212,8 +214,8 @@ cudaError_t launch_kl_dk(const KlArgs& a, cudaStream_t stream);
 // Row values + zeroed accumulator, then the one-pass key-tile kernel (dK and the dQ reduce-adds); the
 // caller converts the accumulator with the attention backward's kBwdConvert step.
 cudaError_t launch_kl_bwd_fused(const KlArgs& a, cudaStream_t stream);
-cudaError_t launch_cache_write(const CacheIoArgs& a, cudaStream_t stream);
-cudaError_t launch_cache_read(const CacheIoArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_write(CacheIoArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_read(CacheIoArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_tile(const CacheAttnArgs& a, cudaStream_t stream);
 // Up to this many query rows a key/value head attn_fwd_cache streams the codes through the warp-level
