@@ -130,15 +130,19 @@ struct Bars {
 // (MASKED).  All 128 scores are read for the maximum; the upper 64 are read again for P, which saves the
 // registers that they would hold meanwhile.  P's packed columns overwrite scores of the lower 64 only.
 // wait_pv() runs (warp-uniformly) before O is rescaled: the chain's last product may still be under way.
-template <int D, bool MASKED, typename WaitPv>
-__device__ __forceinline__ void softmax_scaled(uint32_t tS, uint32_t tO, const float* sc, int lim, float fac, bool first,
-                                               float& m, float& l, float& vref, float& vinv, WaitPv&& wait_pv) {
-  uint32_t sr[4][32];
+// HALF: the row is here twice, and this thread has 64 of its 128 scores: from column 64 `half` on, `sc` and `lim` likewise.
+// The other half of its P is zero.
+template <int D, bool MASKED, bool HALF, typename WaitPv>
+__device__ __forceinline__ void softmax_scaled(uint32_t tS, int half, uint32_t tO, const float* sc, int lim, float fac,
+                                               bool first, float& m, float& l, float& vref, float& vinv, WaitPv&& wait_pv) {
+  constexpr int CHUNKS = HALF ? 2 : 4, GROUPS = 2 * CHUNKS;
+  const uint32_t tX = HALF ? tS + half * 64 : tS, tP = HALF ? tS + half * 32 : tS;
+  uint32_t sr[CHUNKS][32];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
-  float f[8], vs[8];
+  for (int c = 0; c < CHUNKS; ++c) tmem_ld32(tX + c * 32, sr[c]);
+  float f[GROUPS], vs[GROUPS];
 #pragma unroll
-  for (int g = 0; g < 8; g += 4) {
+  for (int g = 0; g < GROUPS; g += 4) {
     const float4 k = *reinterpret_cast<const float4*>(sc + g), v = *reinterpret_cast<const float4*>(sc + 8 + g);
     f[g] = fac * k.x;
     f[g + 1] = fac * k.y;
@@ -151,10 +155,10 @@ __device__ __forceinline__ void softmax_scaled(uint32_t tS, uint32_t tO, const f
   }
   tmem_wait_ld();
 #pragma unroll
-  for (int c = 0; c < 4; ++c) reg_fence32(sr[c]);
+  for (int c = 0; c < CHUNKS; ++c) reg_fence32(sr[c]);
   float m_new = -INFINITY, v_new = -INFINITY;
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
+  for (int g = 0; g < GROUPS; ++g) {
     float a = -INFINITY, b = -INFINITY;  // a NaN is passed over: it is met below
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
@@ -228,19 +232,29 @@ __device__ __forceinline__ void softmax_scaled(uint32_t tS, uint32_t tO, const f
         pk[i] = pack2<false>(y0, y1);
       }
     }
-    tmem_st16(tS + c * 16, pk);
+    tmem_st16(tP + c * 16, pk);
   };
   chunk(0, sr[0]);
-  uint32_t x2[32], x3[32];
-  tmem_ld32(tS + 64, x2);
-  chunk(1, sr[1]);
-  tmem_wait_ld();
-  reg_fence32(x2);
-  tmem_ld32(tS + 96, x3);
-  chunk(2, x2);
-  tmem_wait_ld();
-  reg_fence32(x3);
-  chunk(3, x3);
+  if constexpr (HALF) {
+    chunk(1, sr[1]);
+    uint32_t none[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) none[i] = 0u;
+    const uint32_t tZ = tS + (1 - half) * 32;
+    tmem_st16(tZ, none);
+    tmem_st16(tZ + 16, none);
+  } else {
+    uint32_t x2[32], x3[32];
+    tmem_ld32(tS + 64, x2);
+    chunk(1, sr[1]);
+    tmem_wait_ld();
+    reg_fence32(x2);
+    tmem_ld32(tS + 96, x3);
+    chunk(2, x2);
+    tmem_wait_ld();
+    reg_fence32(x3);
+    chunk(3, x3);
+  }
   float s0, s1;
   f2_unpack(f2_add(acc[0], acc[1]), s0, s1);
   l += s0 + s1;
@@ -643,7 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     uint32_t seq = 0;                        // steps of both chains in earlier pieces
     uint32_t jc = 0, dc = 0;                 // waits of join and stored
     bool ok = true;
-    const int ri = (PAIR ? t * 128 : 0) + r;  // row of the item
+    const bool twice = !PAIR && rows <= 64;  // lanes 64 + r have row r as well, and the second half of each tile's keys
+    const int half = twice ? quarter >> 1 : 0;
+    const int ri = PAIR ? t * 128 + r : twice ? r & 63 : r;  // row of the item
     // Both softmax warpgroups meet (!PAIR), or one.  Bounded waits: after a failed one elsewhere these give up too.
     auto join = [&]() -> bool {
       __syncwarp();
@@ -716,10 +732,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
                   tc_fence_after();
                 }
               };
-              if ((i + 1) * kTK > lim_min)
-                softmax_scaled<D, true>(tS + b * 128, tO, scales, lim_row - i * kTK, fac, j == 0, m, l, vref, vinv, wait_pv);
-              else
-                softmax_scaled<D, false>(tS + b * 128, tO, scales, kTK, fac, j == 0, m, l, vref, vinv, wait_pv);
+              const bool masked = (i + 1) * kTK > lim_min;
+              const int lim = lim_row - i * kTK;
+              if (!PAIR && twice) {
+                if (masked)
+                  softmax_scaled<D, true, true>(tS + b * 128, half, tO, scales + 4 * half, lim - 64 * half, fac, j == 0, m, l, vref, vinv, wait_pv);
+                else
+                  softmax_scaled<D, false, true>(tS + b * 128, half, tO, scales + 4 * half, kTK, fac, j == 0, m, l, vref, vinv, wait_pv);
+              } else if (masked) {
+                softmax_scaled<D, true, false>(tS + b * 128, 0, tO, scales, lim, fac, j == 0, m, l, vref, vinv, wait_pv);
+              } else {
+                softmax_scaled<D, false, false>(tS + b * 128, 0, tO, scales, kTK, fac, j == 0, m, l, vref, vinv, wait_pv);
+              }
               tmem_wait_st();
             }
             tc_fence_before();
@@ -746,13 +770,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           tc_fence_before();
           if (!(ok = ok && join())) break;
           use1 = both;
-          const float2 x = stat[r], y = stat[128 + r];
-          const float mx = fmaxf(x.x, y.x), ms = mx == -INFINITY ? 0.f : mx;
-          const float e0 = x.y == 0.f ? 0.f : ex2_approx(x.x - ms), e1 = y.y == 0.f ? 0.f : ex2_approx(y.x - ms);
-          const float sum = (x.y == 0.f ? 0.f : e0 * x.y) + (y.y == 0.f ? 0.f : e1 * y.y);
+          // The row's statistics: of both chains, and of both halves of the keys.
+          float2 x = stat[r], y = stat[128 + r], x2 = make_float2(-INFINITY, 0.f), y2 = x2;
+          if (twice) {
+            x2 = stat[r ^ 64];
+            y2 = stat[128 + (r ^ 64)];
+          }
+          const float mx = fmaxf(fmaxf(x.x, y.x), fmaxf(x2.x, y2.x)), ms = mx == -INFINITY ? 0.f : mx;
+          auto share = [&](float2 v) { return v.y == 0.f ? 0.f : ex2_approx(v.x - ms); };
+          auto part_sum = [&](float2 v) { return v.y == 0.f ? 0.f : share(v) * v.y; };
+          const float sum = part_sum(x) + part_sum(y) + (part_sum(x2) + part_sum(y2));
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          w0 = e0 * stat_v[quarter] * inv;
-          w1 = use1 ? e1 * stat_v[4 + quarter] * inv : 0.f;
+          w0 = share(x) * stat_v[quarter] * inv;
+          w1 = use1 ? share(y) * stat_v[4 + quarter] * inv : 0.f;
           lse2 = sum == 0.f ? -INFINITY : ms - kShift + __log2f(sum);
         }
         if (!ok) break;
@@ -765,10 +795,28 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         auto part_of = [&](int slot) {
           return reinterpret_cast<float4*>(ws.o) + (static_cast<size_t>(slot) * (D / 4) + c0 / 4) * C::R + ri;
         };
-        if (!idle) {
+        const uint32_t at0 = PAIR ? tO : tmem + C::TM_O + lane_bits;
+        // Two halves meet in the query tile, which is free: column by column, the rows side by side.
+        float* const meet = reinterpret_cast<float*>(smem_raw + C::OFF_Q) + c0 * 64 + ri;
+        if (!PAIR && twice) {
+          if (half && !idle) {
+#pragma unroll 1
+            for (int c = 0; c < COLS; c += 16) {
+              uint32_t x[16], y[16];
+              tmem_ld16(at0 + c0 + c, x);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = 0u;
+              if (use1) tmem_ld16(at0 + C::TM_OT + c0 + c, y);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) meet[(c + e) * 64] = fmaf(__uint_as_float(y[e]), w1, __uint_as_float(x[e]) * w0);
+            }
+          }
+          if (!(ok = stored())) break;
+        }
+        const bool writes = !idle && half == 0;
+        if (writes) {
           uint16_t* dst = out_row(p, w) + c0;
           float4* part = part_of(max(slot, 0));
-          const uint32_t at0 = PAIR ? tO : tmem + C::TM_O + lane_bits;
 #pragma unroll 1
           for (int c = 0; c < COLS; c += 16) {
             uint32_t x[16];
@@ -781,6 +829,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
             } else {
 #pragma unroll
               for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * w0);
+            }
+            if (!PAIR && twice) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) + meet[(c + e) * 64]);
             }
             if (slot >= 0) {
 #pragma unroll
@@ -814,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
             if (lane == 0) merge_flag[t] = all;
           }
           if (!(ok = stored())) break;
-          if (merge_flag[t] && !idle) {
+          if (merge_flag[t] && writes) {
             // L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s over the row's pieces in key order.
             const int np = p.pieces;
             auto lse_at = [&](int s) { return __ldcg(ws.l + (static_cast<size_t>(s) * 2 + t) * C::R + ri); };
