@@ -34,6 +34,24 @@ __device__ __forceinline__ int cache_page(const CacheView& c, int b, int t) {
   return cache_page_checked(c, cache_page_number(c, b, t));
 }
 
+// A page's scale of the values.  An infinite one counts as NaN: as a number it would set the reference that the
+// rows' probabilities are scaled by, for rows that do not see the page as well.
+__device__ __forceinline__ float cache_v_scale(const CacheView& c, long long page_head) {
+  const float s = c.v_scale[page_head];
+  return s == INFINITY ? __int_as_float(0x7fffffff) : s;
+}
+
+// The upper bits of the bytes of w that are an e4m3 NaN.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t nan_codes(const uint4& w) {
+  return nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w);
+}
+// w with zeros in their place.
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) { return w & ~((nan_codes(w) >> 7) * 0xffu); }
+__device__ __forceinline__ uint4 without_nan(const uint4& w) {
+  return make_uint4(without_nan(w.x), without_nan(w.y), without_nan(w.z), without_nan(w.w));
+}
+
 // Four codes as two fp16 pairs: bytes 0, 1 and bytes 2, 3.  fp16 holds every code exactly: e4m3 has 4
 // significant bits and exponents from -9, and an integer of 8 bits has 8.
 template <int FMT>

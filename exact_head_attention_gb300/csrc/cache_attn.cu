@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
         if (r1.page >= 0) {
           const long long h = static_cast<long long>(r1.page) * a.c.heads + r1.head;
           r1.ks = a.c.k_scale[h];
-          r1.vs = a.c.v_scale[h];
+          r1.vs = cache_v_scale(a.c, h);
         } else if (there) {
           record_page_error(a.err_word);
         }
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
   regs_increase<kComputeRegs>();
   const int gw = warp % kGroup, tid = threadIdx.x % (32 * kGroup);  // in the worker
   const int g = lane >> 2, t4 = lane & 3;
-  const uint8_t* ring = smem_raw + warp * (NST * 2 * C::TILE);
+  uint8_t* ring = smem_raw + warp * (NST * 2 * C::TILE);
   float* st_m = reinterpret_cast<float*>(wmem + C::W_STAT);
   float* st_l = st_m + kGroup * C::R;
   float* st_v = st_l + kGroup * C::R;
@@ -496,6 +496,36 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
             y1 = x1 == -INFINITY ? 0.f : y1;
           }
           pb[nt][nb] = transpose8(pack2<false>(y0, y1));
+        }
+      }
+
+      // A NaN among the values of a token that some row does not see would reach that row through its zero
+      // probability: such codes become zero, and the sums of the rows that see the token NaN.
+      if (FMT == kE4M3 && masked && lim_min < len) {
+        uint32_t found = 0u;
+#pragma unroll
+        for (int i = 0; i < C::TILE / 512; ++i) found |= nan_codes(reinterpret_cast<const uint4*>(bv)[i * 32 + lane]);
+        if (__any_sync(0xffffffffu, found != 0u)) {
+#pragma unroll 1
+          for (int r = 0; r < C::TK; r += 32) {
+            bool bad = false;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint4* at = reinterpret_cast<uint4*>(ring + s * 2 * C::TILE + C::TILE + tile_at<D>(r + lane, c));
+              bad = bad || nan_codes(*at) != 0u;
+              *at = without_nan(*at);
+            }
+            const uint32_t tokens = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int seen = lim[nt][e] - key0 - r;
+                if (seen > 0 && (tokens & (seen >= 32 ? ~0u : (1u << seen) - 1u)) != 0u) l[nt][e] = __int_as_float(0x7fffffff);
+              }
+          }
+          __syncwarp();
+          fence_proxy_async_smem();  // the next copy into the slot comes after these writes
         }
       }
 

@@ -196,7 +196,7 @@ struct CacheWalk {
       step = blocks;
     } else {
       at = block * C;
-      stop = min(total, at + C);
+      stop = total - at > C ? at + C : total;
       step = 0;
     }
   }

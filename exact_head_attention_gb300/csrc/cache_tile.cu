@@ -29,6 +29,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "cache8.cuh"
 #include "cache_sched.cuh"
 #include "kernels.h"
@@ -44,6 +46,9 @@ static_assert(2 * kRegsSoftmax + 2 * kRegsOther == 4 * 128, "register split must
 constexpr int kTK = 128;
 constexpr uint32_t kChunk = 128 * 128;  // 128 rows x 128 bytes
 constexpr int kPieceRing = 3, kMetaRing = 16;
+// Flags of tiles that an item's rows see in part: at most 3 at a piece's end (the rows of an item see the keys of at
+// most 256 tokens less or more), and the converters are at most NS tiles further.
+constexpr int kFlagRing = 8;
 constexpr float kShift = 3.f, kVrefLag = 16.f;  // as in cache_attn.cu
 
 template <int D, bool PAIR>
@@ -59,6 +64,7 @@ struct Cfg {
   static_assert((NR + 1) / 2 + NS + NB + 1 <= kMetaRing, "scales of the tiles under way");
   static constexpr uint32_t TM_O = NB * 128;                   // O_t at TM_O + t TM_OT
   static constexpr uint32_t TM_OT = D;
+  static_assert(3 + NS <= kFlagRing, "flags of the tiles under way");
   static_assert(TM_O + 2 * TM_OT <= 512, "tensor memory");
   using Walk = CacheWalk<R, kTK, 32, MIN_TILES>;
   static constexpr uint32_t OFF_Q = 0;
@@ -67,7 +73,8 @@ struct Cfg {
   static constexpr uint32_t OFF_RAW = OFF_V + NS * TILE;
   static constexpr uint32_t OFF_META = OFF_RAW + NR * RAW;           // [kMetaRing] ks[8], vs[8]
   static constexpr uint32_t OFF_STAT = OFF_META + kMetaRing * 64;    // !PAIR: {m, l} [2][128], vref [2][4]
-  static constexpr uint32_t OFF_PIECE = OFF_STAT + (PAIR ? 0 : 2 * 128 * 8 + 32);
+  static constexpr uint32_t OFF_FLAG = OFF_STAT + (PAIR ? 0 : 2 * 128 * 8 + 32);  // [kFlagRing][128]: a token has a NaN value
+  static constexpr uint32_t OFF_PIECE = OFF_FLAG + kFlagRing * 128;
   static constexpr uint32_t OFF_BAR = OFF_PIECE + kPieceRing * kPieceInts * 4;
   static constexpr int NBAR = 2 + 4 * NS + 2 * NR + 6 + kMetaRing + 2 * kPieceRing + 4;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
@@ -334,6 +341,30 @@ struct Third {
     for (int i = 0; i < MOST; ++i)
       if (i < LEAST || i < steps) c[i] = *reinterpret_cast<const uint4*>(src + i * ROWS * D);
   }
+  // NaN codes become zero where they lie, before load(); bit i: the unit of step i had one.  (In registers, between
+  // load() and store(), this took the registers that both need: 3 % of the whole.)
+  __device__ __forceinline__ uint32_t drop_nan(uint8_t* raw) const {
+    uint32_t bad = 0u;
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i) {
+      uint4* at = reinterpret_cast<uint4*>(raw + (row0 + i * ROWS) * D + chunk * 64 + q * 16);
+      if (nan_codes(*at) != 0u) {
+        *at = without_nan(*at);
+        bad |= 1u << i;
+      }
+    }
+    fence_proxy_async_smem();  // the next copy comes after these writes
+    return bad;
+  }
+  // Flags of the tokens that had one.
+  __device__ __forceinline__ void mark(uint8_t* flags, uint32_t bad) const {
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i)
+      if (q == 0 && chunk == 0) flags[row0 + i * ROWS] = 0;
+    __syncwarp();
+#pragma unroll 1
+    for (; bad != 0u; bad &= bad - 1u) flags[row0 + (__ffs(bad) - 1) * ROWS] = 1;
+  }
   template <int FMT>
   __device__ __forceinline__ void store(uint32_t tile, int valid) const {
     const uint32_t dst = tile + chunk * kChunk;
@@ -421,6 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     const CachePiece* p = pieces + i % kPieceRing;
     return p->b >= 0 ? p : nullptr;
   };
+  // The least number of keys that a row of a piece's item sees.  In tiles that some row sees in part only, a NaN among
+  // the values would reach rows that do not see it through their zero probabilities.  There the converters turn
+  // e4m3 NaN into zero and mark the token, and the softmax makes the sums of the rows that see it NaN.
+  auto least_limit = [&](const CachePiece& p) { return cache_row_limit(a.mask, p.len, a.Nq, p.rt * C::R / a.group); };
   // Whether both chains have steps in a piece, and the steps of chain t.
   auto both_chains = [&](const CachePiece& p) { return PAIR ? rows - p.rt * C::R > 128 : p.end - p.begin > 1; };
   auto chain_steps = [&](const CachePiece& p, int t) {
@@ -512,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           if (r1.page >= 0) {
             const long long h = static_cast<long long>(r1.page) * a.c.heads + r1.head;
             r1.ks = a.c.k_scale[h];
-            r1.vs = a.c.v_scale[h];
+            r1.vs = cache_v_scale(a.c, h);
           } else if (there) {
             record_page_error(a.err_word);
           }
@@ -625,20 +660,30 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       Third<D> part(third, lane);
       const CachePiece* p;
       for (int pi = 0; ok && (p = next_piece(pi)) != nullptr; ++pi) {
-        const int len = p->len, end = p->end;
-        for (int t = p->begin; t < end; ++t, ++kt) {
+        const int len = p->len, end = p->end, lim_min = least_limit(*p);
+        const int partly = FMT == kE4M3 && v && lim_min < len ? lim_min / kTK : end;  // the first tile that some row sees in part
+        int t = p->begin;
+        auto convert = [&](auto drop) __attribute__((always_inline)) -> bool {  // drop: NaN among the values
+          constexpr bool kDrop = decltype(drop)::value;
           const int s = kt % NS, raws = 2 * kt + v, rs = raws % NR;
-          if (!(ok = mbar_wait_warp(bars.raw_full(rs), (raws / NR) & 1, wc))) break;
+          if (!mbar_wait_warp(bars.raw_full(rs), (raws / NR) & 1, wc)) return false;
+          uint32_t bad = 0u;
+          if constexpr (kDrop) bad = part.drop_nan(smem_raw + C::OFF_RAW + rs * C::RAW);
           part.load(smem_raw + C::OFF_RAW + rs * C::RAW);
           __syncwarp();
           if (lane == 0) mbar_arrive(bars.raw_empty(rs));
-          if (!(ok = mbar_wait_warp(v ? bars.v_empty(s) : bars.k_empty(s), ((kt / NS) & 1) ^ 1, wc))) break;
+          if (!mbar_wait_warp(v ? bars.v_empty(s) : bars.k_empty(s), ((kt / NS) & 1) ^ 1, wc)) return false;
           // Hidden keys' scores are set aside by the softmax; their values must be finite.
+          if constexpr (kDrop) part.mark(smem_raw + C::OFF_FLAG + kt % kFlagRing * 128, bad);
           part.template store<FMT>(sbase + (v ? C::OFF_V : C::OFF_K) + s * C::TILE, len - t * kTK);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(v ? bars.v_full(s) : bars.k_full(s));
-        }
+          return true;
+        };
+        for (; ok && t < min(partly, end); ++t, ++kt) ok = convert(std::false_type{});
+        if constexpr (FMT == kE4M3)
+          for (; ok && t < end; ++t, ++kt) ok = convert(std::true_type{});
         if (ok && lane == 0) mbar_arrive(bars.piece_empty(pi % kPieceRing));
       }
     }
@@ -713,8 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           const float fac = a.scale * 1.4426950408889634f * back;
           const int key_first = p.begin * kTK;
           const int lim_row = cache_row_limit(a.mask, p.len, a.Nq, w.tok) - key_first;
-          // the least of this warp's rows
-          const int lim_min = cache_row_limit(a.mask, p.len, a.Nq, min(row_first, rows - 1) / a.group) - key_first;
+          const int lim_min = least_limit(p) - key_first;
           for (int j = 0; j < n; ++j) {
             const int i = PAIR ? j : 2 * j + t, nt = kt + i;  // key tile
             const uint32_t g = seq + (both ? 2 * j + t : j), b = g % NB;
@@ -752,7 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
             if (!ok) break;
           }
         }
-        // Every product of the piece has completed once its last value tile is free: this chain's and the other's.
+        // Every product of the piece has completed once its last value tile is free.  (!PAIR: the chain that had no part
+        // in that tile may find the barrier a phase behind and pass early; it goes on only once both have met below.)
         if (ok) {
           const int nv = kt + p.end - p.begin - 1;
           ok = mbar_wait_warp(bars.v_empty(nv % NS), (nv / NS) & 1, wc);
@@ -787,6 +832,27 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         }
         if (!ok) break;
         tc_fence_after();
+        // Rows that see a token with a NaN among its values.  Flags are written before their tile's products are issued,
+        // and those have completed.  (Looked at tile by tile in the loop, 4 % of the whole.)
+        if (FMT == kE4M3 && !idle) {
+          const int lim_min = least_limit(p), lim_row = cache_row_limit(a.mask, p.len, a.Nq, row_of(p).tok);
+          if (lim_min < p.len) {
+#pragma unroll 1
+            for (int tile = max(p.begin, lim_min / kTK); tile < p.end; ++tile) {
+              const uint8_t* flags = smem_raw + C::OFF_FLAG + ((kt + tile - p.begin) % kFlagRing) * 128;
+              uint32_t found = 0u;
+#pragma unroll 1
+              for (int c = 0; c < 128; c += 16) {
+                const uint4 x = *reinterpret_cast<const uint4*>(flags + c);
+                found |= x.x | x.y | x.z | x.w;
+              }
+              if (found == 0u) continue;
+#pragma unroll 1
+              for (int c = 0; c < min(lim_row - tile * kTK, 128); ++c)
+                if (flags[c]) w0 = w1 = lse2 = __int_as_float(0x7fffffff);
+            }
+          }
+        }
         constexpr int COLS = PAIR ? D : D / 2;  // this thread's columns of its row
         const int c0 = PAIR ? 0 : t * COLS;
         const Row w = row_of(p);

@@ -532,6 +532,8 @@ attn_status attn_bwd_noalloc(const void* Q, const void* K, const void* V, const 
  * outside [0, num_pages) makes its tokens NaN when read and keeps them from
  * being written.  Each of these records ATTN_ERR_PAGE in the device error word
  * (attn_check_device_error); no memory outside the arrays is touched.
+ * Scales are not negative; a NaN scale makes its tokens NaN, and so does an
+ * infinite one of the values in the attention.
  * The pages of the reference describe caches in the attention's own type only;
  * the 8-bit cache has no counterpart there.
  */
@@ -571,8 +573,8 @@ typedef struct attn_cache {
  * values makes that page's scale for the head NaN: all its tokens read as NaN.
  * Rows of a page past start + count keep their codes.  A sequence whose start
  * is negative, or the part of one past its page table, is not written
- * (ATTN_ERR_PAGE in the error word); count[b] is taken within [0, N].  One
- * launch; no workspace.  Errors as attn_fwd_strided, plus ATTN_ERR_INVALID_ARG
+ * (ATTN_ERR_PAGE in the error word); count[b] is taken within [0, N], with the
+ * same error where it is not.  One launch; no workspace.  Errors as attn_fwd_strided, plus ATTN_ERR_INVALID_ARG
  * for a cache that breaks the rules above.  The pages have no counterpart.
  */
 attn_status attn_cache_write(const attn_cache* cache, const void* K, attn_strides k_strides, const void* V,
@@ -598,13 +600,17 @@ attn_status attn_cache_read(const attn_cache* cache, const int* start, const int
  * last tokens).  Q, O: [B, H, Nq, d] 16-bit views; LSE [B, H, Nq] fp32.  H is
  * a multiple of cache->heads, and query head h reads key/value head
  * h / (H / cache->heads).  A row that sees no token gets O = 0, LSE = -inf.  A
- * NaN token makes the rows that see it NaN, and no others.
+ * token with a NaN scale makes the rows that see it NaN, and a NaN code (E4M3)
+ * at least the components that it enters; a row that does not see the token is
+ * not touched by either.
  * The codes are multiplied as they are (fp16 holds every code exactly) and the
  * scales applied to the products; Q in bf16 is scaled by a power of two per
  * row to fit fp16; the probabilities are rounded to fp16, sums are fp32.  The
  * same bits on every run.
  * workspace: attn_fwd_cache_workspace_size bytes, 256-byte aligned, contents
- * on entry irrelevant; calls that may run at the same time need one each.
+ * on entry irrelevant; calls that may run at the same time need one each.  After
+ * a wait that timed out (attn_check_device_error), the workspace of a captured
+ * call has to be set to zeros before the graph is replayed.
  * Errors as attn_fwd_strided, plus ATTN_ERR_WORKSPACE, and
  * ATTN_ERR_INVALID_ARG for a cache that breaks the rules of attn_cache, an H
  * that is no multiple of its heads, and more than 2^31 - 1 query rows, or tiles

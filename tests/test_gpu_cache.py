@@ -204,6 +204,103 @@ def test_nan_codes_behind_the_length_are_not_met():
         check_attention(_q(3, 4, 2, 128, "bf16"), cache, host, table, lens)
 
 
+def _plain_rows(q, cache, lens, mask):
+    o, lse = exattn.forward_cache(q.to(DEV), cache, torch.tensor(lens, dtype=torch.int32, device=DEV), mask)
+    assert exattn.check_device_error() == 0
+    return o.cpu(), lse.cpu()
+
+
+ROWS = [(1, 5), (2, 8), (3, 10), (1, 40), (2, 32), (1, 65), (1, 128), (1, 200), (2, 150)]
+
+
+@pytest.mark.parametrize("mask", ["bottom_right", True], ids=str)
+@pytest.mark.parametrize("group,n", ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_codes_hidden_from_some_rows(group, n, mask, d):
+    """A NaN among the codes of a token that only a sequence's last queries see."""
+    lens = [n + 37, 300, n]
+    cache, host, table = make_cache(3, 2, 16, d, 20, "e4m3", seed=21)
+    q = _q(3, 2 * group, n, d, "bf16", seed=5)
+    want, want_lse = _plain_rows(q, cache, lens, mask)
+    for b, head, at, col in ((0, 1, (lens[0] if mask == "bottom_right" else n) - 2, 5), (2, 0, n // 2, d - 1)):
+        cache.v.view(torch.uint8)[table[b, at // 16].item(), head, at % 16, col] = 0xFF
+        o, lse = _plain_rows(q, cache, lens, mask)
+        first = at - (lens[b] - n if mask == "bottom_right" else 0)  # the first query that sees it
+        sees = torch.zeros(want.shape[:3], dtype=torch.bool)
+        sees[b, head * group : (head + 1) * group, first:] = True
+        assert torch.isnan(o[..., col][sees]).all()
+        assert torch.equal(o[~sees], want[~sees]) and torch.equal(lse[~sees], want_lse[~sees])
+        cache.v.view(torch.uint8)[table[b, at // 16].item(), head, at % 16, col] = 0
+        want, want_lse = _plain_rows(q, cache, lens, mask)
+        # in a key: the scores of the rows that see it are NaN, the others' are as they were
+        was = cache.k.view(torch.uint8)[table[b, at // 16].item(), head, at % 16, col].item()
+        cache.k.view(torch.uint8)[table[b, at // 16].item(), head, at % 16, col] = 0x7F
+        o, lse = _plain_rows(q, cache, lens, mask)
+        assert torch.equal(torch.isnan(lse), sees) and torch.equal(torch.isnan(o).all(-1), sees)
+        assert not torch.isnan(o[~sees]).any()
+        cache.k.view(torch.uint8)[table[b, at // 16].item(), head, at % 16, col] = was
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("group,n", ROWS)
+def test_infinite_scale_hidden_from_some_rows(group, n, code):
+    lens = [(n + 47) // 16 * 16 + 3, n]
+    cache, host, table = make_cache(2, 2, 16, 128, 20, code, seed=22)
+    q = _q(2, 2 * group, n, 128, "fp16", seed=6)
+    ro, rlse, vmax = plain_attention(q, host, table, lens, "bottom_right", 1 / math.sqrt(128))
+    page = (lens[0] - 1) // 16  # the last page: queries before its first token do not see it
+    sees = torch.zeros(ro.shape[:3], dtype=torch.bool)
+    sees[0, group:, max(0, page * 16 - (lens[0] - n)) :] = True
+    for value in (math.inf, math.nan):
+        cache.v_scale[table[0, page].item(), 1] = value
+        o, lse = _plain_rows(q, cache, lens, "bottom_right")
+        assert torch.isnan(o[sees]).all() and not torch.isnan(o[~sees]).any()
+        assert torch.all((o.double() - ro).abs()[~sees] <= (2.0 ** -10 * vmax + 2.0 ** -11 * ro.abs())[~sees])
+        assert torch.all((lse.double() - rlse).abs()[~sees] <= 1e-4)
+
+
+def test_pages_shared_by_sequences():
+    """A common prefix in one set of pages."""
+    lens = [200, 170, 130, 128]
+    cache, host, table = make_cache(4, 2, 32, 64, 7, "int8", seed=23)
+    table[1:, :4] = table[0, :4]
+    shared = exattn.QuantCache(cache.k, cache.v, cache.k_scale, cache.v_scale, table.to(DEV))
+    for n in (1, 12, 50):
+        check_attention(_q(4, 4, n, 64, "bf16"), shared, host, table, lens)
+    k, v = exattn.cache_read(shared, torch.tensor(lens, dtype=torch.int32, device=DEV), rows=200)
+    for b in range(4):
+        assert torch.equal(k[b, :, :128], k[0, :, :128]) and torch.equal(v[b, :, :128], v[0, :, :128])
+
+
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 16, 17, 24, 25, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 384, 385])
+def test_row_counts_at_the_variants_edges(rows):
+    lens = [rows + 130, max(1, rows - 3), 2]
+    cache, host, table = make_cache(3, 1, 16, 64, 36, "int8", seed=24)
+    check_attention(_q(3, 1, rows, 64, "fp16"), cache, host, table, lens)
+
+
+def test_pool_beyond_32_bits():
+    """Pages whose codes lie past 2^32 bytes."""
+    pages, page, d = 270_000, 128, 128
+    k, v = (torch.zeros((pages, 1, page, d), dtype=torch.int8, device=DEV) for _ in range(2))
+    ks, vs = (torch.zeros((pages, 1), device=DEV) for _ in range(2))
+    table = torch.tensor([[pages - 1, pages - 7, 262_143, 262_144]], dtype=torch.int32)
+    cache = exattn.QuantCache(k, v, ks, vs, table.to(DEV))
+    g = torch.Generator().manual_seed(3)
+    new = [torch.randn((1, 1, 500, d), generator=g).to(torch.bfloat16) for _ in range(2)]
+    exattn.cache_write(cache, new[0].to(DEV), new[1].to(DEV))
+    ids = table[0].to(DEV).long()
+    host = {"k": k[ids].cpu(), "v": v[ids].cpu(), "k_scale": ks[ids].cpu(), "v_scale": vs[ids].cpu()}
+    near = torch.arange(4, dtype=torch.int32)[None]
+    assert (host["k"].float() * host["k_scale"][..., None, None]).reshape(-1, d)[:500].sub(new[0][0, 0].float()).abs().max() < 0.05
+    for n in (1, 20, 60, 100, 300):
+        check_attention(_q(1, 1, n, d, "bf16"), cache, host, near, [500])
+    got = exattn.cache_read(cache, torch.tensor([500], dtype=torch.int32, device=DEV), rows=500)
+    for t, name in zip(got, "kv"):
+        want = tokens(host, name, near, 0, 500)
+        assert torch.all((t[0].double().cpu() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -23))
+
+
 def test_bad_page_numbers_and_lengths():
     lens = [64, 64, 64]
     cache, host, table = make_cache(3, 2, 16, 64, 4, "int8", seed=12)
@@ -464,3 +561,59 @@ def test_two_streams_with_a_workspace_each():
     torch.cuda.synchronize()
     for q, (o, lse) in zip(qs, out):
         check_attention(q, cache, host, table, lens, o=o, lse=lse)
+
+
+def test_two_graphs_replayed_side_by_side():
+    """Two captured calls, each with its workspace, whose replays overlap on two streams."""
+    cache, host, table = make_cache(2, 2, 64, 128, 90, "e4m3", seed=42)
+    lens = [5600, 3000]
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    qs = [_q(2, 4, rows, 128, "bf16", seed=rows) for rows in (3, 40)]
+    calls = []
+    for q in qs:
+        dev, graph, side = q.to(DEV), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        ws = torch.empty(exattn.cache_workspace_size(cache, 4, q.shape[2]), dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            out = exattn.forward_cache(dev, cache, n, workspace=ws)
+        calls.append((dev, graph, side, ws, out))
+    for _ in range(6):
+        for _, graph, side, _, _ in calls:
+            with torch.cuda.stream(side):
+                graph.replay()
+    torch.cuda.synchronize()
+    for q, (_, _, _, _, (o, lse)) in zip(qs, calls):
+        check_attention(q, cache, host, table, lens, o=o, lse=lse)
+
+
+def test_one_workspace_for_calls_in_turn():
+    """Calls of different shapes one behind the other in one workspace, captured in one graph."""
+    cache, host, table = make_cache(2, 2, 64, 64, 80, "int8", seed=43)
+    lens = [5000, 4200]
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    qs = [_q(2, 2, rows, 64, "fp16", seed=rows) for rows in (1, 20, 64, 200, 2)]
+    dev = [q.to(DEV) for q in qs]
+    ws = torch.empty(max(exattn.cache_workspace_size(cache, 2, q.shape[2]) for q in qs), dtype=torch.uint8, device=DEV)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        out = [exattn.forward_cache(q, cache, n, workspace=ws) for q in dev]
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for q, (o, lse) in zip(qs, out):
+        check_attention(q, cache, host, table, lens, o=o, lse=lse)
+
+
+def test_refused_workspaces():
+    cache, host, table = make_cache(1, 2, 16, 64, 4, "e4m3", seed=44)
+    q = _q(1, 2, 1, 64, "bf16").to(DEV)
+    n = torch.tensor([50], dtype=torch.int32, device=DEV)
+    size = exattn.cache_workspace_size(cache, 2, 1)
+    room = torch.empty(size + 256, dtype=torch.uint8, device=DEV)
+    assert room.data_ptr() % 256 == 0
+    for ws, status in ((room[: size - 1], "ATTN_ERR_WORKSPACE"), (room[16 : size + 16], "ATTN_ERR_MISALIGNED")):
+        with pytest.raises(exattn.AttnError) as e:
+            exattn.forward_cache(q, cache, n, workspace=ws)
+        assert exattn.STATUS_NAMES[e.value.status] == status
+    check_attention(q.cpu(), cache, host, table, [50], o=(r := exattn.forward_cache(q, cache, n, workspace=room))[0], lse=r[1])
