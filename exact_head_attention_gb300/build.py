@@ -16,7 +16,7 @@ LIB = os.path.join(PKG, "libexattn.so")
 SOURCES = ["api.cu", "attn_fwd.cu", "fwd_schedule.cu", "attn_bwd.cu", "attn_bwd_dq.cu", "attn_splitkv.cu", "attn_kl.cu", "attn_kl_bwd.cu", "noalloc.cu",
            "cache_api.cu", "cache_io.cu", "cache_attn.cu", "cache_tile.cu"]
 HEADERS = ["ptx.cuh", "kernels.h", "softmax.cuh", "ds_ops.cuh", "kv_order.cuh", "fwd_schedule.h", "fwd_tile.cuh",
-           "api_internal.h", "cache8.cuh", "cache_sched.cuh"]
+           "api_internal.h", "cache.h", "cache8.cuh", "cache_sched.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -15,6 +15,7 @@
 #include "../../include/exattn.h"
 #include "api_internal.h"
 #include "fwd_schedule.h"
+#include "cache.h"
 #include "kernels.h"
 #include "ptx.cuh"
 

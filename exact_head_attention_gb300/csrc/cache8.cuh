@@ -5,7 +5,7 @@
 #include <cstdint>
 
 #include "../../include/exattn.h"
-#include "kernels.h"
+#include "cache.h"
 #include "ptx.cuh"
 
 namespace exattn {

@@ -5,7 +5,7 @@
 #include <random>
 
 #include "api_internal.h"
-#include "kernels.h"
+#include "cache.h"
 
 using namespace exattn;
 

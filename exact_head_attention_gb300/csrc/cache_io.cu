@@ -12,7 +12,7 @@
 #include <cuda_fp16.h>
 
 #include "cache8.cuh"
-#include "kernels.h"
+#include "cache.h"
 #include "ptx.cuh"
 
 namespace exattn {

@@ -33,7 +33,7 @@
 
 #include "cache8.cuh"
 #include "cache_sched.cuh"
-#include "kernels.h"
+#include "cache.h"
 #include "ptx.cuh"
 
 namespace exattn {

@@ -72,7 +72,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 }
 
 // Error codes a kernel records in the device error word.
-enum : uint32_t { kErrNone = 0, kErrTimeout = 5, kErrSmemAlign = 8, kErrPage = 9 };
+enum : uint32_t { kErrNone = 0, kErrTimeout = 5, kErrSmemAlign = 8 };
 
 // Dynamic shared memory must start 1024-byte aligned for kernels that request
 // no alignment slack; checked once at kernel entry (uniform across the CTA).
