@@ -76,7 +76,7 @@ struct Cfg {
   static constexpr uint32_t OFF_FLAG = OFF_STAT + (PAIR ? 0 : 2 * 128 * 8 + 32);  // [kFlagRing][128]: a token has a NaN value
   static constexpr uint32_t OFF_PIECE = OFF_FLAG + kFlagRing * 128;
   static constexpr uint32_t OFF_BAR = OFF_PIECE + kPieceRing * kPieceInts * 4;
-  static constexpr int NBAR = 2 + 4 * NS + 2 * NR + 6 + kMetaRing + 2 * kPieceRing + 4;
+  static constexpr int NBAR = 2 + 4 * NS + NR + 2 * ((NR + 1) / 2) + 6 + kMetaRing + 2 * kPieceRing + 4;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t OFF_SCHED = OFF_MISC + 16;
   static constexpr uint32_t BYTES = OFF_SCHED + sizeof(typename Walk::Shared);
@@ -118,9 +118,15 @@ struct Bars {
   __device__ uint32_t k_empty(int s) const { return at(2 + NS + s); }
   __device__ uint32_t v_full(int s) const { return at(2 + 2 * NS + s); }
   __device__ uint32_t v_empty(int s) const { return at(2 + 3 * NS + s); }
-  __device__ uint32_t raw_full(int s) const { return at(2 + 4 * NS + s); }
-  __device__ uint32_t raw_empty(int s) const { return at(2 + 4 * NS + NR + s); }
-  static constexpr int kB = 2 + 4 * NS + 2 * NR;
+  // Keys and values take the slots of codes in turn, but the barriers of their arrival are apart: with an odd number of
+  // slots a converter would else wait on one whose last phase was the other operand's.  It has not seen that end, and
+  // where that copy is still under way it finds the barrier a phase behind and passes early.  Two for each operand do
+  // for three slots: the second copy after one is issued only once that one has been read.
+  static constexpr int FR = (NR + 1) / 2;
+  __device__ uint32_t raw_full(int v, int tile) const { return at(2 + 4 * NS + v * FR + tile % FR); }
+  static __device__ uint32_t raw_parity(int tile) { return (tile / FR) & 1; }
+  __device__ uint32_t raw_empty(int s) const { return at(2 + 4 * NS + 2 * FR + s); }
+  static constexpr int kB = 2 + 4 * NS + NR + 2 * FR;
   __device__ uint32_t s_full(int b) const { return at(kB + b); }
   __device__ uint32_t p_full(int b) const { return at(kB + 3 + b); }
   static constexpr int kC = kB + 6;
@@ -419,10 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       mbar_init(bars.v_full(s), 3);
       mbar_init(bars.v_empty(s), 1);
     }
-    for (int s = 0; s < NR; ++s) {
-      mbar_init(bars.raw_full(s), 1);
-      mbar_init(bars.raw_empty(s), 3);
-    }
+    for (int s = 0; s < NR; ++s) mbar_init(bars.raw_empty(s), 3);
+    for (int i = 0; i < 2 * bars.FR; ++i) mbar_init(bars.raw_full(i & 1, i >> 1), 1);
     for (int s = 0; s < kMetaRing; ++s) mbar_init(bars.meta_full(s), 1);
     for (int s = 0; s < kPieceRing; ++s) {
       mbar_init(bars.piece_full(s), 1);
@@ -486,14 +490,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       r1.tiles = r2.tiles = 0;
       auto copy = [&](const uint8_t* codes, const Round& r, int q) -> bool {
         const int s = raws % NR;
+        const uint32_t full = bars.raw_full(raws & 1, raws >> 1);
         if (!mbar_wait_warp(bars.raw_empty(s), ((raws / NR) & 1) ^ 1, wc)) return false;
         const bool mine = lane >> 3 == q && leads && r.page >= 0;
         const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
-        if (lane == 0) mbar_arrive_expect_tx(bars.raw_full(s), n * box * D);
+        if (lane == 0) mbar_arrive_expect_tx(full, n * box * D);
         __syncwarp();
         if (mine) {
           const long long row = ((static_cast<long long>(r.page) * a.c.heads + r.head) << psh) + (r.key & ((1 << psh) - 1));
-          bulk_load(sbase + C::OFF_RAW + s * C::RAW + group * 16 * D, codes + row * D, box * D, bars.raw_full(s));
+          bulk_load(sbase + C::OFF_RAW + s * C::RAW + group * 16 * D, codes + row * D, box * D, full);
         }
         ++raws;
         return true;
@@ -556,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       cache_empty_items<D, C::R, kTK, C::MIN_TILES>(a, blockIdx.x, gridDim.x);
       // Every copy issued must land before the block exits, also where the other roles gave up.
       if (lane == 0)
-        for (int n = max(0, raws - NR); n < raws; ++n) mbar_drain(bars.raw_full(n % NR), (n / NR) & 1, a.timeout_ns);
+        for (int n = max(0, raws - NR); n < raws; ++n) mbar_drain(bars.raw_full(n & 1, n >> 1), bars.raw_parity(n >> 1), a.timeout_ns);
     } else if (warp == 8) {
       // ------------------------------------------------------------ MMA issuer
       // The warp stays together and one elected lane issues: what the issue takes is then the same for all
@@ -666,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         auto convert = [&](auto drop) __attribute__((always_inline)) -> bool {  // drop: NaN among the values
           constexpr bool kDrop = decltype(drop)::value;
           const int s = kt % NS, raws = 2 * kt + v, rs = raws % NR;
-          if (!mbar_wait_warp(bars.raw_full(rs), (raws / NR) & 1, wc)) return false;
+          if (!mbar_wait_warp(bars.raw_full(v, kt), bars.raw_parity(kt), wc)) return false;
           uint32_t bad = 0u;
           if constexpr (kDrop) bad = part.drop_nan(smem_raw + C::OFF_RAW + rs * C::RAW);
           part.load(smem_raw + C::OFF_RAW + rs * C::RAW);
