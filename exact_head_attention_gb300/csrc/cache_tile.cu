@@ -807,6 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           const int nv = kt + p.end - p.begin - 1;
           ok = mbar_wait_warp(bars.v_empty(nv % NS), (nv / NS) & 1, wc);
         }
+        if (PAIR && !both && ok) ok = join();  // lets the other warpgroup go on, see below
 
         // ------------------------------------------------------------ epilogue
         float w0 = 0.f, w1 = 0.f, lse2;  // factors of O_0 and O_1 (PAIR: of O_t)
@@ -986,8 +987,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         }
         // O_t, the statistics and the query tile are free once both warpgroups are here.
         if (!PAIR && !(ok = join())) break;
-      } else if (lane == 0) {
-        mbar_arrive(bars.q_full(t));
+      } else {
+        // No rows here in this piece (PAIR).  Its steps use the barriers that this warpgroup waits on next, so that it
+        // must not wait for its own steps of a later piece before they have ended.
+        if (lane == 0) mbar_arrive(bars.q_full(t));
+        ok = join();
       }
       kt += p.end - p.begin;
       seq += chain_steps(p, 0) + chain_steps(p, 1);

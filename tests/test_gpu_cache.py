@@ -279,6 +279,38 @@ def test_row_counts_at_the_variants_edges(rows):
     check_attention(_q(3, 1, rows, 64, "fp16"), cache, host, table, lens)
 
 
+@pytest.mark.parametrize("group,n", [(3, 128), (1, 300), (2, 150), (1, 257), (5, 90)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_items_of_one_and_of_two_row_tiles_in_turn(group, n, d):
+    """More items than blocks, every second one with 128 rows or fewer of the 256 that the others have."""
+    lens = [700, 1, 513, 650, 129, 400, 0, 1000, 333, 90, 870, 256] * 2
+    cache, host, table = make_cache(len(lens), 6, 128, d, 8, "int8", seed=25)
+    q = _q(len(lens), 6 * group, n, d, "bf16")
+    first = exattn.forward_cache(q.to(DEV), cache, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    check_attention(q, cache, host, table, lens, o=first[0], lse=first[1])
+    for _ in range(20):
+        again = exattn.forward_cache(q.to(DEV), cache, torch.tensor(lens, dtype=torch.int32, device=DEV))
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+    assert exattn.check_device_error() == 0
+
+
+@pytest.mark.parametrize("rows,d", [(40, 128), (100, 128), (40, 64), (200, 128), (20, 128)])
+def test_long_runs_of_copies(rows, d):
+    """The same bits from many calls over long sequences, the copies of keys and values always under way."""
+    cache, host, table = make_cache(4, 12, 64, d, 256, "e4m3", seed=26)
+    lens = torch.tensor([16384] * 4, dtype=torch.int32, device=DEV)
+    q = _q(4, 12, rows, d, "bf16").to(DEV)
+    first = exattn.forward_cache(q, cache, lens)
+    for _ in range(60):
+        again = exattn.forward_cache(q, cache, lens)
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+    assert exattn.check_device_error() == 0
+    few = exattn.forward_cache(q[:, :, -3:].contiguous(), cache, lens)  # another kernel's result
+    # each within 2^-10 of the largest |v|, 6 here, and half a step of bf16
+    assert torch.all((few[0].float() - first[0][:, :, -3:].float()).abs() <= 2 * (6 * 2.0 ** -10 + 2.0 ** -8 * first[0][:, :, -3:].float().abs()))
+    assert torch.all((few[1] - first[1][:, :, -3:]).abs() <= 2e-4)
+
+
 def test_pool_beyond_32_bits():
     """Pages whose codes lie past 2^32 bytes."""
     pages, page, d = 270_000, 128, 128
