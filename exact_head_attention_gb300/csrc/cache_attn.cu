@@ -8,16 +8,19 @@
 // are (fp16 holds them exactly).  Pieces of the key axis are merged by their log-sum-exp.
 //
 // Bound.  With one to some tens of query rows a key/value head the time is that of reading the codes: 2 d
-// bytes a token and head against 4 d rows flops.  A block (one an SM) therefore keeps 128 to 192 KB of
-// copies under way: four producer warps walk the block's share of the work (cache_sched.cuh), look the pages
-// up and have the copy engine fill, for each of the 8 or 12 computing warps, a ring of two tiles of 4 KB of
-// keys and 4 KB of values.  A computing warp owns every eighth or twelfth tile of a piece and its own
+// bytes a token and head against 4 d rows flops.  A block (one an SM) therefore keeps 128 to 192 KB of copies
+// under way.  It holds two workers, each with its own share of the work (cache_sched.cuh): two producer warps walk
+// it, look the pages up and have the copy engine fill, for each of the worker's four computing warps, a ring of two or
+// three tiles of 4 KB of keys and 4 KB of values.  A computing warp owns every fourth tile of a piece and its own
 // (m, l, O), and meets the others only at the end of a piece, where their results are joined in shared memory.
 //
-// Measured on GB300 (12 heads of 128, one token over 32k cached tokens of 8 sequences, 805 MB of codes):
-// 129 us, 92 % of the measured copy rate.  From 162 us: four producer warps instead of one (142), 32-bit
-// arithmetic and one pass in the division of the work, and a merge that loads its pieces side by side
-// (130), the query rows copied ahead with each piece (128).
+// Measured on GB300: 12 heads of 128, one token over 32k cached tokens of 8 sequences (805 MB of codes) in 124 us,
+// 95 % of the measured copy rate; 64 sequences of 1 to 8191 tokens, 8 heads of 128 with 8 query heads each, pages of 16,
+// in 101 us (79 %; the uneven end of the blocks' shares, and a copy for each 16 tokens).  From 162 us for the first:
+// four producer warps instead of one, 142 (one took 190 cycles for each 4 KB box, and they arrive every 175); 32-bit
+// arithmetic and one pass in the division of the work, 130; the query rows copied ahead with each piece, 128; two
+// workers, 124.  A call over one short sequence takes 6.3 us, 20 rows instead of 8 add 3 us and a division of the keys
+// 6 us: code that runs once a piece comes from far, and is kept short.
 //
 // Products.  The tensor cores are far from busy here, so the work goes through the warp-level m16n8k16
 // product with keys (for the scores) and d positions (for O) as its M and query rows as its N, eight at a
@@ -758,8 +761,8 @@ cudaError_t launch_m(const CacheAttnArgs& a, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.group) * a.Nq;
   if (rows <= 8) return launch_t<D, FMT, BF16, 1>(a, stream);
   if (rows <= 16) return launch_t<D, FMT, BF16, 2>(a, stream);
-  if (rows <= 24) return launch_t<D, FMT, BF16, 3>(a, stream);
-  return launch_t<D, FMT, BF16, 4>(a, stream);
+  static_assert(kCacheStreamRows == 24, "the variants of launch_m");
+  return launch_t<D, FMT, BF16, 3>(a, stream);
 }
 
 template <int D>

@@ -11,17 +11,28 @@
 // Two chains of (scores, softmax, product) alternate on the tensor cores, one softmax warpgroup each:
 //   PAIR    more than 128 rows: an item has 256, chain t works on rows [128 t, 128 t + 128)
 //   else    an item has 128 rows, and chain t works on every second key tile; the two results are joined in
-//           the epilogue.  Both chains then have work at any number of rows.
+//           the epilogue.  Both chains then have work at any number of rows.  Up to 64 rows lie in the query tile
+//           twice, and each copy's softmax takes half of a tile's keys (64 queries over 16k tokens on 16 heads of 64:
+//           55 us without, 51 us with it).
 // The chains' steps (one 128-token tile of one chain) form one sequence, and step i has score buffer i mod NB,
 // which its P overwrites: S[0] .. S[NB-1] | O[0] S[NB] O[1] S[NB+1] ...  At d = 64 tensor memory has room for three
 // buffers, so that a chain's next scores are there when its softmax has finished a step; at d = 128 for two.
 // Steps of 64 keys with two buffers a chain were tried for d = 128: a score product of 64 columns takes as long as one
 // of 128 (72 cycles for each 16 positions), and the whole became 1.4 times slower.
 //
+// Measured on GB300: 512 queries at the end of 12289 cached tokens, 2 sequences, 8 heads of 128 with 4 query heads each,
+// in 180 us, 1.12 PFLOP/s, 58 % of the measured cuBLAS rate; 64 queries over 16k tokens of 4 sequences, 16 heads of 64, in
+// 53 us (2.5 TB/s of codes).  The products take 60 % of the first; the warp that issues them, whose instructions come
+// back into an instruction cache that the softmax fills, is busy all the time: 1750 cycles for the two products of a
+// step, 1100 of them in the tensor cores.  Dropped, with what 176 us (before NaN codes were looked for) became:
+// no issuing warp, each chain's softmax warps issuing its products (180, and 67 for the other's 56); the issuing warp's
+// ring positions a lane each instead of all in every lane (181); the softmax as a loop over 64 keys, a quarter of the
+// code (197).
+//
 // Warp roles (512 threads, registers re-split per warpgroup):
 //   warps 0-3, 4-7  softmax of chain 0 and 1 (thread = query row = TMEM lane); they also bring the query rows
 //                   into their operand tile and write the results
-//   warp  8         MMA issuer (one thread) and TMEM owner
+//   warp  8         product issue (the warp together, one elected lane), TMEM owner
 //   warp  9         producer: walks the block's pieces (cache_sched.cuh), looks pages up, copies codes
 //   warps 10-12, 13-15  converters of the keys and of the values, about 43 tokens of each tile apiece
 // Tensor memory: score buffer b (P over its first 64 columns) at 128 b, O_t behind the buffers.
