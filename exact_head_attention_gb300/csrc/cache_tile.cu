@@ -22,9 +22,9 @@
 //
 // Measured on GB300: 512 queries at the end of 12289 cached tokens, 2 sequences, 8 heads of 128 with 4 query heads each,
 // in 180 us, 1.12 PFLOP/s, 58 % of the measured cuBLAS rate; 64 queries over 16k tokens of 4 sequences, 16 heads of 64, in
-// 53 us (2.5 TB/s of codes).  The products take 60 % of the first; the warp that issues them, whose instructions come
-// back into an instruction cache that the softmax fills, is busy all the time: 1750 cycles for the two products of a
-// step, 1100 of them in the tensor cores.  Dropped, with what 176 us (before NaN codes were looked for) became:
+// 53 us (2.5 TB/s of codes).  The tensor pipe is active for 45 % of the first (ncu).  The warp that issues the
+// products, whose instructions come back into an instruction cache that the softmax fills, is busy all the time: 1750
+// cycles for the two products of a step.  Dropped, with what 176 us (before NaN codes were looked for) became:
 // no issuing warp, each chain's softmax warps issuing its products (180, and 67 for the other's 56); the issuing warp's
 // ring positions a lane each instead of all in every lane (181); the softmax as a loop over 64 keys, a quarter of the
 // code (197).
