@@ -641,6 +641,13 @@ def cache_read(cache: QuantCache, lens, rows: int | None = None, start=None, dty
     return _run(cache, stream, call)
 
 
+def _cache_workspace(workspace, cache: QuantCache):
+    """(address, bytes) of a caller's workspace."""
+    if workspace.get_device() != cache.index or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the cache's device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def cache_workspace_size(cache: QuantCache, H: int, Nq: int) -> int:
     """Workspace bytes of forward_cache (attn_fwd_cache_workspace_size)."""
     return int(load().attn_fwd_cache_workspace_size(cache._ref, cache.B, H, Nq))
@@ -654,7 +661,7 @@ def fwd_cache_raw(q, cache: QuantCache, lens, o, lse, causal, scale: float, work
     if o.shape != q.shape or lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or lse.get_device() != cache.index:
         raise ValueError("o must be shaped as q, lse float32 [B, H, Nq], on the cache's device")
     return load().attn_fwd_cache(qp, qs, cache._ref, _int32(lens, cache, "lens"), op, os_, _ptr(lse), B, H, Nq,
-                                 mask_code(causal), scale, _dtype_code(q), *_workspace(workspace), _stream(stream))
+                                 mask_code(causal), scale, _dtype_code(q), *_cache_workspace(workspace, cache), _stream(stream))
 
 
 def forward_cache(q, cache: QuantCache, lens, causal="bottom_right", scale: float | None = None, workspace=None,
@@ -678,11 +685,12 @@ def forward_cache(q, cache: QuantCache, lens, causal="bottom_right", scale: floa
             if workspace is None:
                 size = lib.attn_fwd_cache_workspace_size(cache._ref, B, H, Nq)
                 space = torch.empty(size, dtype=torch.uint8, device=cache.device)
+                at = space.data_ptr()
             else:
-                size, space = workspace.numel() * workspace.element_size(), workspace
+                at, size = _cache_workspace(workspace, cache)
             op, os_ = _cache_view(o, cache, q.dtype)
             st = lib.attn_fwd_cache(qp, qs, cache._ref, lens_at, op, os_, lse.data_ptr(), B, H, Nq, mask, scale, code,
-                                    space.data_ptr(), size, handle)
+                                    at, size, handle)
             if st != ATTN_OK:
                 raise AttnError(st, "attn_fwd_cache")
         return o, lse

@@ -649,3 +649,40 @@ def test_refused_workspaces():
             exattn.forward_cache(q, cache, n, workspace=ws)
         assert exattn.STATUS_NAMES[e.value.status] == status
     check_attention(q.cpu(), cache, host, table, [50], o=(r := exattn.forward_cache(q, cache, n, workspace=room))[0], lse=r[1])
+
+
+def test_refused_tensors():
+    """What the binding refuses before anything is launched."""
+    cache, host, table = make_cache(2, 2, 16, 64, 4, "e4m3", seed=45)
+    q = _q(2, 4, 3, 64, "bf16").to(DEV)
+    n = torch.tensor([50, 20], dtype=torch.int32, device=DEV)
+    size = exattn.cache_workspace_size(cache, 4, 3)
+    new = torch.zeros((2, 2, 5, 64), dtype=torch.bfloat16, device=DEV)
+    refused = [
+        lambda: exattn.forward_cache(q, cache, n, workspace=torch.empty(size, dtype=torch.uint8)),
+        lambda: exattn.forward_cache(q, cache, n, workspace=torch.empty((size, 2), dtype=torch.uint8, device=DEV)[:, 0]),
+        lambda: exattn.forward_cache(q.cpu(), cache, n),
+        lambda: exattn.forward_cache(q, cache, n.cpu()),
+        lambda: exattn.forward_cache(q, cache, n.long()),
+        lambda: exattn.forward_cache(q, cache, n[:1]),
+        lambda: exattn.forward_cache(q[:1], cache, n),
+        lambda: exattn.forward_cache(q.transpose(2, 3), cache, n),
+        lambda: exattn.cache_write(cache, new, new[:, :1], n),
+        lambda: exattn.cache_write(cache, new, new.half(), n),
+        lambda: exattn.cache_write(cache, new.cpu(), new.cpu(), n),
+        lambda: exattn.cache_write(cache, new, new, n.cpu()),
+        lambda: exattn.cache_read(cache, n),
+        lambda: exattn.cache_read(cache, n, out=(new, new[:, :, :4])),
+        lambda: exattn.cache_read(cache, n.float(), rows=4),
+        lambda: exattn.QuantCache(cache.k, cache.v, cache.k_scale, cache.v_scale.cpu(), cache.page_table),
+        lambda: exattn.QuantCache(cache.k, cache.v, cache.k_scale[:-1], cache.v_scale[:-1], cache.page_table),
+        lambda: exattn.QuantCache(cache.k, cache.v[:-1], cache.k_scale, cache.v_scale, cache.page_table),
+    ]
+    for i, call in enumerate(refused):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    with pytest.raises(exattn.AttnError):  # five query heads on two key/value heads
+        exattn.forward_cache(torch.zeros((2, 5, 1, 64), dtype=torch.bfloat16, device=DEV), cache, n)
+    torch.cuda.synchronize()
+    assert exattn.check_device_error() == 0
