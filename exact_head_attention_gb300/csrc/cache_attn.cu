@@ -67,7 +67,8 @@ struct Cfg {
   static constexpr int TILE = TK * D;                         // bytes of codes, K or V
   static constexpr int STAGES = NT == 1 ? 3 : 2;              // of K and V together, a warp
   static constexpr int RING = W * STAGES * 2 * TILE;          // 192 or 128 KB
-  static constexpr int JR = NT == 1 ? 512 / D : 1024 / D;     // rows joined at a time
+  // Rows joined at a time, a power of two: all of them where shared memory has the room.
+  static constexpr int JR = D == 64 ? (NT == 3 ? 32 : R) : NT == 1 ? 4 : NT == 2 ? R : 8;
   static constexpr int JOIN = kGroup * JR * D * 4;            // a worker
   static constexpr bool Q_IN_SMEM = NT > 2;                   // registers hold Q up to 16 rows
   static constexpr int QBYTES = Q_IN_SMEM ? NT * (D / 16) * 32 * 8 : 0;
