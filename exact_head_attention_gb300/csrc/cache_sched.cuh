@@ -4,17 +4,18 @@
 // TK tokens.  All tiles of all items, in the order (sequence, head, row tile, key tile), are numbered
 // 0 .. T - 1 (below 2^31: the host checks the largest T that the page table allows).  With
 // C = ceil(T / P) for P blocks (or workers, several to a block),
-//   * more than kMinTiles tiles a block: block c takes the tiles [c C, (c + 1) C), whichever items they
-//     belong to, so every block has the same work however uneven the lengths are;
-//   * fewer: C = kMinTiles, and a block takes whole pieces of at most C tiles that begin at an item's
-//     start or C, 2 C, ... tiles behind it, so that short items are not cut for nothing.
+//   * in general block c takes the tiles [c C, (c + 1) C), whichever items they belong to, so every block has the
+//     same work however uneven the lengths are;
+//   * where the items cut into pieces of C = kMinTiles tiles make no more pieces than there are blocks, a block takes
+//     one of those, so that short items are not cut for nothing, and none is cut shorter.
 // In the first form an item also counts kItemCost tiles that are not there, before its own: what it costs to
 // begin and to end a piece.  Without them a block whose share were many short sequences took 1.6 times as
 // long as the average block (64 sequences spread over 1 to 8191 tokens, 8 heads).
 // A piece is a run of an item's tiles in one block.  Where an item has several, each leaves a partial
 // result in slot 2 (start / C) + (start != item's first tile) of the workspace, `start` being the number
-// of the piece's first tile (kItemCost past the item's first number): at most one piece in each block begins an item that it does not finish, and
-// at most one continues an item, so no two pieces share a slot.
+// of the piece's first tile (kItemCost past the item's first number): at most one piece in each block begins an item
+// that it does not finish, and at most one continues an item, so no two pieces share a slot.  In the second form the
+// pieces are numbered, and that takes the place of start / C.
 #pragma once
 
 #include <cstdint>
@@ -37,7 +38,7 @@ struct CacheWs {
   float* l;                   // [slots][2][R]
 };
 
-// Slots are numbered below 2 (T / C + 1) <= 2 (P + 1), T with the items' costs.
+// Slots are numbered below 2 (T / C + 1) <= 2 (P + 1), T with the items' costs, or below 2 P.
 inline __host__ __device__ size_t cache_slots(int sm_count) { return 2 * (static_cast<size_t>(sm_count) + 1); }
 
 inline __host__ __device__ size_t cache_ws_bytes(int R, int D, int sm_count) {
@@ -98,7 +99,7 @@ struct CachePiece {
   int b, head, rt, len;  // b < 0: there are no more
   int begin, end;        // key tiles of the item
   int slot;              // -1: the whole item, else its place in the workspace
-  int bucket, pieces;    // first / C of the item's first tile, and the item's pieces
+  int bucket, pieces;    // first / C of the item's first tile, or the number of its first piece; and its pieces
 
   __device__ int slot_of(int i) const { return 2 * (bucket + i) + (i != 0); }  // of the item's i-th piece
 };
@@ -184,7 +185,7 @@ struct CacheWalk {
       total += sh.warp_sums[2 * w];
       pieces += sh.warp_sums[2 * w + 1];
     }
-    by_piece = total <= blocks * kMinTiles;
+    by_piece = pieces <= blocks;
     C = by_piece ? kMinTiles : (total - 1) / blocks + 1;
     sh.tiles[tid + 1] = x;
     sh.units[tid + 1] = by_piece ? y : x;
@@ -236,6 +237,7 @@ struct CacheWalk {
   }
 
   __device__ bool next(CachePiece& p) {
+    int first_piece = 0;  // the number of the item's first
     for (;;) {
       if (at >= stop) return false;
       int x;  // unit of the item at which the piece begins
@@ -260,6 +262,7 @@ struct CacheWalk {
       if (by_piece) {
         tile = x * kMinTiles;
         p.end = min(ntiles, tile + kMinTiles);
+        first_piece = at - x;
         at += step;
       } else {
         const int y = min(items.cost(ntiles), x + (stop - at));
@@ -276,7 +279,7 @@ struct CacheWalk {
     p.len = len;
     p.begin = tile;
     const int first = item_first + items.kItemCost;
-    p.bucket = first / C;
+    p.bucket = by_piece ? first_piece : first / C;
     p.pieces = by_piece ? (ntiles + C - 1) / C : (first + ntiles - 1) / C - p.bucket + 1;
     p.slot = p.pieces == 1 ? -1 : p.slot_of(by_piece ? tile / C : (first + tile) / C - p.bucket);
     return true;
