@@ -6,8 +6,11 @@
 // C = ceil(T / P) for P blocks (or workers, several to a block),
 //   * in general block c takes the tiles [c C, (c + 1) C), whichever items they belong to, so every block has the
 //     same work however uneven the lengths are;
-//   * where the items cut into pieces of C = kMinTiles tiles make no more pieces than there are blocks, a block takes
-//     one of those, so that short items are not cut for nothing, and none is cut shorter.
+//   * where the items cut into pieces of C tiles make no more pieces than there are blocks, a block takes one of
+//     those, so that short items are not cut for nothing.  C is kMinTiles, twice that where it cuts no item at all (a
+//     merge takes longer than kMinTiles more tiles), or 2 or 4 times that where smaller ones are too many and blocks
+//     would have as many tiles in the first form.  Measured, five tokens on 32 sequences, 4 heads of 64, 20 rows each:
+//     1024 cached tokens 16.3 us, 2048 22.0 us; with kMinTiles alone 16.8 and 26.0.
 // In the first form an item also counts kItemCost tiles that are not there, before its own: what it costs to
 // begin and to end a piece.  Without them a block whose share were many short sequences took 1.6 times as
 // long as the average block (64 sequences spread over 1 to 8191 tokens, 8 heads).
@@ -76,20 +79,16 @@ struct CacheItems {
     return (cache_row_limit(a.mask, len, a.Nq, tok) + TK - 1) / TK;
   }
   __device__ static int cost(int tiles) { return tiles > 0 ? tiles + kItemCost : 0; }
-  // Tiles of one head of a sequence with the items' costs, and its pieces of at most kMinTiles tiles.
-  __device__ void head_units(const CacheAttnArgs& a, int len, int& ntiles, int& npieces) const {
+  __device__ static int cut(int tiles, int shift) { return (tiles + (1 << shift) - 1) >> shift; }
+  // Tiles of one head of a sequence with the items' costs, and its pieces of at most 2^shift tiles.
+  __device__ void head_units(const CacheAttnArgs& a, int len, int shift, int& ntiles, int& npieces) const {
     ntiles = npieces = 0;
 #pragma unroll 1
     for (int rt = 0; rt < row_tiles; ++rt) {
       const int t = tiles(a, len, rt);
       ntiles += cost(t);
-      npieces += (t + kMinTiles - 1) / kMinTiles;
+      npieces += cut(t, shift);
     }
-  }
-  __device__ int head_tiles(const CacheAttnArgs& a, int len) const {
-    int t, p;
-    head_units(a, len, t, p);
-    return t;
   }
   __device__ int seq_len(const CacheAttnArgs& a, int b) const { return cache_len(a.c, a.lens[b]); }
 };
@@ -134,13 +133,13 @@ __device__ __forceinline__ bool cache_piece_done(const CacheWs& ws, const CacheP
 template <int R, int TK, int NT, int kMinTiles>
 struct CacheWalk {
   struct Shared {  // first tile and first unit of each of the NT runs that the sequences are summed in
-    int tiles[NT + 1], units[NT + 1], warp_sums[2 * (NT / 32)];
+    int tiles[NT + 1], units[NT + 1], warp_sums[NT / 32][5];
   };
   const CacheAttnArgs& a;
   Shared& sh;
   CacheItems<R, TK, kMinTiles> items;
   int at, stop, step;  // first form: tile numbers; second: piece numbers
-  int C, per;          // per: sequences a run
+  int C, shift, per;   // C: 2^shift by pieces; per: sequences a run
   bool by_piece, placed = false;
   // place of the next tile (first form)
   int b = 0, head = 0, rt = 0, len = 0, tile = 0, ntiles = 0, item_first = 0;
@@ -150,45 +149,59 @@ struct CacheWalk {
     per = (a.B + NT - 1) / NT;
     const int b0 = static_cast<int>(min(static_cast<long long>(a.B), static_cast<long long>(tid) * per));
     const int b1 = min(a.B - b0, per) + b0;
-    int n = 0, m = 0;
+    constexpr int kLog = kMinTiles == 2 ? 1 : kMinTiles == 4 ? 2 : 3;
+    static_assert(1 << kLog == kMinTiles, "a power of two");
+    int n[4] = {0, 0, 0, 0}, count = 0;  // tiles; pieces of 1, 2 and 4 kMinTiles; items
     for (int i = b0; i < b1; ++i) {
       const int raw = a.lens[i], l = cache_len(a.c, raw);
       if (raw != l && block == 0) record_page_error(a.err_word);
-      int t, p;
-      items.head_units(a, l, t, p);
-      n += a.c.heads * t;
-      m += a.c.heads * p;
+#pragma unroll 1
+      for (int r = 0; r < items.row_tiles; ++r) {
+        const int t = items.tiles(a, l, r);
+        n[0] += a.c.heads * items.cost(t);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) n[1 + k] += a.c.heads * items.cut(t, kLog + k);
+        count += t > 0 ? a.c.heads : 0;
+      }
     }
     // inclusive sums over the warp, then over the warps
     const int lane = tid & 31, warp = tid >> 5;
-    int x = n, y = m;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) {
-        x += u;
-        y += v;
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int u = __shfl_up_sync(0xffffffffu, n[k], o);
+        if (lane >= o) n[k] += u;
       }
-    }
+    count = __reduce_add_sync(0xffffffffu, count);
     if (lane == 31) {
-      sh.warp_sums[2 * warp] = x;
-      sh.warp_sums[2 * warp + 1] = y;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sh.warp_sums[warp][k] = n[k];
+      sh.warp_sums[warp][4] = count;
     }
     sync(bar);
-    int total = 0, pieces = 0;
+    int sum[5] = {0, 0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
-      if (w < warp) {
-        x += sh.warp_sums[2 * w];
-        y += sh.warp_sums[2 * w + 1];
+#pragma unroll
+      for (int k = 0; k < 5; ++k) {
+        const int s = sh.warp_sums[w][k];
+        if (k < 4 && w < warp) n[k] += s;
+        sum[k] += s;
       }
-      total += sh.warp_sums[2 * w];
-      pieces += sh.warp_sums[2 * w + 1];
     }
-    by_piece = pieces <= blocks;
-    C = by_piece ? kMinTiles : (total - 1) / blocks + 1;
-    sh.tiles[tid + 1] = x;
-    sh.units[tid + 1] = by_piece ? y : x;
+    const int total = sum[0], even = (total - 1) / blocks + 1;
+    int k = -1;
+    if (sum[2] == sum[4] && sum[2] <= blocks) k = 1;
+    else if (sum[1] <= blocks) k = 0;
+    else if (sum[2] <= blocks && 2 * kMinTiles <= even) k = 1;
+    else if (sum[3] <= blocks && 4 * kMinTiles <= even) k = 2;
+    by_piece = k >= 0;
+    shift = kLog + max(k, 0);
+    C = by_piece ? 1 << shift : even;
+    const int pieces = k == 0 ? sum[1] : k == 1 ? sum[2] : sum[3];
+    sh.tiles[tid + 1] = n[0];
+    sh.units[tid + 1] = k < 0 ? n[0] : k == 0 ? n[1] : k == 1 ? n[2] : n[3];
     if (tid == 0) sh.tiles[0] = sh.units[0] = 0;
     sync(bar);
     if (by_piece) {
@@ -217,7 +230,7 @@ struct CacheWalk {
     int ht, hp, hu;
     for (b = run * per;; ++b) {
       len = items.seq_len(a, b);
-      items.head_units(a, len, ht, hp);
+      items.head_units(a, len, shift, ht, hp);
       hu = by_piece ? hp : ht;
       if (x < hu * a.c.heads) break;
       x -= hu * a.c.heads;
@@ -228,7 +241,7 @@ struct CacheWalk {
     item_first += head * ht;
     for (rt = 0;; ++rt) {
       ntiles = items.tiles(a, len, rt);
-      const int u = by_piece ? (ntiles + kMinTiles - 1) / kMinTiles : items.cost(ntiles);
+      const int u = by_piece ? items.cut(ntiles, shift) : items.cost(ntiles);
       if (x < u) break;
       x -= u;
       item_first += items.cost(ntiles);
@@ -260,8 +273,8 @@ struct CacheWalk {
         } while (ntiles == 0);
       }
       if (by_piece) {
-        tile = x * kMinTiles;
-        p.end = min(ntiles, tile + kMinTiles);
+        tile = x << shift;
+        p.end = min(ntiles, tile + C);
         first_piece = at - x;
         at += step;
       } else {
@@ -280,7 +293,7 @@ struct CacheWalk {
     p.begin = tile;
     const int first = item_first + items.kItemCost;
     p.bucket = by_piece ? first_piece : first / C;
-    p.pieces = by_piece ? (ntiles + C - 1) / C : (first + ntiles - 1) / C - p.bucket + 1;
+    p.pieces = by_piece ? items.cut(ntiles, shift) : (first + ntiles - 1) / C - p.bucket + 1;
     p.slot = p.pieces == 1 ? -1 : p.slot_of(by_piece ? tile / C : (first + tile) / C - p.bucket);
     return true;
   }
