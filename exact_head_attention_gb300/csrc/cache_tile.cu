@@ -783,10 +783,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
             tc_fence_after();
             if (!idle) {
               const float* scales = meta + (nt % kMetaRing) * 16;
-              // The chain's last product: with two buffers these scores were issued after it.  With three, its end
-              // (and that of the other chain's on the same values) frees the tile's slot.
+              // The chain's last product.  With two buffers that the chains share, these scores were issued after it.
+              // With three, or with two and the steps of one chain only, it may still be under way: its end (and that
+              // of the other chain's on the same values) frees the tile's slot.
               auto wait_pv = [&] {
-                if (NB > 2) {
+                if (NB > 2 || (PAIR && !both)) {
                   const int nv = nt - (PAIR ? 1 : 2);
                   if (!mbar_wait_warp(bars.v_empty(nv % NS), (nv / NS) & 1, wc)) ok = false;
                   tc_fence_after();

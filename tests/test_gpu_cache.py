@@ -367,6 +367,86 @@ def test_same_bits_and_a_dirty_workspace():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+# ------------------------------------------------------------------ scores and scales that rise along the keys
+
+# Rows a key/value head: both sides of every choice between kernels and row tiles, and items whose last row tile has
+# 128 rows or fewer of 256.
+RISING_ROWS = [1, 8, 12, 24, 25, 40, 64, 65, 100, 128, 129, 200, 256, 257, 300, 384, 385, 513, 520]
+
+
+def _copies(host, table, B):
+    """B sequences over the pages of one."""
+    return exattn.QuantCache(*(host[n].to(DEV) for n in ("k", "v", "k_scale", "v_scale")), table.expand(B, -1).contiguous().to(DEV))
+
+
+def check_copies(q, host, table, lens, check, **kw):
+    """Attention of equal queries over equal tokens: alone, where its keys are cut into the smallest pieces, and 64 times in
+    one call, where pieces are long.  `check` compares the results for one sequence; and the same bits each time."""
+    cache = _copies(host, table, 64 * len(lens))
+    for copies in (1, 64):
+        part = _copies(host, table, copies * len(lens)) if copies == 1 else cache
+        n = torch.tensor(lens * copies, dtype=torch.int32, device=DEV)
+        o, lse = exattn.forward_cache(q.repeat(copies, 1, 1, 1).to(DEV), part, n)
+        for _ in range(2):
+            again = exattn.forward_cache(q.repeat(copies, 1, 1, 1).to(DEV), part, n)
+            assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+        assert exattn.check_device_error() == 0
+        for c in range(0, copies, 21):
+            at = slice(c * len(lens), (c + 1) * len(lens))
+            check(q, None, host, table.expand(len(lens), -1), lens, o=o[at], lse=lse[at], **kw)
+
+
+def rising_scores(rows, d, code, level, tokens_, seed):
+    """Queries and a cache in which the scores of token t lie about level(t) in base 2, for all of a row's keys times that
+    row's 1, 0 or 1/2: the first component of each is given to it.  |level| <= 30, and the other components add a deviation
+    of 1 to 2, so that |s| <= 40 as the tolerances count."""
+    page = 32 if d == 64 else 64
+    cache, host, table = make_cache(1, 2, page, d, -(-tokens_ // page), code, seed=seed)
+    lv = torch.tensor([float(level(t)) for t in range(table.shape[1] * page)]).reshape(-1, 1, page)
+    ids = table[0].long()
+    codes = host["k"].float()
+    codes[ids, :, :, 0] = lv / 15 / host["k_scale"][ids][:, :, None]  # at most 2, which the smallest scale can hold
+    codes = codes.clamp(-LARGEST[code], LARGEST[code])
+    host["k"] = (codes if code == "e4m3" else codes.round()).to(CODES[code])
+    q = torch.randn((2, 2, rows, d), generator=torch.Generator().manual_seed(seed + 1))
+    q[:, :, :, 0] = 15 * math.sqrt(d) / math.log2(math.e) * torch.tensor([1.0, 0.0, 0.5])[torch.arange(rows) % 3]
+    q[1] = q[0]
+    return q, host, table
+
+
+@pytest.mark.parametrize("rows", RISING_ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_scores_that_rise_from_tile_to_tile(rows, d, code):
+    """The running maximum is passed by more than the factor that it may lag by, so that the accumulator is rescaled."""
+    lens = [1192, 700]
+    for by in (10, 20, 40):
+        q, host, table = rising_scores(rows, d, code, lambda t: min(30, t // 128 * by - 30), lens[0], seed=60)
+        check_copies(q.to(torch.bfloat16), host, table, lens, check_attention)
+
+
+@pytest.mark.parametrize("rows", RISING_ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_large_score(rows, d):
+    lens = [1192, 700]
+    for at in (128 + 77, 2 * 128 + 3, 1191):
+        q, host, table = rising_scores(rows, d, "e4m3", lambda t: 30 if t == at else -10, lens[0], seed=61)
+        check_copies(q.to(torch.float16), host, table, lens, check_attention)
+
+
+@pytest.mark.parametrize("rows", RISING_ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_value_scales_that_rise_from_page_to_page(rows, d, code):
+    lens = [1192, 700]
+    for page, ratio, span in ((128, 20, 6), (128, 1000, 4), (16, 20, 6)):
+        cache, host, table = make_cache(1, 2, page, d, -(-lens[0] // page), code, seed=62)
+        f = torch.tensor([float(ratio) ** (j % span - span + 1) for j in range(table.shape[1])])
+        host["v_scale"][table[0].long()] *= f[:, None]
+        q = _q(1, 2, rows, d, "fp16", seed=63).repeat(2, 1, 1, 1)
+        check_copies(q, host, table, lens, check_attention)
+
+
 # ------------------------------------------------------------------ write and read
 
 
