@@ -154,7 +154,9 @@ __global__ void __launch_bounds__(kIoThreads, 4) cache_write_kernel(const __grid
     if (old >= f || old != old) s = old;  // a NaN on either side stays
     grew = s > old;
   }
-  const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;  // NaN scale: codes 0, every token reads as NaN
+  // A scale that the page came with may be so small that its reciprocal is infinite, and zeros would become NaN.
+  // NaN scale: codes 0, every token reads as NaN.
+  const float inv = s > 0.f ? fminf(__fdiv_rn(1.f, s), 3.402823466e38f) : 0.f;
   if (tid == 0) *scale_at = s;
   const bool alive = s > 0.f;
   const float again = old * inv;

@@ -569,8 +569,9 @@ typedef struct attn_cache {
  *   new codes      round(x * (1 / s)), nearest even, at most the largest code
  *   earlier codes  round(code * (old scale * (1 / s))) where s > old scale,
  *                  else unchanged
- * in fp32; with s = 0 the codes are 0.  A NaN or infinity among a page's new
- * values makes that page's scale for the head NaN: all its tokens read as NaN.
+ * in fp32, with 1 / s at most the largest fp32 number; with s = 0 the codes
+ * are 0.  A NaN or infinity among a page's new values makes that page's scale
+ * for the head NaN: all its tokens read as NaN.
  * Rows of a page past start + count keep their codes.  A sequence whose start
  * is negative, or the part of one past its page table, is not written
  * (ATTN_ERR_PAGE in the error word); count[b] is taken within [0, N], with the

@@ -574,6 +574,27 @@ def test_write_refuses_what_is_out_of_range():
     assert_cache_equal(cache, host)
 
 
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_write_behind_a_scale_below_the_smallest_normal_number(code):
+    """The reciprocal of such a scale is beyond fp32 and taken as the largest number: zeros stay zeros."""
+    for power in (-127, -130, -149):
+        cache, host, table = make_cache(2, 2, 16, 64, 2, code, seed=70)
+        ids = table[:, 0].long()
+        host["k_scale"][ids] = host["v_scale"][ids] = 2.0 ** power
+        cache = exattn.QuantCache(*(host[x].to(DEV) for x in ("k", "v", "k_scale", "v_scale")), cache.page_table)
+        x = torch.zeros((2, 2, 3, 64))
+        x[1, :, :, ::5] = 2.0 ** -128
+        x[1, :, 1, 1] = -2.0 ** -120
+        x = x.to(torch.bfloat16)
+        exattn.cache_write(cache, x.to(DEV), x.to(DEV), torch.tensor([4, 5], dtype=torch.int32, device=DEV))
+        assert exattn.check_device_error() == 0
+        inverse = torch.tensor(2.0 ** -power).clamp(max=torch.finfo(torch.float32).max)
+        for n in ("k", "v"):
+            for b, start in ((0, 4), (1, 5)):
+                host[n].view(torch.uint8)[ids[b], :, start : start + 3] = round_code(x[b].float() * inverse, code).view(torch.uint8)
+        assert_cache_equal(cache, host)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("page", [16, 128])
 @pytest.mark.parametrize("code", ["e4m3", "int8"])
