@@ -47,6 +47,7 @@ namespace {
 // P is held times 2^kShift, so that fewer of the small ones become subnormal in fp16.  It stays below 2^15: the
 // running maximum may lag by 2^8, and vref by kVrefLag = 2^4.
 constexpr float kShift = 3.f, kVrefLag = 16.f;
+constexpr float kVrefLeast = 1.17549435e-38f;  // 2^-126: the reciprocal is finite
 
 constexpr int kWorkers = 2;                     // of a block: each with its own share of the work
 constexpr int kGroup = 4;                       // computing warps of a worker
@@ -458,8 +459,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
       if (__any_sync(0xffffffffu, grow)) {
         float vr = 1.f;
         if (vnew > vref) {
-          vr = vref / vnew;
-          vref = vnew;
+          const float to = fmaxf(vnew, kVrefLeast);
+          vr = vref / to;
+          vref = to;
           vinv = 1.f / vref;
         }
 #pragma unroll

@@ -60,7 +60,7 @@ constexpr int kPieceRing = 3, kMetaRing = 16;
 // Flags of tiles that an item's rows see in part: at most 3 at a piece's end (the rows of an item see the keys of at
 // most 256 tokens less or more), and the converters are at most NS tiles further.
 constexpr int kFlagRing = 8;
-constexpr float kShift = 3.f, kVrefLag = 16.f;  // as in cache_attn.cu
+constexpr float kShift = 3.f, kVrefLag = 16.f, kVrefLeast = 1.17549435e-38f;  // as in cache_attn.cu
 
 template <int D, bool PAIR>
 struct Cfg {
@@ -204,10 +204,10 @@ __device__ __forceinline__ void softmax_scaled(uint32_t tS, int half, uint32_t t
     const float al = need && !first ? ex2_approx(m - to) : 1.0f;
     float ov = al;
     if (first || v_new > vref) {
-      const float v = fmaxf(v_new, 0.f);
+      const float v = fmaxf(v_new, kVrefLeast);
       ov *= vref / v;
       vref = v;
-      vinv = v > 0.f ? 1.0f / v : 0.f;
+      vinv = 1.0f / v;
     }
     if (!first) {
       wait_pv();

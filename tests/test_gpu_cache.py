@@ -447,6 +447,31 @@ def test_value_scales_that_rise_from_page_to_page(rows, d, code):
         check_copies(q, host, table, lens, check_attention)
 
 
+# ------------------------------------------------------------------ value scales far apart
+
+
+@pytest.mark.parametrize("group,n", [(1, 1), (1, 12), (2, 12), (1, 60), (1, 100), (1, 300)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_value_scales_below_the_smallest_normal_number(group, n, d):
+    """Their reciprocals are beyond fp32.  O is off by no more than elsewhere, where the smallest bf16 numbers allow that:
+    2^-10 of the largest |v|, and with a reference of at least 2^-126 for P * vs, whose rounding to fp16 is 2^-28 of the
+    largest, 448 * 2^-154 for each of 700 keys, together with half a bf16 step of 2^-133 under 2^-133."""
+    lens = [700, 130]
+    for powers in ([-127], [-130], [-149], [-128, -126, -140], [-149, 0, -130, -129]):
+        cache, host, table = make_cache(2, 2, 32, d, 22, "e4m3", seed=68)
+        f = torch.tensor([2.0 ** powers[j % len(powers)] for j in range(table.shape[1])])
+        for b in range(2):
+            host["v_scale"][table[b].long()] = f[:, None].expand(-1, 2)
+        cache = exattn.QuantCache(*(host[x].to(DEV) for x in ("k", "v", "k_scale", "v_scale")), cache.page_table)
+        q = _q(2, 2 * group, n, d, "bf16", seed=69)
+        o, lse = exattn.forward_cache(q.to(DEV), cache, torch.tensor(lens, dtype=torch.int32, device=DEV))
+        ro, rlse, vmax = plain_attention(q, host, table, lens, "bottom_right", 1 / math.sqrt(d))
+        some = rlse > -math.inf
+        assert torch.all((lse.double().cpu() - rlse)[some].abs() <= 1e-4)
+        tol = 2.0 ** -10 * vmax + 2.0 ** -8 * ro.abs() + 2.0 ** -133
+        assert torch.all((o.double().cpu() - ro).abs() <= tol), (powers, ((o.double().cpu() - ro).abs() / tol).max())
+
+
 # ------------------------------------------------------------------ write and read
 
 
