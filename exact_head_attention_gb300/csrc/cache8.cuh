@@ -34,11 +34,42 @@ __device__ __forceinline__ int cache_page(const CacheView& c, int b, int t) {
   return cache_page_checked(c, cache_page_number(c, b, t));
 }
 
-// A page's scale of the values.  An infinite one counts as NaN: as a number it would set the reference that the
-// rows' probabilities are scaled by, for rows that do not see the page as well.
+// A page's scale of the values.  An infinite one counts as NaN.
 __device__ __forceinline__ float cache_v_scale(const CacheView& c, long long page_head) {
   const float s = c.v_scale[page_head];
   return s == INFINITY ? __int_as_float(0x7fffffff) : s;
+}
+
+// What the attention kernels scale their O by.  Each row keeps, besides m >= max s - 8, a number w over the keys that it
+// sees, with w >= max(s + log2 vs) - kValueLag and no greater than that maximum, vs the value scale of a key's page.  Its
+// probabilities go into the product as 2^(s - m + 3) vs 2^(m - w), below 2^15 in fp16 whatever the scales are, and the
+// sum of the products counts 2^(w - 3).  So a large scale costs the others nothing where it has no weight for the row:
+// behind the row's last key, or with small scores.  (A reference over the scales alone lost such rows: with a hidden page's
+// scale 2^28 times the others', a row's O was 0.)
+constexpr float kValueLag = 12.f;
+// w is no less than m - kValueFloor, so that 2^(m - w) is finite.
+constexpr float kValueFloor = 126.f;
+
+// log2 of a value scale, -inf below 2^-126; it needs no more accuracy than w's bounds do.
+__device__ __forceinline__ float cache_log2(float vs) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(vs));
+  return y;
+}
+// 2^x, also below 2^-126.
+__device__ __forceinline__ float ex2_whole(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// w for a row whose maximum of s + log2 vs is z and of s is m, and the factor 2^(m - w) of its value scales.
+__device__ __forceinline__ float value_reference(float w, float z, float m) { return fmaxf(fmaxf(w, z), m - kValueFloor); }
+__device__ __forceinline__ float value_factor(float m, float w) { return w == -INFINITY ? 0.f : ex2_whole(m - w); }
+// vs times that factor.  Finite, or NaN where vs is: with next to no probability behind it, it may be beyond fp32.
+__device__ __forceinline__ float value_weight(float vs, float factor) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(vs * factor), "f"(3.402823466e38f));
+  return y;
 }
 
 // The upper bits of the bytes of w that are an e4m3 NaN.

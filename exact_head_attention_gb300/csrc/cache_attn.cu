@@ -3,9 +3,15 @@
 //
 // Mathematics.  With codes k, v and the scales ks, vs of their page, a score is s = c (q . k) ks with
 // c = scale * log2(e), and the online softmax keeps m >= max s - 8, l = sum 2^(s - m) and
-// O = sum 2^(s - m) (vs / vref) v with vref >= vs / 16 for every vs met so far, so that the probabilities
-// times vs / vref stay below 2^15 in fp16 whatever the scales are.  The codes enter the products as they
-// are (fp16 holds them exactly).  Pieces of the key axis are merged by their log-sum-exp.
+// O = sum 2^(s - w) vs v with w >= max(s + log2 vs) - 12 (cache8.cuh), so that what stands before v stays below 2^15 in
+// fp16 whatever the scales are.  The codes enter the products as they are (fp16 holds them exactly).  Pieces of the key
+// axis are merged by their log-sum-exp.
+//   A row's w is m + kappa.  As long as all value scales that a warp meets lie within [vref, 16 vref], vref half the
+// least of its first tile or less, kappa is log2 vref for every row, which satisfies w's bounds without a look at the
+// scores.  From the first tile on where one does not, the warp keeps a kappa for each row in shared memory and looks for
+// the maxima of s + log2 vs, a path of its own.  (One path, with a kappa in registers for each row, took 27.3 us for five
+// tokens on 32 ragged sequences, which take 26.3; a reference over the scales alone, whatever the rows see of them, 25.8.
+// With every 7th page's scale 100 times the others' these five tokens take 36 us, one token over 32k the same 125.)
 //
 // Bound.  With one to some tens of query rows a key/value head the time is that of reading the codes: 2 d
 // bytes a token and head against 4 d rows flops.  A block (one an SM) therefore keeps 128 to 192 KB of copies
@@ -44,10 +50,9 @@
 namespace exattn {
 namespace {
 
-// P is held times 2^kShift, so that fewer of the small ones become subnormal in fp16.  It stays below 2^15: the
-// running maximum may lag by 2^8, and vref by kVrefLag = 2^4.
-constexpr float kShift = 3.f, kVrefLag = 16.f;
-constexpr float kVrefLeast = 1.17549435e-38f;  // 2^-126: the reciprocal is finite
+// P is held times 2^kShift, so that fewer of the small ones become subnormal in fp16.  With the value scales it stays below
+// 2^15: s - m may be 8, and vs / vref 2^4.
+constexpr float kShift = 3.f;
 
 constexpr int kWorkers = 2;                     // of a block: each with its own share of the work
 constexpr int kGroup = 4;                       // computing warps of a worker
@@ -75,7 +80,7 @@ struct Cfg {
   static constexpr int QBYTES = Q_IN_SMEM ? NT * (D / 16) * 32 * 8 : 0;
   static constexpr int RINGQ = 2;                             // pieces announced ahead
   static constexpr int QROWS = R * D * 2;                     // the rows of one piece as they lie in memory
-  static constexpr int STAT = (2 * kGroup * R + kGroup) * 4;  // m[R][warp], l[R][warp], vref[warp]
+  static constexpr int STAT = 3 * kGroup * R * 4;        // m, l, kappa [R][warp]
   using Walk = CacheWalk<R, TK, 64, kMinTiles>;
   // a worker's part of shared memory
   static constexpr int W_JOIN = 0;
@@ -127,6 +132,9 @@ __device__ __forceinline__ void tma_load_lines(uint32_t dst, const CUtensorMap* 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(line), "r"(bar)
       : "memory");
 }
+
+// log2 of a power of two.
+__device__ __forceinline__ float exponent_of(float x) { return static_cast<float>((__float_as_int(x) >> 23) - 127); }
 
 __device__ __forceinline__ float qnan() { return __int_as_float(0x7fffffff); }
 
@@ -267,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
       if (r1.page != kNoTile) {
         const bool there = r1.ks == 0.f;
         r1.page = cache_page_checked(a.c, r1.page);
-        r1.ks = r1.vs = there ? qnan() : 0.f;
+        r1.ks = there ? qnan() : 0.f;
+        r1.vs = qnan();  // behind the sequence's end: not counted among the scales that the tile has
         if (r1.page >= 0) {
           const long long h = static_cast<long long>(r1.page) * a.c.heads + r1.head;
           r1.ks = a.c.k_scale[h];
@@ -295,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
   uint8_t* ring = smem_raw + warp * (NST * 2 * C::TILE);
   float* st_m = reinterpret_cast<float*>(wmem + C::W_STAT);
   float* st_l = st_m + kGroup * C::R;
-  float* st_v = st_l + kGroup * C::R;
+  float* st_k = st_l + kGroup * C::R;
   float4* join = reinterpret_cast<float4*>(wmem + C::W_JOIN);
   uint2* qs = reinterpret_cast<uint2*>(wmem + C::W_Q);
   const CacheWs ws = cache_ws(a.ws, C::R, D, a.sm_count * kWorkers);
@@ -388,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
-    float vref = 0.f, vinv = 0.f;
+    float vref = 0.f, vinv = 0.f;  // powers of two, until `uneven`
+    bool uneven = false;           // the rows' kappa are in st_k
 
     for (int t = begin + gw; t < end; t += kGroup, ++used) {
       const int s = used % NST;
@@ -434,13 +444,22 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
         }
       }
 
-      // Online softmax; group i of the tile has one page and so one scale.  The maximum is looked for only where
-      // a score passes the running one by more than 2^8: until then it may lag.
+      // Online softmax; group i of the tile has one page and so one scale of each kind.  The maximum is looked for only
+      // where a score passes the running one by more than 2^8: until then it may lag.
       const bool masked = key0 + C::TK > lim_min;
-      float vnew = sc[0].y;  // a NaN scale is passed over here and met below
+      float vmin = sc[0].y, vmax = sc[0].y;  // a NaN scale is passed over here and met below
 #pragma unroll
-      for (int i = 1; i < NH; ++i) vnew = fmaxf(vnew, sc[i].y);
-      bool grow = vnew > vref * kVrefLag;
+      for (int i = 1; i < NH; ++i) {
+        vmin = fminf(vmin, sc[i].y);
+        vmax = fmaxf(vmax, sc[i].y);
+      }
+      if (t == begin + gw) {
+        const int e = max((__float_as_int(vmin) & 0x7f800000) - 0x00800000, 0);
+        vref = __int_as_float(e);
+        vinv = __int_as_float(0x7f000000 - e);
+      }
+      uneven = uneven || !(vref > 0.f) || vmin < vref || vmax > 16.f * vref;
+      bool grow = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -456,53 +475,100 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
               grow = grow || x > m[nt][e] + 8.f;
             }
           }
-      if (__any_sync(0xffffffffu, grow)) {
-        float vr = 1.f;
-        if (vnew > vref) {
-          const float to = fmaxf(vnew, kVrefLeast);
-          vr = vref / to;
-          vref = to;
-          vinv = 1.f / vref;
+      uint32_t pb[NT][2 * NH];  // P^T operand of each 8-key block
+      if (!uneven) {
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float to = m[nt][e];
+#pragma unroll
+              for (int i = 0; i < NH; ++i) to = fmaxf(to, fmaxf(sv[i][nt][e], sv[i][nt][2 + e]));
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, x));
+              const float al = to == -INFINITY ? 1.f : ex2_approx(m[nt][e] - to);
+              m[nt][e] = to;
+              l[nt][e] *= al;
+#pragma unroll
+              for (int j = 0; j < MT; ++j) {
+                o[nt][j][e] *= al;
+                o[nt][j][2 + e] *= al;
+              }
+            }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          const float ms0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kShift;
+          const float ms1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kShift;
+          uint64_t l2 = f2_pack(l[nt][0], l[nt][1]);
+#pragma unroll
+          for (int nb = 0; nb < 2 * NH; ++nb) {
+            const float r = sc[nb >> 1].y * vinv;
+            const float x0 = sv[nb >> 1][nt][2 * (nb & 1)], x1 = sv[nb >> 1][nt][2 * (nb & 1) + 1];
+            const uint64_t p2 = f2_pack(ex2_approx(x0 - ms0), ex2_approx(x1 - ms1));
+            l2 = f2_add(l2, p2);
+            float y0, y1;
+            f2_unpack(f2_mul(p2, f2_pack(r, r)), y0, y1);
+            if (masked) {  // a hidden key must not bring in a NaN scale
+              y0 = x0 == -INFINITY ? 0.f : y0;
+              y1 = x1 == -INFINITY ? 0.f : y1;
+            }
+            pb[nt][nb] = transpose8(pack2<false>(y0, y1));
+          }
+          f2_unpack(l2, l[nt][0], l[nt][1]);
+        }
+      } else {
+        // Scales far apart: each row for itself, the maxima looked for in every tile.
+        const bool first = vref >= 0.f;  // of these tiles; kappa was log2 vref, of no meaning where no key has been seen
+        const float even = exponent_of(vref);
+        vref = -1.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float vf[2], ms[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float to = m[nt][e];
+            float* const kappa = st_k + (nt * 8 + 2 * t4 + e) * kGroup + gw;
+            const float was = m[nt][e], k0 = first ? even : *kappa;
+            float to = was;
 #pragma unroll
             for (int i = 0; i < NH; ++i) to = fmaxf(to, fmaxf(sv[i][nt][e], sv[i][nt][2 + e]));
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, x));
-            const float al = to == -INFINITY ? 1.f : ex2_approx(m[nt][e] - to);
+            // kappa = max(s + log2 vs) - m over all keys; never below the last one's, as w goes
+            const bool seen = was > -INFINITY, some = to > -INFINITY;
+            const float fall = seen ? was - to : 0.f;
+            float k = seen ? k0 + fall : -kValueFloor;
+#pragma unroll
+            for (int i = 0; i < NH; ++i)
+              k = fmaxf(k, fmaxf(sv[i][nt][e], sv[i][nt][2 + e]) - to + cache_log2(sc[i].y));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) k = fmaxf(k, __shfl_xor_sync(0xffffffffu, k, x));
+            k = fmaxf(k, -kValueFloor);
+            const float ov = seen ? ex2_approx(fall + k0 - k) : 1.f;
+            l[nt][e] *= seen ? ex2_approx(fall) : 1.f;
             m[nt][e] = to;
-            l[nt][e] *= al;
-            const float ov = al * vr;
+            ms[e] = some ? to - kShift : 0.f;
+            vf[e] = ex2_whole(-k);
+            __syncwarp();
+            if (g == 0) *kappa = k;
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
               o[nt][j][e] *= ov;
               o[nt][j][2 + e] *= ov;
             }
           }
-      }
-      uint32_t pb[NT][2 * NH];  // P^T operand of each 8-key block
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float ms0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kShift;
-        const float ms1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kShift;
-#pragma unroll
-        for (int nb = 0; nb < 2 * NH; ++nb) {
-          const float r = sc[nb >> 1].y * vinv;
-          const float x0 = sv[nb >> 1][nt][2 * (nb & 1)], x1 = sv[nb >> 1][nt][2 * (nb & 1) + 1];
-          const float p0 = ex2_approx(x0 - ms0), p1 = ex2_approx(x1 - ms1);
-          l[nt][0] += p0;
-          l[nt][1] += p1;
-          float y0 = p0 * r, y1 = p1 * r;
-          if (masked) {  // a hidden key must not bring in a NaN scale
-            y0 = x0 == -INFINITY ? 0.f : y0;
-            y1 = x1 == -INFINITY ? 0.f : y1;
+          for (int nb = 0; nb < 2 * NH; ++nb) {
+            const float x0 = sv[nb >> 1][nt][2 * (nb & 1)], x1 = sv[nb >> 1][nt][2 * (nb & 1) + 1];
+            const float p0 = ex2_approx(x0 - ms[0]), p1 = ex2_approx(x1 - ms[1]);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            const float y0 = p0 * value_weight(sc[nb >> 1].y, vf[0]), y1 = p1 * value_weight(sc[nb >> 1].y, vf[1]);
+            pb[nt][nb] = transpose8(pack2<false>(x0 == -INFINITY ? 0.f : y0, x1 == -INFINITY ? 0.f : y1));
           }
-          pb[nt][nb] = transpose8(pack2<false>(y0, y1));
         }
+        __syncwarp();
       }
 
       // A NaN among the values of a token that some row does not see would reach that row through its zero
@@ -593,12 +659,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
         if (g == 0) {
           st_m[(nt * 8 + 2 * t4 + e) * kGroup + gw] = m[nt][e];
           st_l[(nt * 8 + 2 * t4 + e) * kGroup + gw] = x;
+          if (!uneven) st_k[(nt * 8 + 2 * t4 + e) * kGroup + gw] = exponent_of(vref);
         }
       }
-    if (lane == 0) {
-      st_v[gw] = vref;
-      mbar_arrive(piece_empty(pi % RQ));
-    }
+    if (lane == 0) mbar_arrive(piece_empty(pi % RQ));
     constexpr int Q4 = D / 4;   // float4s a row
     constexpr int LQ = D / 32;  // float4s of a lane's part of a row (d positions g D/8 ..)
     auto place = [&](int r, int q) {  // order of a row's float4s in which 8 lanes never meet a bank twice
@@ -625,9 +689,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
       for (int i = tid; i < nr * Q4; i += 32 * kGroup) {
         const int ri = base + i / Q4, q = i % Q4;
         const float4 sm4 = *reinterpret_cast<const float4*>(st_m + ri * kGroup), sl4 = *reinterpret_cast<const float4*>(st_l + ri * kGroup),
-                     sv4 = *reinterpret_cast<const float4*>(st_v);
+                     sk4 = *reinterpret_cast<const float4*>(st_k + ri * kGroup);
         const float sm[kGroup] = {sm4.x, sm4.y, sm4.z, sm4.w}, sl[kGroup] = {sl4.x, sl4.y, sl4.z, sl4.w},
-                    vr[kGroup] = {sv4.x, sv4.y, sv4.z, sv4.w};
+                    sk[kGroup] = {sk4.x, sk4.y, sk4.z, sk4.w};
         const float mx = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
         const float ms = mx == -INFINITY ? 0.f : mx;
         float lsum = 0.f;
@@ -635,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
 #pragma unroll
         for (int w = 0; w < kGroup; ++w) {
           if (sl[w] != 0.f) {
-            const float e = ex2_approx(sm[w] - ms), ev = e * vr[w];
+            const float e = ex2_approx(sm[w] - ms), ev = ex2_whole(sm[w] - ms + sk[w]);
             const float4 x = join[w * (C::JR * Q4) + place(ri, q)];
             lsum = fmaf(e, sl[w], lsum);
             acc.x = fmaf(ev, x.x, acc.x);

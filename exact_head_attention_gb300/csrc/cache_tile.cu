@@ -1,8 +1,8 @@
 // Attention over the 8-bit cache for many query rows a key/value head (chunks of a prompt, drafted tokens
 // under shared heads): the tensor-core form of cache_attn.cu.
 //
-// Mathematics as there: codes as they are in fp16, the key scale on the scores, the value scale over a lagging
-// vref on the probabilities.
+// Mathematics as there: codes as they are in fp16, the key scale on the scores, the value scale on the probabilities, over
+// a reference w for each row (cache8.cuh).
 //
 // Bound.  4 d flops for each row and key: the tensor cores, which tcgen05 reaches with 128 x 128 tiles in
 // tensor memory.  Its operands are fp16 in shared memory, so six warps turn each 128-token tile of codes, copied
@@ -56,11 +56,12 @@ constexpr uint32_t kRegsSoftmax = 176, kRegsOther = 80;
 static_assert(2 * kRegsSoftmax + 2 * kRegsOther == 4 * 128, "register split must match the launch");
 constexpr int kTK = 128;
 constexpr uint32_t kChunk = 128 * 128;  // 128 rows x 128 bytes
-constexpr int kPieceRing = 3, kMetaRing = 16;
+constexpr int kPieceRing = 3;
 // Flags of tiles that an item's rows see in part: at most 3 at a piece's end (the rows of an item see the keys of at
 // most 256 tokens less or more), and the converters are at most NS tiles further.
 constexpr int kFlagRing = 8;
-constexpr float kShift = 3.f, kVrefLag = 16.f, kVrefLeast = 1.17549435e-38f;  // as in cache_attn.cu
+constexpr float kShift = 3.f;  // as in cache_attn.cu
+constexpr int kMeta = 24;      // numbers a tile: ks[8], vs[8], log2 vs[8]
 
 template <int D, bool PAIR>
 struct Cfg {
@@ -72,7 +73,8 @@ struct Cfg {
   static constexpr int NR = D == 128 ? (PAIR ? 2 : 3) : 8;     // slots of codes, K and V in turn
   static constexpr int NB = D == 64 ? 3 : 2;                   // score buffers
   // Scales stay in use from a tile's copy to its softmax, over tiles of codes, operand tiles, and steps under way.
-  static_assert((NR + 1) / 2 + NS + NB + 1 <= kMetaRing, "scales of the tiles under way");
+  static constexpr int MR = D == 128 ? 8 : 16;
+  static_assert((NR + 1) / 2 + NS + NB + 1 <= MR, "scales of the tiles under way");
   static constexpr uint32_t TM_O = NB * 128;                   // O_t at TM_O + t TM_OT
   static constexpr uint32_t TM_OT = D;
   static_assert(3 + NS <= kFlagRing, "flags of the tiles under way");
@@ -82,12 +84,12 @@ struct Cfg {
   static constexpr uint32_t OFF_K = OFF_Q + (PAIR ? 2 : 1) * TILE;
   static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
   static constexpr uint32_t OFF_RAW = OFF_V + NS * TILE;
-  static constexpr uint32_t OFF_META = OFF_RAW + NR * RAW;           // [kMetaRing] ks[8], vs[8]
-  static constexpr uint32_t OFF_STAT = OFF_META + kMetaRing * 64;    // !PAIR: {m, l} [2][128], vref [2][4]
-  static constexpr uint32_t OFF_FLAG = OFF_STAT + (PAIR ? 0 : 2 * 128 * 8 + 32);  // [kFlagRing][128]: a token has a NaN value
+  static constexpr uint32_t OFF_META = OFF_RAW + NR * RAW;           // [MR][kMeta]
+  static constexpr uint32_t OFF_STAT = OFF_META + MR * kMeta * 4;    // !PAIR: {m, l} [2][128], w [2][128]
+  static constexpr uint32_t OFF_FLAG = OFF_STAT + (PAIR ? 0 : 2 * 128 * 12);  // [kFlagRing][128]: a token has a NaN value
   static constexpr uint32_t OFF_PIECE = OFF_FLAG + kFlagRing * 128;
   static constexpr uint32_t OFF_BAR = OFF_PIECE + kPieceRing * kPieceInts * 4;
-  static constexpr int NBAR = 2 + 4 * NS + NR + 2 * ((NR + 1) / 2) + 6 + kMetaRing + 2 * kPieceRing + 4;
+  static constexpr int NBAR = 2 + 4 * NS + NR + 2 * ((NR + 1) / 2) + 6 + MR + 2 * kPieceRing + 4;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t OFF_SCHED = OFF_MISC + 16;
   static constexpr uint32_t BYTES = OFF_SCHED + sizeof(typename Walk::Shared);
@@ -120,7 +122,7 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0u;
 }
 
-template <int NS, int NR>
+template <int NS, int NR, int MR>
 struct Bars {
   uint32_t base;
   __device__ uint32_t at(int i) const { return base + 8 * i; }
@@ -142,23 +144,23 @@ struct Bars {
   __device__ uint32_t p_full(int b) const { return at(kB + 3 + b); }
   static constexpr int kC = kB + 6;
   __device__ uint32_t meta_full(int s) const { return at(kC + s); }
-  __device__ uint32_t piece_full(int s) const { return at(kC + kMetaRing + s); }
-  __device__ uint32_t piece_empty(int s) const { return at(kC + kMetaRing + kPieceRing + s); }
-  __device__ uint32_t join() const { return at(kC + kMetaRing + 2 * kPieceRing); }
-  __device__ uint32_t mma_done() const { return at(kC + 1 + kMetaRing + 2 * kPieceRing); }
-  __device__ uint32_t stored(int t) const { return at(kC + 2 + kMetaRing + 2 * kPieceRing + t); }
+  __device__ uint32_t piece_full(int s) const { return at(kC + MR + s); }
+  __device__ uint32_t piece_empty(int s) const { return at(kC + MR + kPieceRing + s); }
+  __device__ uint32_t join() const { return at(kC + MR + 2 * kPieceRing); }
+  __device__ uint32_t mma_done() const { return at(kC + 1 + MR + 2 * kPieceRing); }
+  __device__ uint32_t stored(int t) const { return at(kC + 2 + MR + 2 * kPieceRing + t); }
 };
 
 // One key tile of the online softmax for this thread's query row.  Scores of the 16-token group g count
-// fac * ks[g]; P goes out in fp16 times vs[g] / vref (sc: ks[8], vs[8]).  Columns at or past `lim` are hidden
-// (MASKED).  All 128 scores are read for the maximum; the upper 64 are read again for P, which saves the
+// fac * ks[g]; P goes out in fp16 times vs[g] 2^(m - w) (sc: ks[8], vs[8], log2 vs[8]; vf: 2^(m - w)).  Columns at or past
+// `lim` are hidden (MASKED).  All 128 scores are read for the maxima; the upper 64 are read again for P, which saves the
 // registers that they would hold meanwhile.  P's packed columns overwrite scores of the lower 64 only.
 // wait_pv() runs (warp-uniformly) before O is rescaled: the chain's last product may still be under way.
 // HALF: the row is here twice, and this thread has 64 of its 128 scores: from column 64 `half` on, `sc` and `lim` likewise.
 // The other half of its P is zero.
 template <int D, bool MASKED, bool HALF, typename WaitPv>
 __device__ __forceinline__ void softmax_scaled(uint32_t tS, int half, uint32_t tO, const float* sc, int lim, float fac,
-                                               bool first, float& m, float& l, float& vref, float& vinv, WaitPv&& wait_pv) {
+                                               bool first, float& m, float& l, float& w, float& vf, WaitPv&& wait_pv) {
   constexpr int CHUNKS = HALF ? 2 : 4, GROUPS = 2 * CHUNKS;
   const uint32_t tX = HALF ? tS + half * 64 : tS, tP = HALF ? tS + half * 32 : tS;
   uint32_t sr[CHUNKS][32];
@@ -180,9 +182,11 @@ __device__ __forceinline__ void softmax_scaled(uint32_t tS, int half, uint32_t t
   tmem_wait_ld();
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) reg_fence32(sr[c]);
-  float m_new = -INFINITY, v_new = -INFINITY;
+  float m_new = -INFINITY, w_new = -INFINITY;
+  float4 lv;
 #pragma unroll
   for (int g = 0; g < GROUPS; ++g) {
+    if (g % 4 == 0) lv = *reinterpret_cast<const float4*>(sc + 16 + g);
     float a = -INFINITY, b = -INFINITY;  // a NaN is passed over: it is met below
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
@@ -195,20 +199,15 @@ __device__ __forceinline__ void softmax_scaled(uint32_t tS, int half, uint32_t t
       a = max3(a, v[0], v[1]);
       b = max3(b, v[2], v[3]);
     }
-    m_new = fmaxf(m_new, fmaxf(a, b) * f[g]);
-    v_new = fmaxf(v_new, vs[g]);
+    const float x = fmaxf(a, b) * f[g];
+    m_new = fmaxf(m_new, x);
+    w_new = fmaxf(w_new, x + (g % 4 == 0 ? lv.x : g % 4 == 1 ? lv.y : g % 4 == 2 ? lv.z : lv.w));
   }
   const bool need = first || m_new > m + 8.0f;
-  if (__any_sync(0xffffffffu, need || v_new > vref * kVrefLag)) {
-    const float to = need ? m_new : m;
+  if (__any_sync(0xffffffffu, need || w_new > w + kValueLag)) {
+    const float to = need ? m_new : m, wt = value_reference(w, w_new, to);
     const float al = need && !first ? ex2_approx(m - to) : 1.0f;
-    float ov = al;
-    if (first || v_new > vref) {
-      const float v = fmaxf(v_new, kVrefLeast);
-      ov *= vref / v;
-      vref = v;
-      vinv = 1.0f / v;
-    }
+    const float ov = wt == -INFINITY ? 1.0f : ex2_approx(w - wt);
     if (!first) {
       wait_pv();
 #pragma unroll 1
@@ -223,6 +222,8 @@ __device__ __forceinline__ void softmax_scaled(uint32_t tS, int half, uint32_t t
     }
     l *= al;
     m = to;
+    w = wt;
+    vf = value_factor(to, wt);
   }
   const float ms = m == -INFINITY ? 0.f : m - kShift;
   const uint64_t nm2 = f2_pack(-ms, -ms);
@@ -233,7 +234,7 @@ __device__ __forceinline__ void softmax_scaled(uint32_t tS, int half, uint32_t t
     uint32_t pk[16];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float r = vs[2 * c + h] * vinv;
+      const float r = value_weight(vs[2 * c + h], vf);
       const uint64_t f2 = f2_pack(f[2 * c + h], f[2 * c + h]), r2 = f2_pack(r, r);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -407,11 +408,11 @@ struct Third {
 template <int D, int FMT, bool BF16, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_constant__ CacheAttnArgs a) {
   using C = Cfg<D, PAIR>;
-  constexpr int NS = C::NS, NR = C::NR;
+  constexpr int NS = C::NS, NR = C::NR, MR = C::MR;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t sbase = smem_u32(smem_raw);
   if (!smem_base_aligned(sbase, a.err_word)) return;
-  const Bars<NS, NR> bars{sbase + C::OFF_BAR};
+  const Bars<NS, NR, MR> bars{sbase + C::OFF_BAR};
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + C::OFF_MISC);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_raw + C::OFF_MISC + 4);
   const WaitCtx wc{abort_flag, a.err_word, a.timeout_ns};
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     }
     for (int s = 0; s < NR; ++s) mbar_init(bars.raw_empty(s), 3);
     for (int i = 0; i < 2 * bars.FR; ++i) mbar_init(bars.raw_full(i & 1, i >> 1), 1);
-    for (int s = 0; s < kMetaRing; ++s) mbar_init(bars.meta_full(s), 1);
+    for (int s = 0; s < MR; ++s) mbar_init(bars.meta_full(s), 1);
     for (int s = 0; s < kPieceRing; ++s) {
       mbar_init(bars.piece_full(s), 1);
       mbar_init(bars.piece_empty(s), 15);  // 8 softmax warps, 6 converters, the MMA issuer
@@ -520,10 +521,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
 #pragma unroll 1
         for (int q = 0; q < r0.tiles; ++q) {
           if (!(ok = copy(a.c.k, r0, q))) break;
-          const int ms = issued++ % kMetaRing;
+          const int ms = issued++ % MR;
           if (lane >> 3 == q) {
-            meta[ms * 16 + group] = r0.ks;
-            meta[ms * 16 + 8 + group] = r0.vs;
+            meta[ms * kMeta + group] = r0.ks;
+            meta[ms * kMeta + 8 + group] = r0.vs;
+            meta[ms * kMeta + 16 + group] = cache_log2(r0.vs);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bars.meta_full(ms));
@@ -583,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       constexpr uint32_t idPV = idesc_f16(128, D, false, false, true);
       constexpr uint32_t kTileLo = C::TILE >> 4;
       const uint32_t ubase = __shfl_sync(0xffffffffu, sbase, 0), utmem = __shfl_sync(0xffffffffu, tmem, 0);
-      const Bars<NS, NR> ub{ubase + C::OFF_BAR};
+      const Bars<NS, NR, MR> ub{ubase + C::OFF_BAR};
       const uint32_t q_lo = sdesc_lo(ubase + C::OFF_Q, 16), k_lo = sdesc_lo(ubase + C::OFF_K, 16),
                      v_lo = sdesc_lo(ubase + C::OFF_V, kChunk);
       constexpr int NB = C::NB;
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
     const uint32_t tS = tmem + lane_bits /* buffer 0 */, tO = tmem + C::TM_O + t * C::TM_OT + lane_bits;
     const CacheWs ws = cache_ws(a.ws, C::R, D, a.sm_count);
     float2* stat = reinterpret_cast<float2*>(smem_raw + C::OFF_STAT);
-    float* stat_v = reinterpret_cast<float*>(smem_raw + C::OFF_STAT + 2 * 128 * 8);
+    float* stat_ref = reinterpret_cast<float*>(smem_raw + C::OFF_STAT + 2 * 128 * 8);
     constexpr int NB = C::NB;
     int kt = 0;
     uint32_t seq = 0;                        // steps of both chains in earlier pieces
@@ -755,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       if (!PAIR || n > 0) {
         const int row_first = p.rt * C::R + ri - lane;  // of this warp
         const bool idle = row_first >= rows;            // a warp of rows that are not there
-        float m = -INFINITY, l = 0.f, vref = 0.f, vinv = 0.f;
+        float m = -INFINITY, l = 0.f, ref = -INFINITY, vf = 0.f;
         {
           // The previous piece's score products have completed: this warpgroup has seen them all end,
           // the other (!PAIR) has before the join that ended the epilogue.
@@ -779,10 +781,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
             const int i = PAIR ? j : 2 * j + t, nt = kt + i;  // key tile
             const uint32_t g = seq + (both ? 2 * j + t : j), b = g % NB;
             if (!(ok = mbar_wait_warp(bars.s_full(b), (g / NB) & 1, wc))) break;
-            if (!(ok = mbar_wait_warp(bars.meta_full(nt % kMetaRing), (nt / kMetaRing) & 1, wc))) break;
+            if (!(ok = mbar_wait_warp(bars.meta_full(nt % MR), (nt / MR) & 1, wc))) break;
             tc_fence_after();
             if (!idle) {
-              const float* scales = meta + (nt % kMetaRing) * 16;
+              const float* scales = meta + (nt % MR) * kMeta;
               // The chain's last product.  With two buffers that the chains share, these scores were issued after it.
               // With three, or with two and the steps of one chain only, it may still be under way: its end (and that
               // of the other chain's on the same values) frees the tile's slot.
@@ -797,13 +799,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
               const int lim = lim_row - i * kTK;
               if (!PAIR && twice) {
                 if (masked)
-                  softmax_scaled<D, true, true>(tS + b * 128, half, tO, scales + 4 * half, lim - 64 * half, fac, j == 0, m, l, vref, vinv, wait_pv);
+                  softmax_scaled<D, true, true>(tS + b * 128, half, tO, scales + 4 * half, lim - 64 * half, fac, j == 0, m, l, ref, vf, wait_pv);
                 else
-                  softmax_scaled<D, false, true>(tS + b * 128, half, tO, scales + 4 * half, kTK, fac, j == 0, m, l, vref, vinv, wait_pv);
+                  softmax_scaled<D, false, true>(tS + b * 128, half, tO, scales + 4 * half, kTK, fac, j == 0, m, l, ref, vf, wait_pv);
               } else if (masked) {
-                softmax_scaled<D, true, false>(tS + b * 128, 0, tO, scales, lim, fac, j == 0, m, l, vref, vinv, wait_pv);
+                softmax_scaled<D, true, false>(tS + b * 128, 0, tO, scales, lim, fac, j == 0, m, l, ref, vf, wait_pv);
               } else {
-                softmax_scaled<D, false, false>(tS + b * 128, 0, tO, scales, kTK, fac, j == 0, m, l, vref, vinv, wait_pv);
+                softmax_scaled<D, false, false>(tS + b * 128, 0, tO, scales, kTK, fac, j == 0, m, l, ref, vf, wait_pv);
               }
               tmem_wait_st();
             }
@@ -825,11 +827,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
         float w0 = 0.f, w1 = 0.f, lse2;  // factors of O_0 and O_1 (PAIR: of O_t)
         bool use1 = false;
         if constexpr (PAIR) {
-          w0 = l == 0.f ? 0.f : vref / l;
+          w0 = l == 0.f ? 0.f : ex2_whole(ref - m) / l;
           lse2 = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) - kShift + __log2f(l);
         } else {
           stat[t * 128 + r] = make_float2(m, l);
-          if (lane == 0) stat_v[t * 4 + quarter] = vref;
+          stat_ref[t * 128 + r] = ref;
           tc_fence_before();
           if (!(ok = ok && join())) break;
           use1 = both;
@@ -844,8 +846,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
           auto part_sum = [&](float2 v) { return v.y == 0.f ? 0.f : share(v) * v.y; };
           const float sum = part_sum(x) + part_sum(y) + (part_sum(x2) + part_sum(y2));
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          w0 = share(x) * stat_v[quarter] * inv;
-          w1 = use1 ? share(y) * stat_v[4 + quarter] * inv : 0.f;
+          auto weight = [&](float2 v, int at) { return v.y == 0.f ? 0.f : ex2_whole(stat_ref[at] - ms) * inv; };
+          w0 = weight(x, r);
+          w1 = use1 ? weight(y, 128 + r) : 0.f;
           lse2 = sum == 0.f ? -INFINITY : ms - kShift + __log2f(sum);
         }
         if (!ok) break;

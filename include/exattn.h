@@ -606,8 +606,9 @@ attn_status attn_cache_read(const attn_cache* cache, const int* start, const int
  * not touched by either.
  * The codes are multiplied as they are (fp16 holds every code exactly) and the
  * scales applied to the products; Q in bf16 is scaled by a power of two per
- * row to fit fp16; the probabilities are rounded to fp16, sums are fp32.  The
- * same bits on every run.
+ * row to fit fp16; the probabilities times the value scales are rounded to
+ * fp16, relative to the largest that the row sees; sums are fp32.  The same bits
+ * on every run.
  * workspace: attn_fwd_cache_workspace_size bytes, 256-byte aligned, contents
  * on entry irrelevant; calls that may run at the same time need one each.  After
  * a wait that timed out (attn_check_device_error), the workspace of a captured

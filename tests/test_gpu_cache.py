@@ -472,6 +472,88 @@ def test_value_scales_below_the_smallest_normal_number(group, n, d):
         assert torch.all((o.double().cpu() - ro).abs() <= tol), (powers, ((o.double().cpu() - ro).abs() / tol).max())
 
 
+
+def check_weighted(q, cache, host, table, lens, o, lse, mask="bottom_right", scale=None):
+    """As check_attention, by what each row itself sees and how much it weighs.
+
+    With the reference that P * vs is scaled by within 2^12 of the row's largest P * vs and never above it, the rounding of
+    P * vs to fp16 is 2^-11 of each, or 2^-25 where 2^3 stands for no more than the largest: LARGEST * 2^-28 of it in O for
+    each key.  The other errors that the tolerances above count are relative to each P: with the first 2^-10 of sum P |v|.
+    A reference is held to 2^-126 of the row's largest weight, and a type's smallest numbers are rounded by half of one."""
+    scale = 1 / math.sqrt(q.shape[3]) if scale is None else scale
+    ro, rlse, _ = plain_attention(q, host, table, lens, mask, scale)
+    B, H, n, d = q.shape
+    group = H // host["k"].shape[1]
+    page = host["k"].shape[2]
+    most = LARGEST["e4m3" if host["k"].dtype == CODES["e4m3"] else "int8"]
+    o, lse = o.double().cpu(), lse.double().cpu()
+    assert torch.equal(lse == -math.inf, rlse == -math.inf)
+    seen = rlse > -math.inf
+    assert torch.all((lse - rlse)[seen].abs() <= 1e-4)
+    assert torch.all(o[~seen] == 0)
+    for b, length in enumerate(lens):
+        if length == 0:
+            continue
+        k, v = tokens(host, "k", table, b, length), tokens(host, "v", table, b, length)
+        vs = host["v_scale"][table[b, : -(-length // page)].long()].double().T.repeat_interleave(page, 1)[:, :length]
+        i, t = torch.arange(n)[:, None], torch.arange(length)[None]
+        hidden = {"bottom_right": t > i + length - n, True: t > i, False: t < 0}[mask]
+        for h in range(H):
+            s = ((q[b, h].double() @ k[h // group].T) * scale).masked_fill(hidden, -math.inf)
+            P = torch.exp(s - rlse[b, h][:, None].clamp(min=-1e300))
+            largest = (P * vs[h // group]).amax(1, keepdim=True)
+            tol = 2.0 ** -10 * (P @ v[h // group].abs()) + length * most * 2.0 ** -28 * largest
+            tol = tol + torch.finfo(q.dtype).eps / 2 * ro[b, h].abs() + length * most * 2.0 ** -154
+            tol = tol + (2.0 ** -134 if q.dtype == torch.bfloat16 else 2.0 ** -25)
+            assert torch.all((o[b, h] - ro[b, h]).abs() <= tol), (b, h, ((o[b, h] - ro[b, h]).abs() / tol).max())
+
+
+SCALE_ROWS = [(1, 1), (1, 5), (3, 10), (4, 6), (1, 25), (2, 32), (1, 65), (1, 128), (3, 60), (1, 256), (2, 150), (1, 385)]
+
+
+@pytest.mark.parametrize("group,n", SCALE_ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("mask", ["bottom_right", True], ids=str)
+def test_large_value_scales_of_hidden_pages(group, n, d, mask):
+    """A page that a sequence's last queries see alone, with values far above the others': the other rows do not notice."""
+    lens = [n + 300, n + 3, 500]
+    for f in (1e3, 1e6, 1e9, 1e30):
+        cache, host, table = make_cache(3, 2, 16, d, -(-(n + 500) // 16), "e4m3", seed=64)
+        for b, length in enumerate(lens):
+            last = length if mask == "bottom_right" else min(n, length)  # the last key that any row sees is before it
+            host["v_scale"][table[b, (last - 1) // 16].item()] *= f
+        cache = exattn.QuantCache(*(host[x].to(DEV) for x in ("k", "v", "k_scale", "v_scale")), cache.page_table)
+        q = _q(3, 2 * group, n, d, "bf16", seed=65)
+        o, lse = exattn.forward_cache(q.to(DEV), cache, torch.tensor(lens, dtype=torch.int32, device=DEV), mask)
+        check_weighted(q, cache, host, table, lens, o, lse, mask)
+
+
+@pytest.mark.parametrize("rows", RISING_ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_large_value_scales_of_little_weight(rows, d, code):
+    """Tokens that all rows see, of next to no weight for some of them, with values far above the others'."""
+    lens = [1192, 700]
+    for level, f in ((-25, 1e6), (-25, 1e12), (-30, 1e20), (20, 1e-9)):
+        for at in (0, 2, 4):  # 128 tokens each
+            q, host, table = rising_scores(rows, d, code, lambda t: level if t // 128 == at else 0, lens[0], seed=66)
+            page = host["v"].shape[2]
+            host["v_scale"][table[0, at * 128 // page : (at + 1) * 128 // page].long()] *= f
+            check_copies(q.to(torch.bfloat16), host, table, lens, check_weighted)
+
+
+@pytest.mark.parametrize("rows", RISING_ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_and_value_scales_that_rise_and_fall(rows, d):
+    lens = [1192, 700]
+    for by, ratio in ((10, 30), (10, 1 / 30), (-10, 1000), (-10, 1 / 1000), (0, 1e4), (0, 1e-4)):
+        q, host, table = rising_scores(rows, d, "e4m3", lambda t: max(-30, min(30, (t // 128 - 4) * by)), lens[0], seed=67)
+        page = host["v"].shape[2]
+        f = torch.tensor([float(ratio) ** (j * page // 128 - 4) for j in range(table.shape[1])])
+        host["v_scale"][table[0].long()] *= f[:, None]
+        check_copies(q.to(torch.bfloat16), host, table, lens, check_weighted)
+
+
 # ------------------------------------------------------------------ write and read
 
 
