@@ -95,10 +95,10 @@ cudaError_t launch_cache_tile(const CacheAttnArgs& a, cudaStream_t stream);
 // Up to this many query rows a key/value head attn_fwd_cache streams the codes through the warp-level products
 // (cache_attn.cu), above it through the tensor-memory ones (cache_tile.cu).  The first keep Q and O in registers: with
 // 32 rows those run out, with 24 the codes still set the pace.  Measured, warp-level against tensor-memory:
-//   8 sequences of 32k tokens, 12 heads of 128   17 rows 155 : 239 us   24 rows 157 : 240 us   32 rows 272 : 241 us
-//   the same, 24 heads of 64                     17 rows 194 : 220 us   24 rows 195 : 220 us   32 rows 277 : 221 us
-//   4 sequences of 300 tokens, 4 heads of 128    20 rows 17.5 : 13.8 us                        32 rows 29.5 : 14.5 us
-// (the lengths are not known where the choice is made).
+//   8 sequences of 32k tokens, 12 heads of 128   17 rows 158 : 242 us   24 rows 160 : 243 us   32 rows 272 : 243 us
+//   the same, 24 heads of 64                     17 rows 197 : 221 us   24 rows 197 : 221 us   32 rows 277 : 221 us
+//   4 sequences of 300 tokens, 4 heads of 128    20 rows 15.6 : 13.8 us                        32 rows 29.5 : 14.5 us
+// (the lengths are not known where the choice is made; the warp-level form for 32 rows is gone since its measurement).
 constexpr int kCacheStreamRows = 24;
 // Tokens per box of the tensor maps launch_cache_attn wants; query rows and keys of its tiles for so many
 // rows a key/value head; its workspace bytes.

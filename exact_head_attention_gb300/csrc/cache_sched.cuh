@@ -9,8 +9,8 @@
 //   * where the items cut into pieces of C tiles make no more pieces than there are blocks, a block takes one of
 //     those, so that short items are not cut for nothing.  C is kMinTiles, twice that where it cuts no item at all (a
 //     merge takes longer than kMinTiles more tiles), or 2 or 4 times that where smaller ones are too many and blocks
-//     would have as many tiles in the first form.  Measured, five tokens on 32 sequences, 4 heads of 64, 20 rows each:
-//     1024 cached tokens 16.3 us, 2048 22.0 us; with kMinTiles alone 16.8 and 26.0.
+//     would have as many tiles in the first form.  Measured when this was chosen, five tokens on 32 sequences, 4 heads of
+//     64, 20 rows each: 1024 cached tokens 16.3 us, 2048 22.0 us (16.5 and 22.3 now); with kMinTiles alone 16.8 and 26.0.
 // In the first form an item also counts kItemCost tiles that are not there, before its own: what it costs to
 // begin and to end a piece.  Without them a block whose share were many short sequences took 1.6 times as
 // long as the average block (64 sequences spread over 1 to 8191 tokens, 8 heads).
@@ -105,14 +105,15 @@ struct CachePiece {
 constexpr int kPieceInts = 12;  // room for one
 
 // Called by a warp (all lanes) after the block's worker, or the warpgroup `part`, has stored its piece and met:
-// counts the piece; true where every piece of the item has been, and the count is at rest again.
+// counts the piece; true where every piece of the item has been, and the count is at rest again.  The other pieces'
+// partial results are then visible to lane 0, and to other threads once they have met it at a barrier.
 __device__ __forceinline__ bool cache_piece_done(const CacheWs& ws, const CachePiece& p, int part, unsigned long long tag) {
   bool all = false;
   if ((threadIdx.x & 31) == 0) {
     unsigned long long* at = ws.count + 2 * p.slot_of(0) + part;
     const unsigned long long n = static_cast<unsigned long long>(p.pieces);
     unsigned long long seen, old;
-    // release: the partial result before the count; acquire: the others' partial results after it
+    // release: the partial result before the count; acquire: the others' partial results after it, for this lane
     asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(seen) : "l"(at) : "memory");
     for (;;) {
       if ((seen & ~0xffffull) == tag) {  // nobody puts it to rest before this piece is counted

@@ -523,7 +523,7 @@ attn_status attn_bwd_noalloc(const void* Q, const void* K, const void* V, const 
  *                    t % page_size.  Entries past a sequence's last page are
  *                    not read.  A page may stand in several sequences' tables
  *                    (a shared prefix), but a write must reach each page from
- *                    one sequence only.
+ *                    one place of one sequence's table only.
  *   heads            key/value heads; page_size 16, 32, 64 or 128; d 64 or 128
  * num_pages * heads * page_size * d / 128 must be below 2^31.
  * Lengths and positions are int32 arrays on the device, so that a captured
