@@ -105,6 +105,13 @@ attn_status device_state(DeviceState** out) {
     st.ready = true;
   }
   if (!st.supported) return ATTN_ERR_UNSUPPORTED;
+  // A host thread that has made no runtime call of its own yet (an autograd worker) has no context bound, which the
+  // tensor-map encoder needs; setting the device binds it.
+  thread_local int bound = -1;
+  if (bound != dev) {
+    if ((e = cudaSetDevice(dev)) != cudaSuccess) return cuda_fail("cudaSetDevice", e);
+    bound = dev;
+  }
   *out = &st;
   return ATTN_OK;
 }
