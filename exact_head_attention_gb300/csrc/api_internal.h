@@ -9,6 +9,7 @@
 
 #include "../../include/exattn.h"
 #include "kernels.h"
+#include "rope.h"
 
 namespace exattn {
 
@@ -27,6 +28,8 @@ attn_status api_finish(cudaError_t e, cudaStream_t stream);
 attn_status api_driver_fail(const char* what, int code);
 // attn_strides rules; extents of 1 get a stride that nothing uses.
 bool api_strides(const attn_strides& in, int B, int H, int d, RowStrides* out);
+// attn_rope rules, and its view for the kernels; `normed`: there are weights of a norm.
+attn_status api_rope(const attn_rope* rope, int B, int N, int d, bool normed, RopeView* out);
 // 2-D byte map {128, lines} over contiguous 128-byte lines, box {128, box_lines}, 128-byte swizzle.
 CUresult api_encode_lines(CUtensorMap* map, const void* base, uint64_t lines, uint32_t box_lines);
 

@@ -7,6 +7,7 @@ no fallback: if the library is missing or fails to load, these functions raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -41,6 +42,14 @@ class CacheStruct(ctypes.Structure):
     """attn_cache"""
     _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "page_table")]
                 + [(n, ctypes.c_int) for n in ("num_pages", "heads", "page_size", "d", "table_width", "format")])
+
+
+class RopeStruct(ctypes.Structure):
+    """attn_rope"""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("freq", "start", "offsets")] + [("offset_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in ("q_weight", "k_weight")]
+                + [(n, ctypes.c_int) for n in ("rotary_dim", "layout", "weight_fp32")]
+                + [(n, ctypes.c_float) for n in ("amplitude", "eps")])
 
 
 class AttnError(RuntimeError):
@@ -125,6 +134,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.attn_fwd_cache.restype = i
             lib.attn_fwd_cache_workspace_size.argtypes = [cp, i, i, i]
             lib.attn_fwd_cache_workspace_size.restype = sz
+            rp = ctypes.POINTER(RopeStruct)
+            lib.attn_rope_fwd.argtypes = [vp, st, vp, st, vp, st, vp, st, i, i, i, i, i, rp, i, vp]
+            lib.attn_rope_fwd.restype = i
+            lib.attn_rope_bwd.argtypes = [vp, st, vp, st, vp, st, vp, st, vp, st, vp, st, vp, vp, i, i, i, i, i, rp, i, vp,
+                                          sz, vp]
+            lib.attn_rope_bwd.restype = i
+            lib.attn_rope_bwd_workspace_size.argtypes = [i]
+            lib.attn_rope_bwd_workspace_size.restype = sz
             lib.attn_status_string.argtypes = [i]
             lib.attn_status_string.restype = ctypes.c_char_p
             lib.attn_check_device_error.argtypes = [vp]
@@ -560,13 +577,7 @@ def _int32(t, cache: QuantCache, name: str):
 _STRIDES: dict = {}  # Strides objects by their values (building one costs more than the rest of a view's marshalling)
 
 
-def _cache_view(t, cache: QuantCache, dtype):
-    """(pointer, Strides) of a 16-bit [B, H, N, d] view that goes with the cache."""
-    shape = t.shape
-    if len(shape) != 4 or shape[0] != cache.B or shape[3] != cache.d:
-        raise ValueError("tensors must be [B, H, N, d] with the page table's B and the cache's d")
-    if t.get_device() != cache.index or t.dtype != dtype:
-        raise ValueError("tensors must be of one dtype, on the cache's device")
+def _strides(t) -> Strides:
     sb, sh, sn, sd = t.stride()
     if sd != 1:
         raise ValueError("tensors must have a contiguous last dimension")
@@ -575,23 +586,36 @@ def _cache_view(t, cache: QuantCache, dtype):
         if len(_STRIDES) >= 4096:
             _STRIDES.clear()
         st = _STRIDES[(sb, sh, sn)] = Strides(sb, sh, sn)
-    return t.data_ptr(), st
+    return st
 
 
-def _on(cache: QuantCache, stream, call):
-    """Runs `call` with the cache's device current and, where given, on `stream`: what it allocates belongs to it."""
-    with torch.cuda.device(cache.device):
+def _cache_view(t, cache: QuantCache, dtype):
+    """(pointer, Strides) of a 16-bit [B, H, N, d] view that goes with the cache."""
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != cache.B or shape[3] != cache.d:
+        raise ValueError("tensors must be [B, H, N, d] with the page table's B and the cache's d")
+    if t.get_device() != cache.index or t.dtype != dtype:
+        raise ValueError("tensors must be of one dtype, on the cache's device")
+    return t.data_ptr(), _strides(t)
+
+
+def _on(index: int, stream, call):
+    """Runs `call` with that device current and, where given, on `stream`: what it allocates belongs to it."""
+    with torch.cuda.device(index):
         if stream is None:
             return call(_stream(None))
         with torch.cuda.stream(stream):
             return call(_stream(stream))
 
 
-def _run(cache: QuantCache, stream, call):
-    index = torch.cuda.current_device()
-    if stream is None and index == cache.index and _RAW_STREAM is not None:
+def _run_at(index: int, stream, call):
+    if stream is None and _RAW_STREAM is not None and index == torch.cuda.current_device():
         return call(_RAW_STREAM(index))
-    return _on(cache, stream, call)
+    return _on(index, stream, call)
+
+
+def _run(cache: QuantCache, stream, call):
+    return _run_at(cache.index, stream, call)
 
 
 def cache_write(cache: QuantCache, k, v, start=None, count=None, stream=None) -> None:
@@ -696,3 +720,221 @@ def forward_cache(q, cache: QuantCache, lens, causal="bottom_right", scale: floa
         return o, lse
 
     return _run(cache, stream, call)
+
+
+# ------------------------------------------------------------------ rotary positions and norms per head
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_NO_STRIDES = Strides(0, 0, 0)  # of a tensor that is left out
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     trained: int | None = None, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """(freq, amplitude) for rope_forward and cache_append: freq [rotary_dim / 2] fp64 on `device`, radians a position.
+
+    Pair i turns by base^(-2 i / rotary_dim) a position.  scaling for contexts `factor` times the trained length:
+      None      as they are
+      "linear"  positions divided by the factor
+      "ntk"     the base raised so that the slowest pair is interpolated and the fastest stays
+      "yarn"    (Peng et al., 2023) pairs with more than `fast` turns over the `trained` positions as they are, with fewer
+                than `slow` interpolated, a ramp between; the amplitude 0.1 ln(factor) + 1 on queries and keys"""
+    if rotary_dim <= 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and above 0")
+    if not (base > 0 and factor > 0):
+        raise ValueError("base and factor must be above 0")
+    amplitude = 1.0
+    if scaling == "ntk":
+        if rotary_dim == 2:
+            raise ValueError("the ntk scaling needs more than one pair")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    freq = [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    elif scaling == "yarn":
+        if not trained or not fast > slow:
+            raise ValueError("the yarn scaling needs the trained length, and fast above slow")
+        keep = [min(1.0, max(0.0, (trained * f / (2.0 * math.pi) - slow) / (fast - slow))) for f in freq]
+        freq = [f * k + f / factor * (1.0 - k) for f, k in zip(freq, keep)]
+        amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return torch.tensor(freq, dtype=torch.float64, device=device), amplitude
+
+
+def _rope_struct(freq, B: int, N: int, d: int, dtype, index: int, start, offsets, layout: str, amplitude: float, q_weight,
+                 k_weight, eps: float) -> RopeStruct:
+    """attn_rope of the caller's tensors; freq None: norms only."""
+    code = ROPE_LAYOUTS.get(layout)
+    if code is None:
+        raise ValueError(f"unknown rotary layout {layout!r}")
+    at_freq = at_start = at_offsets = at_q = at_k = None
+    rot, stride, wide = 0, 0, 0
+    if freq is not None:
+        if freq.dtype != torch.float64 or freq.dim() != 1 or not freq.is_contiguous() or freq.get_device() != index:
+            raise ValueError("freq must be a contiguous float64 tensor [rotary_dim / 2] on the tensors' device")
+        rot, at_freq = 2 * freq.shape[0], freq.data_ptr()
+    if start is not None:
+        if start.dtype != torch.int32 or start.shape != (B,) or start.get_device() != index or not start.is_contiguous():
+            raise ValueError("start must be a contiguous int32 tensor of one entry a sequence on the tensors' device")
+        at_start = start.data_ptr()
+    if offsets is not None:
+        shape = offsets.shape
+        if offsets.dtype != torch.int32 or offsets.get_device() != index or shape not in ((B, N), (1, N), (N,)) or (
+                N > 1 and offsets.stride(-1) != 1):
+            raise ValueError("offsets must be an int32 tensor [B, N], [1, N] or [N], last dimension contiguous, on the tensors' device")
+        stride = offsets.stride(0) if len(shape) == 2 and shape[0] > 1 else 0
+        at_offsets = offsets.data_ptr()
+    for w in (q_weight, k_weight):
+        if w is None:
+            continue
+        if w.shape != (d,) or w.dtype not in (dtype, torch.float32) or w.get_device() != index or not w.is_contiguous():
+            raise ValueError("weights must be contiguous [d], float32 or of the tensors' dtype, on their device")
+    if q_weight is not None:
+        at_q, wide = q_weight.data_ptr(), int(q_weight.dtype == torch.float32)
+    if k_weight is not None:
+        if q_weight is not None and q_weight.dtype != k_weight.dtype:
+            raise TypeError("both weights must be of one dtype")
+        at_k, wide = k_weight.data_ptr(), int(k_weight.dtype == torch.float32)
+    return RopeStruct(at_freq, at_start, at_offsets, stride, at_q, at_k, rot, code, wide, amplitude, eps)
+
+
+def _rope_pair(q, k, names=("q", "k")):
+    """(the first that is there, heads of q, heads of k) of two [B, H, N, d] tensors, one of which may be None."""
+    x = k if q is None else q
+    if x is None:
+        raise ValueError(f"{names[0]} or {names[1]} is needed")
+    if x.dim() != 4 or (k is not None and q is not None and (k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[2:] != q.shape[2:])):
+        raise ValueError(f"{names[0]} and {names[1]} must be [B, H, N, d] with the same B, N and d")
+    if q is not None and k is not None and (q.dtype != k.dtype or q.get_device() != k.get_device()):
+        raise ValueError(f"{names[0]} and {names[1]} must be of one dtype, on one device")
+    if not x.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    return x, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+
+
+def _rope_view(t):
+    """(pointer, Strides) of a tensor that may be left out."""
+    return (None, _NO_STRIDES) if t is None else (t.data_ptr(), _strides(t))
+
+
+def _rope_like(t, like):
+    """_rope_view of a caller's tensor that must be as another is."""
+    if t is not None and (like is None or t.shape != like.shape or t.dtype != like.dtype or t.get_device() != like.get_device()):
+        raise ValueError("tensors must match in shape, dtype and device")
+    return _rope_view(t)
+
+
+def rope_forward(q, k, freq, start=None, offsets=None, layout="half", amplitude: float = 1.0, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, out=None, stream=None):
+    """Queries [B, H, N, d] and keys [B, Hk, N, d] with their heads' norms and rotary positions (attn_rope_fwd): (q, k).
+
+    freq: fp64 [rotary_dim / 2] (rope_frequencies), None for norms alone.  Row n of sequence b stands at position
+    start[b] + offsets[b, n] (int32 CUDA tensors; None: 0, and n; offsets of one row are all sequences').  layout "half":
+    pairs (i, i + rotary_dim / 2), or "interleaved": (2 i, 2 i + 1).  amplitude multiplies what turns.  q_weight, k_weight:
+    the norms' [d] weights (fp32 or as the tensors), None: no norm.  q or k may be None.  out: a pair to write to, which may
+    be (q, k) itself."""
+    x, H, Hk = _rope_pair(q, k)
+    B, _, N, d = x.shape
+    code, index = _dtype_code(x), x.get_device()
+    rope = _rope_struct(freq, B, N, d, x.dtype, index, start, offsets, layout, amplitude, q_weight, k_weight, eps)
+    views = (*_rope_view(q), *_rope_view(k))
+
+    def call(handle):
+        if out is None:
+            oq, ok = None if q is None else torch.empty_like(q), None if k is None else torch.empty_like(k)
+            to = (*_rope_view(oq), *_rope_view(ok))
+        else:
+            oq, ok = out
+            if (oq is None) != (q is None) or (ok is None) != (k is None):
+                raise ValueError("out must be a pair of what q and k are")
+            to = (*_rope_like(oq, q), *_rope_like(ok, k))
+        if B and N and (H or Hk):
+            st = load().attn_rope_fwd(*views, *to, B, H, Hk, N, d, rope, code, handle)
+            if st != ATTN_OK:
+                raise AttnError(st, "attn_rope_fwd")
+        return oq, ok
+
+    return _run_at(index, stream, call)
+
+
+def rope_bwd_workspace_size(d: int) -> int:
+    """Workspace bytes of rope_backward with weights (attn_rope_bwd_workspace_size)."""
+    return int(load().attn_rope_bwd_workspace_size(d))
+
+
+def rope_backward(dq, dk, q, k, freq, start=None, offsets=None, layout="half", amplitude: float = 1.0, q_weight=None,
+                  k_weight=None, eps: float = 1e-6, workspace=None, stream=None):
+    """Gradients of rope_forward (attn_rope_bwd): (dq, dk, dq_weight, dk_weight) from those of its outputs.
+
+    q and k are its inputs (not read, and may be None, where that tensor has no weights); the other arguments as there.
+    The weights' gradients are summed in a fixed order; None where there are no weights.  `workspace` (uint8 CUDA tensor of
+    rope_bwd_workspace_size bytes, one for each call that may run at the same time) is allocated if omitted."""
+    x, H, Hk = _rope_pair(dq, dk, ("dq", "dk"))
+    B, _, N, d = x.shape
+    code, index = _dtype_code(x), x.get_device()
+    rope = _rope_struct(freq, B, N, d, x.dtype, index, start, offsets, layout, amplitude, q_weight, k_weight, eps)
+    wq, wk = q_weight if H else None, k_weight if Hk else None
+    if (wq is not None and q is None) or (wk is not None and k is None):
+        raise ValueError("the gradients of a norm need its input")
+    views = (*_rope_view(dq), *_rope_view(dk), *_rope_like(q if wq is not None else None, dq),
+             *_rope_like(k if wk is not None else None, dk))
+    if workspace is not None and (workspace.get_device() != index or not workspace.is_contiguous()):
+        raise ValueError("the workspace must be contiguous and on the tensors' device")
+
+    def call(handle):
+        oq, ok = None if dq is None else torch.empty_like(dq), None if dk is None else torch.empty_like(dk)
+        if not (B and N and (H or Hk)):
+            return oq, ok, None if q_weight is None else torch.zeros_like(q_weight), None if k_weight is None else torch.zeros_like(k_weight)
+        dwq, dwk = None if wq is None else torch.empty_like(wq), None if wk is None else torch.empty_like(wk)
+        lib = load()
+        space, size = None, 0
+        if wq is not None or wk is not None:
+            size = lib.attn_rope_bwd_workspace_size(d)
+            space = torch.empty(size, dtype=torch.uint8, device=x.device) if workspace is None else workspace
+            size = space.numel() * space.element_size()
+        st = lib.attn_rope_bwd(*views, *_rope_view(oq), *_rope_view(ok), None if dwq is None else dwq.data_ptr(),
+                               None if dwk is None else dwk.data_ptr(), B, H, Hk, N, d, rope, code,
+                               None if space is None else space.data_ptr(), size, handle)
+        if st != ATTN_OK:
+            raise AttnError(st, "attn_rope_bwd")
+        if q_weight is not None and dwq is None:
+            dwq = torch.zeros_like(q_weight)
+        if k_weight is not None and dwk is None:
+            dwk = torch.zeros_like(k_weight)
+        return oq, ok, dwq, dwk
+
+    return _run_at(index, stream, call)
+
+
+def _plain_strides(t):
+    """t itself where the library takes its strides, else a contiguous copy (an expanded gradient, say)."""
+    if t is None:
+        return t
+    sb, sh, sn, sd = t.stride()
+    good = sd == 1 and sn >= t.shape[3] and sn % 8 == 0 and t.data_ptr() % 16 == 0
+    if good and all(n == 1 or (s > 0 and s % 8 == 0) for n, s in ((t.shape[0], sb), (t.shape[1], sh))):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+class _RopeFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, freq, start, offsets, layout, amplitude, eps):
+        ctx.save_for_backward(q if q_weight is not None else None, k if k_weight is not None else None, q_weight, k_weight,
+                              freq, start, offsets)
+        ctx.rest = (layout, amplitude, eps)
+        return rope_forward(q, k, freq, start, offsets, layout, amplitude, q_weight, k_weight, eps)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        q, k, q_weight, k_weight, freq, start, offsets = ctx.saved_tensors
+        layout, amplitude, eps = ctx.rest
+        dq, dk, dqw, dkw = rope_backward(_plain_strides(dq), _plain_strides(dk), q, k, freq, start, offsets, layout, amplitude,
+                                         q_weight, k_weight, eps)
+        return dq, dk, dqw, dkw, None, None, None, None, None, None
+
+
+def rope(q, k, freq, start=None, offsets=None, layout="half", amplitude: float = 1.0, q_weight=None, k_weight=None,
+         eps: float = 1e-6):
+    """Autograd-aware rope_forward: (q, k); gradients flow to q, k and the weights."""
+    return _RopeFunction.apply(q, k, q_weight, k_weight, freq, start, offsets, layout, amplitude, eps)

@@ -634,6 +634,81 @@ attn_status attn_fwd_cache(const void* Q, attn_strides q_strides, const attn_cac
  */
 size_t attn_fwd_cache_workspace_size(const attn_cache* cache, int B, int H, int Nq);
 
+/*
+ * Rotary positions, with RMS norms of single heads on the way (attn_rope_fwd,
+ * attn_rope_bwd, attn_cache_append).  A head x of d values of the token in row
+ * n of sequence b, at position p = start[b] + offsets[b][n], becomes
+ *   y = x w / sqrt(mean(x^2) + eps)    with the tensor's weights w, else y = x
+ *   (y_a, y_b) -> (y_a c - y_b s, y_a s + y_b c)
+ *       c = amplitude cos(p freq[i]),  s = amplitude sin(p freq[i])
+ * for the pairs i < rotary_dim / 2: (a, b) = (i, i + rotary_dim / 2) in the half
+ * layout, (2 i, 2 i + 1) in the interleaved one.  Components from rotary_dim on
+ * stay y.  All in fp32, rounded once (squares beyond fp32 are infinite); the
+ * angle is reduced to one turn exactly, so that its error does not grow with the
+ * position.
+ *   freq       [rotary_dim / 2] fp64 on the device: radians a position, of any
+ *              sign (one that is not finite makes its pairs NaN).  Frequencies
+ *              scaled for long contexts are the caller's to choose.
+ *   start      [B] int32 on the device, or NULL: 0
+ *   offsets    int32 on the device, row n of sequence b at b * offset_stride + n
+ *              (offset_stride 0: the same for all sequences), or NULL: n
+ *   q_weight, k_weight  [d] on the device, or NULL: no norm of that tensor; fp32
+ *              where weight_fp32, else of the tensors' dtype; 16-byte aligned
+ *   rotary_dim a multiple of 16 from 0 (norms only) to d
+ *   eps        above 0 and finite, where there are weights
+ * SparkAttention and the other pages take Q and K as given; these operators have
+ * no counterpart there.
+ */
+typedef enum { ATTN_ROPE_HALF = 0, ATTN_ROPE_INTERLEAVED = 1 } attn_rope_layout;
+
+typedef struct attn_rope {
+  const double* freq;
+  const int* start;
+  const int* offsets;
+  long long offset_stride;
+  const void* q_weight;
+  const void* k_weight;
+  int rotary_dim;
+  int layout; /* an attn_rope_layout value */
+  int weight_fp32;
+  float amplitude; /* finite */
+  float eps;
+} attn_rope;
+
+/*
+ * Q [B, H, N, d] and K [B, Hk, N, d] (16-bit views, attn_strides) with norm and
+ * rotation, into Qr and Kr of the same shapes.  Either tensor may be left out
+ * (0 heads; its pointers are then not read).  An output may be its input in
+ * place (the same pointer and strides), else it must not overlap any input.
+ * One launch; no workspace.
+ * Errors as attn_fwd_strided, plus ATTN_ERR_INVALID_ARG for a rope that breaks
+ * the rules above, more than 65535 heads of a tensor and 2^31 or more tokens.
+ */
+attn_status attn_rope_fwd(const void* Q, attn_strides q_strides, const void* K, attn_strides k_strides, void* Qr,
+                          attn_strides qr_strides, void* Kr, attn_strides kr_strides, int B, int H, int Hk, int N, int d,
+                          const attn_rope* rope, attn_dtype dtype, void* stream);
+
+/*
+ * Gradients of attn_rope_fwd.  dQr and dKr are those of its outputs; dQ, dK those
+ * of its inputs Q and K, which are read (and may else be NULL) where the tensor
+ * has weights.  dq_weight, dk_weight [d] in the weights' dtype get the weights'
+ * gradients, summed over all tokens and heads in fp32 in a fixed order: the same
+ * bits on every run.  dQ may be dQr in place, and dK dKr.
+ * workspace: attn_rope_bwd_workspace_size(d) bytes, 256-byte aligned, contents
+ * on entry irrelevant; needed where there are weights.  Errors as
+ * attn_rope_fwd, plus ATTN_ERR_WORKSPACE and ATTN_ERR_MISALIGNED.
+ */
+attn_status attn_rope_bwd(const void* dQr, attn_strides dqr_strides, const void* dKr, attn_strides dkr_strides,
+                          const void* Q, attn_strides q_strides, const void* K, attn_strides k_strides, void* dQ,
+                          attn_strides dq_strides, void* dK, attn_strides dk_strides, void* dq_weight, void* dk_weight,
+                          int B, int H, int Hk, int N, int d, const attn_rope* rope, attn_dtype dtype, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of attn_rope_bwd on the current device: a row of d sums for
+ * each of its blocks.  0 for a d other than 64 or 128, or where no device
+ * answers.  The pages have no counterpart. */
+size_t attn_rope_bwd_workspace_size(int d);
+
 /* Static description of a status code (a diagnostic of this library; the
  * pages have no counterpart).  Never NULL: unknown codes give
  * "unknown status". */

@@ -1,0 +1,109 @@
+"""Rotary positions: the tests' plain form against differences, the frequencies, and what the C entry points refuse (no GPU)."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import plain_rope
+from exact_head_attention_gb300 import build, exattn
+
+FAKE = 0x10000  # 16-byte aligned, never dereferenced: validation happens first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return exattn.load()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("norm", [False, True])
+def test_plain_gradients_against_differences(layout, norm):
+    g = torch.Generator().manual_seed(1)
+    x, dy = (torch.randn((2, 2, 3, 16), generator=g, dtype=torch.float64) for _ in range(2))
+    w = 1 + 0.3 * torch.randn(16, generator=g, dtype=torch.float64) if norm else None
+    freq, amplitude = exattn.rope_frequencies(8, device="cpu")[0], 1.3
+    pos = plain_rope.positions(2, 3, torch.tensor([5, 70]))
+    loss = lambda x, w: (plain_rope.norm_rotate(x, freq, pos, layout, amplitude, w)[0] * dy).sum()  # noqa: E731
+    dx, dw, _, _ = plain_rope.gradients(dy, x, freq, pos, layout, amplitude, w)
+    for i in (0, 17, 63, 100, 191):
+        h = torch.zeros(x.numel(), dtype=torch.float64)
+        h[i] = 1e-5
+        h = h.reshape(x.shape)
+        assert abs((loss(x + h, w) - loss(x - h, w)) / 2e-5 - dx.reshape(-1)[i]) < 1e-8
+    if norm:
+        for i in range(16):
+            h = torch.zeros(16, dtype=torch.float64)
+            h[i] = 1e-5
+            assert abs((loss(x, w + h) - loss(x, w - h)) / 2e-5 - dw[i]) < 1e-8
+
+
+def test_plain_angles():
+    freq = torch.tensor([1.0, 0.25, -3.5], dtype=torch.float64)
+    pos = torch.tensor([[0, 1, 1000]])
+    t = pos[..., None] * freq
+    got = plain_rope.angles(pos, freq)
+    assert torch.all((got.cos() - t.cos()).abs() < 1e-12) and torch.all((got.sin() - t.sin()).abs() < 1e-12)
+
+
+def test_frequencies():
+    freq, amplitude = exattn.rope_frequencies(64, 10000.0, device="cpu")
+    assert freq.dtype == torch.float64 and freq.shape == (32,) and amplitude == 1.0
+    assert freq[0] == 1.0 and abs(freq[16] - 0.01) < 1e-15
+    linear, _ = exattn.rope_frequencies(64, scaling="linear", factor=4.0, device="cpu")
+    assert torch.allclose(linear * 4, freq, rtol=1e-15, atol=0)
+    ntk, _ = exattn.rope_frequencies(64, scaling="ntk", factor=4.0, device="cpu")
+    assert ntk[0] == 1.0 and abs(ntk[-1] * 4 / freq[-1] - 1) < 1e-12
+    yarn, a = exattn.rope_frequencies(64, scaling="yarn", factor=16.0, trained=4096, device="cpu")
+    assert abs(a - (0.1 * math.log(16) + 1)) < 1e-15
+    turns = 4096 * freq / (2 * math.pi)
+    assert torch.equal(yarn[turns > 32], freq[turns > 32]) and torch.allclose(yarn[turns < 1] * 16, freq[turns < 1], rtol=1e-15, atol=0)
+    between = (turns >= 1) & (turns <= 32)
+    assert between.any() and torch.all(yarn[between] <= freq[between]) and torch.all(yarn[between] >= freq[between] / 16)
+    for args in [(0,), (-2,), (7,), (64, -1.0)]:
+        with pytest.raises(ValueError):
+            exattn.rope_frequencies(*args, device="cpu")
+    for kw in [dict(scaling="other"), dict(scaling="yarn"), dict(scaling="yarn", trained=10, fast=1.0), dict(factor=0.0)]:
+        with pytest.raises(ValueError):
+            exattn.rope_frequencies(64, device="cpu", **kw)
+
+
+def _calls(lib, q=FAKE, k=FAKE, out=FAKE, dw=FAKE, ws=FAKE, ws_bytes=1 << 40, B=2, H=4, Hk=2, N=3, d=64, dtype=0, row=64, null=False, freq=FAKE,
+           start=FAKE, offsets=FAKE, stride=3, qw=FAKE, kw=FAKE, rot=64, layout=0, amplitude=1.0, eps=1e-6):
+    """Status of the forward and the backward with the given arguments."""
+    st = exattn.Strides(8192, 2048, row)
+    rope = None if null else ctypes.byref(exattn.RopeStruct(freq, start, offsets, stride, qw, kw, rot, layout, 0, amplitude, eps))
+    vp = ctypes.c_void_p
+    fwd = lib.attn_rope_fwd(vp(q), st, vp(k), st, vp(out), st, vp(out), st, B, H, Hk, N, d, rope, dtype, None)
+    bwd = lib.attn_rope_bwd(vp(out), st, vp(out), st, vp(q), st, vp(k), st, vp(out), st, vp(out), st, vp(dw), vp(dw), B, H, Hk, N, d, rope,
+                            dtype, vp(ws), ws_bytes, None)
+    return {"fwd": fwd, "bwd": bwd}
+
+
+@pytest.mark.parametrize("kw,calls,code", [
+    (dict(B=0), "fwd bwd", 1), (dict(N=-1), "fwd bwd", 1), (dict(H=-1), "fwd bwd", 1), (dict(H=0, Hk=0), "fwd bwd", 1),
+    (dict(H=65536), "fwd bwd", 1), (dict(B=2 ** 20, N=2 ** 11), "fwd bwd", 1), (dict(d=96), "fwd bwd", 2), (dict(dtype=2), "fwd bwd", 1),
+    (dict(q=None), "fwd bwd", 1), (dict(k=None), "fwd bwd", 1), (dict(out=None), "fwd bwd", 1), (dict(dw=None), "bwd", 1),
+    (dict(ws=None), "bwd", 6), (dict(ws=FAKE + 128), "bwd", 3), (dict(q=FAKE + 8), "fwd bwd", 3), (dict(out=FAKE + 2), "fwd bwd", 3),
+    (dict(row=60), "fwd bwd", 1), (dict(row=68), "fwd bwd", 1), (dict(null=True), "fwd bwd", 1), (dict(freq=None), "fwd bwd", 1),
+    (dict(freq=FAKE + 4), "fwd bwd", 3), (dict(start=FAKE + 2), "fwd bwd", 3), (dict(offsets=FAKE + 1), "fwd bwd", 3),
+    (dict(stride=2), "fwd bwd", 1), (dict(stride=-3), "fwd bwd", 1), (dict(qw=FAKE + 8), "fwd bwd", 3), (dict(kw=FAKE + 4), "fwd bwd", 3),
+    (dict(rot=-16), "fwd bwd", 1), (dict(rot=24), "fwd bwd", 1), (dict(rot=80), "fwd bwd", 1), (dict(layout=2), "fwd bwd", 1),
+    (dict(amplitude=math.nan), "fwd bwd", 1), (dict(eps=0.0), "fwd bwd", 1), (dict(eps=-1.0), "fwd bwd", 1), (dict(eps=math.inf), "fwd bwd", 1),
+], ids=str)
+def test_rules(lib, kw, calls, code):
+    got = _calls(lib, **kw)
+    for name in calls.split():
+        assert got[name] == code, (name, got)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="valid calls with fake pointers must not reach a GPU")
+@pytest.mark.parametrize("kw", [{}, dict(rot=0, freq=None), dict(H=0, q=None), dict(Hk=0, k=None), dict(stride=0), dict(qw=None, kw=None, eps=0.0),
+                                dict(start=None, offsets=None)], ids=str)
+def test_valid_calls_reach_the_device(lib, kw):
+    assert set(_calls(lib, **kw).values()) <= {2, 4}  # no such device, or no driver
+
+
+def test_workspace_size_of_other_heads(lib):
+    assert exattn.rope_bwd_workspace_size(96) == 0
