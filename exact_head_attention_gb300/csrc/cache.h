@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include "kernels.h"
+#include "rope.h"
 
 namespace exattn {
 
@@ -35,6 +36,16 @@ struct CacheIoArgs {
   int sm_count;
   bool bf16;
   uint32_t* err_word;
+};
+
+// Writing with norm and rotation on the way.  rope: of the keys, and the queries (side[0], where it has heads) from and to
+// memory.  rope.r.start: where the positions begin, which may be io.start.
+struct CacheAppendArgs {
+  CacheIoArgs io;
+  RopeArgs rope;
+  const void* k_weight;
+  int blocks;  // of the keys, and of the values
+  int q_token_blocks;
 };
 
 // Attention over the cache.  The query rows of a key/value head are its group's heads and the Nq tokens
@@ -89,6 +100,7 @@ cudaError_t launch_dependent(void (*kernel)(const Args), dim3 grid, dim3 block, 
 }
 
 cudaError_t launch_cache_write(CacheIoArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_append(CacheAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_read(CacheIoArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_tile(const CacheAttnArgs& a, cudaStream_t stream);

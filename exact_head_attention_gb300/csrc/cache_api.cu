@@ -116,6 +116,43 @@ extern "C" attn_status attn_cache_write(const attn_cache* cache, const void* K, 
   return api_finish(launch_cache_write(a, s), s);
 }
 
+extern "C" attn_status attn_cache_append(const attn_cache* cache, const void* Q, attn_strides q_strides, void* Qr,
+                                         attn_strides qr_strides, const void* K, attn_strides k_strides, const void* V,
+                                         attn_strides v_strides, const int* start, const int* count, int B, int H, int N,
+                                         const attn_rope* rope, attn_dtype dtype, void* stream) {
+  CacheAppendArgs a;
+  std::memset(&a, 0, sizeof(a));
+  attn_status st = io_args(cache, K, k_strides, V, v_strides, start, count, B, N, dtype, &a.io);
+  if (st != ATTN_OK) return st;
+  if (H < 0 || H > 65535 || static_cast<long long>(B) * N > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  const bool normed = rope && ((H && rope->q_weight) || rope->k_weight);
+  if ((st = api_rope(rope, B, N, cache->d, normed, &a.rope.r)) != ATTN_OK) return st;
+  if (!a.rope.r.start) a.rope.r.start = start;
+  if (H > 0) {
+    RopeSide& q = a.rope.side[0];
+    if (!Q || !Qr || !api_strides(q_strides, B, H, cache->d, &q.sx) || !api_strides(qr_strides, B, H, cache->d, &q.sy))
+      return ATTN_ERR_INVALID_ARG;
+    if (!aligned(Q, 16) || !aligned(Qr, 16)) return ATTN_ERR_MISALIGNED;
+    q.x = Q;
+    q.y = Qr;
+    q.weight = rope->q_weight;
+    q.heads = H;
+  }
+  DeviceInfo dev;
+  if ((st = api_device(&dev)) != ATTN_OK) return st;
+  a.io.err_word = dev.err_word;
+  a.io.sm_count = a.rope.sm_count = dev.sm_count;
+  a.rope.B = B;
+  a.rope.N = N;
+  a.rope.d = cache->d;
+  a.rope.tokens = B * N;
+  a.rope.bf16 = a.io.bf16;
+  a.rope.weight_fp32 = rope->weight_fp32 != 0;
+  a.k_weight = rope->k_weight;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return api_finish(launch_cache_append(a, s), s);
+}
+
 extern "C" attn_status attn_cache_read(const attn_cache* cache, const int* start, const int* lens, void* K,
                                        attn_strides k_strides, void* V, attn_strides v_strides, int B, int N,
                                        attn_dtype dtype, void* stream) {

@@ -198,34 +198,10 @@ int token_shift(int tokens, int groups) {
   return s;
 }
 
-template <int D>
-long long chunk_blocks(int heads_q, int heads_k, int span, int shift) {
-  const int per = (kRopeThreads / RopeLane<D>::LANES) >> shift, chunks = (heads_q + span - 1) / span + (heads_k + span - 1) / span;
-  return (chunks + per - 1) / per;
-}
-
 template <int D, bool BF16>
 cudaError_t fwd_d(RopeArgs& a, cudaStream_t stream) {
-  const int hq = a.side[0].heads, hk = a.side[1].heads;
-  a.token_shift = token_shift(a.tokens, kRopeThreads / RopeLane<D>::LANES);
-  const long long token_blocks = (static_cast<long long>(a.tokens) + (1 << a.token_shift) - 1) >> a.token_shift;
-  // Heads a thread: what it does before the first takes about as long as four of them, and a last wave of few blocks as long
-  // as a full one.  12 heads of 128 each, 32768 tokens: 100 us with 2, 70.9 with 4, 62.7 with 6, 62.9 with 12; 28 and 4 heads
-  // of 64, 4611 tokens: 9.0, 7.3, 6.2 (the one with a single wave) and 9.6 us.
-  const long long slots = static_cast<long long>(kFwdBlocks) * a.sm_count;
-  long long best = 0;
-  const int most = hq > hk ? hq : hk;
-  for (int s : {1, 2, 3, 4, 6, 8, 12}) {
-    if (s > 1 && s > most) break;
-    const long long blocks = token_blocks * chunk_blocks<D>(hq, hk, s, a.token_shift), cost = ((blocks + slots - 1) / slots) * (4 + s);
-    if (best == 0 || cost < best) {
-      best = cost;
-      a.span = s;
-    }
-  }
-  a.q_chunks = (hq + a.span - 1) / a.span;
-  const dim3 grid(static_cast<unsigned>(token_blocks), static_cast<unsigned>(chunk_blocks<D>(hq, hk, a.span, a.token_shift)));
-  return launch_dependent(rope_kernel<D, BF16>, grid, dim3(kRopeThreads), 0, stream, a);
+  const RopeGrid g = rope_plan(a);
+  return launch_dependent(rope_kernel<D, BF16>, dim3(g.token_blocks, g.chunk_blocks), dim3(kRopeThreads), 0, stream, a);
 }
 
 template <int D, bool BF16>
@@ -273,6 +249,36 @@ cudaError_t bwd_d(RopeArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+RopeGrid rope_plan(RopeArgs& a) {
+  // Heads a thread: what it does before the first takes about as long as four of them, and a last wave of few blocks as long
+  // as a full one.  12 heads of 128 each, 32768 tokens: 100 us with 2, 70.9 with 4, 62.7 with 6, 62.9 with 12; 28 and 4 heads
+  // of 64, 4611 tokens: 9.0, 7.3, 6.2 (the one with a single wave) and 9.6 us.
+  const int hq = a.side[0].heads, hk = a.side[1].heads, most = hq > hk ? hq : hk, groups = kRopeThreads / (a.d / 16);
+  a.token_shift = token_shift(a.tokens, groups);
+  const int per = groups >> a.token_shift;  // chunks a block
+  const long long token_blocks = (static_cast<long long>(a.tokens) + (1 << a.token_shift) - 1) >> a.token_shift;
+  const long long slots = static_cast<long long>(kFwdBlocks) * a.sm_count;
+  long long best = 0, chunk_blocks = 0;
+  for (int s : {1, 2, 3, 4, 6, 8, 12}) {
+    if (s > 1 && s > most) break;
+    const long long chunks = (hq + s - 1) / s + (hk + s - 1) / s, cb = (chunks + per - 1) / per;
+    const long long cost = ((token_blocks * cb + slots - 1) / slots) * (4 + s);
+    if (best == 0 || cost < best) {
+      best = cost;
+      chunk_blocks = cb;
+      a.span = s;
+    }
+  }
+  a.q_chunks = (hq + a.span - 1) / a.span;
+  // a side without heads has rows that no load reads, but whose addresses are formed
+  for (int i = 0; i < 2; ++i)
+    if (a.side[i].heads == 0) {
+      a.side[i].x = a.side[1 - i].x;
+      a.side[i].weight = nullptr;
+    }
+  return {static_cast<unsigned>(token_blocks), static_cast<unsigned>(chunk_blocks)};
+}
 
 cudaError_t launch_rope(RopeArgs& a, cudaStream_t stream) {
   if (a.d == 128) return a.bf16 ? fwd_d<128, true>(a, stream) : fwd_d<128, false>(a, stream);

@@ -46,6 +46,12 @@ struct RopeArgs {
   int blocks[2];  // backward: blocks of the queries and of the keys
 };
 
+// Chooses how the forward is divided over blocks of 256 threads: token_shift, span and q_chunks, and the blocks of tokens and
+// of chunks.
+struct RopeGrid {
+  unsigned token_blocks, chunk_blocks;
+};
+RopeGrid rope_plan(RopeArgs& a);
 cudaError_t launch_rope(RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_rope_bwd(RopeArgs& a, cudaStream_t stream);
 size_t rope_bwd_workspace(int d, int sm_count);

@@ -140,6 +140,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.attn_rope_bwd.argtypes = [vp, st, vp, st, vp, st, vp, st, vp, st, vp, st, vp, vp, i, i, i, i, i, rp, i, vp,
                                           sz, vp]
             lib.attn_rope_bwd.restype = i
+            lib.attn_cache_append.argtypes = [cp, vp, st, vp, st, vp, st, vp, st, vp, vp, i, i, i, rp, i, vp]
+            lib.attn_cache_append.restype = i
             lib.attn_rope_bwd_workspace_size.argtypes = [i]
             lib.attn_rope_bwd_workspace_size.restype = sz
             lib.attn_status_string.argtypes = [i]
@@ -938,3 +940,46 @@ def rope(q, k, freq, start=None, offsets=None, layout="half", amplitude: float =
          eps: float = 1e-6):
     """Autograd-aware rope_forward: (q, k); gradients flow to q, k and the weights."""
     return _RopeFunction.apply(q, k, q_weight, k_weight, freq, start, offsets, layout, amplitude, eps)
+
+
+def cache_append(cache: QuantCache, k, v, freq, start=None, count=None, offsets=None, q=None, layout="half",
+                 amplitude: float = 1.0, q_weight=None, k_weight=None, eps: float = 1e-6, position_start=None, out=None,
+                 stream=None):
+    """cache_write with norm and rotary positions of the keys on the way (attn_cache_append); returns the rotated queries.
+
+    k, v, start, count as in cache_write; freq, offsets, layout, amplitude, weights and eps as in rope_forward, the position
+    of row n of sequence b being start[b] + offsets[b, n] (position_start, where given, in place of start).  q: [B, H, N, d]
+    of the same tokens, or None; all its rows are turned, into `out` (which may be q) where that is given."""
+    shape = k.shape
+    if v.shape != shape or len(shape) != 4 or shape[1] != cache.heads:
+        raise ValueError("k and v must be [B, heads, N, d] with the cache's heads")
+    kp, ks = _cache_view(k, cache, k.dtype)
+    vp, vs = _cache_view(v, cache, k.dtype)
+    B, _, N, d = shape
+    H, qp, qs = 0, None, _NO_STRIDES
+    if q is not None:
+        qp, qs = _cache_view(q, cache, k.dtype)
+        if q.shape[2] != N:
+            raise ValueError("q must be [B, H, N, d] of the new tokens")
+        H = q.shape[1]
+    elif q_weight is not None or out is not None:
+        raise ValueError("a weight or an output for queries that are not there")
+    code, start_at, count_at = _dtype_code(k), _int32(start, cache, "start"), _int32(count, cache, "count")
+    rope = _rope_struct(freq, B, N, d, k.dtype, cache.index, position_start, offsets, layout, amplitude, q_weight, k_weight, eps)
+
+    def call(handle):
+        if q is None:
+            to, tp, ts = None, None, _NO_STRIDES
+        elif out is None:
+            to = torch.empty_like(q)
+            tp, ts = _rope_view(to)
+        else:
+            to = out
+            tp, ts = _rope_like(to, q)
+        if B and N:
+            st = load().attn_cache_append(cache._ref, qp, qs, tp, ts, kp, ks, vp, vs, start_at, count_at, B, H, N, rope, code, handle)
+            if st != ATTN_OK:
+                raise AttnError(st, "attn_cache_append")
+        return to
+
+    return _run(cache, stream, call)

@@ -709,6 +709,23 @@ attn_status attn_rope_bwd(const void* dQr, attn_strides dqr_strides, const void*
  * answers.  The pages have no counterpart. */
 size_t attn_rope_bwd_workspace_size(int d);
 
+/*
+ * attn_cache_write with norm and rotary positions of the new keys on the way,
+ * and of the same tokens' queries: the rows of K become what attn_rope_fwd makes
+ * of them (with rope's k_weight), in fp32, and are quantised from there without a
+ * rounding between; V as in attn_cache_write; and Q [B, H, N, d], where H is above
+ * 0, goes to Qr as in attn_rope_fwd (all N rows of it, whatever count says; Qr
+ * may be Q in place).  Positions begin at rope->start where that is given, else
+ * at `start`; token n's is that plus offsets[b][n] (or n).  A key that norm and
+ * rotation bring beyond fp32 counts as an infinite one.
+ * One launch; no workspace.  Errors as attn_cache_write and attn_rope_fwd.  The
+ * pages have no counterpart.
+ */
+attn_status attn_cache_append(const attn_cache* cache, const void* Q, attn_strides q_strides, void* Qr,
+                              attn_strides qr_strides, const void* K, attn_strides k_strides, const void* V,
+                              attn_strides v_strides, const int* start, const int* count, int B, int H, int N,
+                              const attn_rope* rope, attn_dtype dtype, void* stream);
+
 /* Static description of a status code (a diagnostic of this library; the
  * pages have no counterpart).  Never NULL: unknown codes give
  * "unknown status". */

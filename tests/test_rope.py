@@ -107,3 +107,42 @@ def test_valid_calls_reach_the_device(lib, kw):
 
 def test_workspace_size_of_other_heads(lib):
     assert exattn.rope_bwd_workspace_size(96) == 0
+
+
+def _append(lib, cache, q=FAKE, out=FAKE, k=FAKE, v=FAKE, start=FAKE, count=None, B=2, H=4, N=3, dtype=0, row=64, null=False, **rope):
+    st, vp = exattn.Strides(8192, 2048, row), ctypes.c_void_p
+    f = dict(freq=FAKE, start=None, offsets=None, offset_stride=0, q_weight=FAKE, k_weight=FAKE, rotary_dim=64, layout=0, weight_fp32=0,
+             amplitude=1.0, eps=1e-6)
+    f.update(rope)
+    r = None if null else ctypes.byref(exattn.RopeStruct(**f))
+    return lib.attn_cache_append(None if cache is None else ctypes.byref(cache), vp(q), st, vp(out), st, vp(k), st, vp(v), st, vp(start),
+                                 vp(count), B, H, N, r, dtype, None)
+
+
+def _cache(**kw):
+    f = dict(k=FAKE, v=FAKE, k_scale=FAKE, v_scale=FAKE, page_table=FAKE, num_pages=10, heads=2, page_size=16, d=64, table_width=4, format=0)
+    f.update(kw)
+    return exattn.CacheStruct(**f)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=0), 1), (dict(N=0), 1), (dict(H=-1), 1), (dict(H=65536), 1), (dict(dtype=2), 1), (dict(q=None), 1), (dict(out=None), 1),
+    (dict(k=None), 1), (dict(v=None), 1), (dict(q=FAKE + 8), 3), (dict(out=FAKE + 4), 3), (dict(k=FAKE + 2), 3), (dict(start=FAKE + 2), 3),
+    (dict(count=FAKE + 1), 3), (dict(row=60), 1), (dict(null=True), 1), (dict(freq=None), 1), (dict(rotary_dim=40), 1),
+    (dict(rotary_dim=128), 1), (dict(layout=-1), 1), (dict(eps=0.0), 1), (dict(amplitude=math.inf), 1), (dict(k_weight=FAKE + 8), 3),
+    (dict(offsets=FAKE, offset_stride=1), 1), (dict(B=2 ** 30), 1),
+], ids=str)
+def test_append_rules(lib, kw, code):
+    assert _append(lib, _cache(), **kw) == code
+
+
+def test_append_rules_of_the_cache(lib):
+    assert _append(lib, None) == 1
+    assert _append(lib, _cache(page_size=24)) == 1 and _append(lib, _cache(d=96)) == 2 and _append(lib, _cache(k=FAKE + 1)) == 3
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="valid calls with fake pointers must not reach a GPU")
+@pytest.mark.parametrize("kw", [{}, dict(H=0, q=None, out=None), dict(rotary_dim=0, freq=None), dict(start=None), dict(k_weight=None, q_weight=None, eps=0.0)],
+                         ids=str)
+def test_valid_appends_reach_the_device(lib, kw):
+    assert _append(lib, _cache(), **kw) in (2, 4)
