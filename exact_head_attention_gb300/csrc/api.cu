@@ -513,6 +513,7 @@ extern "C" const char* attn_status_string(attn_status status) {
     case ATTN_ERR_WORKSPACE: return "workspace missing or too small";
     case ATTN_ERR_NOT_IMPLEMENTED: return "not implemented";
     case ATTN_ERR_PAGE: return "a cache page number or length out of range";
+    case ATTN_ERR_TREE: return "a drafted token's parent is not an earlier one";
   }
   return "unknown status";
 }
@@ -534,6 +535,10 @@ extern "C" attn_status attn_check_device_error(void* stream) {
       std::snprintf(g_last_error, sizeof(g_last_error),
                     "device error word 9: a cache call met a page number outside the pool, or a length outside its page table");
       return ATTN_ERR_PAGE;
+    }
+    if (code == kErrTree) {
+      std::snprintf(g_last_error, sizeof(g_last_error), "device error word 10: a drafted token's parent is not an earlier one");
+      return ATTN_ERR_TREE;
     }
     if (code == 8) {
       std::snprintf(g_last_error, sizeof(g_last_error), "device error word 8: dynamic shared memory not 1024-byte aligned");

@@ -15,6 +15,8 @@ namespace exattn {
 
 // Device error word, besides the kErr* of ptx.cuh: a page number outside the pool, or a length outside its page table.
 constexpr uint32_t kErrPage = 9;
+// A drafted token's parent that is not an earlier one.
+constexpr uint32_t kErrTree = 10;
 
 // The 8-bit key/value cache (attn_cache) as the kernels take it.
 struct CacheView {
@@ -66,6 +68,11 @@ struct CacheAttnArgs {
   bool bf16;
   float scale;
   uint64_t timeout_ns;
+  // A tree of the Nq tokens at a sequence's end (mask is then ATTN_MASK_CAUSAL_BOTTOM_RIGHT): bit j of row i of a sequence's
+  // [Nq][tree_words] says whether token i sees token j.
+  const uint32_t* tree;
+  long long tree_stride;  // words between sequences
+  int tree_words;
 };
 
 // Allows `kernel` its dynamic shared memory, once on each device (`done`: a bit for each of the first 64).
@@ -104,6 +111,18 @@ cudaError_t launch_cache_append(CacheAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_read(CacheIoArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_tile(const CacheAttnArgs& a, cudaStream_t stream);
+// The same with a tree.
+cudaError_t launch_cache_attn_tree(const CacheAttnArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_tile_tree(const CacheAttnArgs& a, cudaStream_t stream);
+// The mask's words and the depths of trees of N tokens from their parents.
+struct DraftTreeArgs {
+  const int* parents;  // [B][N]
+  uint32_t* mask;      // [B][N][ceil(N / 32)]
+  int* depth;          // [B][N]
+  int N;
+  uint32_t* err_word;
+};
+cudaError_t launch_draft_tree(const DraftTreeArgs& a, int B, cudaStream_t stream);
 // Up to this many query rows a key/value head attn_fwd_cache streams the codes through the warp-level products
 // (cache_attn.cu), above it through the tensor-memory ones (cache_tile.cu).  The first keep Q and O in registers: with
 // 32 rows those run out, with 24 the codes still set the pace.  Measured, warp-level against tensor-memory:

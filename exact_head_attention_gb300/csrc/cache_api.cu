@@ -176,10 +176,12 @@ extern "C" size_t attn_fwd_cache_workspace_size(const attn_cache* cache, int B, 
   return cache_attn_workspace(static_cast<long long>(H / cache->heads) * Nq, cache->d, sms);
 }
 
-extern "C" attn_status attn_fwd_cache(const void* Q, attn_strides q_strides, const attn_cache* cache, const int* lens,
-                                      void* O, attn_strides o_strides, float* LSE, int B, int H, int Nq, int causal,
-                                      float scale, attn_dtype dtype, void* workspace, size_t workspace_bytes,
-                                      void* stream) {
+namespace {
+
+// attn_fwd_cache, and with a tree attn_fwd_cache_tree.
+attn_status fwd_cache(const void* Q, attn_strides q_strides, const attn_cache* cache, const int* lens, void* O,
+                      attn_strides o_strides, float* LSE, int B, int H, int Nq, int causal, float scale, attn_dtype dtype,
+                      void* workspace, size_t workspace_bytes, void* stream, const uint32_t* tree, long long tree_stride) {
   CacheAttnArgs a;
   std::memset(&a, 0, sizeof(a));
   attn_status st = check_attn(cache, B, H, Nq, &a.c);
@@ -221,6 +223,41 @@ extern "C" attn_status attn_fwd_cache(const void* Q, attn_strides q_strides, con
   a.bf16 = dtype == ATTN_BF16;
   a.scale = scale;
   a.timeout_ns = api_wait_timeout_ns();
+  a.tree = tree;
+  a.tree_stride = tree_stride;
+  a.tree_words = (Nq + 31) / 32;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return api_finish(launch_cache_attn(a, s), s);
+  return api_finish(tree ? launch_cache_attn_tree(a, s) : launch_cache_attn(a, s), s);
+}
+
+}  // namespace
+
+extern "C" attn_status attn_fwd_cache(const void* Q, attn_strides q_strides, const attn_cache* cache, const int* lens,
+                                      void* O, attn_strides o_strides, float* LSE, int B, int H, int Nq, int causal,
+                                      float scale, attn_dtype dtype, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  return fwd_cache(Q, q_strides, cache, lens, O, o_strides, LSE, B, H, Nq, causal, scale, dtype, workspace, workspace_bytes,
+                   stream, nullptr, 0);
+}
+
+extern "C" attn_status attn_fwd_cache_tree(const void* Q, attn_strides q_strides, const attn_cache* cache, const int* lens,
+                                           const uint32_t* tree, long long tree_stride, void* O, attn_strides o_strides,
+                                           float* LSE, int B, int H, int Nq, float scale, attn_dtype dtype, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  if (!tree || Nq > ATTN_TREE_MAX_TOKENS) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(tree, 4)) return ATTN_ERR_MISALIGNED;
+  const long long words = (Nq + 31) / 32 * static_cast<long long>(Nq);
+  if (B > 1 && tree_stride != 0 && (tree_stride < words || tree_stride > (1ll << 39))) return ATTN_ERR_INVALID_ARG;
+  return fwd_cache(Q, q_strides, cache, lens, O, o_strides, LSE, B, H, Nq, ATTN_MASK_CAUSAL_BOTTOM_RIGHT, scale, dtype, workspace,
+                   workspace_bytes, stream, tree, B > 1 ? tree_stride : 0);
+}
+
+extern "C" attn_status attn_draft_tree(const int* parents, uint32_t* mask, int* depth, int B, int N, void* stream) {
+  if (!parents || !mask || !depth || B <= 0 || N <= 0 || N > ATTN_TREE_MAX_TOKENS) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(parents, 4) || !aligned(mask, 4) || !aligned(depth, 4)) return ATTN_ERR_MISALIGNED;
+  DeviceInfo dev;
+  const attn_status st = api_device(&dev);
+  if (st != ATTN_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return api_finish(launch_draft_tree(DraftTreeArgs{parents, mask, depth, N, dev.err_word}, B, s), s);
 }

@@ -66,6 +66,23 @@ __device__ __forceinline__ int cache_row_limit(int mask, int len, int Nq, int i)
   return max(0, len - Nq + i + 1);
 }
 
+// A tree's rows.  Token i of the Nq at a sequence's end sees what is before them, and of them those j <= i whose bit is set:
+// a part of what it sees under the bottom-right mask, which divides the work.
+constexpr int kTreeMost = ATTN_TREE_MAX_TOKENS;
+__device__ __forceinline__ const uint32_t* tree_row(const CacheAttnArgs& a, int b, int i) {
+  return a.tree + b * a.tree_stride + static_cast<long long>(i) * a.tree_words;
+}
+// The n lowest bits, n from below 0 to above 32.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n > 0 ? (1u << n) - 1u : 0u; }
+// The 32 tokens of the tree from s on (below 0: what is before it) that token i sees, `row` its words.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, int i, int s) {
+  if (s <= -32) return ~0u;
+  if (s > i) return 0u;
+  const int w = s >> 5;  // -1 to words - 1
+  const uint32_t lo = w < 0 ? ~0u : row[w], hi = w + 1 < words ? row[w + 1] : 0u;
+  return __funnelshift_r(lo, hi, s & 31) & low_bits(i - s + 1);
+}
+
 // R query rows an item, TK keys a tile.
 template <int R, int TK, int kMinTiles>
 struct CacheItems {

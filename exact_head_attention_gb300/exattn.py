@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libexattn.so")
 ATTN_OK = 0
 STATUS_NAMES = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ERR_MISALIGNED",
                 4: "ATTN_ERR_CUDA", 5: "ATTN_ERR_TIMEOUT", 6: "ATTN_ERR_WORKSPACE", 7: "ATTN_ERR_NOT_IMPLEMENTED",
-                8: "ATTN_ERR_PAGE"}
+                8: "ATTN_ERR_PAGE", 9: "ATTN_ERR_TREE"}
 ATTN_BF16, ATTN_FP16 = 0, 1
 # attn_mask: none, top-left causal (query q sees keys k <= q), bottom-right causal (k <= q + Nk - Nq)
 ATTN_MASK_NONE, ATTN_MASK_CAUSAL, ATTN_MASK_CAUSAL_BOTTOM_RIGHT = 0, 1, 2
@@ -134,6 +134,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.attn_fwd_cache.restype = i
             lib.attn_fwd_cache_workspace_size.argtypes = [cp, i, i, i]
             lib.attn_fwd_cache_workspace_size.restype = sz
+            lib.attn_fwd_cache_tree.argtypes = [vp, st, cp, vp, vp, ctypes.c_longlong, vp, st, vp, i, i, i, f, i, vp, sz, vp]
+            lib.attn_fwd_cache_tree.restype = i
+            lib.attn_draft_tree.argtypes = [vp, vp, vp, i, i, vp]
+            lib.attn_draft_tree.restype = i
             rp = ctypes.POINTER(RopeStruct)
             lib.attn_rope_fwd.argtypes = [vp, st, vp, st, vp, st, vp, st, i, i, i, i, i, rp, i, vp]
             lib.attn_rope_fwd.restype = i
@@ -698,9 +702,14 @@ def forward_cache(q, cache: QuantCache, lens, causal="bottom_right", scale: floa
     h // (H // heads)).  causal "bottom_right" (the default): the queries are a sequence's last Nq tokens; also
     False and True (top-left) as in forward().  lens: int32 CUDA tensor [B].  `workspace` (uint8 CUDA tensor of
     cache_workspace_size bytes, one for each call that may run at the same time) is allocated if omitted."""
+    return _forward_cache(q, cache, lens, mask_code(causal), scale, workspace, stream, None)
+
+
+def _forward_cache(q, cache: QuantCache, lens, mask: int, scale, workspace, stream, tree):
+    """forward_cache with an attn_mask value, or forward_cache_tree with `tree`: (address, words between sequences)."""
     qp, qs = _cache_view(q, cache, q.dtype)
     B, H, Nq, d = q.shape
-    code, mask, lens_at = _dtype_code(q), mask_code(causal), _int32(lens, cache, "lens")
+    code, lens_at = _dtype_code(q), _int32(lens, cache, "lens")
     scale = (1.0 / d ** 0.5) if scale is None else scale
 
     def call(handle):
@@ -715,13 +724,54 @@ def forward_cache(q, cache: QuantCache, lens, causal="bottom_right", scale: floa
             else:
                 at, size = _cache_workspace(workspace, cache)
             op, os_ = _cache_view(o, cache, q.dtype)
-            st = lib.attn_fwd_cache(qp, qs, cache._ref, lens_at, op, os_, lse.data_ptr(), B, H, Nq, mask, scale, code,
-                                    at, size, handle)
+            if tree is None:
+                st = lib.attn_fwd_cache(qp, qs, cache._ref, lens_at, op, os_, lse.data_ptr(), B, H, Nq, mask, scale, code,
+                                        at, size, handle)
+            else:
+                st = lib.attn_fwd_cache_tree(qp, qs, cache._ref, lens_at, *tree, op, os_, lse.data_ptr(), B, H, Nq, scale, code,
+                                             at, size, handle)
             if st != ATTN_OK:
-                raise AttnError(st, "attn_fwd_cache")
+                raise AttnError(st, "attn_fwd_cache" if tree is None else "attn_fwd_cache_tree")
         return o, lse
 
     return _run(cache, stream, call)
+
+
+def draft_tree(parents, stream=None):
+    """Masks and depths of trees of drafted tokens (attn_draft_tree): (mask [B, N, ceil(N / 32)], depth [B, N]), int32.
+
+    parents: int32 CUDA tensor [B, N] (or [N], one tree for all sequences: B is 1), -1 or the number of an earlier token.
+    The mask has each token's ancestors and itself as bits, for forward_cache_tree; the depth is its number of drafted
+    ancestors, the offsets of rope_forward and cache_append."""
+    shape = parents.shape
+    if parents.dtype != torch.int32 or not parents.is_cuda or len(shape) not in (1, 2) or not parents.is_contiguous():
+        raise ValueError("parents must be a contiguous int32 CUDA tensor [B, N] or [N]")
+    B, N = (1, shape[0]) if len(shape) == 1 else shape
+
+    def call(handle):
+        mask = torch.empty((B, N, (N + 31) // 32), dtype=torch.int32, device=parents.device)
+        depth = torch.empty((B, N), dtype=torch.int32, device=parents.device)
+        if B and N:
+            st = load().attn_draft_tree(parents.data_ptr(), mask.data_ptr(), depth.data_ptr(), B, N, handle)
+            if st != ATTN_OK:
+                raise AttnError(st, "attn_draft_tree")
+        return mask, depth
+
+    return _run_at(parents.get_device(), stream, call)
+
+
+def forward_cache_tree(q, cache: QuantCache, lens, tree, scale: float | None = None, workspace=None, stream=None):
+    """forward_cache for a tree of drafted tokens (attn_fwd_cache_tree): the queries are a sequence's last Nq tokens; each
+    sees what is before those, and of them what its bits in `tree` say.
+
+    tree: int32 CUDA tensor [B, Nq, ceil(Nq / 32)], or [1, ...] for all sequences alike (draft_tree): bit j % 32 of word
+    j // 32 of row i, for j <= i.  The other arguments as in forward_cache."""
+    shape = tree.shape
+    Nq = q.shape[2] if q.dim() == 4 else 0
+    if tree.dtype != torch.int32 or tree.get_device() != cache.index or not tree.is_contiguous() or len(shape) != 3 or (
+            shape[0] not in (1, cache.B) or shape[1] != Nq or shape[2] != (Nq + 31) // 32):
+        raise ValueError("tree must be a contiguous int32 tensor [B, Nq, ceil(Nq / 32)] or [1, ...] on the cache's device")
+    return _forward_cache(q, cache, lens, 2, scale, workspace, stream, (tree.data_ptr(), shape[1] * shape[2] if shape[0] > 1 else 0))
 
 
 # ------------------------------------------------------------------ rotary positions and norms per head

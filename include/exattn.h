@@ -63,8 +63,9 @@ typedef enum {
   ATTN_ERR_TIMEOUT = 5,         /* a bounded device wait expired (kernel exited early) */
   ATTN_ERR_WORKSPACE = 6,       /* workspace null or smaller than attn_bwd_workspace_size */
   ATTN_ERR_NOT_IMPLEMENTED = 7,
-  ATTN_ERR_PAGE = 8             /* device error word: a cache call met a page number outside the pool, or a
+  ATTN_ERR_PAGE = 8,            /* device error word: a cache call met a page number outside the pool, or a
                                    length outside its page table (see attn_cache) */
+  ATTN_ERR_TREE = 9             /* device error word: attn_draft_tree met a parent that is not an earlier token */
 } attn_status;
 
 typedef enum { ATTN_BF16 = 0, ATTN_FP16 = 1 } attn_dtype;
@@ -725,6 +726,41 @@ attn_status attn_cache_append(const attn_cache* cache, const void* Q, attn_strid
                               attn_strides qr_strides, const void* K, attn_strides k_strides, const void* V,
                               attn_strides v_strides, const int* start, const int* count, int B, int H, int N,
                               const attn_rope* rope, attn_dtype dtype, void* stream);
+
+/*
+ * Attention for trees of drafted tokens over the cache (speculative decoding).
+ * The Nq queries are the last Nq of a sequence's lens[b] cached tokens, which
+ * stand in any order that has each token behind its ancestors.  Query i sees
+ * every token before those Nq (the prefix), and of the drafted ones each j <= i
+ * whose bit is set in its row of `tree`: bit j % 32 of word j / 32 of
+ * tree + b * tree_stride + i * ceil(Nq / 32) (tree_stride 0: one tree for all
+ * sequences).  Bits of j > i are not looked at.  attn_draft_tree makes such masks
+ * from parents, with each token's own bit; any other mask may be given, and a
+ * query that sees nothing gets O = 0, LSE = -inf.  Sequences with fewer drafted
+ * tokens than Nq: pad behind them, with tokens that no other row sees.
+ * Everything else as attn_fwd_cache (lens, NaN, workspace of
+ * attn_fwd_cache_workspace_size, the same bits on every run), and a mask that
+ * lets every query see all j <= i gives the bits of
+ * ATTN_MASK_CAUSAL_BOTTOM_RIGHT there.  Nq is at most ATTN_TREE_MAX_TOKENS.
+ * Errors as there, plus ATTN_ERR_INVALID_ARG for a larger Nq and a tree_stride
+ * below a tree's words.  The pages have no counterpart.
+ */
+#define ATTN_TREE_MAX_TOKENS 512
+attn_status attn_fwd_cache_tree(const void* Q, attn_strides q_strides, const attn_cache* cache, const int* lens,
+                                const uint32_t* tree, long long tree_stride, void* O, attn_strides o_strides, float* LSE,
+                                int B, int H, int Nq, float scale, attn_dtype dtype, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * The masks and depths of B trees of N drafted tokens: parents [B][N] on the
+ * device, -1 or the number of an earlier token.  mask [B][N][ceil(N / 32)]: each
+ * token's ancestors and itself, as attn_fwd_cache_tree takes them; depth [B][N]:
+ * the number of its drafted ancestors, so that start + depth is its position (the
+ * offsets of attn_rope).  One for all layers of a step.  A parent that is no
+ * earlier token counts as -1 (ATTN_ERR_TREE in the error word).  N is at most
+ * ATTN_TREE_MAX_TOKENS.  One launch; no workspace.  The pages have no counterpart.
+ */
+attn_status attn_draft_tree(const int* parents, uint32_t* mask, int* depth, int B, int N, void* stream);
 
 /* Static description of a status code (a diagnostic of this library; the
  * pages have no counterpart).  Never NULL: unknown codes give

@@ -146,3 +146,30 @@ def test_append_rules_of_the_cache(lib):
                          ids=str)
 def test_valid_appends_reach_the_device(lib, kw):
     assert _append(lib, _cache(), **kw) in (2, 4)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(tree=None), 1), (dict(Nq=513), 1), (dict(Nq=0), 1), (dict(tree=FAKE + 2), 3), (dict(stride=39), 1), (dict(stride=-40), 1),
+    (dict(scale=0.0), 1), (dict(ws=None), 6), (dict(ws=FAKE + 128), 3), (dict(lens=None), 1), (dict(H=3), 1), (dict(q=None), 1),
+    (dict(dtype=5), 1),
+], ids=str)
+def test_tree_rules(lib, kw, code):
+    f = dict(q=FAKE, tree=FAKE, stride=40, lens=FAKE, H=4, Nq=40, scale=0.1, dtype=0, ws=FAKE)
+    f.update(kw)
+    st, vp = exattn.Strides(8192, 4096, 64), ctypes.c_void_p
+    if "stride" not in kw:
+        f["stride"] = 80
+    got = lib.attn_fwd_cache_tree(vp(f["q"]), st, ctypes.byref(_cache()), vp(f["lens"]), vp(f["tree"]), f["stride"], vp(FAKE), st, vp(FAKE), 2,
+                                  f["H"], f["Nq"], f["scale"], f["dtype"], vp(f["ws"]), 1 << 40, None)
+    assert got == code
+
+
+@pytest.mark.parametrize("args,code", [((None, FAKE, FAKE, 1, 4), 1), ((FAKE, None, FAKE, 1, 4), 1), ((FAKE, FAKE, None, 1, 4), 1), ((FAKE, FAKE, FAKE, 0, 4), 1),
+                                       ((FAKE, FAKE, FAKE, 1, 0), 1), ((FAKE, FAKE, FAKE, 1, 513), 1), ((FAKE + 2, FAKE, FAKE, 1, 4), 3),
+                                       ((FAKE, FAKE + 1, FAKE, 1, 4), 3), ((FAKE, FAKE, FAKE + 2, 1, 4), 3)], ids=str)
+def test_draft_tree_rules(lib, args, code):
+    assert lib.attn_draft_tree(*map(ctypes.c_void_p, args[:3]), *args[3:], None) == code
+
+
+def test_tree_status(lib):
+    assert exattn.STATUS_NAMES[9] == "ATTN_ERR_TREE" and "parent" in exattn.status_string(9)
