@@ -46,8 +46,11 @@ struct CacheAppendArgs {
   CacheIoArgs io;
   RopeArgs rope;
   const void* k_weight;
-  int blocks;  // of the keys, and of the values
+  int blocks;       // of the keys, and of the values: page_blocks for each chunk of `span` heads
+  int page_blocks;
+  int span, head_shift;  // log2 of the heads side by side in a block
   int q_token_blocks;
+  int slots_at;  // where the rows under way lie in shared memory
 };
 
 // Attention over the cache.  The query rows of a key/value head are its group's heads and the Nq tokens
