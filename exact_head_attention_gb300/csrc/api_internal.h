@@ -30,6 +30,8 @@ attn_status api_driver_fail(const char* what, int code);
 bool api_strides(const attn_strides& in, int B, int H, int d, RowStrides* out);
 // attn_rope rules, and its view for the kernels; `normed`: there are weights of a norm.
 attn_status api_rope(const attn_rope* rope, int B, int N, int d, bool normed, RopeView* out);
+// A number that no earlier call and no old contents of a workspace are likely to hold, its low 16 bits zero.
+unsigned long long api_next_tag();
 // 2-D byte map {128, lines} over contiguous 128-byte lines, box {128, box_lines}, 128-byte swizzle.
 CUresult api_encode_lines(CUtensorMap* map, const void* base, uint64_t lines, uint32_t box_lines);
 

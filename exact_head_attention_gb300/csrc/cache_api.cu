@@ -1,8 +1,6 @@
 // C-ABI entry points of the 8-bit key/value cache: argument checks, tensor maps and dispatch.
-#include <atomic>
 #include <cmath>
 #include <cstring>
-#include <random>
 
 #include "api_internal.h"
 #include "cache.h"
@@ -12,21 +10,6 @@ using namespace exattn;
 namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-// A number that no earlier call and no old contents of a workspace are likely to hold: a counter from a random
-// start, through the finaliser of the splitmix64 generator (Steele, Lea and Flood, 2014).
-unsigned long long next_tag() {
-  static std::atomic<unsigned long long> count{[] {
-    std::random_device r;
-    return (static_cast<unsigned long long>(r()) << 32) ^ r();
-  }()};
-  unsigned long long z = count.fetch_add(0x9e3779b97f4a7c15ull, std::memory_order_relaxed);
-  z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
-  z = (z ^ (z >> 27)) * 0x94d049bb133111ebull;
-  z ^= z >> 31;
-  z &= ~0xffffull;                  // the count's place
-  return z ? z : 0x10000ull;  // zero is a count at rest
-}
 
 // The rules of attn_cache, and its view for the kernels.
 attn_status check_cache(const attn_cache* c, CacheView* out) {
@@ -213,7 +196,7 @@ attn_status fwd_cache(const void* Q, attn_strides q_strides, const attn_cache* c
   a.lens = lens;
   a.lse = LSE;
   a.ws = static_cast<uint8_t*>(workspace);
-  a.tag = next_tag();
+  a.tag = api_next_tag();
   a.err_word = dev.err_word;
   a.B = B;
   a.Nq = Nq;

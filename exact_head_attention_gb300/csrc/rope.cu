@@ -31,6 +31,28 @@ __global__ void __launch_bounds__(kRopeThreads, kFwdBlocks) rope_kernel(const __
 
 constexpr int kBwdBlocks = 2;  // resident an SM
 
+// A count of the blocks that are done.  It needs no preparation: every block first makes it the call's tag where its upper 48
+// bits are another (cache_sched.cuh), which costs nothing beside the block's first loads, and the last to be counted puts it
+// to rest.
+__device__ __forceinline__ void count_open(unsigned long long* at, unsigned long long tag) {
+  unsigned long long seen, old;
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(seen) : "l"(at) : "memory");
+  while ((seen & ~0xffffull) != tag) {
+    asm volatile("atom.relaxed.gpu.global.cas.b64 %0, [%1], %2, %3;" : "=l"(old) : "l"(at), "l"(seen), "l"(tag) : "memory");
+    if (old == seen) break;
+    seen = old;
+  }
+}
+// Adds one, by a thread whose block has met; true for the last of `n`: what the others' blocks wrote is then visible to it, and
+// to its block after a barrier.
+__device__ __forceinline__ bool count_close(unsigned long long* at, unsigned n) {
+  unsigned long long old;
+  asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;" : "=l"(old) : "l"(at), "l"(1ull) : "memory");
+  const bool all = (old & 0xffffull) + 1ull == n;
+  if (all) asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(at), "l"(0ull) : "memory");
+  return all;
+}
+
 // One thread takes `span` heads of a token after another (an item), the block's threads different tokens or chunks of heads.
 // Its loads are a row ahead, by way of places of its own in shared memory, so that they stay under way while it computes
 // (held in registers, two rows at a time, the whole took 111 us for 96; two and more rows ahead 97 to 111).
@@ -107,6 +129,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdBlocks) rope_bwd_kernel(cons
     }
   };
   issue();
+  if (threadIdx.x == 0 && a.tag != 0) count_open(a.count + is_k, a.tag);
 
   table.fill(a.r, threadIdx.x, kRopeThreads);
   __syncthreads();
@@ -160,15 +183,52 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdBlocks) rope_bwd_kernel(cons
     for (int e = 0; e < 16; ++e) sums[threadIdx.x >> 5][8 * (e < 8 ? l.ua : l.ub) + (e & 7)] = dw[e];
   }
   __syncthreads();
+  float* const mine = a.sums + static_cast<size_t>(blockIdx.x) * D;
   for (int col = threadIdx.x; col < D; col += kRopeThreads) {
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < kRopeThreads / 32; ++i) v += sums[i][col];
-    a.ws[static_cast<size_t>(blockIdx.x) * D + col] = v;
+    mine[col] = v;
+  }
+  if (a.tag == 0) return;  // rope_dw_kernel adds them up
+  // The side's last block to come here does.
+  __shared__ bool last;
+  __syncthreads();
+  if (threadIdx.x == 0) last = count_close(a.count + is_k, blocks);
+  __syncthreads();
+  if (!last) return;
+  constexpr int COLS = D / 4, PARTS = kRopeThreads / COLS;  // four columns a thread, every PARTS-th block
+  const float4* parts = reinterpret_cast<const float4*>(a.sums + (is_k ? static_cast<size_t>(a.blocks[0]) * D : 0));
+  const int col = threadIdx.x % COLS, part = threadIdx.x / COLS;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (unsigned i = part; i < blocks; i += PARTS) {
+    const float4 x = __ldcg(parts + static_cast<size_t>(i) * COLS + col);
+    v.x += x.x;
+    v.y += x.y;
+    v.z += x.z;
+    v.w += x.w;
+  }
+  float4* const joint = reinterpret_cast<float4*>(slots);  // every copy into them has landed
+  joint[part * COLS + col] = v;
+  __syncthreads();
+  if (threadIdx.x < COLS) {
+#pragma unroll
+    for (int i = 1; i < PARTS; ++i) {
+      const float4 x = joint[i * COLS + col];
+      v.x += x.x;
+      v.y += x.y;
+      v.z += x.z;
+      v.w += x.w;
+    }
+    if (a.weight_fp32)
+      reinterpret_cast<float4*>(sd.dweight)[col] = v;
+    else
+      reinterpret_cast<uint2*>(sd.dweight)[col] = make_uint2(pack2<BF16>(v.x, v.y), pack2<BF16>(v.z, v.w));
   }
 }
 
-// dw from the blocks' sums: 32 columns a block, each over 32 threads.
+// dw from the blocks' sums where those are many: 32 columns a block, each over 32 threads.
 template <bool BF16>
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float sums[32][33];
@@ -178,7 +238,7 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const __grid_constant__ R
   const int first = blockIdx.y ? a.blocks[0] : 0, blocks = a.blocks[blockIdx.y];
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float v = 0.f;
-  for (int i = part; i < blocks; i += 32) v += a.ws[static_cast<size_t>(first + i) * a.d + col];
+  for (int i = part; i < blocks; i += 32) v += a.sums[static_cast<size_t>(first + i) * a.d + col];
   sums[part][lane] = v;
   __syncthreads();
   v = sums[lane][part];
@@ -202,13 +262,6 @@ template <int D, bool BF16>
 cudaError_t fwd_d(RopeArgs& a, cudaStream_t stream) {
   const RopeGrid g = rope_plan(a);
   return launch_dependent(rope_kernel<D, BF16>, dim3(g.token_blocks, g.chunk_blocks), dim3(kRopeThreads), 0, stream, a);
-}
-
-template <int D, bool BF16>
-cudaError_t bwd_t(RopeArgs& a, cudaStream_t stream) {
-  const cudaError_t e = launch_dependent(rope_bwd_kernel<D, BF16>, dim3(a.blocks[0] + a.blocks[1]), dim3(kRopeThreads), 0, stream, a);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(rope_dw_kernel<BF16>, dim3(D / 32, 2), dim3(1024), 0, stream, a);
 }
 
 template <int D, bool BF16>
@@ -245,7 +298,13 @@ cudaError_t bwd_d(RopeArgs& a, cudaStream_t stream) {
     if (share < 1) share = 1;
     a.blocks[i] = static_cast<int>(items < share ? items : share);
   }
-  return bwd_t<D, BF16>(a, stream);
+  // Few blocks' sums are added up by the last one, many by a launch of their own, more of whose loads are under way: 110 blocks
+  // 6.8 us and 29 for the host's part, 5.9 and 32 with a second launch; 304 blocks 98.8 us, 96.6 with a second launch.
+  const int blocks = a.blocks[0] + a.blocks[1];
+  if (blocks > a.sm_count) a.tag = 0;
+  const cudaError_t e = launch_dependent(rope_bwd_kernel<D, BF16>, dim3(blocks), dim3(kRopeThreads), 0, stream, a);
+  if (e != cudaSuccess || a.tag != 0) return e;
+  return launch_dependent(rope_dw_kernel<BF16>, dim3(D / 32, 2), dim3(1024), 0, stream, a);
 }
 
 }  // namespace
@@ -285,8 +344,8 @@ cudaError_t launch_rope(RopeArgs& a, cudaStream_t stream) {
   return a.bf16 ? fwd_d<64, true>(a, stream) : fwd_d<64, false>(a, stream);
 }
 
-// A row of sums for each block: no more than two an SM, and one more for either side.
-size_t rope_bwd_workspace(int d, int sm_count) { return static_cast<size_t>(kBwdBlocks * sm_count + 2) * d * sizeof(float); }
+// Two counts, and a row of sums for each block: no more than two an SM, and one more for either side.
+size_t rope_bwd_workspace(int d, int sm_count) { return kRopeSumsAt + static_cast<size_t>(kBwdBlocks * sm_count + 2) * d * sizeof(float); }
 
 cudaError_t launch_rope_bwd(RopeArgs& a, cudaStream_t stream) {
   // A side without weights needs no more than the rotation turned back.

@@ -42,8 +42,11 @@ struct RopeArgs {
   int q_chunks;     // forward: chunks of `span` heads of the queries
   bool bf16, weight_fp32;
   int sm_count;
-  float* ws;      // backward: a row of d sums for each block
-  int blocks[2];  // backward: blocks of the queries and of the keys
+  // backward
+  unsigned long long* count;  // blocks that are done, of the queries and of the keys
+  unsigned long long tag;     // of this call's counts, the low 16 bits zero; 0: there are none
+  float* sums;                // a row of d for each block
+  int blocks[2];              // of the queries and of the keys
 };
 
 // Chooses how the forward is divided over blocks of 256 threads: token_shift, span and q_chunks, and the blocks of tokens and
@@ -54,6 +57,7 @@ struct RopeGrid {
 RopeGrid rope_plan(RopeArgs& a);
 cudaError_t launch_rope(RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_rope_bwd(RopeArgs& a, cudaStream_t stream);
+constexpr size_t kRopeSumsAt = 256;  // of the workspace, behind the counts
 size_t rope_bwd_workspace(int d, int sm_count);
 
 }  // namespace exattn

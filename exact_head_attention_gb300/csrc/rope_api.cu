@@ -1,6 +1,8 @@
 // C-ABI entry points of the rotary positions: argument checks and dispatch.
+#include <atomic>
 #include <cmath>
 #include <cstring>
+#include <random>
 
 #include "api_internal.h"
 #include "rope.h"
@@ -27,6 +29,20 @@ attn_status check_tensor(const void* p, const attn_strides& st, int B, int heads
 }
 
 }  // namespace
+
+// A counter from a random start, through the finaliser of the splitmix64 generator (Steele, Lea and Flood, 2014).
+unsigned long long exattn::api_next_tag() {
+  static std::atomic<unsigned long long> count{[] {
+    std::random_device r;
+    return (static_cast<unsigned long long>(r()) << 32) ^ r();
+  }()};
+  unsigned long long z = count.fetch_add(0x9e3779b97f4a7c15ull, std::memory_order_relaxed);
+  z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
+  z = (z ^ (z >> 27)) * 0x94d049bb133111ebull;
+  z ^= z >> 31;
+  z &= ~0xffffull;                  // the count's place
+  return z ? z : 0x10000ull;  // zero is a count at rest
+}
 
 attn_status exattn::api_rope(const attn_rope* rope, int B, int N, int d, bool normed, RopeView* out) {
   if (!rope) return ATTN_ERR_INVALID_ARG;
@@ -122,7 +138,7 @@ extern "C" attn_status attn_rope_bwd(const void* dQr, attn_strides dqr_strides, 
     if (w[i] == nullptr) continue;
     if ((st = check_tensor(in[i], *sin[i], B, heads[i], d, &sd.sin)) != ATTN_OK) return st;
     if (!dw[i]) return ATTN_ERR_INVALID_ARG;
-    if (!aligned(dw[i], 4)) return ATTN_ERR_MISALIGNED;
+    if (!aligned(dw[i], 16)) return ATTN_ERR_MISALIGNED;
     sd.in = in[i];
     sd.weight = w[i];
     sd.dweight = dw[i];
@@ -139,7 +155,11 @@ extern "C" attn_status attn_rope_bwd(const void* dQr, attn_strides dqr_strides, 
   a.bf16 = dtype == ATTN_BF16;
   a.weight_fp32 = rope->weight_fp32 != 0;
   a.sm_count = dev.sm_count;
-  a.ws = static_cast<float*>(workspace);
+  if (normed) {
+    a.count = static_cast<unsigned long long*>(workspace);
+    a.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRopeSumsAt);
+    a.tag = api_next_tag();
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return api_finish(launch_rope_bwd(a, s), s);
 }

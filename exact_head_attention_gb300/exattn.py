@@ -777,6 +777,7 @@ def forward_cache_tree(q, cache: QuantCache, lens, tree, scale: float | None = N
 # ------------------------------------------------------------------ rotary positions and norms per head
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_DTYPE_CODES = {torch.bfloat16: ATTN_BF16, torch.float16: ATTN_FP16}
 _NO_STRIDES = Strides(0, 0, 0)  # of a tensor that is left out
 
 
@@ -820,48 +821,60 @@ def _rope_struct(freq, B: int, N: int, d: int, dtype, index: int, start, offsets
     if code is None:
         raise ValueError(f"unknown rotary layout {layout!r}")
     at_freq = at_start = at_offsets = at_q = at_k = None
-    rot, stride, wide = 0, 0, 0
+    rot = stride = wide = 0
     if freq is not None:
-        if freq.dtype != torch.float64 or freq.dim() != 1 or not freq.is_contiguous() or freq.get_device() != index:
+        if freq.dtype is not torch.float64 or freq.dim() != 1 or not freq.is_contiguous() or freq.get_device() != index:
             raise ValueError("freq must be a contiguous float64 tensor [rotary_dim / 2] on the tensors' device")
-        rot, at_freq = 2 * freq.shape[0], freq.data_ptr()
+        rot, at_freq = 2 * freq.numel(), freq.data_ptr()
     if start is not None:
-        if start.dtype != torch.int32 or start.shape != (B,) or start.get_device() != index or not start.is_contiguous():
+        if start.dtype is not torch.int32 or start.shape != (B,) or start.get_device() != index or not start.is_contiguous():
             raise ValueError("start must be a contiguous int32 tensor of one entry a sequence on the tensors' device")
         at_start = start.data_ptr()
     if offsets is not None:
         shape = offsets.shape
-        if offsets.dtype != torch.int32 or offsets.get_device() != index or shape not in ((B, N), (1, N), (N,)) or (
+        if offsets.dtype is not torch.int32 or offsets.get_device() != index or shape not in ((B, N), (1, N), (N,)) or (
                 N > 1 and offsets.stride(-1) != 1):
             raise ValueError("offsets must be an int32 tensor [B, N], [1, N] or [N], last dimension contiguous, on the tensors' device")
         stride = offsets.stride(0) if len(shape) == 2 and shape[0] > 1 else 0
         at_offsets = offsets.data_ptr()
-    for w in (q_weight, k_weight):
-        if w is None:
-            continue
-        if w.shape != (d,) or w.dtype not in (dtype, torch.float32) or w.get_device() != index or not w.is_contiguous():
-            raise ValueError("weights must be contiguous [d], float32 or of the tensors' dtype, on their device")
     if q_weight is not None:
-        at_q, wide = q_weight.data_ptr(), int(q_weight.dtype == torch.float32)
+        at_q, wide = _rope_weight(q_weight, d, dtype, index)
     if k_weight is not None:
-        if q_weight is not None and q_weight.dtype != k_weight.dtype:
+        at_k, k_wide = _rope_weight(k_weight, d, dtype, index)
+        if at_q is not None and wide != k_wide:
             raise TypeError("both weights must be of one dtype")
-        at_k, wide = k_weight.data_ptr(), int(k_weight.dtype == torch.float32)
+        wide = k_wide
     return RopeStruct(at_freq, at_start, at_offsets, stride, at_q, at_k, rot, code, wide, amplitude, eps)
 
 
+def _rope_weight(w, d: int, dtype, index: int):
+    """(address, whether it is fp32) of a norm's weights."""
+    wide = w.dtype is torch.float32
+    if not (wide or w.dtype is dtype) or w.shape != (d,) or w.get_device() != index or not w.is_contiguous():
+        raise ValueError("weights must be contiguous [d], float32 or of the tensors' dtype, on their device")
+    return w.data_ptr(), wide
+
+
 def _rope_pair(q, k, names=("q", "k")):
-    """(the first that is there, heads of q, heads of k) of two [B, H, N, d] tensors, one of which may be None."""
+    """(shape, dtype, device index, heads of q, heads of k) of two [B, H, N, d] tensors, one of which may be None."""
     x = k if q is None else q
     if x is None:
         raise ValueError(f"{names[0]} or {names[1]} is needed")
-    if x.dim() != 4 or (k is not None and q is not None and (k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[2:] != q.shape[2:])):
-        raise ValueError(f"{names[0]} and {names[1]} must be [B, H, N, d] with the same B, N and d")
-    if q is not None and k is not None and (q.dtype != k.dtype or q.get_device() != k.get_device()):
-        raise ValueError(f"{names[0]} and {names[1]} must be of one dtype, on one device")
-    if not x.is_cuda:
+    shape, index = x.shape, x.get_device()
+    if index < 0:
         raise ValueError("tensors must be CUDA tensors")
-    return x, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+    if len(shape) != 4:
+        raise ValueError(f"{names[0]} and {names[1]} must be [B, H, N, d]")
+    if q is None:
+        return shape, x.dtype, index, 0, shape[1]
+    if k is None:
+        return shape, x.dtype, index, shape[1], 0
+    other = k.shape
+    if len(other) != 4 or other[0] != shape[0] or other[2] != shape[2] or other[3] != shape[3]:
+        raise ValueError(f"{names[0]} and {names[1]} must be [B, H, N, d] with the same B, N and d")
+    if k.dtype is not x.dtype or k.get_device() != index:
+        raise ValueError(f"{names[0]} and {names[1]} must be of one dtype, on one device")
+    return shape, x.dtype, index, shape[1], other[1]
 
 
 def _rope_view(t):
@@ -871,7 +884,7 @@ def _rope_view(t):
 
 def _rope_like(t, like):
     """_rope_view of a caller's tensor that must be as another is."""
-    if t is not None and (like is None or t.shape != like.shape or t.dtype != like.dtype or t.get_device() != like.get_device()):
+    if t is not None and (like is None or t.shape != like.shape or t.dtype is not like.dtype or t.get_device() != like.get_device()):
         raise ValueError("tensors must match in shape, dtype and device")
     return _rope_view(t)
 
@@ -885,10 +898,11 @@ def rope_forward(q, k, freq, start=None, offsets=None, layout="half", amplitude:
     pairs (i, i + rotary_dim / 2), or "interleaved": (2 i, 2 i + 1).  amplitude multiplies what turns.  q_weight, k_weight:
     the norms' [d] weights (fp32 or as the tensors), None: no norm.  q or k may be None.  out: a pair to write to, which may
     be (q, k) itself."""
-    x, H, Hk = _rope_pair(q, k)
-    B, _, N, d = x.shape
-    code, index = _dtype_code(x), x.get_device()
-    rope = _rope_struct(freq, B, N, d, x.dtype, index, start, offsets, layout, amplitude, q_weight, k_weight, eps)
+    (B, _, N, d), dtype, index, H, Hk = _rope_pair(q, k)
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}; expected bfloat16 or float16")
+    rope = _rope_struct(freq, B, N, d, dtype, index, start, offsets, layout, amplitude, q_weight, k_weight, eps)
     views = (*_rope_view(q), *_rope_view(k))
 
     def call(handle):
@@ -921,10 +935,11 @@ def rope_backward(dq, dk, q, k, freq, start=None, offsets=None, layout="half", a
     q and k are its inputs (not read, and may be None, where that tensor has no weights); the other arguments as there.
     The weights' gradients are summed in a fixed order; None where there are no weights.  `workspace` (uint8 CUDA tensor of
     rope_bwd_workspace_size bytes, one for each call that may run at the same time) is allocated if omitted."""
-    x, H, Hk = _rope_pair(dq, dk, ("dq", "dk"))
-    B, _, N, d = x.shape
-    code, index = _dtype_code(x), x.get_device()
-    rope = _rope_struct(freq, B, N, d, x.dtype, index, start, offsets, layout, amplitude, q_weight, k_weight, eps)
+    (B, _, N, d), dtype, index, H, Hk = _rope_pair(dq, dk, ("dq", "dk"))
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}; expected bfloat16 or float16")
+    rope = _rope_struct(freq, B, N, d, dtype, index, start, offsets, layout, amplitude, q_weight, k_weight, eps)
     wq, wk = q_weight if H else None, k_weight if Hk else None
     if (wq is not None and q is None) or (wk is not None and k is None):
         raise ValueError("the gradients of a norm need its input")
@@ -942,8 +957,10 @@ def rope_backward(dq, dk, q, k, freq, start=None, offsets=None, layout="half", a
         space, size = None, 0
         if wq is not None or wk is not None:
             size = lib.attn_rope_bwd_workspace_size(d)
-            space = torch.empty(size, dtype=torch.uint8, device=x.device) if workspace is None else workspace
-            size = space.numel() * space.element_size()
+            if workspace is None:
+                space = torch.empty(size, dtype=torch.uint8, device=(dq if dk is None else dk).device)
+            else:
+                space, size = workspace, workspace.numel() * workspace.element_size()
         st = lib.attn_rope_bwd(*views, *_rope_view(oq), *_rope_view(ok), None if dwq is None else dwq.data_ptr(),
                                None if dwk is None else dwk.data_ptr(), B, H, Hk, N, d, rope, code,
                                None if space is None else space.data_ptr(), size, handle)

@@ -692,11 +692,13 @@ attn_status attn_rope_fwd(const void* Q, attn_strides q_strides, const void* K, 
 /*
  * Gradients of attn_rope_fwd.  dQr and dKr are those of its outputs; dQ, dK those
  * of its inputs Q and K, which are read (and may else be NULL) where the tensor
- * has weights.  dq_weight, dk_weight [d] in the weights' dtype get the weights'
+ * has weights.  dq_weight, dk_weight [d] in the weights' dtype (16-byte aligned) get the weights'
  * gradients, summed over all tokens and heads in fp32 in a fixed order: the same
- * bits on every run.  dQ may be dQr in place, and dK dKr.
+ * bits on every run.  dQ may be dQr in place, and dK dKr.  One to three
+ * launches.
  * workspace: attn_rope_bwd_workspace_size(d) bytes, 256-byte aligned, contents
- * on entry irrelevant; needed where there are weights.  Errors as
+ * on entry irrelevant, one for each call that may run at the same time; needed
+ * where there are weights.  Errors as
  * attn_rope_fwd, plus ATTN_ERR_WORKSPACE and ATTN_ERR_MISALIGNED.
  */
 attn_status attn_rope_bwd(const void* dQr, attn_strides dqr_strides, const void* dKr, attn_strides dkr_strides,

@@ -335,3 +335,42 @@ def test_refused_tensors():
         exattn.rope_backward(q, q, None, q, freq, q_weight=w)
     with pytest.raises(exattn.AttnError):
         exattn.rope_backward(q, q, q, q, freq, q_weight=w, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+
+
+def test_workspaces_of_graphs_in_turn():
+    """One workspace for two graphs' calls in turn and an eager one between, its contents overwritten now and then."""
+    q, k, wq, wk, freq, start, _ = make(2, 4, 2, 500, 64, 64, "bf16", True, True, seed=18)
+    ws = torch.full((exattn.rope_bwd_workspace_size(64),), 255, dtype=torch.uint8, device=DEV)
+    sets = []
+    for seed in (90, 92):
+        args = _gpu(_normal(q.shape, seed, q.dtype), _normal(k.shape, seed + 1, q.dtype), q, k, freq, start)
+        kw = dict(q_weight=wq.to(DEV), k_weight=wk.to(DEV), workspace=ws)
+        want = exattn.rope_backward(*args, **kw)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = exattn.rope_backward(*args, **kw)
+        sets.append((graph, got, want, args, kw))
+    for turn in range(3):
+        for graph, got, want, args, kw in sets:
+            for t in got:
+                t.fill_(math.nan)
+            graph.replay()
+            if turn == 1:
+                ws.random_(0, 256)
+            again = exattn.rope_backward(*args, **kw)
+            for a, b, c in zip(got, want, again):
+                assert torch.equal(a, b) and torch.equal(c, b)
+
+
+@pytest.mark.parametrize("N", [600, 4000])
+def test_sums_of_few_and_of_many_blocks(N):
+    """The weights' gradients where the last block adds them up and where a launch of its own does, on a dirty workspace."""
+    q, k, wq, wk, freq, start, _ = make(4, 4, 4, N, 64, 64, "bf16", True, True, seed=19)
+    check_backward(q, k, wq, wk, freq, start, None)
+    args = _gpu(_normal(q.shape, 94, q.dtype), _normal(k.shape, 95, q.dtype), q, k, freq, start)
+    kw = dict(q_weight=wq.to(DEV), k_weight=wk.to(DEV))
+    want = exattn.rope_backward(*args, **kw)
+    ws = torch.full((exattn.rope_bwd_workspace_size(64),), 0x5A, dtype=torch.uint8, device=DEV)
+    for _ in range(3):
+        for a, b in zip(exattn.rope_backward(*args, workspace=ws, **kw), want):
+            assert torch.equal(a, b)
