@@ -22,6 +22,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "cache8.cuh"
 
@@ -148,28 +149,50 @@ __device__ __forceinline__ bool cache_piece_done(const CacheWs& ws, const CacheP
 }
 // The division, and a block's walk over its pieces.  Built by NT threads of a block (numbered `tid`, whole
 // warps that meet at hardware barrier `bar`), then walked by each of their warps, all lanes alike.
-template <int R, int TK, int NT, int kMinTiles>
+// A third form, for trees over many query rows (WHOLE): no item is divided, and so nothing is stored, counted and merged.  Where
+// there are more items than blocks they go, longest sequences first, to the blocks in turn, there and back (block c has the
+// c-th, the (2 P - 1 - c)-th, the (2 P + c)-th ...).  It is taken where the block with the most has no more than kWholeSlack
+// tiles, items' costs counted, above what the other forms give each: dividing items costs about as much.  Measured, divided
+// against whole, 8 heads of 128:
+//   16 sequences of 4096 tokens, 96 rows  71.5 : 61.4 us;  of 2048, 256 rows  62.2 : 45.3 us;  of 4096, 256 rows  86.2 : 75.3 us
+//   32 sequences spread over 1 to 4065 tokens, 256 rows  111.4 : 89.2 us
+// and where the rule does not take it, 40 sequences of 2048 tokens, 4 heads, 64 rows (20 tiles above)  59.2 : 69.4 us, 8 of
+// 2088, 4 heads, 256 rows (18 above)  38.5 : 47.2 us.
+// (attn_fwd_cache keeps the first two forms, and with them the bits of its results.)
+constexpr int kWholeMost = 64;   // sequences
+constexpr int kWholeTurns = 8;   // items a block
+constexpr int kWholeSlack = 15;  // tiles
+template <int NT>
+struct CacheWalkShared {  // first tile and first unit of each of the NT runs that the sequences are summed in
+  int tiles[NT + 1], units[NT + 1], warp_sums[NT / 32][5];
+};
+struct CacheWholeShared : CacheWalkShared<32> {  // and the sequences by length
+  uint8_t order[kWholeMost];
+};
+template <int R, int TK, int NT, int kMinTiles, bool WHOLE = false>
 struct CacheWalk {
-  struct Shared {  // first tile and first unit of each of the NT runs that the sequences are summed in
-    int tiles[NT + 1], units[NT + 1], warp_sums[NT / 32][5];
-  };
+  using Shared = std::conditional_t<WHOLE, CacheWholeShared, CacheWalkShared<NT>>;
   const CacheAttnArgs& a;
   Shared& sh;
   CacheItems<R, TK, kMinTiles> items;
   int at, stop, step;  // first form: tile numbers; second: piece numbers
   int C, shift, per;   // C: 2^shift by pieces; per: sequences a run
   bool by_piece, placed = false;
+  bool whole = false, sorted = false;  // third form
+  int turn = 0, block, blocks, per_seq = 1;
+  float per_seq_inverse = 1.f;
   // place of the next tile (first form)
   int b = 0, head = 0, rt = 0, len = 0, tile = 0, ntiles = 0, item_first = 0;
 
-  __device__ CacheWalk(const CacheAttnArgs& args, Shared& s, int tid, int bar, int block, int blocks)
-      : a(args), sh(s), items(args) {
+  __device__ CacheWalk(const CacheAttnArgs& args, Shared& s, int tid, int bar, int block_, int blocks_)
+      : a(args), sh(s), items(args), block(block_), blocks(blocks_) {
     per = (a.B + NT - 1) / NT;
     const int b0 = static_cast<int>(min(static_cast<long long>(a.B), static_cast<long long>(tid) * per));
     const int b1 = min(a.B - b0, per) + b0;
     constexpr int kLog = kMinTiles == 2 ? 1 : kMinTiles == 4 ? 2 : 3;
     static_assert(1 << kLog == kMinTiles, "a power of two");
     int n[4] = {0, 0, 0, 0}, count = 0;  // tiles; pieces of 1, 2 and 4 kMinTiles; items
+    int longest = 0;                     // WHOLE: the most tiles of an item, with its cost
     for (int i = b0; i < b1; ++i) {
       const int raw = a.lens[i], l = cache_len(a.c, raw);
       if (raw != l && block == 0) record_page_error(a.err_word);
@@ -180,6 +203,7 @@ struct CacheWalk {
 #pragma unroll
         for (int k = 0; k < 3; ++k) n[1 + k] += a.c.heads * items.cut(t, kLog + k);
         count += t > 0 ? a.c.heads : 0;
+        if constexpr (WHOLE) longest = max(longest, items.cost(t));
       }
     }
     // inclusive sums over the warp, then over the warps
@@ -231,6 +255,73 @@ struct CacheWalk {
       stop = total - at > C ? at + C : total;
       step = 0;
     }
+    if constexpr (WHOLE) {
+      static_assert(NT == 32 && kWholeMost <= 256, "one warp, and a byte a sequence");
+      const long long n = static_cast<long long>(a.B) * a.c.heads * items.row_tiles;
+      per_seq = a.c.heads * items.row_tiles;
+      per_seq_inverse = 1.f / static_cast<float>(per_seq);
+      if (n <= blocks) {  // an item a block: in any order
+        whole = __reduce_max_sync(0xffffffffu, longest) <= C + kWholeSlack;
+      } else if (a.B <= kWholeMost && n <= kWholeTurns * blocks) {
+        sorted = true;
+        // A sequence's place among all, the lengths by shuffles.  (Loops are kept as such: what runs once comes from far, and
+        // unrolled this took 4 us of a call instead of 1.)
+#pragma unroll 1
+        for (int g = tid; g - tid < a.B; g += 32) {
+          const int own = g < a.B ? items.seq_len(a, g) : -1;
+          int rank = 0;
+#pragma unroll 1
+          for (int h = tid; h - tid < a.B; h += 32) {
+            const int others = h < a.B ? items.seq_len(a, h) : -1;
+#pragma unroll 1
+            for (int j = 0; j < 32; ++j) {
+              const int other = __shfl_sync(0xffffffffu, others, j);
+              rank += other > own || (other == own && h - tid + j < g);
+            }
+          }
+          if (g < a.B) sh.order[rank] = static_cast<uint8_t>(g);
+        }
+        __syncwarp();
+        // the tiles of 32 of the blocks, evenly chosen
+        const int c = static_cast<int>(static_cast<unsigned>(blocks * tid) / NT);
+        int worst = 0;
+#pragma unroll 1
+        for (int k = 0; k < kWholeTurns; ++k) {
+          const int i = whole_item(k, c);
+          if (i >= n) break;
+          const int rank = whole_rank(i);
+          worst += items.cost(whole_tiles(rank, i - rank * per_seq));
+        }
+        whole = __reduce_max_sync(0xffffffffu, worst) <= C + kWholeSlack;
+      }
+    }
+  }
+  // The third form's items: number k of block c, in the order of length, there and back; the place of item i's sequence (items
+  // are few, and the quotient exact); and the tiles of one of a sequence's items.
+  __device__ int whole_item(int k, int c) const { return k & 1 ? (k + 1) * blocks - 1 - c : k * blocks + c; }
+  __device__ int whole_rank(int i) const { return static_cast<int>((static_cast<float>(i) + 0.5f) * per_seq_inverse); }
+  __device__ int whole_tiles(int rank, int rest) const {
+    return items.tiles(a, items.seq_len(a, whole_seq(rank)), items.row_tiles == 1 ? 0 : rest % items.row_tiles);
+  }
+  __device__ int whole_seq(int rank) const { return sorted ? sh.order[rank] : rank; }
+  __device__ bool next_whole(CachePiece& p) {
+    int i, rank, rest;
+    do {
+      i = whole_item(turn++, block);
+      if (i >= a.B * per_seq) return false;
+      rank = whole_rank(i);
+      rest = i - rank * per_seq;
+      p.end = whole_tiles(rank, rest);
+    } while (p.end == 0);
+    p.b = whole_seq(rank);
+    p.head = items.row_tiles == 1 ? rest : rest / items.row_tiles;
+    p.rt = rest - p.head * items.row_tiles;
+    p.len = items.seq_len(a, p.b);
+    p.begin = 0;
+    p.slot = -1;
+    p.bucket = 0;
+    p.pieces = 1;
+    return true;
   }
 
   __device__ static void sync(int bar) {
@@ -268,6 +359,9 @@ struct CacheWalk {
   }
 
   __device__ bool next(CachePiece& p) {
+    if constexpr (WHOLE) {
+      if (whole) return next_whole(p);
+    }
     int first_piece = 0;  // the number of the item's first
     for (;;) {
       if (at >= stop) return false;

@@ -66,7 +66,7 @@ static_assert((kTreeMost + 126) / kTK + 1 <= 5, "tiles that a tree's tokens reac
 constexpr float kShift = 3.f;  // as in cache_attn.cu
 constexpr int kMeta = 24;      // numbers a tile: ks[8], vs[8], log2 vs[8]
 
-template <int D, bool PAIR>
+template <int D, bool PAIR, bool TREE>
 struct Cfg {
   static constexpr int R = PAIR ? 256 : 128;
   static constexpr int MIN_TILES = PAIR ? 2 : 4;
@@ -82,7 +82,7 @@ struct Cfg {
   static constexpr uint32_t TM_OT = D;
   static_assert(5 + NS <= kFlagRing, "flags of the tiles under way");
   static_assert(TM_O + 2 * TM_OT <= 512, "tensor memory");
-  using Walk = CacheWalk<R, kTK, 32, MIN_TILES>;
+  using Walk = CacheWalk<R, kTK, 32, MIN_TILES, TREE>;
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_K = OFF_Q + (PAIR ? 2 : 1) * TILE;
   static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
@@ -414,7 +414,7 @@ struct Third {
 
 template <int D, int FMT, bool BF16, bool PAIR, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_constant__ CacheAttnArgs a) {
-  using C = Cfg<D, PAIR>;
+  using C = Cfg<D, PAIR, TREE>;
   constexpr int NS = C::NS, NR = C::NR, MR = C::MR;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t sbase = smem_u32(smem_raw);
@@ -1044,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
 
 template <int D, int FMT, bool BF16, bool PAIR, bool TREE>
 cudaError_t launch_t(const CacheAttnArgs& a, cudaStream_t stream) {
-  using C = Cfg<D, PAIR>;
+  using C = Cfg<D, PAIR, TREE>;
   auto kern = cache_tile_kernel<D, FMT, BF16, PAIR, TREE>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(kern, C::BYTES, done);

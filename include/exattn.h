@@ -741,9 +741,8 @@ attn_status attn_cache_append(const attn_cache* cache, const void* Q, attn_strid
  * query that sees nothing gets O = 0, LSE = -inf.  Sequences with fewer drafted
  * tokens than Nq: pad behind them, with tokens that no other row sees.
  * Everything else as attn_fwd_cache (lens, NaN, workspace of
- * attn_fwd_cache_workspace_size, the same bits on every run), and a mask that
- * lets every query see all j <= i gives the bits of
- * ATTN_MASK_CAUSAL_BOTTOM_RIGHT there.  Nq is at most ATTN_TREE_MAX_TOKENS.
+ * attn_fwd_cache_workspace_size, the same bits on every run).  Nq is at most
+ * ATTN_TREE_MAX_TOKENS.
  * Errors as there, plus ATTN_ERR_INVALID_ARG for a larger Nq and a tree_stride
  * below a tree's words.  The pages have no counterpart.
  */

@@ -144,15 +144,25 @@ def test_masks_that_are_no_trees(group, n, d):
 @pytest.mark.parametrize("group,n", [(1, 9), (2, 10), (1, 24), (1, 60), (4, 130), (1, 512)])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("code", ["e4m3", "int8"])
-def test_full_masks_give_the_causal_bits(group, n, d, code):
+def test_full_masks_are_causal(group, n, d, code):
+    """Every drafted token sees all before it; one mask for all sequences and one for each give the same bits."""
     lens = [n, 3, 1000 + n, 0, 640 + n]
     cache, host, table = make_cache(len(lens), 2, 32, d, -(-max(lens) // 32), code, seed=43)
-    q, at = _q(len(lens), 2 * group, n, d, "fp16").to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
-    want = exattn.forward_cache(q, cache, at)
+    q, at = _q(len(lens), 2 * group, n, d, "fp16"), torch.tensor(lens, dtype=torch.int32, device=DEV)
     full = torch.full((1, n, (n + 31) // 32), -1, dtype=torch.int32, device=DEV)
-    for tree in (full, full.expand(len(lens), -1, -1).contiguous()):
-        got = exattn.forward_cache_tree(q, cache, at, tree)
-        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    one, each = (exattn.forward_cache_tree(q.to(DEV), cache, at, t) for t in (full, full.expand(len(lens), -1, -1).contiguous()))
+    check(q, cache, host, table, lens, torch.ones((1, n, n), dtype=torch.bool), got=one)
+    assert torch.equal(one[0], each[0]) and torch.equal(one[1], each[1])
+
+
+@pytest.mark.parametrize("B,heads,group,n,lens", [(5, 3, 2, 40, [2000, 0, 17, 900, 2100]), (128, 1, 1, 30, None), (129, 1, 1, 30, None), (90, 2, 9, 29, None),
+                                                  (3, 40, 1, 300, [310, 5, 1290]), (1, 1, 1, 33, [33]), (40, 4, 1, 64, None), (2, 8, 1, 200, [20000, 300])], ids=str)
+@pytest.mark.parametrize("d", [64, 128])
+def test_items_whole_and_divided(B, heads, group, n, lens, d):
+    """Batches on both sides of the rule that keeps items whole: equal and spread lengths, more items than blocks and fewer."""
+    lens = lens or [n + (977 * b) % 1500 if b % 7 else 0 for b in range(B)]
+    cache, host, table = make_cache(B, heads, 64, d, -(-max(lens) // 64), "e4m3", seed=49)
+    check(_q(B, heads * group, n, d, "bf16"), cache, host, table, lens, plain_tree(random_parents(1, n, 7, 6))[0])
 
 
 @pytest.mark.parametrize("group,n", [(1, 6), (1, 30), (2, 100)])
@@ -233,8 +243,7 @@ def test_views_streams_and_graphs(group, n):
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     other.fill_(-1)
     graph.replay()
-    full = exattn.forward_cache(q, cache, at)
-    assert torch.equal(o, full[0]) and torch.equal(lse, full[1])
+    check(q.cpu(), cache, host, table, lens, torch.ones((1, n, n), dtype=torch.bool), got=(o, lse))
 
 
 def test_a_step_of_drafting():
