@@ -1,4 +1,5 @@
-"""Thin ctypes binding over libexattn.so (include/exattn.h).
+"""Thin binding over libexattn.so (include/exattn.h): ctypes, and for the calls
+whose kernels take a few microseconds the compiled _binding.so.
 
 Argument marshalling only: every step of attention runs in the library's
 CUDA kernels.  torch supplies device memory and the current stream.  There is
@@ -156,6 +157,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.attn_last_error.restype = ctypes.c_char_p
             _lib = lib
     return _lib
+
+
+_compiled = None
+
+
+def binding():
+    """The compiled binding (_binding.so), behind the library that it calls."""
+    global _compiled
+    if _compiled is None:
+        load()
+        from exact_head_attention_gb300 import _binding
+        _binding.set_error_class(AttnError)
+        _compiled = _binding
+    return _compiled
 
 
 def status_string(status: int) -> str:
@@ -535,7 +550,8 @@ class QuantCache:
     k, v: [num_pages, heads, page, d] float8_e4m3fn or int8 codes; k_scale, v_scale: [num_pages, heads] fp32; a
     code stands for code * scale of its page and head.  page_table: [B, width] int32, the pages of each sequence
     in order.  All contiguous, on one CUDA device; the tensors are used in place."""
-    __slots__ = ("k", "v", "k_scale", "v_scale", "page_table", "device", "index", "B", "heads", "d", "struct", "_ref")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "page_table", "device", "index", "B", "heads", "d", "struct", "_ref",
+                 "address")
 
     def __init__(self, k, v, k_scale, v_scale, page_table):
         fmt = _CACHE_DTYPES.get(k.dtype)
@@ -558,6 +574,7 @@ class QuantCache:
         self.struct = CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   page_table.data_ptr(), pages, heads, page, d, rows[1], fmt)
         self._ref = ctypes.byref(self.struct)
+        self.address = ctypes.addressof(self.struct)
 
     @classmethod
     def empty(cls, num_pages: int, heads: int, page: int, d: int, page_table, format: str = "e4m3"):
@@ -583,7 +600,13 @@ def _int32(t, cache: QuantCache, name: str):
 _STRIDES: dict = {}  # Strides objects by their values (building one costs more than the rest of a view's marshalling)
 
 
-def _strides(t) -> Strides:
+def _cache_view(t, cache: QuantCache, dtype):
+    """(pointer, Strides) of a 16-bit [B, H, N, d] view that goes with the cache."""
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != cache.B or shape[3] != cache.d:
+        raise ValueError("tensors must be [B, H, N, d] with the page table's B and the cache's d")
+    if t.get_device() != cache.index or t.dtype != dtype:
+        raise ValueError("tensors must be of one dtype, on the cache's device")
     sb, sh, sn, sd = t.stride()
     if sd != 1:
         raise ValueError("tensors must have a contiguous last dimension")
@@ -592,36 +615,23 @@ def _strides(t) -> Strides:
         if len(_STRIDES) >= 4096:
             _STRIDES.clear()
         st = _STRIDES[(sb, sh, sn)] = Strides(sb, sh, sn)
-    return st
+    return t.data_ptr(), st
 
 
-def _cache_view(t, cache: QuantCache, dtype):
-    """(pointer, Strides) of a 16-bit [B, H, N, d] view that goes with the cache."""
-    shape = t.shape
-    if len(shape) != 4 or shape[0] != cache.B or shape[3] != cache.d:
-        raise ValueError("tensors must be [B, H, N, d] with the page table's B and the cache's d")
-    if t.get_device() != cache.index or t.dtype != dtype:
-        raise ValueError("tensors must be of one dtype, on the cache's device")
-    return t.data_ptr(), _strides(t)
-
-
-def _on(index: int, stream, call):
-    """Runs `call` with that device current and, where given, on `stream`: what it allocates belongs to it."""
-    with torch.cuda.device(index):
+def _on(cache: QuantCache, stream, call):
+    """Runs `call` with the cache's device current and, where given, on `stream`: what it allocates belongs to it."""
+    with torch.cuda.device(cache.device):
         if stream is None:
             return call(_stream(None))
         with torch.cuda.stream(stream):
             return call(_stream(stream))
 
 
-def _run_at(index: int, stream, call):
-    if stream is None and _RAW_STREAM is not None and index == torch.cuda.current_device():
-        return call(_RAW_STREAM(index))
-    return _on(index, stream, call)
-
-
 def _run(cache: QuantCache, stream, call):
-    return _run_at(cache.index, stream, call)
+    index = torch.cuda.current_device()
+    if stream is None and index == cache.index and _RAW_STREAM is not None:
+        return call(_RAW_STREAM(index))
+    return _on(cache, stream, call)
 
 
 def cache_write(cache: QuantCache, k, v, start=None, count=None, stream=None) -> None:
@@ -702,14 +712,9 @@ def forward_cache(q, cache: QuantCache, lens, causal="bottom_right", scale: floa
     h // (H // heads)).  causal "bottom_right" (the default): the queries are a sequence's last Nq tokens; also
     False and True (top-left) as in forward().  lens: int32 CUDA tensor [B].  `workspace` (uint8 CUDA tensor of
     cache_workspace_size bytes, one for each call that may run at the same time) is allocated if omitted."""
-    return _forward_cache(q, cache, lens, mask_code(causal), scale, workspace, stream, None)
-
-
-def _forward_cache(q, cache: QuantCache, lens, mask: int, scale, workspace, stream, tree):
-    """forward_cache with an attn_mask value, or forward_cache_tree with `tree`: (address, words between sequences)."""
     qp, qs = _cache_view(q, cache, q.dtype)
     B, H, Nq, d = q.shape
-    code, lens_at = _dtype_code(q), _int32(lens, cache, "lens")
+    code, mask, lens_at = _dtype_code(q), mask_code(causal), _int32(lens, cache, "lens")
     scale = (1.0 / d ** 0.5) if scale is None else scale
 
     def call(handle):
@@ -724,17 +729,21 @@ def _forward_cache(q, cache: QuantCache, lens, mask: int, scale, workspace, stre
             else:
                 at, size = _cache_workspace(workspace, cache)
             op, os_ = _cache_view(o, cache, q.dtype)
-            if tree is None:
-                st = lib.attn_fwd_cache(qp, qs, cache._ref, lens_at, op, os_, lse.data_ptr(), B, H, Nq, mask, scale, code,
-                                        at, size, handle)
-            else:
-                st = lib.attn_fwd_cache_tree(qp, qs, cache._ref, lens_at, *tree, op, os_, lse.data_ptr(), B, H, Nq, scale, code,
-                                             at, size, handle)
+            st = lib.attn_fwd_cache(qp, qs, cache._ref, lens_at, op, os_, lse.data_ptr(), B, H, Nq, mask, scale, code,
+                                    at, size, handle)
             if st != ATTN_OK:
-                raise AttnError(st, "attn_fwd_cache" if tree is None else "attn_fwd_cache_tree")
+                raise AttnError(st, "attn_fwd_cache")
         return o, lse
 
     return _run(cache, stream, call)
+
+
+def _fast(stream, call):
+    """Runs a call of the compiled binding, on `stream` where that is given: what it allocates belongs to it."""
+    if stream is None:
+        return call()
+    with torch.cuda.device(stream.device), torch.cuda.stream(stream):
+        return call()
 
 
 def draft_tree(parents, stream=None):
@@ -743,21 +752,7 @@ def draft_tree(parents, stream=None):
     parents: int32 CUDA tensor [B, N] (or [N], one tree for all sequences: B is 1), -1 or the number of an earlier token.
     The mask has each token's ancestors and itself as bits, for forward_cache_tree; the depth is its number of drafted
     ancestors, the offsets of rope_forward and cache_append."""
-    shape = parents.shape
-    if parents.dtype != torch.int32 or not parents.is_cuda or len(shape) not in (1, 2) or not parents.is_contiguous():
-        raise ValueError("parents must be a contiguous int32 CUDA tensor [B, N] or [N]")
-    B, N = (1, shape[0]) if len(shape) == 1 else shape
-
-    def call(handle):
-        mask = torch.empty((B, N, (N + 31) // 32), dtype=torch.int32, device=parents.device)
-        depth = torch.empty((B, N), dtype=torch.int32, device=parents.device)
-        if B and N:
-            st = load().attn_draft_tree(parents.data_ptr(), mask.data_ptr(), depth.data_ptr(), B, N, handle)
-            if st != ATTN_OK:
-                raise AttnError(st, "attn_draft_tree")
-        return mask, depth
-
-    return _run_at(parents.get_device(), stream, call)
+    return _fast(stream, lambda: binding().draft_tree(parents))
 
 
 def forward_cache_tree(q, cache: QuantCache, lens, tree, scale: float | None = None, workspace=None, stream=None):
@@ -766,19 +761,12 @@ def forward_cache_tree(q, cache: QuantCache, lens, tree, scale: float | None = N
 
     tree: int32 CUDA tensor [B, Nq, ceil(Nq / 32)], or [1, ...] for all sequences alike (draft_tree): bit j % 32 of word
     j // 32 of row i, for j <= i.  The other arguments as in forward_cache."""
-    shape = tree.shape
-    Nq = q.shape[2] if q.dim() == 4 else 0
-    if tree.dtype != torch.int32 or tree.get_device() != cache.index or not tree.is_contiguous() or len(shape) != 3 or (
-            shape[0] not in (1, cache.B) or shape[1] != Nq or shape[2] != (Nq + 31) // 32):
-        raise ValueError("tree must be a contiguous int32 tensor [B, Nq, ceil(Nq / 32)] or [1, ...] on the cache's device")
-    return _forward_cache(q, cache, lens, 2, scale, workspace, stream, (tree.data_ptr(), shape[1] * shape[2] if shape[0] > 1 else 0))
+    return _fast(stream, lambda: binding().forward_cache_tree(cache.address, cache.index, cache.B, q, lens, tree, scale, workspace))
 
 
 # ------------------------------------------------------------------ rotary positions and norms per head
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
-_DTYPE_CODES = {torch.bfloat16: ATTN_BF16, torch.float16: ATTN_FP16}
-_NO_STRIDES = Strides(0, 0, 0)  # of a tensor that is left out
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -814,79 +802,11 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None
     return torch.tensor(freq, dtype=torch.float64, device=device), amplitude
 
 
-def _rope_struct(freq, B: int, N: int, d: int, dtype, index: int, start, offsets, layout: str, amplitude: float, q_weight,
-                 k_weight, eps: float) -> RopeStruct:
-    """attn_rope of the caller's tensors; freq None: norms only."""
+def _layout(layout: str) -> int:
     code = ROPE_LAYOUTS.get(layout)
     if code is None:
         raise ValueError(f"unknown rotary layout {layout!r}")
-    at_freq = at_start = at_offsets = at_q = at_k = None
-    rot = stride = wide = 0
-    if freq is not None:
-        if freq.dtype is not torch.float64 or freq.dim() != 1 or not freq.is_contiguous() or freq.get_device() != index:
-            raise ValueError("freq must be a contiguous float64 tensor [rotary_dim / 2] on the tensors' device")
-        rot, at_freq = 2 * freq.numel(), freq.data_ptr()
-    if start is not None:
-        if start.dtype is not torch.int32 or start.shape != (B,) or start.get_device() != index or not start.is_contiguous():
-            raise ValueError("start must be a contiguous int32 tensor of one entry a sequence on the tensors' device")
-        at_start = start.data_ptr()
-    if offsets is not None:
-        shape = offsets.shape
-        if offsets.dtype is not torch.int32 or offsets.get_device() != index or shape not in ((B, N), (1, N), (N,)) or (
-                N > 1 and offsets.stride(-1) != 1):
-            raise ValueError("offsets must be an int32 tensor [B, N], [1, N] or [N], last dimension contiguous, on the tensors' device")
-        stride = offsets.stride(0) if len(shape) == 2 and shape[0] > 1 else 0
-        at_offsets = offsets.data_ptr()
-    if q_weight is not None:
-        at_q, wide = _rope_weight(q_weight, d, dtype, index)
-    if k_weight is not None:
-        at_k, k_wide = _rope_weight(k_weight, d, dtype, index)
-        if at_q is not None and wide != k_wide:
-            raise TypeError("both weights must be of one dtype")
-        wide = k_wide
-    return RopeStruct(at_freq, at_start, at_offsets, stride, at_q, at_k, rot, code, wide, amplitude, eps)
-
-
-def _rope_weight(w, d: int, dtype, index: int):
-    """(address, whether it is fp32) of a norm's weights."""
-    wide = w.dtype is torch.float32
-    if not (wide or w.dtype is dtype) or w.shape != (d,) or w.get_device() != index or not w.is_contiguous():
-        raise ValueError("weights must be contiguous [d], float32 or of the tensors' dtype, on their device")
-    return w.data_ptr(), wide
-
-
-def _rope_pair(q, k, names=("q", "k")):
-    """(shape, dtype, device index, heads of q, heads of k) of two [B, H, N, d] tensors, one of which may be None."""
-    x = k if q is None else q
-    if x is None:
-        raise ValueError(f"{names[0]} or {names[1]} is needed")
-    shape, index = x.shape, x.get_device()
-    if index < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    if len(shape) != 4:
-        raise ValueError(f"{names[0]} and {names[1]} must be [B, H, N, d]")
-    if q is None:
-        return shape, x.dtype, index, 0, shape[1]
-    if k is None:
-        return shape, x.dtype, index, shape[1], 0
-    other = k.shape
-    if len(other) != 4 or other[0] != shape[0] or other[2] != shape[2] or other[3] != shape[3]:
-        raise ValueError(f"{names[0]} and {names[1]} must be [B, H, N, d] with the same B, N and d")
-    if k.dtype is not x.dtype or k.get_device() != index:
-        raise ValueError(f"{names[0]} and {names[1]} must be of one dtype, on one device")
-    return shape, x.dtype, index, shape[1], other[1]
-
-
-def _rope_view(t):
-    """(pointer, Strides) of a tensor that may be left out."""
-    return (None, _NO_STRIDES) if t is None else (t.data_ptr(), _strides(t))
-
-
-def _rope_like(t, like):
-    """_rope_view of a caller's tensor that must be as another is."""
-    if t is not None and (like is None or t.shape != like.shape or t.dtype is not like.dtype or t.get_device() != like.get_device()):
-        raise ValueError("tensors must match in shape, dtype and device")
-    return _rope_view(t)
+    return code
 
 
 def rope_forward(q, k, freq, start=None, offsets=None, layout="half", amplitude: float = 1.0, q_weight=None, k_weight=None,
@@ -898,29 +818,11 @@ def rope_forward(q, k, freq, start=None, offsets=None, layout="half", amplitude:
     pairs (i, i + rotary_dim / 2), or "interleaved": (2 i, 2 i + 1).  amplitude multiplies what turns.  q_weight, k_weight:
     the norms' [d] weights (fp32 or as the tensors), None: no norm.  q or k may be None.  out: a pair to write to, which may
     be (q, k) itself."""
-    (B, _, N, d), dtype, index, H, Hk = _rope_pair(q, k)
-    code = _DTYPE_CODES.get(dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dtype}; expected bfloat16 or float16")
-    rope = _rope_struct(freq, B, N, d, dtype, index, start, offsets, layout, amplitude, q_weight, k_weight, eps)
-    views = (*_rope_view(q), *_rope_view(k))
-
-    def call(handle):
-        if out is None:
-            oq, ok = None if q is None else torch.empty_like(q), None if k is None else torch.empty_like(k)
-            to = (*_rope_view(oq), *_rope_view(ok))
-        else:
-            oq, ok = out
-            if (oq is None) != (q is None) or (ok is None) != (k is None):
-                raise ValueError("out must be a pair of what q and k are")
-            to = (*_rope_like(oq, q), *_rope_like(ok, k))
-        if B and N and (H or Hk):
-            st = load().attn_rope_fwd(*views, *to, B, H, Hk, N, d, rope, code, handle)
-            if st != ATTN_OK:
-                raise AttnError(st, "attn_rope_fwd")
-        return oq, ok
-
-    return _run_at(index, stream, call)
+    oq, ok = (None, None) if out is None else out
+    if out is not None and oq is None and ok is None:
+        raise ValueError("out must be a pair of what q and k are")
+    code = _layout(layout)
+    return _fast(stream, lambda: binding().rope_forward(q, k, freq, start, offsets, code, amplitude, q_weight, k_weight, eps, oq, ok))
 
 
 def rope_bwd_workspace_size(d: int) -> int:
@@ -935,44 +837,8 @@ def rope_backward(dq, dk, q, k, freq, start=None, offsets=None, layout="half", a
     q and k are its inputs (not read, and may be None, where that tensor has no weights); the other arguments as there.
     The weights' gradients are summed in a fixed order; None where there are no weights.  `workspace` (uint8 CUDA tensor of
     rope_bwd_workspace_size bytes, one for each call that may run at the same time) is allocated if omitted."""
-    (B, _, N, d), dtype, index, H, Hk = _rope_pair(dq, dk, ("dq", "dk"))
-    code = _DTYPE_CODES.get(dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dtype}; expected bfloat16 or float16")
-    rope = _rope_struct(freq, B, N, d, dtype, index, start, offsets, layout, amplitude, q_weight, k_weight, eps)
-    wq, wk = q_weight if H else None, k_weight if Hk else None
-    if (wq is not None and q is None) or (wk is not None and k is None):
-        raise ValueError("the gradients of a norm need its input")
-    views = (*_rope_view(dq), *_rope_view(dk), *_rope_like(q if wq is not None else None, dq),
-             *_rope_like(k if wk is not None else None, dk))
-    if workspace is not None and (workspace.get_device() != index or not workspace.is_contiguous()):
-        raise ValueError("the workspace must be contiguous and on the tensors' device")
-
-    def call(handle):
-        oq, ok = None if dq is None else torch.empty_like(dq), None if dk is None else torch.empty_like(dk)
-        if not (B and N and (H or Hk)):
-            return oq, ok, None if q_weight is None else torch.zeros_like(q_weight), None if k_weight is None else torch.zeros_like(k_weight)
-        dwq, dwk = None if wq is None else torch.empty_like(wq), None if wk is None else torch.empty_like(wk)
-        lib = load()
-        space, size = None, 0
-        if wq is not None or wk is not None:
-            size = lib.attn_rope_bwd_workspace_size(d)
-            if workspace is None:
-                space = torch.empty(size, dtype=torch.uint8, device=(dq if dk is None else dk).device)
-            else:
-                space, size = workspace, workspace.numel() * workspace.element_size()
-        st = lib.attn_rope_bwd(*views, *_rope_view(oq), *_rope_view(ok), None if dwq is None else dwq.data_ptr(),
-                               None if dwk is None else dwk.data_ptr(), B, H, Hk, N, d, rope, code,
-                               None if space is None else space.data_ptr(), size, handle)
-        if st != ATTN_OK:
-            raise AttnError(st, "attn_rope_bwd")
-        if q_weight is not None and dwq is None:
-            dwq = torch.zeros_like(q_weight)
-        if k_weight is not None and dwk is None:
-            dwk = torch.zeros_like(k_weight)
-        return oq, ok, dwq, dwk
-
-    return _run_at(index, stream, call)
+    code = _layout(layout)
+    return _fast(stream, lambda: binding().rope_backward(dq, dk, q, k, freq, start, offsets, code, amplitude, q_weight, k_weight, eps, workspace))
 
 
 def _plain_strides(t):
@@ -1017,36 +883,6 @@ def cache_append(cache: QuantCache, k, v, freq, start=None, count=None, offsets=
     k, v, start, count as in cache_write; freq, offsets, layout, amplitude, weights and eps as in rope_forward, the position
     of row n of sequence b being start[b] + offsets[b, n] (position_start, where given, in place of start).  q: [B, H, N, d]
     of the same tokens, or None; all its rows are turned, into `out` (which may be q) where that is given."""
-    shape = k.shape
-    if v.shape != shape or len(shape) != 4 or shape[1] != cache.heads:
-        raise ValueError("k and v must be [B, heads, N, d] with the cache's heads")
-    kp, ks = _cache_view(k, cache, k.dtype)
-    vp, vs = _cache_view(v, cache, k.dtype)
-    B, _, N, d = shape
-    H, qp, qs = 0, None, _NO_STRIDES
-    if q is not None:
-        qp, qs = _cache_view(q, cache, k.dtype)
-        if q.shape[2] != N:
-            raise ValueError("q must be [B, H, N, d] of the new tokens")
-        H = q.shape[1]
-    elif q_weight is not None or out is not None:
-        raise ValueError("a weight or an output for queries that are not there")
-    code, start_at, count_at = _dtype_code(k), _int32(start, cache, "start"), _int32(count, cache, "count")
-    rope = _rope_struct(freq, B, N, d, k.dtype, cache.index, position_start, offsets, layout, amplitude, q_weight, k_weight, eps)
-
-    def call(handle):
-        if q is None:
-            to, tp, ts = None, None, _NO_STRIDES
-        elif out is None:
-            to = torch.empty_like(q)
-            tp, ts = _rope_view(to)
-        else:
-            to = out
-            tp, ts = _rope_like(to, q)
-        if B and N:
-            st = load().attn_cache_append(cache._ref, qp, qs, tp, ts, kp, ks, vp, vs, start_at, count_at, B, H, N, rope, code, handle)
-            if st != ATTN_OK:
-                raise AttnError(st, "attn_cache_append")
-        return to
-
-    return _run(cache, stream, call)
+    code = _layout(layout)
+    return _fast(stream, lambda: binding().cache_append(cache.address, cache.index, cache.B, k, v, freq, start, count, offsets, q, code,
+                                                        amplitude, q_weight, k_weight, eps, position_start, out))

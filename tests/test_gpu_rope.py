@@ -202,8 +202,8 @@ def test_gradients_in_place_of_the_outputs():
     q, k, wq, wk, freq, start, _ = make(2, 3, 2, 70, 64, 32, "bf16", True, False, seed=12)
     dq, dk = _normal(q.shape, 60, q.dtype), _normal(k.shape, 61, q.dtype)
     want = exattn.rope_backward(*_gpu(dq, dk, q, k, freq, start), q_weight=wq.to(DEV), k_weight=wk.to(DEV))
-    lib, gd, st = exattn.load(), _gpu(dq, dk, q, k, freq, start, wq, wk), exattn._strides
-    rope = exattn._rope_struct(gd[4], 2, 70, 64, q.dtype, 0, gd[5], None, "half", 1.0, gd[6], gd[7], 1e-6)
+    lib, gd, st = exattn.load(), _gpu(dq, dk, q, k, freq, start, wq, wk), lambda t: exattn.Strides(*t.stride()[:3])
+    rope = exattn.RopeStruct(gd[4].data_ptr(), gd[5].data_ptr(), None, 0, gd[6].data_ptr(), gd[7].data_ptr(), 32, 0, 0, 1.0, 1e-6)
     dw = torch.empty((2, 64), dtype=q.dtype, device=DEV)
     ws = torch.full((exattn.rope_bwd_workspace_size(64),), 255, dtype=torch.uint8, device=DEV)
     views = [x for t in (gd[0], gd[1], gd[2], gd[3], gd[0], gd[1]) for x in (t.data_ptr(), st(t))]
