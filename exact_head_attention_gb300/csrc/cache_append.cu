@@ -33,9 +33,9 @@ namespace {
 
 static_assert(kIoThreads == kRopeThreads, "one launch for both");
 constexpr int kAppendBlocks = 3;  // resident an SM where a thread has two rows
-// Shared memory: a cosine and a sine for each pair of a thread's NV * 8 values, and those twice in 16 bits.
+// Shared memory: a cosine and a sine for each pair of a thread's NV * 8 values, and those in 16 bits.
 template <int NV>
-constexpr int kMostShared = kIoThreads * NV * (8 * 4 + 2 * 16);
+constexpr int kMostShared = kIoThreads * NV * (8 * 4 + 16);
 static_assert(sizeof(RopeShared) <= kMostShared<4>, "room for the queries' part");
 
 __device__ __forceinline__ uint2 to_codes_of(int format, const float (&y)[8]) {
@@ -146,9 +146,8 @@ __global__ void __launch_bounds__(kIoThreads, NV == 4 ? kAppendBlocks : 2) cache
   const int r0 = un.r0, r1 = un.page < 0 ? r0 : un.r1, inside = un.inside;
   const Lane l(rv, u);
 
-  // The page's rows under way: a thread's two units of each of its rows, of the head at hand and the next.  Rows that are not
-  // new stay zero.
-  uint4 (*const slots)[NV][kIoThreads] = reinterpret_cast<uint4 (*)[NV][kIoThreads]>(smem_raw + a.slots_at);
+  // A head's rows under way: a thread's two units of each of its rows.  Rows that are not new stay zero.
+  uint4 (*const slots)[kIoThreads] = reinterpret_cast<uint4 (*)[kIoThreads]>(smem_raw + a.slots_at);
   const RowStrides& st = is_v ? a.io.sv : a.io.sk;
   const int row0 = tid / Lane::LANES;
   const uint16_t* src = static_cast<const uint16_t*>(is_v ? a.io.v : a.io.k) + b * st.b + head0 * st.h + (un.row_of_r0 - r0 + row0) * st.n + 8 * l.ua;
@@ -159,25 +158,22 @@ __global__ void __launch_bounds__(kIoThreads, NV == 4 ? kAppendBlocks : 2) cache
   for (int i = 0; i < ROWS; ++i) {
     const int row = row0 + i * STEP;
     there[i] = row >= r0 && row < r1;
-    if (!there[i]) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) slots[k >> 1][2 * i + (k & 1)][threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
-    }
+    if (!there[i]) slots[2 * i][threadIdx.x] = slots[2 * i + 1][threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
   }
-  auto load = [&](bool some, int turn) {
+  auto load = [&](bool some) {
     if (some) {
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
         if (there[i]) {
-          copy16(&slots[turn][2 * i][threadIdx.x], src + i * next_row);
-          copy16(&slots[turn][2 * i + 1][threadIdx.x], src + i * next_row + to_ub);
+          copy16(&slots[2 * i][threadIdx.x], src + i * next_row);
+          copy16(&slots[2 * i + 1][threadIdx.x], src + i * next_row + to_ub);
         }
       }
       src += next_head;
     }
     copies_commit();
   };
-  load(head0 < heads, 0);
+  load(head0 < heads);
 
   float* const cosines = reinterpret_cast<float*>(smem_raw) + pg * PAGE * SLOTS;
   float* const sines = cosines + (UNITS >> a.head_shift) * PAGE * SLOTS;
@@ -205,15 +201,37 @@ __global__ void __launch_bounds__(kIoThreads, NV == 4 ? kAppendBlocks : 2) cache
         bool finite;
         const uint64_t turns = turns_of(rv.freq[pair], finite);
         const float amplitude = finite ? rv.amplitude : __int_as_float(0x7fffffff);
-        int row = r0 + (threads < SLOTS ? 0 : at / SLOTS);
-        uint64_t angle = static_cast<uint64_t>(first + row) * turns;  // of rows in order
-#pragma unroll 2
-        for (; row < r1; row += step, angle += step * turns) {
-          if (offsets) angle = static_cast<uint64_t>(first + offsets[row]) * turns;
-          float si, co;
-          sin_cos_turns(static_cast<uint32_t>(angle >> 32), si, co);
-          cosines[row * SLOTS + slot] = co * amplitude;
-          sines[row * SLOTS + slot] = si * amplitude;
+        const int first_row = r0 + (threads < SLOTS ? 0 : at / SLOTS);
+        auto direct = [&](uint64_t angle, float& co, float& si) { sin_cos_turns(static_cast<uint32_t>(angle >> 32), si, co); };
+        auto put = [&](int row, float co, float si) {
+          cosines[row * SLOTS + slot] = co;
+          sines[row * SLOTS + slot] = si;
+        };
+        if (offsets || r1 - r0 < 4 * step) {
+          for (int row = first_row; row < r1; row += step) {
+            float co, si;
+            direct(static_cast<uint64_t>(first + (offsets ? offsets[row] : row)) * turns, co, si);
+            put(row, co * amplitude, si * amplitude);
+          }
+        } else {
+          // Rows in order: every fourth angle of a thread's is computed, and the three behind it are that turned by one, two
+          // and three steps.
+          const uint64_t ahead = step * turns;
+          float ch[3], sh[3];
+#pragma unroll
+          for (int k = 0; k < 3; ++k) direct((k + 1) * ahead, ch[k], sh[k]);
+          uint64_t angle = static_cast<uint64_t>(first + first_row) * turns;
+#pragma unroll 1
+          for (int row = first_row; row < r1; row += 4 * step, angle += 4 * ahead) {
+            float co, si;
+            direct(angle, co, si);
+            co *= amplitude;
+            si *= amplitude;
+            put(row, co, si);
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              if (row + (k + 1) * step < r1) put(row + (k + 1) * step, co * ch[k] - si * sh[k], co * sh[k] + si * ch[k]);
+          }
         }
       }
     }
@@ -233,14 +251,19 @@ __global__ void __launch_bounds__(kIoThreads, NV == 4 ? kAppendBlocks : 2) cache
   for (int head = head0; head < heads; head += side, turn ^= 1, scale_at += side, codes += side * (PAGE * D)) {
     float old = 0.f;
     if (inside > 0) old = *scale_at;
-    load(head + side < heads, turn ^ 1);
-    copies_wait<1>();
+    copies_wait<0>();
+    uint4 raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) raw[i] = slots[i][threadIdx.x];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) loaded(raw[i]);  // the places are free once the values are here
+    load(head + side < heads);
     PairedRow<INTER> x[ROWS];
     float r[ROWS], most = 0.f;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       float v[16];
-      Lane::template widen<BF16>(slots[turn][2 * i][threadIdx.x], slots[turn][2 * i + 1][threadIdx.x], v);
+      Lane::template widen<BF16>(raw[2 * i], raw[2 * i + 1], v);
       x[i].set(v);
       r[i] = 1.f;
     }
@@ -358,7 +381,7 @@ cudaError_t append_t(CacheAppendArgs& a, cudaStream_t stream) {
   a.q_token_blocks = 1;
   size_t smem = a.rope.r.rot > 0 ? static_cast<size_t>(2) * groups * PAGE * (D / 2) * sizeof(float) : 0;
   a.slots_at = static_cast<int>(smem);
-  smem += 2 * NV * kIoThreads * sizeof(uint4);
+  smem += NV * kIoThreads * sizeof(uint4);
   if (a.rope.side[0].heads > 0) {
     const RopeGrid grid = rope_plan(a.rope);
     a.q_token_blocks = static_cast<int>(grid.token_blocks);

@@ -2,7 +2,9 @@
 
 Keys are compared with the definition in 64 bits (plain_rope), values with the write's own rule, which must be followed to
 the bit; queries must be rope_forward's bits, and without norm and rotation the whole must be cache_write's.  Tolerances:
-  rotated keys  under 2^-19 of the size that plain_rope gives (test_gpu_rope.py), in fp32
+  rotated keys  the norm's error as in test_gpu_rope.py, 1.04e-6; angles of rows in order are the product of two, each sine
+                and cosine within 1e-7 and its angle within 2^-25.3, and three roundings: 4.2e-7, and 2.4e-7 for the
+                amplitude, the products and the sum: together under 2^-19 of the size that plain_rope gives, in fp32
   scale         that of the largest key, over the largest code, and two roundings: 2^-19 of the largest size and 2^-23 of it
   codes         half a code's step: relative 2^-4 for e4m3 from 2^-6 of a scale on, 2^-10 of a scale below; half a scale for
                 int8; to the key's own error and that of the scale (2^-22 of the value for the reciprocal and the product)
@@ -266,3 +268,46 @@ def test_refused_tensors():
         with pytest.raises(exattn.AttnError):
             exattn.cache_append(cache, k, k, freq, **kw)
     assert exattn.check_device_error() == 0
+
+
+def test_onto_pages_of_nan():
+    """A page whose scale is NaN stays so, its earlier codes as they were, and the other pages and heads are not touched by it."""
+    cache, host, table = make_cache(2, 2, 16, 64, 3, "e4m3", seed=39)
+    bad = int(table[0, 1])
+    cache.k_scale[bad, 0] = math.nan
+    before = cache.k.view(torch.uint8).clone()
+    k = torch.randn((2, 2, 20, 64), generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    freq, starts = exattn.rope_frequencies(64, device="cpu")[0], [20, 3]
+    exattn.cache_append(cache, *_on(k, k, freq, _i32(starts)))
+    assert exattn.check_device_error() == 0
+    assert torch.isnan(cache.k_scale[bad, 0]) and torch.isfinite(cache.k_scale[bad, 1])
+    codes = cache.k.view(torch.uint8)[bad, 0]
+    assert torch.equal(codes[:4], before[bad, 0, :4]) and torch.all(codes[4:] == 0)
+    y, _ = plain_rope.norm_rotate(k, freq, plain_rope.positions(2, 20, _i32(starts)))
+    s = cache.k_scale[int(table[0, 2]), 0].double().cpu()
+    got = cache.k[int(table[0, 2]), 0, :8].float().double().cpu() * s
+    assert torch.all((got - y[0, 0, 12:]).abs() <= code_step(y[0, 0, 12:], s, "e4m3") * 1.001)
+
+
+def test_pool_beyond_32_bits():
+    """Pages whose codes lie past 4 GB of the pool."""
+    pages, heads, page, d = 70_000, 8, 128, 64
+    codes = [torch.empty((pages, heads, page, d), dtype=torch.int8, device=DEV) for _ in range(2)]
+    scales = [torch.zeros((pages, heads), device=DEV) for _ in range(2)]
+    table = torch.tensor([[pages - 1, 3], [pages - 2, 69_000]], dtype=torch.int32, device=DEV)
+    for t in codes:
+        t[table.reshape(-1).long()] = 0
+    cache = exattn.QuantCache(*codes, *scales, table)
+    k = torch.randn((2, heads, 200, d), generator=torch.Generator().manual_seed(6)).to(torch.bfloat16)
+    freq, starts = exattn.rope_frequencies(d, device="cpu")[0], [0, 50]
+    exattn.cache_append(cache, *_on(k, k, freq, _i32(starts)))
+    assert exattn.check_device_error() == 0
+    y, size = plain_rope.norm_rotate(k, freq, plain_rope.positions(2, 200, _i32(starts)))
+    at = table.cpu()
+    for b in range(2):
+        for n in (0, 77, 78, 127, 128, 199):
+            t = starts[b] + n
+            p = int(at[b, t // page])
+            s = scales[0][p].double().cpu()[:, None]
+            got = codes[0][p, :, t % page].double().cpu() * s
+            assert torch.all((got - y[b, :, n]).abs() <= 0.5 * s * 1.001 + 2.0 ** -18 * size[b, :, n])

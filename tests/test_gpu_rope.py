@@ -3,9 +3,9 @@
 Every result is compared with the definition in 64 bits on the CPU (plain_rope).  Tolerances, from the roundings that the
 operators make; e = 2^-24 is half an fp32 step, relative:
   norm      the sum of d squares, none negative, 16 products and up to 4 joins deep: 21 e, half of it through the root; the
-            reciprocal root 2 steps (4 e), eps and the mean 2 e, two products 2 e: under 2^-19.5 of y
-  angle     2^-32 turns cut off (2^-29.3), half an fp32 step at up to half a turn (pi 2^-25 = 2^-23.3), sine and cosine 2
-            steps (2^-23 each), the amplitude and the pair's two products and sum 4 e: under 2^-20.5 of |a| + |b|
+            reciprocal root 2 steps (4 e), eps and the mean 2 e, halved too, two products 2 e: 17.5 e, under 2^-19.8 of y
+  angle     2^-32 turns cut off (2^-29.3), half an fp32 step at up to an eighth of a turn (2^-25.3), sine and cosine within
+            1e-7, the amplitude and the pair's two products and sum 4 e: 3.7e-7, under 2^-21.3 of |a| + |b|
   together  under 2^-19 of the size that plain_rope gives, and half a step of the output
   gradients the turned gradient as above, r as above (twice), and the mean of d products, 21 e of their absolute sum:
             under 2^-17.5 of the size, and half a step

@@ -308,3 +308,29 @@ def test_refused():
     mask, depth = exattn.draft_tree(torch.zeros((0, 4), dtype=torch.int32, device=DEV))
     assert mask.shape == (0, 4, 1) and depth.shape == (0, 4)
     assert exattn.check_device_error() == 0
+
+
+def test_two_graphs_side_by_side():
+    """Two captured steps, a workspace each, replayed on two streams at the same time."""
+    sets = []
+    for seed, (group, n) in ((60, (1, 18)), (61, (3, 40))):
+        lens = [700 + n, n, 90]
+        cache, host, table = make_cache(3, 2, 16, 64, -(-max(lens) // 16), "int8", seed=seed)
+        sees = plain_tree(random_parents(3, n, seed))[0]
+        q, at, tree = _q(3, 2 * group, n, 64, "fp16").to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV), words(sees).to(DEV)
+        ws = torch.zeros(exattn.cache_workspace_size(cache, 2 * group, n), dtype=torch.uint8, device=DEV)
+        exattn.forward_cache_tree(q, cache, at, tree, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = exattn.forward_cache_tree(q, cache, at, tree, workspace=ws)
+        sets.append((graph, got, (q.cpu(), cache, host, table, lens, sees), (q, at, tree, ws)))  # what a graph reads is kept
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(20):
+        for s, (graph, _, _, _) in zip(streams, sets):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, got, args, _ in sets:
+        check(*args, got=got)
+    assert exattn.check_device_error() == 0
