@@ -284,6 +284,39 @@ PyObject* rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// k, v, k_scale, v_scale, page_table: the attn_cache of checked tensors, as bytes
+PyObject* cache_struct(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 5);
+    const at::Tensor &k = tensor(a[0]), &v = tensor(a[1]), &ks = tensor(a[2]), &vs = tensor(a[3]), &table = tensor(a[4]);
+    const at::ScalarType t = k.scalar_type();
+    if ((t != at::kFloat8_e4m3fn && t != at::kChar) || v.scalar_type() != t)
+      throw BadType{std::string("unsupported cache dtypes ") + c10::toString(t) + ", " + c10::toString(v.scalar_type()) +
+                    "; expected float8_e4m3fn or int8 for both"};
+    if (ks.scalar_type() != at::kFloat || vs.scalar_type() != at::kFloat || table.scalar_type() != at::kInt)
+      throw BadType{"scales must be float32 and the page table int32"};
+    require(k.dim() == 4 && k.sizes() == v.sizes() && table.dim() == 2, "k, v must be [num_pages, heads, page, d] and the page table [B, width]");
+    require(ks.dim() == 2 && ks.size(0) == k.size(0) && ks.size(1) == k.size(1) && ks.sizes() == vs.sizes(), "scales must be [num_pages, heads]");
+    for (const at::Tensor* x : {&k, &v, &ks, &vs, &table})
+      require(x->is_cuda() && x->get_device() == k.get_device() && x->is_contiguous(), "cache tensors must be contiguous and on one CUDA device");
+    for (int i = 0; i < 4; ++i) require(k.size(i) <= INT32_MAX, "tensors are too large");
+    require(table.size(0) <= INT32_MAX && table.size(1) <= INT32_MAX, "tensors are too large");
+    attn_cache c = {};
+    c.k = k.data_ptr();
+    c.v = v.data_ptr();
+    c.k_scale = static_cast<float*>(ks.data_ptr());
+    c.v_scale = static_cast<float*>(vs.data_ptr());
+    c.page_table = static_cast<const int*>(table.data_ptr());
+    c.num_pages = static_cast<int>(k.size(0));
+    c.heads = static_cast<int>(k.size(1));
+    c.page_size = static_cast<int>(k.size(2));
+    c.d = static_cast<int>(k.size(3));
+    c.table_width = static_cast<int>(table.size(1));
+    c.format = t == at::kChar ? ATTN_CACHE_INT8 : ATTN_CACHE_E4M3;
+    return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&c), sizeof(c));
+  });
+}
+
 // A QuantCache: the address of its attn_cache, its device and its sequences.
 struct Cache {
   const attn_cache* c;
@@ -426,6 +459,7 @@ PyMethodDef methods[] = {method<rope_forward>("rope_forward"),
                          method<cache_append>("cache_append"),
                          method<forward_cache_tree>("forward_cache_tree"),
                          method<draft_tree>("draft_tree"),
+                         method<cache_struct>("cache_struct"),
                          {"set_error_class", set_error_class, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef definition = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -541,7 +541,6 @@ def attention_kl(q1, k1, q2, k2, causal=False, scale: float | None = None, train
 # ------------------------------------------------------------------ 8-bit key/value cache
 
 CACHE_FORMATS = {"e4m3": 0, "int8": 1}
-_CACHE_DTYPES = {torch.float8_e4m3fn: 0, torch.int8: 1}
 
 
 class QuantCache:
@@ -554,27 +553,12 @@ class QuantCache:
                  "address")
 
     def __init__(self, k, v, k_scale, v_scale, page_table):
-        fmt = _CACHE_DTYPES.get(k.dtype)
-        if fmt is None or v.dtype != k.dtype:
-            raise TypeError(f"unsupported cache dtypes {k.dtype}, {v.dtype}; expected float8_e4m3fn or int8 for both")
-        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or page_table.dtype != torch.int32:
-            raise TypeError("scales must be float32 and the page table int32")
-        shape, rows = k.shape, page_table.shape
-        if len(shape) != 4 or v.shape != shape or len(rows) != 2:
-            raise ValueError("k, v must be [num_pages, heads, page, d] and the page table [B, width]")
-        pages, heads, page, d = shape
-        if k_scale.shape != (pages, heads) or v_scale.shape != (pages, heads):
-            raise ValueError("scales must be [num_pages, heads]")
-        index = k.get_device()
-        for t in (k, v, k_scale, v_scale, page_table):
-            if not t.is_cuda or t.get_device() != index or not t.is_contiguous():
-                raise ValueError("cache tensors must be contiguous and on one CUDA device")
-        self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
-        self.device, self.index, self.B, self.heads, self.d = k.device, index, rows[0], heads, d
-        self.struct = CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                  page_table.data_ptr(), pages, heads, page, d, rows[1], fmt)
+        self.struct = CacheStruct.from_buffer_copy(binding().cache_struct(k, v, k_scale, v_scale, page_table))
         self._ref = ctypes.byref(self.struct)
         self.address = ctypes.addressof(self.struct)
+        self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
+        self.device, self.index, self.B = k.device, k.get_device(), page_table.shape[0]
+        self.heads, self.d = self.struct.heads, self.struct.d
 
     @classmethod
     def empty(cls, num_pages: int, heads: int, page: int, d: int, page_table, format: str = "e4m3"):
