@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
     // one are loaded while the scales of the round before are, and the codes of the one before that copied.
     const int pw = (warp - W) & 1;
     typename C::Walk walk(a, *reinterpret_cast<typename C::Walk::Shared*>(wmem + C::W_SCHED), pw * 32 + lane, 1 + worker,
-                          blockIdx.x * kWorkers + worker, gridDim.x * kWorkers);
+                          blockIdx.x * kWorkers + worker, gridDim.x * kWorkers, worker * gridDim.x + blockIdx.x);
     const int psh = a.c.page_shift;
     const bool feeds = lane < 2 * NH;
     const int gw = feeds ? 2 * pw + lane / NH : 0;  // the computing warp in its worker

@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tile_kernel(const __grid_co
       // In rounds of four tiles: lane 8 q + g looks after 16-token group g of the round's tile q.  Page numbers,
       // scales and copies of a tile hang on one another, so rounds run through three stages, one behind the other.
       typename C::Walk walk(a, *reinterpret_cast<typename C::Walk::Shared*>(smem_raw + C::OFF_SCHED), lane, 0, blockIdx.x,
-                            gridDim.x);
+                            gridDim.x, blockIdx.x);
       const int psh = a.c.page_shift, box = min(1 << psh, kTK);
       const int group = lane & 7;
       const bool leads = ((16 * group) & (box - 1)) == 0;
