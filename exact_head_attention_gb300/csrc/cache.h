@@ -127,7 +127,7 @@ struct DraftTreeArgs {
 };
 cudaError_t launch_draft_tree(const DraftTreeArgs& a, int B, cudaStream_t stream);
 // Up to this many query rows a key/value head attn_fwd_cache streams the codes through the warp-level products
-// (cache_attn.cu), above it through the tensor-memory ones (cache_tile.cu).  The first keep Q and O in registers: with
+// (cache_attn.cuh), above it through the tensor-memory ones (cache_tile.cuh).  The first keep Q and O in registers: with
 // 32 rows those run out, with 24 the codes still set the pace.  Measured, warp-level against tensor-memory:
 //   8 sequences of 32k tokens, 12 heads of 128   17 rows 158 : 242 us   24 rows 160 : 243 us   32 rows 272 : 243 us
 //   the same, 24 heads of 64                     17 rows 197 : 221 us   24 rows 197 : 221 us   32 rows 277 : 221 us

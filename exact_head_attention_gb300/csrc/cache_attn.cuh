@@ -25,7 +25,7 @@
 // in 102 us (79 %; the uneven end of the blocks' shares, and a copy for each 16 tokens).  From 162 us for the first:
 // four producer warps instead of one, 142 (one took 190 cycles for each 4 KB box, and they arrive every 175); 32-bit
 // arithmetic and one pass in the division of the work, 130; the query rows copied ahead with each piece, 128; two
-// workers, 124.  A call over one short sequence takes 6.5 us, 20 rows instead of 8 add 3 us and a division of the keys
+// workers, 124.  A call over one short sequence takes 6.2 us, 20 rows instead of 8 add 3 us and a division of the keys
 // 6 us: code that runs once a piece comes from far, and is kept short.
 //
 // Products.  The tensor cores are far from busy here, so the work goes through the warp-level m16n8k16

@@ -1,5 +1,5 @@
 // Attention over the 8-bit cache for many query rows a key/value head (chunks of a prompt, drafted tokens
-// under shared heads): the tensor-core form of cache_attn.cu.
+// under shared heads): the tensor-core form of cache_attn.cuh.
 //
 // Mathematics as there: codes as they are in fp16, the key scale on the scores, the value scale on the probabilities, over
 // a reference w for each row (cache8.cuh).
@@ -63,7 +63,7 @@ constexpr int kPieceRing = 3;
 // most 256 tokens less or more; under a tree 5, of kTreeMost tokens), and the converters are at most NS tiles further.
 constexpr int kFlagRing = 8;
 static_assert((kTreeMost + 126) / kTK + 1 <= 5, "tiles that a tree's tokens reach into");
-constexpr float kShift = 3.f;  // as in cache_attn.cu
+constexpr float kShift = 3.f;  // as in cache_attn.cuh
 constexpr int kMeta = 24;      // numbers a tile: ks[8], vs[8], log2 vs[8]
 
 template <int D, bool PAIR, bool TREE>
@@ -319,7 +319,7 @@ __device__ __forceinline__ float stage_query_rows(RowAt&& row_at, uint32_t tile,
         mx = max(mx & 0xffffu, mx >> 16);
 #pragma unroll
         for (int o = 1; o < UNITS; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        // As in cache_attn.cu: the largest value comes to lie in [2^14, 2^15).
+        // As in cache_attn.cuh: the largest value comes to lie in [2^14, 2^15).
         const int e = static_cast<int>(mx >> 7) - 127;
         const int p = mx != 0u && e < 128 ? min(14 - e, 113) : 0;
         const float mul = __int_as_float((127 + p) << 23);

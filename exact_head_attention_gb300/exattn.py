@@ -855,7 +855,10 @@ class _RopeFunction(torch.autograd.Function):
 
 def rope(q, k, freq, start=None, offsets=None, layout="half", amplitude: float = 1.0, q_weight=None, k_weight=None,
          eps: float = 1e-6):
-    """Autograd-aware rope_forward: (q, k); gradients flow to q, k and the weights."""
+    """Autograd-aware rope_forward: (q, k); gradients flow to q, k and the weights.
+
+    A step with its backward can be captured into a CUDA graph as long as no autograd graph of the same leaves that was
+    recorded outside the capture is still alive (torch would join the two streams)."""
     return _RopeFunction.apply(q, k, q_weight, k_weight, freq, start, offsets, layout, amplitude, eps)
 
 
