@@ -35,7 +35,7 @@ namespace exattn {
 // and a captured call, whose tag is the same at each replay, finds zeros.
 
 // Workspace: counts, then the slots (R rows of D values in fp32, normalised by the piece's own sum, in an order
-// that each kernel chooses) and their base-2 log-sum-exps.  Counts and log-sum-exps are kept twice, for the two warpgroups of cache_tile.cu.
+// that each kernel chooses) and their base-2 log-sum-exps.  Counts and log-sum-exps are kept twice, for the two warpgroups of cache_tile.cuh.
 struct CacheWs {
   unsigned long long* count;  // [slots][2]
   float* o;                   // [slots][R * D]
