@@ -173,3 +173,17 @@ def test_draft_tree_rules(lib, args, code):
 
 def test_tree_status(lib):
     assert exattn.STATUS_NAMES[9] == "ATTN_ERR_TREE" and "parent" in exattn.status_string(9)
+
+
+def test_binding_refuses_what_it_cannot_pass_on(lib):
+    """On the CPU, before any device is touched."""
+    q = torch.zeros((1, 2, 3, 64), dtype=torch.bfloat16)
+    freq = exattn.rope_frequencies(64, device="cpu")[0]
+    for call in (lambda: exattn.rope_forward(q, q, freq), lambda: exattn.rope_forward(None, None, freq), lambda: exattn.rope_forward(q, q, freq, layout="x"),
+                 lambda: exattn.rope_backward(q, None, None, None, freq), lambda: exattn.draft_tree(torch.zeros((1, 3), dtype=torch.int32)),
+                 lambda: exattn.rope_forward(q, None, freq, out=(None, None))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: exattn.rope_forward(3, q, freq), lambda: exattn.draft_tree(None), lambda: exattn.rope_forward(q, q, freq, amplitude="x")):
+        with pytest.raises((TypeError, ValueError)):
+            call()
