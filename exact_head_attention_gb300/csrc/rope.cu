@@ -310,9 +310,14 @@ cudaError_t bwd_d(RopeArgs& a, cudaStream_t stream) {
 }  // namespace
 
 RopeGrid rope_plan(RopeArgs& a) {
-  // Heads a thread: what it does before the first takes about as long as four of them, and a last wave of few blocks as long
-  // as a full one.  12 heads of 128 each, 32768 tokens: 100 us with 2, 70.9 with 4, 62.7 with 6, 62.9 with 12; 28 and 4 heads
-  // of 64, 4611 tokens: 9.0, 7.3, 6.2 (the one with a single wave) and 9.6 us.
+  // Heads a thread.  What it does before the first takes about as long as four of them; all threads' work over the blocks that
+  // are resident at once, and about half a thread's for the blocks that end last.  us with 1, 2, 3, 4, 6, 8 and 12:
+  //   12 and 12 heads of 128, 32768 tokens   153  96  78  70  63  65  64
+  //   14 and 2 heads of 64, 20072 tokens     30.0 19.8 17.5 16.3 15.5 14.8 14.5
+  //   28 and 4 heads of 64, 4611 tokens      14.8 9.4 8.4 7.4 6.7 7.9 9.2
+  //   16 and 16 heads of 128, 2048 tokens    15.2 10.7 9.5 8.8 7.5 8.6 10.7
+  //   42 and 6 heads of 128, 114 tokens      3.3 2.9 3.2 3.4 3.8 4.3 5.2
+  // It takes 12, 8, 6, 4 and 2 of them: 63.6, 14.7, 6.7, 8.7 and 3.0 us.
   const int hq = a.side[0].heads, hk = a.side[1].heads, most = hq > hk ? hq : hk, groups = kRopeThreads / (a.d / 16);
   a.token_shift = token_shift(a.tokens, groups);
   const int per = groups >> a.token_shift;  // chunks a block
@@ -322,7 +327,7 @@ RopeGrid rope_plan(RopeArgs& a) {
   for (int s : {1, 2, 3, 4, 6, 8, 12}) {
     if (s > 1 && s > most) break;
     const long long chunks = (hq + s - 1) / s + (hk + s - 1) / s, cb = (chunks + per - 1) / per;
-    const long long cost = ((token_blocks * cb + slots - 1) / slots) * (4 + s);
+    const long long cost = 1600 * token_blocks * (4 * chunks + hq + hk) / per / slots + 900 * (4 + s);
     if (best == 0 || cost < best) {
       best = cost;
       chunk_blocks = cb;

@@ -293,8 +293,9 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, RopeShared& sh, uns
   const bool any_norm = a.side[0].weight != nullptr || a.side[1].weight != nullptr;
   const RopeFactors<D, BF16> f(l, sh.table, p, a.r.back, sd.weight, a.weight_fp32);
   int from = 0;
+  const int rows = __reduce_max_sync(0xffffffffu, max(here, 0));  // of the warp
 #pragma unroll 1
-  for (int i = 0; i < a.span; ++i) {
+  for (int i = 0; i < rows; ++i) {
     issue();
     copies_wait<DEPTH - 1>();
     float x[16];
