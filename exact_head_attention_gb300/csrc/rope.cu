@@ -317,7 +317,7 @@ RopeGrid rope_plan(RopeArgs& a) {
   //   28 and 4 heads of 64, 4611 tokens      14.8 9.4 8.4 7.4 6.7 7.9 9.2
   //   16 and 16 heads of 128, 2048 tokens    15.2 10.7 9.5 8.8 7.5 8.6 10.7
   //   42 and 6 heads of 128, 114 tokens      3.3 2.9 3.2 3.4 3.8 4.3 5.2
-  // It takes 12, 8, 6, 4 and 2 of them: 63.6, 14.7, 6.7, 8.7 and 3.0 us.
+  // It takes 12, 8, 6, 8 and 2 of them.
   const int hq = a.side[0].heads, hk = a.side[1].heads, most = hq > hk ? hq : hk, groups = kRopeThreads / (a.d / 16);
   a.token_shift = token_shift(a.tokens, groups);
   const int per = groups >> a.token_shift;  // chunks a block
@@ -327,7 +327,7 @@ RopeGrid rope_plan(RopeArgs& a) {
   for (int s : {1, 2, 3, 4, 6, 8, 12}) {
     if (s > 1 && s > most) break;
     const long long chunks = (hq + s - 1) / s + (hk + s - 1) / s, cb = (chunks + per - 1) / per;
-    const long long cost = 1600 * token_blocks * (4 * chunks + hq + hk) / per / slots + 900 * (4 + s);
+    const long long cost = 200 * token_blocks * (4 * chunks + hq + hk) / per / slots + 100 * (4 + s);
     if (best == 0 || cost < best) {
       best = cost;
       chunk_blocks = cb;
