@@ -17,7 +17,9 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/variable.h>
 
 #include "../../include/exattn.h"
 
@@ -441,6 +443,22 @@ PyObject* draft_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Any number of tensors, or None: whether one is a leaf whose gradient a living autograd graph adds up on another stream than
+// the current one.  (Torch keeps a leaf's node of that, and its stream, for as long as a graph of it lives.)
+PyObject* leaf_elsewhere(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      const at::Tensor* t = tensor_or_none(a[i]);
+      if (!t || !t->is_cuda() || !t->requires_grad()) continue;
+      const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
+      if (!node) continue;
+      const auto stream = node->stream();
+      if (stream && *stream != c10::cuda::getCurrentCUDAStream(t->get_device()).unwrap()) Py_RETURN_TRUE;
+    }
+    Py_RETURN_FALSE;
+  });
+}
+
 // The class that library failures are raised as.
 PyObject* set_error_class(PyObject*, PyObject* cls) {
   Py_INCREF(cls);
@@ -460,6 +478,7 @@ PyMethodDef methods[] = {method<rope_forward>("rope_forward"),
                          method<forward_cache_tree>("forward_cache_tree"),
                          method<draft_tree>("draft_tree"),
                          method<cache_struct>("cache_struct"),
+                         method<leaf_elsewhere>("leaf_elsewhere"),
                          {"set_error_class", set_error_class, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef definition = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

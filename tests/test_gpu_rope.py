@@ -409,3 +409,30 @@ def test_captured_training_step():
             assert torch.equal(a, b)
         for t in got:
             t.fill_(math.nan)
+
+
+@pytest.mark.parametrize("which", [0, 1, 2, 3])
+def test_capture_beside_a_living_graph_is_refused(which):
+    """A leaf whose gradients an autograd graph recorded outside the capture adds up; once that graph is gone the call is taken."""
+    q, k, wq, wk, freq, start, _ = make(1, 2, 2, 16, 64, 64, "bf16", True, True, seed=24)
+    gf, gs = _gpu(freq, start)
+    leaves = [t.to(DEV).requires_grad_(i == which) for i, t in enumerate((q, k, wq, wk))]
+
+    def turned():
+        return exattn.rope(leaves[0], leaves[1], gf, gs, q_weight=leaves[2], k_weight=leaves[3])
+
+    living = turned()
+    want = [t.detach().clone() for t in living]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="outside"):
+        with torch.cuda.graph(graph):
+            leaves[0].detach().clone()
+            turned()
+    del living
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [t.detach() for t in turned()]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
