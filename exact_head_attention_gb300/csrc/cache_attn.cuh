@@ -145,6 +145,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
   using C = Cfg<D, NT>;
   constexpr int NST = C::STAGES, NH = C::NH, RQ = C::RINGQ;
   constexpr int KS = D / 16, MT = D / 16;  // k-steps of S^T; 16-row tiles of O^T
+  // Where O is as fine as P, P's rounding would be as large an error as O's own: a page's scale takes part in it, so where few
+  // keys count it does not average out (1.4 to 1.8 times the error of rounding O alone).  What the rounding takes off then goes
+  // into a second product.  8 rows, 16 sequences of 4032 tokens, 8 heads of 128: 33.5 us, 32.8 without; 24 rows 56.5, 50.5;
+  // 16 rows over 32k of 8 sequences, 12 heads, 152.9, 134 (no less with the product left out where probabilities are small: its
+  // operands are what costs).  bf16 is without.
+  constexpr bool FINE = TREE && !BF16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t sbase = smem_u32(smem_raw);
   if (!smem_base_aligned(sbase, a.err_word)) return;
@@ -486,6 +492,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
             }
           }
       uint32_t pb[NT][2 * NH];  // P^T operand of each 8-key block
+      uint32_t pr[FINE ? NT : 1][2 * NH];
+      auto operand = [&](int nt, int nb, float y0, float y1) __attribute__((always_inline)) {
+        const uint32_t y = pack2<false>(y0, y1);
+        pb[nt][nb] = transpose8(y);
+        if constexpr (FINE)  // y is below 2^15, or a NaN
+          pr[nt][nb] = transpose8(pack2<false>(y0 - unpack_lo<false>(y), y1 - unpack_hi<false>(y)));
+      };
       if (!uneven) {
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -524,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
               y0 = x0 == -INFINITY ? 0.f : y0;
               y1 = x1 == -INFINITY ? 0.f : y1;
             }
-            pb[nt][nb] = transpose8(pack2<false>(y0, y1));
+            operand(nt, nb, y0, y1);
           }
           f2_unpack(l2, l[nt][0], l[nt][1]);
         }
@@ -575,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
             l[nt][0] += p0;
             l[nt][1] += p1;
             const float y0 = p0 * value_weight(sc[nb >> 1].y, vf[0]), y1 = p1 * value_weight(sc[nb >> 1].y, vf[1]);
-            pb[nt][nb] = transpose8(pack2<false>(x0 == -INFINITY ? 0.f : y0, x1 == -INFINITY ? 0.f : y1));
+            operand(nt, nb, x0 == -INFINITY ? 0.f : y0, x1 == -INFINITY ? 0.f : y1);
           }
         }
         __syncwarp();
@@ -655,8 +668,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_kernel(const __grid_co
 #pragma unroll
           for (int h = 0; h < 2; ++h)  // tile rows g and g + 8: d positions 2 j and 2 j + 1 of the piece
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
               mma16816(o[nt][2 * w + h], x[2 * h], x[2 * h + 1], y[2 * h], y[2 * h + 1], pb[nt][2 * half], pb[nt][2 * half + 1]);
+              if constexpr (FINE)
+                mma16816(o[nt][2 * w + h], x[2 * h], x[2 * h + 1], y[2 * h], y[2 * h + 1], pr[nt][2 * half], pr[nt][2 * half + 1]);
+            }
         }
       }
       __syncwarp();  // every lane has read the tile
