@@ -3,7 +3,6 @@
 //
 // Mathematics: the keys of rope.cu in fp32, unrounded, then the rule of the cache's write (cache_io.cuh): the largest value
 // of a page's new tokens gives its scale, and with that the codes.  So no rotated key is rounded twice or goes through memory.
-// A row's 1 / rms stays apart until its codes are made, which take it and the scale's reciprocal as one factor.
 //
 // Bound: memory, 2 bytes read and 1 written a value, 2 and 2 of the queries; but with 15 operations a value the instructions
 // are close behind, and most of what is below is about them.  As in cache_io.cu one page of one head, keys or values, is held
@@ -85,6 +84,14 @@ struct PairedRow {
     float a, b;
     f2_unpack(f2_add(s, t), a, b);
     return a + b;
+  }
+  __device__ __forceinline__ void times(float f) {
+    const uint64_t f2 = f2_pack(f, f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      p[k] = f2_mul(p[k], f2);
+      q[k] = f2_mul(q[k], f2);
+    }
   }
   __device__ __forceinline__ void times(const ulonglong2 (&w)[4]) {
 #pragma unroll
@@ -259,20 +266,19 @@ __global__ void __launch_bounds__(kIoThreads, NV == 4 ? kAppendBlocks : 2) cache
     for (int i = 0; i < NV; ++i) loaded(raw[i]);  // the places are free once the values are here
     load(head + side < heads);
     PairedRow<INTER> x[ROWS];
-    float r[ROWS], most = 0.f;
+    float most = 0.f;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       float v[16];
       Lane::template widen<BF16>(raw[2 * i], raw[2 * i + 1], v);
       x[i].set(v);
-      r[i] = 1.f;
     }
     if (weight) {
       const ulonglong2* w = reinterpret_cast<const ulonglong2*>(weights[0] + 8 * u);
       const ulonglong2 ws[4] = {w[0], w[1], w[SLOTS / 4], w[SLOTS / 4 + 1]};
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
-        r[i] = rsqrtf(Lane::row_sum(x[i].squares()) * (1.f / D) + rv.eps);
+        x[i].times(rsqrtf(Lane::row_sum(x[i].squares()) * (1.f / D) + rv.eps));
         x[i].times(ws);
       }
     }
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(kIoThreads, NV == 4 ? kAppendBlocks : 2) cache
       }
     }
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) most = max3_nan(most, most, x[i].largest() * r[i]);
+    for (int i = 0; i < ROWS; ++i) most = max3_nan(most, most, x[i].largest());
     uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(most) & 0x7fffffffu);  // a NaN or an infinity above all others
     if constexpr (GT > 32) {
       if ((threadIdx.x & 31) == 0) s_max[turn][threadIdx.x >> 5] = mx;
@@ -314,13 +320,7 @@ __global__ void __launch_bounds__(kIoThreads, NV == 4 ? kAppendBlocks : 2) cache
     for (int i = 0; i < ROWS; ++i) {
       uint2* to = reinterpret_cast<uint2*>(codes + i * STEP * D);
       if (there[i]) {
-        const float f = r[i] * sc.inv;
-        const uint64_t f2 = f2_pack(f, f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x[i].p[k] = f2_mul(x[i].p[k], f2);
-          x[i].q[k] = f2_mul(x[i].q[k], f2);
-        }
+        x[i].times(sc.inv);
         float v[16];
         x[i].get(v);
         uint2 ca = make_uint2(0u, 0u), cb = ca;

@@ -311,3 +311,32 @@ def test_pool_beyond_32_bits():
             s = scales[0][p].double().cpu()[:, None]
             got = codes[0][p, :, t % page].double().cpu() * s
             assert torch.all((got - y[b, :, n]).abs() <= 0.5 * s * 1.001 + 2.0 ** -18 * size[b, :, n])
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("eps", [1e-6, 1e-12])
+def test_very_small_keys_with_norms(code, layout, d, page, eps):
+    """Keys whose norm eps makes, with zeros among their values, and zero keys behind a page of a tiny scale.  Values below
+    2^-126 are whole multiples of 2^-149 in bf16 as well, so that the norm's product with them is off by its own rounding only."""
+    sizes = [1e-36, 1e-37, 3e-38, 1e-39]
+    B = len(sizes) + 1
+    cache, host, table = make_cache(B, 2, page, d, 2, code, seed=40)
+    g = torch.Generator().manual_seed(41)
+    k = torch.randn((B, 2, 3, d), generator=g) * torch.tensor([*sizes, 0.0])[:, None, None, None]
+    k[:, :, :, ::7] = 0
+    k = k.to(torch.bfloat16)
+    w = 1 + 0.3 * torch.randn(d, generator=g)
+    freq, starts = exattn.rope_frequencies(16, device="cpu")[0], [0] * len(sizes) + [5]
+    cache.k_scale[int(table[-1, 0])] = 1e-37
+    before = {"k": cache.k.cpu(), "k_scale": cache.k_scale.cpu()}
+    exattn.cache_append(cache, *_on(k, k, freq, _i32(starts)), layout=layout, k_weight=w.to(DEV), eps=eps)
+    assert exattn.check_device_error() == 0
+    y, size = plain_rope.norm_rotate(k, freq, plain_rope.positions(B, 3, _i32(starts)), layout, weight=w, eps=eps)
+    y[(y.abs().amax((2, 3)) / LARGEST[code] < 2.0 ** -126) & (torch.arange(B) < B - 1)[:, None]] = 0  # a scale that is held as zero
+    check_keys(cache, before, table, y, size, starts, [3] * B, code)
+    codes = cache.k.view(torch.uint8)[table[:, 0].long().to(DEV)].cpu()
+    assert torch.all(codes[-1, :, 5:8] & 0x7F == 0)  # of either sign
+    lone = [i for i in range(16, d) if i % 7 == 0]  # behind the rotated part
+    assert torch.all(codes[:-1, :, :3][..., lone] & 0x7F == 0)
