@@ -355,3 +355,26 @@ def test_two_graphs_side_by_side():
     for _, got, args, _ in sets:
         check(*args, got=got)
     assert exattn.check_device_error() == 0
+
+
+@pytest.mark.parametrize("B,heads", [(39, 4), (51, 3)])
+def test_a_few_items_more_than_blocks_are_divided(B, heads):
+    """One to four items more than blocks, all of one length: kept whole, the blocks with two would take twice as long as the
+    others.  A sequence less keeps an item a block, in 1.02 of which the work would go; half as much again is allowed."""
+    blocks = torch.cuda.get_device_properties(0).multi_processor_count
+    if not blocks < B * heads <= blocks + 4 or (B - 1) * heads > blocks:
+        pytest.skip("sized for 152 blocks")
+    d, n, lens = 64, 64, 8192
+    took = []
+    for b in (B, B - 1):
+        cache = exattn.QuantCache.empty(b * lens // 64, heads, 64, d, torch.arange(b * lens // 64, dtype=torch.int32, device=DEV).view(b, -1))
+        q, at = torch.zeros((b, heads, n, d), dtype=torch.bfloat16, device=DEV), torch.full((b,), lens, dtype=torch.int32, device=DEV)
+        tree, _ = exattn.draft_tree(torch.arange(-1, n - 1, dtype=torch.int32, device=DEV))
+        ws = torch.empty(exattn.cache_workspace_size(cache, heads, n), dtype=torch.uint8, device=DEV)
+        events = [torch.cuda.Event(enable_timing=True) for _ in range(12)]
+        for e in events:
+            exattn.forward_cache_tree(q, cache, at, tree, workspace=ws)
+            e.record()
+        torch.cuda.synchronize()
+        took.append(min(x.elapsed_time(y) for x, y in zip(events[2:], events[3:])))
+    assert took[0] <= 1.5 * took[1], took
