@@ -378,3 +378,26 @@ def test_a_few_items_more_than_blocks_are_divided(B, heads):
         torch.cuda.synchronize()
         took.append(min(x.elapsed_time(y) for x, y in zip(events[2:], events[3:])))
     assert took[0] <= 1.5 * took[1], took
+
+
+@pytest.mark.parametrize("group,n", [(1, 25), (2, 32), (1, 100), (4, 32), (1, 129), (4, 64), (1, 512)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_many_rows_are_about_as_exact_as_their_output(group, n, d, code, wide):
+    """fp16 where many keys count alike.  Probabilities of fp16 are off by errors of their own, uniform within half a step, and so
+    are outputs; relative to a number of mantissa m in [1, 2) that is e / m, in the mean of squares 0.54 e^2 over evenly spread
+    logarithms and e^2 at most.  Values of no common sign make O^2 the sum of p^2 v^2, so that the probabilities' errors add up
+    to e^2 O^2 at most beside the rounding's 0.54: sqrt(1 + 1 / 0.54) = 1.69 times the rounding alone; the scores' 2^-15 as above."""
+    lens = [40 + n, n, 700 + n, 100 + n // 2]
+    _, host, table = make_cache(len(lens), 3, 16, d, -(-max(lens) // 16), code, seed=52)
+    if wide:
+        host["v_scale"][::3] *= 64
+    cache = exattn.QuantCache(*(host[x].to(DEV) for x in ("k", "v", "k_scale", "v_scale")), table.to(DEV))
+    q, (sees, _) = _q(len(lens), 3 * group, n, d, "fp16"), plain_tree(random_parents(len(lens), n, 53))
+    scale = 1 / math.sqrt(d)
+    o, _ = exattn.forward_cache_tree(q.to(DEV), cache, torch.tensor(lens, dtype=torch.int32, device=DEV), words(sees).to(DEV), scale)
+    assert exattn.check_device_error() == 0
+    want = plain_attention(q, host, table, lens, sees, scale)[0]
+    off, own = (torch.linalg.norm(x.double().cpu() - want) / torch.linalg.norm(want) for x in (o, want.half()))
+    assert off <= 1.69 * own + 2.0 ** -15, (off, own)
