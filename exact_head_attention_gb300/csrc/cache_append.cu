@@ -205,9 +205,9 @@ __global__ void __launch_bounds__(kIoThreads, NV == 4 ? kAppendBlocks : 2) cache
         const int h = slot / (SLOTS / 2), lane = slot / 4 % Lane::LANES;
         const int pair = (INTER ? 4 * (lane + h * Lane::LANES) : 8 * lane + 4 * h) + (slot & 3);
         if (pair >= rv.rot >> 1) continue;
-        bool finite;
-        const uint64_t turns = turns_of(rv.freq[pair], finite);
-        const float amplitude = finite ? rv.amplitude : __int_as_float(0x7fffffff);
+        bool good;
+        const uint64_t turns = turns_of(rv.freq[pair], good);
+        const float amplitude = good ? rv.amplitude : __int_as_float(0x7fffffff);
         const int first_row = r0 + (threads < SLOTS ? 0 : at / SLOTS);
         auto direct = [&](uint64_t angle, float& co, float& si) { sin_cos_turns(static_cast<uint32_t>(angle >> 32), si, co); };
         auto put = [&](int row, float co, float si) {

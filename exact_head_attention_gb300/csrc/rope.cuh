@@ -9,8 +9,8 @@
 // f / 2 pi is held as a fraction of a turn in 64 bits, whose product with p wraps round by itself, and the upper 32 bits of
 // it are the angle in units of 2^-32 turns: the quadrant in two bits, and the rest of it within an eighth of a turn of its
 // middle, where short polynomials do.  So no position is too far, and no 64-bit floating-point product (a sixty-fourth of
-// the rate here), no reduction and no table of positions is needed.  Error of an angle: p 2^-64 turns of the frequency,
-// 2^-32 of the cut, and half a step of fp32 at up to an eighth of a turn.
+// the rate here), no reduction and no table of positions is needed.  Error of an angle: 2 p 2^-64 turns of the frequency,
+// whatever its size, 2^-32 of the cut, and half a step of fp32 at up to an eighth of a turn.
 #pragma once
 
 #include <cstdint>
@@ -22,16 +22,23 @@ namespace exattn {
 
 constexpr int kRopeThreads = 256;
 
-// f / 2 pi in units of 2^-64 turns, modulo one turn.  f = m 2^(e - 52) with an m of 53 bits, so that f 2^64 / 2 pi is
-// (m 2^11) (2^66 / 2 pi) 2^-64 shifted by e - 1; 2^66 / 2 pi has 64 bits.
-__device__ __forceinline__ uint64_t turns_of(double f, bool& finite) {
+// f / 2 pi in units of 2^-64 turns, modulo one turn, within two of them.  f = m 2^(e - 52) with an m of 53 bits, so that f 2^64 / 2 pi
+// is (m 2^11) (2^66 / 2 pi) 2^-64 shifted by e - 1; 2^66 / 2 pi has 64 bits and a fraction.  Up to f = 4 the upper half of one
+// product has all bits of the result.  Above, 2^66 / 2 pi shifted by e - 1 has whole turns in front, of which the product's
+// lower 64 bits count, and the bits behind them come out of its fraction.  `good`: f is finite and below 2^63.
+__device__ __forceinline__ uint64_t turns_of(double f, bool& good) {
   const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
   const int e = static_cast<int>((bits >> 52) & 0x7ff);
-  finite = e != 0x7ff;
+  good = e < 1023 + 63;
   const uint64_t m = e == 0 ? 0ull : (bits & 0xfffffffffffffull) | 0x10000000000000ull;  // below 2^-1022: zero
-  const uint64_t t = __umul64hi(m << 11, 0xa2f9836e4e44152aull);
   const int left = e - 1023 - 1;
-  const uint64_t u = left >= 0 ? (left < 64 ? t << left : 0ull) : (left > -64 ? t >> -left : 0ull);
+  uint64_t u = 0ull;
+  if (left <= 0) {
+    if (left > -64) u = __umul64hi(m << 11, 0xa2f9836e4e44152aull) >> -left;  // 2^66 / 2 pi, to the nearest
+  } else if (good) {  // left from 1 to 61
+    constexpr uint64_t whole = 0xa2f9836e4e441529ull, fraction = 0xfc2757d1f534ddc0ull;
+    u = (m << 11) * (whole >> (64 - left)) + __umul64hi(m << 11, (whole << left) | (fraction >> (64 - left)));
+  }
   return bits >> 63 ? 0ull - u : u;
 }
 
@@ -54,16 +61,16 @@ __device__ __forceinline__ void sin_cos_turns(uint32_t h, float& sine, float& co
   cosine = __uint_as_float(__float_as_uint(swap ? s : c) ^ ((q + 0x40000000u) & 0x80000000u));
 }
 
-// The pairs' turns a position and their amplitudes (NaN where the frequency is not finite), in shared memory.
+// The pairs' turns a position and their amplitudes (NaN where the frequency is not finite, or 2^63 or more), in shared memory.
 struct RopeTable {
   alignas(16) uint64_t turns[64];
   alignas(16) float amplitude[64];
 
   __device__ __forceinline__ void fill(const RopeView& r, int thread, int threads) {
     for (int i = thread; i < r.rot >> 1; i += threads) {
-      bool finite;
-      turns[i] = turns_of(r.freq[i], finite);
-      amplitude[i] = finite ? r.amplitude : __int_as_float(0x7fffffff);
+      bool good;
+      turns[i] = turns_of(r.freq[i], good);
+      amplitude[i] = good ? r.amplitude : __int_as_float(0x7fffffff);
     }
   }
 };

@@ -645,11 +645,12 @@ size_t attn_fwd_cache_workspace_size(const attn_cache* cache, int B, int H, int 
  * for the pairs i < rotary_dim / 2: (a, b) = (i, i + rotary_dim / 2) in the half
  * layout, (2 i, 2 i + 1) in the interleaved one.  Components from rotary_dim on
  * stay y.  All in fp32, rounded once (squares beyond fp32 are infinite); the
- * angle is reduced to one turn exactly, so that its error does not grow with the
- * position.
+ * angle is reduced to one turn exactly, so that its error grows neither with the
+ * position nor with the frequency.
  *   freq       [rotary_dim / 2] fp64 on the device: radians a position, of any
- *              sign (one that is not finite makes its pairs NaN).  Frequencies
- *              scaled for long contexts are the caller's to choose.
+ *              sign (one that is not finite, or 2^63 or more either way, makes
+ *              its pairs NaN).  Frequencies scaled for long contexts are the
+ *              caller's to choose.
  *   start      [B] int32 on the device, or NULL: 0
  *   offsets    int32 on the device, row n of sequence b at b * offset_stride + n
  *              (offset_stride 0: the same for all sequences), or NULL: n

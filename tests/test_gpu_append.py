@@ -17,6 +17,7 @@ import torch
 import plain_rope
 from exact_head_attention_gb300 import exattn
 from test_gpu_cache import DEV, LARGEST, TYPES, make_cache, plain_write, tokens
+from test_gpu_rope import LARGE
 
 pytestmark = pytest.mark.gpu
 
@@ -340,3 +341,21 @@ def test_very_small_keys_with_norms(code, layout, d, page, eps):
     assert torch.all(codes[-1, :, 5:8] & 0x7F == 0)  # of either sign
     lone = [i for i in range(16, d) if i % 7 == 0]  # behind the rotated part
     assert torch.all(codes[:-1, :, :3][..., lone] & 0x7F == 0)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("given", [False, True])
+def test_large_frequencies_at_far_positions(layout, given):
+    """Rows in order, whose angles are turned on from one another, and positions of their own."""
+    B, N, d = 3, 70, 64
+    cache, host, table = make_cache(B, 2, 64, d, 3, "e4m3", seed=42)
+    g = torch.Generator().manual_seed(43)
+    k = torch.randn((B, 2, N, d), generator=g).to(torch.bfloat16)
+    freq = torch.tensor(LARGE + [0.1] * 16, dtype=torch.float64)
+    begin = _i32([2 ** 31 - 1, -(2 ** 31), 1_000_003])
+    offsets = torch.randint(0, 2 ** 31 - 1, (B, N), generator=g).to(torch.int32) if given else None
+    before, starts = {"k": cache.k.cpu(), "k_scale": cache.k_scale.cpu()}, [0, 60, 3]
+    exattn.cache_append(cache, *_on(k, k, freq, _i32(starts)), offsets=None if offsets is None else offsets.to(DEV), layout=layout, position_start=begin.to(DEV))
+    assert exattn.check_device_error() == 0
+    y, size = plain_rope.norm_rotate(k, freq, plain_rope.positions(B, N, begin, offsets), layout)
+    check_keys(cache, before, table, y, size, starts, [N] * B, "e4m3")

@@ -436,3 +436,23 @@ def test_capture_beside_a_living_graph_is_refused(which):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+LARGE = [1.9999, 2.0, 3.999999, 4.0, 4.0000001, 8.1, 1e4 + 0.1, 1e6 + 0.3, -1e6 - 0.7, 2.0 ** 30 * 1.2346, -(2.0 ** 40) * 1.7, 2.0 ** 52 + 1,
+         2.0 ** 53 * 1.1, 2.0 ** 62 * 1.99, -(2.0 ** 63 - 1024), 2.0 ** 60]
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_large_frequencies_at_far_positions(layout):
+    """A frequency's turns are within two units of 2^-64 whatever its size, so that an angle at the farthest position, 2^32, is off
+    by 2^-31 turns of it: under a hundredth of the angle's other errors.  From 2^63 on a frequency makes its pairs NaN."""
+    q, k, wq, wk, _, _, _ = make(4, 2, 1, 8, 64, 64, "bf16", False, False, seed=25)
+    freq = torch.tensor(LARGE + [0.1] * 16, dtype=torch.float64)
+    start = torch.tensor([2 ** 31 - 1, -(2 ** 31), 1_000_003, -5], dtype=torch.int32)
+    offsets = torch.tensor([0, 1, 2, 2 ** 31 - 1, 2 ** 20, -(2 ** 31), 77, 123_456_789], dtype=torch.int32)
+    check_forward(q, k, wq, wk, freq, start, offsets, layout)
+    check_backward(q, k, wq, wk, freq, start, offsets, layout)
+    freq[16:20] = torch.tensor([2.0 ** 63, -1e300, math.inf, math.nan], dtype=torch.float64)
+    got = exattn.rope_forward(*_gpu(None, k, freq, start, offsets), layout=layout)[1].cpu()
+    bad = [*range(16, 20), *range(48, 52)] if layout == "half" else range(32, 40)
+    assert torch.isnan(got[..., bad]).all() and torch.isfinite(got[..., [i for i in range(64) if i not in bad]]).all()
