@@ -859,8 +859,8 @@ def rope(q, k, freq, start=None, offsets=None, layout="half", amplitude: float =
 
     A step with its backward can be captured into a CUDA graph as long as no autograd graph of the same leaves that was
     recorded outside the capture is still alive: torch would join the two streams, which can end the process.  Where the
-    leaves are this call's own tensors it is refused (RuntimeError)."""
-    if q is not None and q.is_cuda or k is not None and k.is_cuda:
+    leaves are this call's own tensors it is refused (RuntimeError), unless gradients are off: nothing is recorded then."""
+    if torch.is_grad_enabled() and (q is not None and q.is_cuda or k is not None and k.is_cuda):
         if torch.cuda.is_current_stream_capturing() and binding().leaf_elsewhere(q, k, q_weight, k_weight):
             raise RuntimeError("rope is being captured, and an autograd graph of its leaves that was recorded outside lives")
     return _RopeFunction.apply(q, k, q_weight, k_weight, freq, start, offsets, layout, amplitude, eps)

@@ -456,3 +456,21 @@ def test_large_frequencies_at_far_positions(layout):
     got = exattn.rope_forward(*_gpu(None, k, freq, start, offsets), layout=layout)[1].cpu()
     bad = [*range(16, 20), *range(48, 52)] if layout == "half" else range(32, 40)
     assert torch.isnan(got[..., bad]).all() and torch.isfinite(got[..., [i for i in range(64) if i not in bad]]).all()
+
+
+@pytest.mark.parametrize("off", [torch.no_grad, torch.inference_mode])
+def test_capture_without_gradients_beside_a_living_graph(off):
+    """Weights whose last loss is still held: a capture that records nothing joins nothing."""
+    q, k, wq, wk, freq, start, _ = make(1, 2, 2, 16, 64, 64, "bf16", True, True, seed=26)
+    gq, gk, gf, gs, gwq, gwk = _gpu(q, k, freq, start, wq, wk)
+    for w in (gwq, gwk):
+        w.requires_grad_()
+    living = exattn.rope(gq, gk, gf, gs, q_weight=gwq, k_weight=gwk)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with off(), torch.cuda.graph(graph):
+        got = exattn.rope(gq, gk, gf, gs, q_weight=gwq, k_weight=gwk)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(got, living))
+    assert all(torch.isfinite(g).all() for g in torch.autograd.grad(sum(t.float().sum() for t in living), (gwq, gwk)))
