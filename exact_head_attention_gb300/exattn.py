@@ -836,6 +836,29 @@ def _plain_strides(t):
     return t.clone(memory_format=torch.contiguous_format)
 
 
+class _FirstGradients(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("a gradient of these gradients is asked for: their kernels are differentiable once")
+
+
+def _first_gradients(grads, *inputs):
+    """`grads` of a backward pass, from `inputs` by kernels that record nothing.  Where they are recorded (create_graph=True) and
+    depend on what needs gradients itself, a gradient of them raises instead of lacking their terms."""
+    inputs = [t for t in inputs if t is not None and t.requires_grad]
+    if not inputs or not torch.is_grad_enabled():
+        return grads
+    at = [i for i, g in enumerate(grads) if g is not None]
+    out = list(grads)
+    for i, g in zip(at, _FirstGradients.apply(len(at), *(grads[i] for i in at), *inputs)):
+        out[i] = g
+    return tuple(out)
+
+
 class _RopeFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, freq, start, offsets, layout, amplitude, eps):
@@ -848,14 +871,14 @@ class _RopeFunction(torch.autograd.Function):
     def backward(ctx, dq, dk):
         q, k, q_weight, k_weight, freq, start, offsets = ctx.saved_tensors
         layout, amplitude, eps = ctx.rest
-        dq, dk, dqw, dkw = rope_backward(_plain_strides(dq), _plain_strides(dk), q, k, freq, start, offsets, layout, amplitude,
-                                         q_weight, k_weight, eps)
-        return dq, dk, dqw, dkw, None, None, None, None, None, None
+        grads = rope_backward(_plain_strides(dq), _plain_strides(dk), q, k, freq, start, offsets, layout, amplitude, q_weight,
+                              k_weight, eps)
+        return *_first_gradients(grads, dq, dk, q, k, q_weight, k_weight), None, None, None, None, None, None
 
 
 def rope(q, k, freq, start=None, offsets=None, layout="half", amplitude: float = 1.0, q_weight=None, k_weight=None,
          eps: float = 1e-6):
-    """Autograd-aware rope_forward: (q, k); gradients flow to q, k and the weights.
+    """Autograd-aware rope_forward: (q, k); gradients flow to q, k and the weights, once: a gradient of those raises.
 
     A step with its backward can be captured into a CUDA graph as long as no autograd graph of the same leaves that was
     recorded outside the capture is still alive: torch would join the two streams, which can end the process.  Where the

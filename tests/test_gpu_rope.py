@@ -474,3 +474,30 @@ def test_capture_without_gradients_beside_a_living_graph(off):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(got, living))
     assert all(torch.isfinite(g).all() for g in torch.autograd.grad(sum(t.float().sum() for t in living), (gwq, gwk)))
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("squared", [False, True])
+def test_second_gradients_raise(norm, squared):
+    """A penalty on gradients, beside another term that has its own: raised, not left out.  Where the gradients depend on nothing
+    that needs any (no norm, a loss that is linear) there is nothing to leave out."""
+    q, k, wq, wk, freq, start, _ = make(1, 2, 2, 16, 64, 64, "bf16", norm, True, seed=27)
+    gf, gs = _gpu(freq, start)
+    leaves = [t if t is None else t.to(DEV).requires_grad_() for t in (q, k, wq, wk)]
+    wanted = [t for t in leaves if t is not None]
+
+    def loss():
+        out = exattn.rope(leaves[0], leaves[1], gf, gs, q_weight=leaves[2], k_weight=leaves[3])
+        return sum((t.float().square() if squared else t.float()).sum() for t in out)
+
+    first = torch.autograd.grad(loss(), wanted, create_graph=True)
+    for a, b in zip(first, torch.autograd.grad(loss(), wanted)):
+        assert torch.equal(a, b)
+    penalty = sum(g.float().square().sum() for g in first) + wanted[0].float().square().sum()
+    if norm or squared:
+        with pytest.raises(RuntimeError, match="once"):
+            penalty.backward()
+    else:
+        assert not first[0].requires_grad
+        penalty.backward()
+        assert torch.equal(wanted[0].grad, 2 * wanted[0].detach())
