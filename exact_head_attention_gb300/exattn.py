@@ -412,6 +412,29 @@ def check_device_error(stream=None) -> int:
     return int(load().attn_check_device_error(_stream(stream)))
 
 
+class _FirstGradients(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("a gradient of these gradients is asked for: their kernels are differentiable once")
+
+
+def _first_gradients(grads, *inputs):
+    """`grads` of a backward pass, from `inputs` by kernels that record nothing.  Where they are recorded (create_graph=True) and
+    depend on what needs gradients itself, a gradient of them raises instead of lacking their terms."""
+    inputs = [t for t in inputs if t is not None and t.requires_grad]
+    if not inputs or not torch.is_grad_enabled():
+        return grads
+    at = [i for i, g in enumerate(grads) if g is not None]
+    out = list(grads)
+    for i, g in zip(at, _FirstGradients.apply(len(at), *(grads[i] for i in at), *inputs)):
+        out[i] = g
+    return tuple(out)
+
+
 class _AttnFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, causal, scale, dq_mode):
@@ -425,13 +448,13 @@ class _AttnFunction(torch.autograd.Function):
         q, k, v, o, lse = ctx.saved_tensors
         if do.stride(-1) != 1:
             do = do.contiguous()
-        dq, dk, dv = backward(q, k, v, o, do, lse, ctx.causal, ctx.scale, dq_mode=ctx.dq_mode)
-        return dq, dk, dv, None, None, None
+        grads = backward(q, k, v, o, do, lse, ctx.causal, ctx.scale, dq_mode=ctx.dq_mode)
+        return *_first_gradients(grads, q, k, v, do), None, None, None
 
 
 def attention(q, k, v, causal=False, scale: float | None = None, dq_mode="atomic"):
     """Autograd-aware exact attention over [B, H, N, d] tensors (causal: False, True or "bottom_right";
-    dq_mode: "atomic", "deterministic" or "auto")."""
+    dq_mode: "atomic", "deterministic" or "auto"); a gradient of its gradients raises."""
     scale = (1.0 / q.shape[-1] ** 0.5) if scale is None else scale
     return _AttnFunction.apply(q, k, v, causal, scale, dq_mode)
 
@@ -527,13 +550,15 @@ class _KlFunction(torch.autograd.Function):
         q1, k1, q2, k2, kl, lse1, lse2 = ctx.saved_tensors
         dq, dk = kl_backward(q1, k1, q2, k2, kl, lse1, lse2, g, ctx.train, ctx.causal, ctx.scale,
                              dq_mode=ctx.dq_mode)
+        dq, dk = _first_gradients((dq, dk), q1, k1, q2, k2, g)
         if KL_SETTINGS[ctx.train] == 1:
             return None, None, dq, dk, None, None, None, None
         return dq, dk, None, None, None, None, None, None
 
 
 def attention_kl(q1, k1, q2, k2, causal=False, scale: float | None = None, train="student", dq_mode="atomic"):
-    """Autograd-aware row-wise KL(P1 || P2) [B,H,Nq]; gradients flow to the trained distribution only."""
+    """Autograd-aware row-wise KL(P1 || P2) [B,H,Nq]; gradients flow to the trained distribution only,
+    and a gradient of those raises."""
     scale = (1.0 / q1.shape[-1] ** 0.5) if scale is None else scale
     return _KlFunction.apply(q1, k1, q2, k2, causal, scale, train, dq_mode)
 
@@ -834,29 +859,6 @@ def _plain_strides(t):
     if good and all(n == 1 or (s > 0 and s % 8 == 0) for n, s in ((t.shape[0], sb), (t.shape[1], sh))):
         return t
     return t.clone(memory_format=torch.contiguous_format)
-
-
-class _FirstGradients(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, n, *tensors):
-        return tensors[:n]
-
-    @staticmethod
-    def backward(ctx, *_):
-        raise RuntimeError("a gradient of these gradients is asked for: their kernels are differentiable once")
-
-
-def _first_gradients(grads, *inputs):
-    """`grads` of a backward pass, from `inputs` by kernels that record nothing.  Where they are recorded (create_graph=True) and
-    depend on what needs gradients itself, a gradient of them raises instead of lacking their terms."""
-    inputs = [t for t in inputs if t is not None and t.requires_grad]
-    if not inputs or not torch.is_grad_enabled():
-        return grads
-    at = [i for i, g in enumerate(grads) if g is not None]
-    out = list(grads)
-    for i, g in zip(at, _FirstGradients.apply(len(at), *(grads[i] for i in at), *inputs)):
-        out[i] = g
-    return tuple(out)
 
 
 class _RopeFunction(torch.autograd.Function):
