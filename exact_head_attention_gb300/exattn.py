@@ -864,8 +864,11 @@ def _plain_strides(t):
 class _RopeFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, freq, start, offsets, layout, amplitude, eps):
-        ctx.save_for_backward(q if q_weight is not None else None, k if k_weight is not None else None, q_weight, k_weight,
-                              freq, start, offsets)
+        need_q, need_k, need_qw, need_kw = ctx.needs_input_grad[:4]
+        # the tensors whose gradients are computed: of a norm's weights with its input's
+        ctx.sides = (q is not None and (need_q or need_qw), k is not None and (need_k or need_kw))
+        sides = [(x, w) if some and w is not None else (None, w) for x, w, some in zip((q, k), (q_weight, k_weight), ctx.sides)]
+        ctx.save_for_backward(sides[0][0], sides[1][0], q_weight, k_weight, freq, start, offsets)
         ctx.rest = (layout, amplitude, eps)
         return rope_forward(q, k, freq, start, offsets, layout, amplitude, q_weight, k_weight, eps)
 
@@ -873,9 +876,14 @@ class _RopeFunction(torch.autograd.Function):
     def backward(ctx, dq, dk):
         q, k, q_weight, k_weight, freq, start, offsets = ctx.saved_tensors
         layout, amplitude, eps = ctx.rest
-        grads = rope_backward(_plain_strides(dq), _plain_strides(dk), q, k, freq, start, offsets, layout, amplitude, q_weight,
-                              k_weight, eps)
-        return *_first_gradients(grads, dq, dk, q, k, q_weight, k_weight), None, None, None, None, None, None
+        # weights of a tensor that is not there have gradients of zero
+        weights = [w if some or g is None else None for w, g, some in zip((q_weight, k_weight), (dq, dk), ctx.sides)]
+        dy = [_plain_strides(g) if some else None for g, some in zip((dq, dk), ctx.sides)]
+        if dy[0] is None and dy[1] is None:
+            grads = (None, None, *(None if w is None else torch.zeros_like(w) for w in weights))
+        else:
+            grads = rope_backward(*dy, q, k, freq, start, offsets, layout, amplitude, *weights, eps)
+        return *_first_gradients(grads, *dy, q, k, *weights), None, None, None, None, None, None
 
 
 def rope(q, k, freq, start=None, offsets=None, layout="half", amplitude: float = 1.0, q_weight=None, k_weight=None,

@@ -501,3 +501,41 @@ def test_second_gradients_raise(norm, squared):
         assert not first[0].requires_grad
         penalty.backward()
         assert torch.equal(wanted[0].grad, 2 * wanted[0].detach())
+
+
+@pytest.mark.parametrize("needs", [(1, 0, 0, 0), (0, 1, 0, 0), (0, 0, 1, 0), (0, 0, 0, 1), (1, 0, 1, 0), (1, 1, 0, 0), (0, 1, 1, 0)], ids=str)
+@pytest.mark.parametrize("norm", [False, True])
+def test_gradients_of_some_inputs(needs, norm, monkeypatch):
+    """Inputs and weights that need none: the tensor without is neither kept nor computed, the others' gradients stay as they are."""
+    if not norm and not (needs[0] or needs[1]):
+        pytest.skip("no input needs a gradient")
+    q, k, wq, wk, freq, start, _ = make(2, 4, 2, 50, 64, 64, "bf16", norm, True, seed=28)
+    gf, gs = _gpu(freq, start)
+    leaves = [t if t is None else t.to(DEV) for t in (q, k, wq, wk)]
+    dy = _gpu(_normal(q.shape, 90, q.dtype), _normal(k.shape, 91, k.dtype))
+    want = exattn.rope_backward(*dy, *leaves[:2], gf, gs, q_weight=leaves[2], k_weight=leaves[3])
+    wanted = [i for i in range(4) if needs[i] and leaves[i] is not None]
+    for i in wanted:
+        leaves[i].requires_grad_()
+    calls, plain = [], exattn.rope_backward
+    monkeypatch.setattr(exattn, "rope_backward", lambda *a, **kw: calls.append(a) or plain(*a, **kw))
+    out = exattn.rope(leaves[0], leaves[1], gf, gs, q_weight=leaves[2], k_weight=leaves[3])
+    for i, g in zip(wanted, torch.autograd.grad(out, [leaves[i] for i in wanted], dy)):
+        assert torch.equal(g, want[i])
+    (args,) = calls
+    for side in range(2):
+        some = side in wanted or side + 2 in wanted
+        assert (args[side] is not None) == some and (args[2 + side] is not None) == (some and norm)
+
+
+def test_gradients_of_weights_without_their_tensor():
+    q, _, wq, wk, freq, start, _ = make(1, 2, 2, 16, 64, 64, "bf16", True, True, seed=29)
+    gq, gf, gs, gwq, gwk = _gpu(q, freq, start, wq, wk)
+    for w in (gwq, gwk):
+        w.requires_grad_()
+    out, none = exattn.rope(gq, None, gf, gs, q_weight=gwq, k_weight=gwk)
+    assert none is None
+    a, b = torch.autograd.grad(out.float().sum(), (gwq, gwk))
+    assert torch.any(a != 0) and torch.all(b == 0)
+    out, _ = exattn.rope(gq, None, gf, gs, k_weight=gwk)
+    assert torch.all(torch.autograd.grad(out.float().sum(), gwk)[0] == 0)
