@@ -32,6 +32,7 @@ BWD_STEPS = ("attn_bwd_preprocess", "attn_bwd_kv_blocks", "attn_bwd_dq_convert")
 
 _lock = threading.Lock()
 _lib = None
+_lib_path = None
 
 
 class Strides(ctypes.Structure):
@@ -67,8 +68,9 @@ def last_error() -> str:
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
-    """Load the library (raises OSError if it is missing)."""
-    global _lib
+    """Load the library (raises OSError if it is missing).  With another one than that beside this file the calls of the compiled
+    binding, which calls the latter, are not to be had."""
+    global _lib, _lib_path
     if _lib is not None:
         return _lib
     with _lock:
@@ -155,6 +157,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.attn_check_device_error.restype = i
             lib.attn_last_error.argtypes = []
             lib.attn_last_error.restype = ctypes.c_char_p
+            _lib_path = os.path.realpath(path)
             _lib = lib
     return _lib
 
@@ -163,11 +166,23 @@ _compiled = None
 
 
 def binding():
-    """The compiled binding (_binding.so), behind the library that it calls."""
+    """The compiled binding (_binding.so), behind the library beside it (raises OSError if it is missing or stale)."""
     global _compiled
     if _compiled is None:
         load()
-        from exact_head_attention_gb300 import _binding
+        if _lib_path != os.path.realpath(LIB_PATH):
+            raise OSError(f"{_lib_path} is loaded, and the compiled binding calls {LIB_PATH}: these calls need the latter")
+        from exact_head_attention_gb300 import build
+        hint = "build it with exact_head_attention_gb300.build.build()"
+        if os.path.exists(build.BINDING_STAMP):
+            with open(build.BINDING_STAMP) as f:
+                was = f.read()
+            if was != build._torch_stamp():
+                raise OSError(f"_binding.so is of torch and Python {was}, not {build._torch_stamp()}: {hint}")
+        try:
+            from exact_head_attention_gb300 import _binding
+        except ImportError as e:
+            raise OSError(f"_binding.so not found, or not to be loaded ({e}): {hint}") from e
         _binding.set_error_class(AttnError)
         _compiled = _binding
     return _compiled
@@ -568,6 +583,40 @@ def attention_kl(q1, k1, q2, k2, causal=False, scale: float | None = None, train
 CACHE_FORMATS = {"e4m3": 0, "int8": 1}
 
 
+_CACHE_DTYPES = {torch.float8_e4m3fn: 0, torch.int8: 1}
+_cache_checks = None  # binding().cache_struct, False where there is no binding
+
+
+def _cache_struct(k, v, k_scale, v_scale, page_table) -> CacheStruct:
+    """The attn_cache of checked tensors.  The cache's calls need no compiled binding: it makes this 1.0 us where it is there,
+    for 5.5."""
+    global _cache_checks
+    if _cache_checks is None:
+        try:
+            _cache_checks = binding().cache_struct
+        except OSError:
+            _cache_checks = False
+    if _cache_checks:
+        return CacheStruct.from_buffer_copy(_cache_checks(k, v, k_scale, v_scale, page_table))
+    tensors = (k, v, k_scale, v_scale, page_table)
+    if not all(isinstance(t, torch.Tensor) for t in tensors):
+        raise TypeError("a tensor is wanted")
+    fmt = _CACHE_DTYPES.get(k.dtype)
+    if fmt is None or v.dtype != k.dtype:
+        raise TypeError(f"unsupported cache dtypes {k.dtype}, {v.dtype}; expected float8_e4m3fn or int8 for both")
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or page_table.dtype != torch.int32:
+        raise TypeError("scales must be float32 and the page table int32")
+    if k.dim() != 4 or v.shape != k.shape or page_table.dim() != 2:
+        raise ValueError("k, v must be [num_pages, heads, page, d] and the page table [B, width]")
+    if k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2]:
+        raise ValueError("scales must be [num_pages, heads]")
+    if not all(t.is_cuda and t.get_device() == k.get_device() and t.is_contiguous() for t in tensors):
+        raise ValueError("cache tensors must be contiguous and on one CUDA device")
+    if max(*k.shape, *page_table.shape) > 2 ** 31 - 1:
+        raise ValueError("tensors are too large")
+    return CacheStruct(*(t.data_ptr() for t in tensors), *k.shape, page_table.shape[1], fmt)
+
+
 class QuantCache:
     """An 8-bit key/value cache in pages (attn_cache): the caller's tensors and the struct the library takes.
 
@@ -578,7 +627,7 @@ class QuantCache:
                  "address")
 
     def __init__(self, k, v, k_scale, v_scale, page_table):
-        self.struct = CacheStruct.from_buffer_copy(binding().cache_struct(k, v, k_scale, v_scale, page_table))
+        self.struct = _cache_struct(k, v, k_scale, v_scale, page_table)
         self._ref = ctypes.byref(self.struct)
         self.address = ctypes.addressof(self.struct)
         self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
