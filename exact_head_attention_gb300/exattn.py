@@ -796,10 +796,13 @@ def forward_cache(q, cache: QuantCache, lens, causal="bottom_right", scale: floa
     return _run(cache, stream, call)
 
 
-def _fast(stream, call):
-    """Runs a call of the compiled binding, on `stream` where that is given: what it allocates belongs to it."""
+def _fast(stream, on, call):
+    """Runs a call of the compiled binding on the tensor (or cache) `on`, on `stream` where that is given: what it allocates belongs
+    to it."""
     if stream is None:
         return call()
+    if stream.device != getattr(on, "device", stream.device):
+        raise ValueError("the stream is of another device than the tensors")
     with torch.cuda.device(stream.device), torch.cuda.stream(stream):
         return call()
 
@@ -810,7 +813,7 @@ def draft_tree(parents, stream=None):
     parents: int32 CUDA tensor [B, N] (or [N], one tree for all sequences: B is 1), -1 or the number of an earlier token.
     The mask has each token's ancestors and itself as bits, for forward_cache_tree; the depth is its number of drafted
     ancestors, the offsets of rope_forward and cache_append."""
-    return _fast(stream, lambda: binding().draft_tree(parents))
+    return _fast(stream, parents, lambda: binding().draft_tree(parents))
 
 
 def forward_cache_tree(q, cache: QuantCache, lens, tree, scale: float | None = None, workspace=None, stream=None):
@@ -819,7 +822,7 @@ def forward_cache_tree(q, cache: QuantCache, lens, tree, scale: float | None = N
 
     tree: int32 CUDA tensor [B, Nq, ceil(Nq / 32)], or [1, ...] for all sequences alike (draft_tree): bit j % 32 of word
     j // 32 of row i, for j <= i.  The other arguments as in forward_cache."""
-    return _fast(stream, lambda: binding().forward_cache_tree(cache.address, cache.index, cache.B, q, lens, tree, scale, workspace))
+    return _fast(stream, cache, lambda: binding().forward_cache_tree(cache.address, cache.index, cache.B, q, lens, tree, scale, workspace))
 
 
 # ------------------------------------------------------------------ rotary positions and norms per head
@@ -880,7 +883,8 @@ def rope_forward(q, k, freq, start=None, offsets=None, layout="half", amplitude:
     if out is not None and oq is None and ok is None:
         raise ValueError("out must be a pair of what q and k are")
     code = _layout(layout)
-    return _fast(stream, lambda: binding().rope_forward(q, k, freq, start, offsets, code, amplitude, q_weight, k_weight, eps, oq, ok))
+    return _fast(stream, k if q is None else q,
+                 lambda: binding().rope_forward(q, k, freq, start, offsets, code, amplitude, q_weight, k_weight, eps, oq, ok))
 
 
 def rope_bwd_workspace_size(d: int) -> int:
@@ -896,7 +900,8 @@ def rope_backward(dq, dk, q, k, freq, start=None, offsets=None, layout="half", a
     The weights' gradients are summed in a fixed order; None where there are no weights.  `workspace` (uint8 CUDA tensor of
     rope_bwd_workspace_size bytes, one for each call that may run at the same time) is allocated if omitted."""
     code = _layout(layout)
-    return _fast(stream, lambda: binding().rope_backward(dq, dk, q, k, freq, start, offsets, code, amplitude, q_weight, k_weight, eps, workspace))
+    return _fast(stream, dk if dq is None else dq,
+                 lambda: binding().rope_backward(dq, dk, q, k, freq, start, offsets, code, amplitude, q_weight, k_weight, eps, workspace))
 
 
 def _plain_strides(t):
@@ -957,5 +962,5 @@ def cache_append(cache: QuantCache, k, v, freq, start=None, count=None, offsets=
     of row n of sequence b being start[b] + offsets[b, n] (position_start, where given, in place of start).  q: [B, H, N, d]
     of the same tokens, or None; all its rows are turned, into `out` (which may be q) where that is given."""
     code = _layout(layout)
-    return _fast(stream, lambda: binding().cache_append(cache.address, cache.index, cache.B, k, v, freq, start, count, offsets, q, code,
-                                                        amplitude, q_weight, k_weight, eps, position_start, out))
+    return _fast(stream, cache, lambda: binding().cache_append(cache.address, cache.index, cache.B, k, v, freq, start, count, offsets, q,
+                                                               code, amplitude, q_weight, k_weight, eps, position_start, out))

@@ -187,3 +187,21 @@ def test_binding_refuses_what_it_cannot_pass_on(lib):
     for call in (lambda: exattn.rope_forward(3, q, freq), lambda: exattn.draft_tree(None), lambda: exattn.rope_forward(q, q, freq, amplitude="x")):
         with pytest.raises((TypeError, ValueError)):
             call()
+
+
+def test_a_stream_of_another_device_is_refused(lib):
+    """On the CPU: the tensors' device is compared with the stream's before either is touched."""
+    class Stream:
+        device = torch.device("cuda", 7)
+
+    class Cache:
+        device = torch.device("cuda", 0)
+        address = index = B = 0
+
+    q, freq = torch.zeros((1, 2, 3, 64), dtype=torch.bfloat16), None
+    for call in (lambda s: exattn.rope_forward(q, None, freq, stream=s), lambda s: exattn.rope_forward(None, q, freq, stream=s),
+                 lambda s: exattn.rope_backward(q, None, q, None, freq, stream=s), lambda s: exattn.draft_tree(q, stream=s),
+                 lambda s: exattn.cache_append(Cache(), q, q, freq, stream=s),
+                 lambda s: exattn.forward_cache_tree(q, Cache(), None, None, stream=s)):
+        with pytest.raises(ValueError, match="another device"):
+            call(Stream())
