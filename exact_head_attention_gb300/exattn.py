@@ -839,7 +839,9 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None
       "linear"  positions divided by the factor
       "ntk"     the base raised so that the slowest pair is interpolated and the fastest stays
       "yarn"    (Peng et al., 2023) pairs with more than `fast` turns over the `trained` positions as they are, with fewer
-                than `slow` interpolated, a ramp between; the amplitude 0.1 ln(factor) + 1 on queries and keys"""
+                than `slow` interpolated, between them by a ramp linear in the turns, as the paper's formula has it; the amplitude
+                0.1 ln(factor) + 1 on queries and keys.  Models made with that paper's released code ramp linearly in the
+                pair's number between two rounded bounds instead: their frequencies are to be given as they are."""
     if rotary_dim <= 0 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and above 0")
     if not (base > 0 and factor > 0):
