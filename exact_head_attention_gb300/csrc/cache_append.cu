@@ -200,15 +200,15 @@ __global__ void __launch_bounds__(kIoThreads, NV == 4 ? kAppendBlocks : 2) cache
     if (rv.rot > 0 && r0 < r1) {
       const long long first = (rv.start ? rv.start[b] : 0) + (rv.offsets ? 0 : un.row_of_r0 - r0);
       const int* offsets = rv.offsets ? rv.offsets + b * rv.offset_stride + (un.row_of_r0 - r0) : nullptr;
-      const int threads = GT << a.head_shift, at = threadIdx.x & (threads - 1), step = max(1, threads / SLOTS);
-      for (int slot = threads < SLOTS ? at : at & (SLOTS - 1); slot < SLOTS; slot += threads) {
-        const int h = slot / (SLOTS / 2), lane = slot / 4 % Lane::LANES;
-        const int pair = (INTER ? 4 * (lane + h * Lane::LANES) : 8 * lane + 4 * h) + (slot & 3);
-        if (pair >= rv.rot >> 1) continue;
+      static_assert(GT >= SLOTS, "a thread for each of a row's pairs at least");
+      const int at = threadIdx.x & ((GT << a.head_shift) - 1), step = (GT << a.head_shift) / SLOTS, slot = at & (SLOTS - 1);
+      const int h = slot / (SLOTS / 2), lane = slot / 4 % Lane::LANES;
+      const int pair = (INTER ? 4 * (lane + h * Lane::LANES) : 8 * lane + 4 * h) + (slot & 3);
+      if (pair < rv.rot >> 1) {
         bool good;
         const uint64_t turns = turns_of(rv.freq[pair], good);
         const float amplitude = good ? rv.amplitude : __int_as_float(0x7fffffff);
-        const int first_row = r0 + (threads < SLOTS ? 0 : at / SLOTS);
+        const int first_row = r0 + at / SLOTS;
         auto direct = [&](uint64_t angle, float& co, float& si) { sin_cos_turns(static_cast<uint32_t>(angle >> 32), si, co); };
         auto put = [&](int row, float co, float si) {
           cosines[row * SLOTS + slot] = co;
