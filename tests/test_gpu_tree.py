@@ -401,3 +401,47 @@ def test_many_rows_are_about_as_exact_as_their_output(group, n, d, code, wide):
     want = plain_attention(q, host, table, lens, sees, scale)[0]
     off, own = (torch.linalg.norm(x.double().cpu() - want) / torch.linalg.norm(want) for x in (o, want.half()))
     assert off <= 1.69 * own + 2.0 ** -15, (off, own)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_the_accepted_path_of_every_sequence(code):
+    """What a server does after a step of drafting: each sequence's accepted path is appended over its drafts, as many tokens as it
+    has (the rest of the rows are padding), and the next queries see a plain sequence.  The cache's new keys are compared with the
+    definition, and the attention over it with that over the cache as it then is."""
+    B, heads, group, n, d, page = 2, 2, 3, 11, 64, 16
+    start = torch.tensor([37, 128], dtype=torch.int32)
+    g = torch.Generator().manual_seed(54)
+    parents = random_parents(B, n, 55)
+    sees, depth = plain_tree(parents)
+    prompt = torch.randn((B, heads, 128, d), generator=g).to(torch.bfloat16)
+    q, k, v = (torch.randn((B, h, n, d), generator=g).to(torch.bfloat16) for h in (heads * group, heads, heads))
+    freq, w = exattn.rope_frequencies(d)[0], torch.linspace(0.5, 1.5, d)
+    table = torch.randperm(B * 9, generator=g).reshape(B, 9).to(torch.int32)
+    cache = exattn.QuantCache.empty(B * 9, heads, page, d, table.to(DEV), code)
+    exattn.cache_append(cache, prompt.to(DEV), prompt.to(DEV), freq, None, start.to(DEV), k_weight=w.to(DEV))
+    _, dep = exattn.draft_tree(parents.to(DEV))
+    exattn.cache_append(cache, k.to(DEV), v.to(DEV), freq, start.to(DEV), offsets=dep, k_weight=w.to(DEV))
+    paths = [torch.nonzero(sees[b, int(depth[b].argmax())])[:, 0] for b in range(B)]
+    counts = [len(p) for p in paths]
+    most = max(counts)
+    at = torch.stack([torch.nn.functional.pad(p, (0, most - len(p))) for p in paths])[:, None, :, None]
+    pq, pk, pv = (x.gather(2, at.expand(-1, x.shape[1], -1, d)) for x in (q, k, v))
+    lens = [int(s) + c for s, c in zip(start, counts)]
+    r = exattn.cache_append(cache, *(x.to(DEV) for x in (pk, pv)), freq, start.to(DEV), torch.tensor(counts, dtype=torch.int32, device=DEV),
+                            q=pq.to(DEV), q_weight=w.to(DEV), k_weight=w.to(DEV))
+    assert exattn.check_device_error() == 0
+    host = {x: getattr(cache, x).cpu() for x in ("k", "v", "k_scale", "v_scale")}
+    y, size = plain_rope.norm_rotate(pk, freq.cpu(), start[:, None].long() + torch.arange(most), weight=w)
+    want, _ = plain_rope.norm_rotate(pq, freq.cpu(), start[:, None].long() + torch.arange(most), weight=w)
+    assert torch.all((r.double().cpu() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -18 * want.abs().amax(-1, keepdim=True))
+    for b in range(B):
+        c, s0 = counts[b], int(start[b])
+        scales = torch.stack([host["k_scale"][int(table[b, (s0 + i) // page])] for i in range(c)], 1).double()[..., None]
+        got = tokens(host, "k", table, b, lens[b])[:, s0:]
+        step = 0.5 * scales.expand_as(got) if code == "int8" else torch.maximum(y[b, :, :c].abs() * 2.0 ** -4, scales * 2.0 ** -10)
+        assert torch.all((got - y[b, :, :c]).abs() <= step * (1 + 2.0 ** -18) + 2.0 ** -18 * size[b, :, :c])
+        # this sequence's path alone, as the last tokens of a plain sequence
+        own = exattn.QuantCache(cache.k, cache.v, cache.k_scale, cache.v_scale, table[b : b + 1].to(DEV))
+        o, lse = exattn.forward_cache(r[b : b + 1, :, :c].contiguous(), own, torch.tensor(lens[b : b + 1], dtype=torch.int32, device=DEV))
+        check(r[b : b + 1, :, :c].cpu(), own, host, table[b : b + 1], lens[b : b + 1], torch.ones((1, c, c), dtype=torch.bool), got=(o, lse))
+    assert counts[0] != counts[1]
