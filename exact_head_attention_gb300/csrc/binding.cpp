@@ -1,6 +1,6 @@
 // The Python calls of the operators between projections and attention, and of drafted trees: argument checks, allocation and
 // the C-ABI call in compiled code, for calls whose kernels take a few microseconds.  Marshalled in Python by ctypes, a call
-// that rotates one token took 17.5 us on the host; here it takes 6.6.  exattn.py has the signatures and their documentation.
+// that rotates one token took 17.5 us on the host; here it takes 7 to 8, of which its two outputs and the launch are 6.6.  exattn.py has the signatures and their documentation.
 //
 // The library itself (libexattn.so) knows nothing of torch: this module links against it and is loaded by exattn.py alone.
 #include <Python.h>

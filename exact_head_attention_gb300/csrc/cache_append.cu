@@ -15,7 +15,7 @@
 // Measured, 4 prompts of 8192 tokens, 12 heads of 128, without queries (302 MB, 44.6 us at the copy rate; the write without
 // norm and rotation takes 47.5): each thread the angles of its own page and head 110 us; from shared memory, 64 values a
 // thread, 109 (spilled registers); 32 values and copies ahead 64; fp32 pairs 58; all 12 heads in a block 56.  With as many
-// queries 80 us (503 MB, 93 %).  One token of each of 64 sequences, 8 heads, with 32 query heads: 6.6 us.
+// queries 80 us (503 MB, 93 %).  One token of each of 64 sequences, 8 heads, with 32 query heads: 6.3 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
