@@ -308,13 +308,14 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, RopeShared& sh, uns
     float x[16];
     Lane::template widen<BF16>(sh.slots[from][0][threadIdx.x], sh.slots[from][1][threadIdx.x], x);
     from = from + 1 == DEPTH ? 0 : from + 1;
-    float r = 1.f;
-    if (any_norm) r = Lane::inverse_rms(x, a.r.eps);
-    f.apply(l, x);
-    if (norm) {
+    if (any_norm) {
+      const float r = Lane::inverse_rms(x, a.r.eps);
+      if (norm) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] *= r;
+        for (int e = 0; e < 16; ++e) x[e] *= r;  // first, so that no product of a weight is out of range before
+      }
     }
+    f.apply(l, x);
     if (i < here) l.template store<BF16>(dst, x);
     dst += sd.sy.h;
   }

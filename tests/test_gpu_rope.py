@@ -537,3 +537,18 @@ def test_gradients_of_weights_without_their_tensor():
     assert torch.any(a != 0) and torch.all(b == 0)
     out, _ = exattn.rope(gq, None, gf, gs, k_weight=gwk)
     assert torch.all(torch.autograd.grad(out.float().sum(), gwk)[0] == 0)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_norms_of_very_small_rows_and_very_large_weights(layout, d):
+    """Rows below 2^-126, whose norm eps makes: their products with weights and cosines would lose digits before it.  And weights
+    that would bring a row of 1e15 beyond fp32 before it."""
+    q, k, wq, wk, freq, start, _ = make(2, 3, 2, 21, d, d, "bf16", True, True, seed=30)
+    q = (q.float() * torch.tensor([1e-38, 1e-39, 1e-40])[None, :, None, None]).to(q.dtype)
+    k = (k.float() * 1e15).to(k.dtype)
+    check_forward(q, k, wq, wk * 1e25, freq, start, None, layout, out=exattn.rope_forward(
+        *_gpu(q, k, freq, start), layout=layout, q_weight=wq.to(DEV), k_weight=(wk * 1e25).to(DEV)))
+    pos = plain_rope.positions(2, 21, start)
+    got, _ = exattn.rope_forward(*_gpu(q, None, freq, start), layout=layout, q_weight=wq.to(DEV), eps=1e-12)
+    check(got, *plain_rope.norm_rotate(q, freq, pos, layout, weight=wq, eps=1e-12), 2.0 ** -19)
